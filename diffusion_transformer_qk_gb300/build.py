@@ -41,6 +41,8 @@ SOURCES = [
     "adaln_api.cu",
     "adaln_inst.cu",
     "gn_api.cu",
+    "ln_api.cu",
+    "grad_api.cu",
 ]
 
 

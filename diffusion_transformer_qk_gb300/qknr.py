@@ -45,11 +45,14 @@ EXPORTS = (
     "qknr_gn_args_init", "qknr_gn_workspace_bytes", "qknr_gn_silu_forward", "qknr_gn_sizeof_args",
     "qknr_gn_silu_forward_noalloc", "qknr_gn_query",
     "qknr_host_plan_init", "qknr_host_buffer_bytes", "qknr_forward_host", "qknr_sizeof_host_plan",
+    "qknr_ln_args_init", "qknr_ln_forward", "qknr_ln_workspace_bytes", "qknr_ln_backward", "qknr_ln_sizeof_args",
+    "qknr_grad_args_init", "qknr_grad_workspace_bytes", "qknr_backward", "qknr_sizeof_grad_args",
 )
 GN_MODE = {"auto": 0, "fused": 1, "two_pass": 2, "cluster": 3}
 GN_FLAG_TEST_NO_RECORDS = 0x2
 GN_NOALLOC_SCRATCH_BYTES = 1 << 20
 HOST_MAX_BUFFERS = 4
+LN_UNIT_OFFSET = 0x10
 
 
 class QknrArgs(ctypes.Structure):
@@ -130,6 +133,45 @@ class QknrHostPlan(ctypes.Structure):
     ]
 
 
+class QknrLnArgs(ctypes.Structure):
+    """Mirror of ``qknr_ln_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("x", c_void_p), ("y", c_void_p),
+        ("x_stride", c_int64), ("y_stride", c_int64),
+        ("tokens", c_int64), ("hidden", c_int32), ("rows_per_batch", c_int64),
+        ("weight", c_void_p), ("bias", c_void_p), ("param_dtype", c_int32), ("param_stride", c_int64),
+        ("eps", c_float), ("mean", c_void_p), ("rstd", c_void_p),
+        ("dy", c_void_p), ("dx", c_void_p),
+        ("dy_stride", c_int64), ("dx_stride", c_int64),
+        ("dweight", c_void_p), ("dbias", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32),
+    ]
+
+
+class QknrGradArgs(ctypes.Structure):
+    """Mirror of ``qknr_grad_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p),
+        ("dq_out", c_void_p), ("dk_out", c_void_p), ("dv_out", c_void_p),
+        ("q_stride", c_int64), ("k_stride", c_int64),
+        ("dq_stride", c_int64), ("dk_stride", c_int64), ("dv_stride", c_int64),
+        ("dq_out_stride", c_int64), ("dk_out_stride", c_int64), ("dv_out_stride", c_int64),
+        ("tokens", c_int64),
+        ("n_heads_q", c_int32), ("n_heads_k", c_int32), ("n_heads_v", c_int32), ("head_dim", c_int32),
+        ("gamma_q", c_void_p), ("gamma_k", c_void_p), ("eps", c_float),
+        ("cos", c_void_p), ("sin", c_void_p),
+        ("cos_dtype", c_int32), ("cos_layout", c_int32), ("cos_rows", c_int64), ("rope_style", c_int32),
+        ("dgamma_q", c_void_p), ("dgamma_k", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32),
+    ]
+
+
 class QknrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -195,12 +237,24 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.qknr_forward_host.argtypes = [ctypes.POINTER(QknrArgs), ctypes.POINTER(QknrHostPlan), c_void_p]
         lib.qknr_forward_host.restype = c_int32
         lib.qknr_sizeof_host_plan.restype = c_size_t
+        for name, struct in (("ln", QknrLnArgs), ("grad", QknrGradArgs)):
+            p_struct = ctypes.POINTER(struct)
+            init, space = getattr(lib, f"qknr_{name}_args_init"), getattr(lib, f"qknr_{name}_workspace_bytes")
+            init.argtypes, init.restype = [p_struct], None
+            space.argtypes, space.restype = [p_struct, ctypes.POINTER(c_size_t)], c_int32
+        for fn, struct in ((lib.qknr_ln_forward, QknrLnArgs), (lib.qknr_ln_backward, QknrLnArgs),
+                           (lib.qknr_backward, QknrGradArgs)):
+            fn.argtypes, fn.restype = [ctypes.POINTER(struct), c_void_p], c_int32
+        lib.qknr_ln_sizeof_args.restype = c_size_t
+        lib.qknr_sizeof_grad_args.restype = c_size_t
         if lib.qknr_abi_version() != ABI_VERSION:
             raise RuntimeError("libqknr.so ABI version mismatch")
         if lib.qknr_sizeof_args() != ctypes.sizeof(QknrArgs) or \
                 lib.qknr_sizeof_launch_info() != ctypes.sizeof(QknrLaunchInfo) or \
                 lib.qknr_adaln_sizeof_args() != ctypes.sizeof(QknrAdaLNArgs) or \
                 lib.qknr_gn_sizeof_args() != ctypes.sizeof(QknrGnArgs) or \
+                lib.qknr_ln_sizeof_args() != ctypes.sizeof(QknrLnArgs) or \
+                lib.qknr_sizeof_grad_args() != ctypes.sizeof(QknrGradArgs) or \
                 lib.qknr_sizeof_host_plan() != ctypes.sizeof(QknrHostPlan):
             raise RuntimeError("libqknr.so struct layout differs from the binding")
         if path is None:
@@ -760,3 +814,238 @@ def gn_launch_noalloc(a: QknrGnArgs, stream: Optional[torch.cuda.Stream] = None)
     st = lib.qknr_gn_silu_forward_noalloc(ctypes.byref(a), c_void_p(s.cuda_stream))
     if st != OK:
         raise QknrError(st, lib.qknr_last_error().decode())
+
+
+# ---------------------------------------------------------------------------
+# training: helpers of the entry points below
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor on like's device that belongs to the stream the call runs
+    on, so that its memory is not handed out again while that stream uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _call(fn, a, stream) -> None:
+    """One library call on ``stream`` (default: the current stream)."""
+    s = torch.cuda.current_stream() if stream is None else stream
+    st = fn(ctypes.byref(a), c_void_p(s.cuda_stream))
+    if st != OK:
+        raise QknrError(st, load().qknr_last_error().decode())
+
+
+def _workspace(fn, a, workspace, like, stream):
+    """Put a workspace into ``a``: the caller's, or a new one of the size the
+    library asks for.  Returns the tensor (to be kept until the call)."""
+    if workspace is None:
+        n = c_size_t(0)
+        st = fn(ctypes.byref(a), ctypes.byref(n))
+        if st != OK:
+            raise QknrError(st, load().qknr_last_error().decode())
+        workspace = _empty((max(n.value, 16),), torch.uint8, like, stream)
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _match(t, like, name):
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name} must match {like.dtype} {tuple(like.shape)}")
+    return t
+
+
+def _vector(t, n, name):
+    """A contiguous float32 CUDA tensor of n values."""
+    if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} values")
+    return t
+
+
+# ---------------------------------------------------------------------------
+# layer norm and its backward pass (include/qknr_ln.h)
+
+def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False, eps=1e-6, dev_status=None,
+            flags=0) -> QknrLnArgs:
+    """The arguments both passes share: token rows ``x`` [T, C], ``weight``
+    and ``bias`` [C] or [B, C] (float32 or x's dtype; either may be None) and
+    which of their rows a token takes (t // rows_per_batch; default: one
+    row)."""
+    a = QknrLnArgs()
+    load().qknr_ln_args_init(ctypes.byref(a))
+    if x.dtype not in _ACT:
+        raise ValueError("x must be bfloat16 or float16")
+    a.dtype = _ACT[x.dtype]
+    a.x, a.x_stride = x.data_ptr(), _rows(x, "x")
+    a.tokens, a.hidden = x.shape
+    a.rows_per_batch = rows_per_batch or 0
+    sets = -(-x.shape[0] // rows_per_batch) if rows_per_batch else 1
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        rows = t.view(1, -1) if t.dim() == 1 else t
+        if rows.dim() != 2 or rows.shape[1] != x.shape[1] or rows.shape[0] < sets:
+            raise ValueError(f"{name} must be [C] or [{sets}, C]")
+        if t.dtype not in (torch.float32, x.dtype) or (weight is not None and t.dtype != weight.dtype):
+            raise ValueError("weight and bias must both be float32 or both of x's dtype")
+        stride = _rows(rows, name)
+        if rows.shape[0] > 1 and a.param_stride and stride != a.param_stride:
+            raise ValueError("weight and bias need the same row stride")
+        if rows.shape[0] > 1:
+            a.param_stride = stride
+        a.param_dtype = FP32 if t.dtype == torch.float32 else a.dtype
+        setattr(a, name, t.data_ptr())
+    a.eps = eps
+    a.dev_status = _ptr(dev_status)
+    a.flags = flags | (LN_UNIT_OFFSET if unit_offset else 0)
+    return a
+
+
+def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False, out=None, mean=None, rstd=None,
+               eps=1e-6, stream=None, status=True, **kw):
+    """Layer norm of token rows ``x`` [T, C] for training: returns (y, mean,
+    rstd), the last two float32 [T] for the backward pass.
+
+    ``weight``/``bias`` are [C], or [B, C] with row t taking row
+    t // rows_per_batch; with ``unit_offset`` the gain is 1 + weight (the
+    modulated norm of ``adaln_modulate``).  The result goes to ``out``, a new
+    tensor by default (the backward pass needs x); ``out=x`` is in place."""
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(x.device)
+    a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, **kw)
+    T = x.shape[0]
+    out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
+    mean = _empty((T,), torch.float32, x, stream) if mean is None else _vector(mean, T, "mean")
+    rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd")
+    a.y, a.y_stride = out.data_ptr(), _rows(out, "out")
+    a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
+    _call(load().qknr_ln_forward, a, stream)
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_offset=False, out=None, dweight=None,
+                        dbias=None, workspace=None, stream=None, status=True, **kw):
+    """Gradients of ``layer_norm``: returns (dx, dweight, dbias), the last two
+    float32, of weight's shape ([C] where weight is None).  ``out`` receives
+    dx (default: a new tensor; ``out=dy`` is in place)."""
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(x.device)
+    a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, **kw)
+    T, C = x.shape
+    sets = -(-T // rows_per_batch) if rows_per_batch else 1
+    out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
+    a.dy, a.dy_stride = _match(dy, x, "dy").data_ptr(), _rows(dy, "dy")
+    a.dx, a.dx_stride = out.data_ptr(), _rows(out, "out")
+    a.mean, a.rstd = _vector(mean, T, "mean").data_ptr(), _vector(rstd, T, "rstd").data_ptr()
+    shape = ((sets, C) if rows_per_batch else (C,)) if weight is None else \
+        (weight.shape if weight.dim() == 1 else (sets, C))
+    dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, sets * C, "dweight")
+    dbias = _empty(shape, torch.float32, x, stream) if dbias is None else _vector(dbias, sets * C, "dbias")
+    a.dweight, a.dbias = dweight.data_ptr(), dbias.data_ptr()
+    lib = load()
+    workspace = _workspace(lib.qknr_ln_workspace_bytes, a, workspace, x, stream)
+    _call(lib.qknr_ln_backward, a, stream)
+    return out, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# the backward pass of the fused QK-RMSNorm + RoPE (include/qknr_grad.h)
+
+def grad_args(*, head_dim, q=None, k=None, dq=None, dk=None, dv=None, dq_out=None, dk_out=None, dv_out=None,
+              n_heads_q=0, n_heads_k=0, n_heads_v=0, gamma_q=None, gamma_k=None, cos=None, sin=None,
+              rope_style="interleaved", cos_layout="shared_row", cos_rows=None, eps=1e-6, tokens=0, dev_status=None,
+              flags=0) -> QknrGradArgs:
+    """Build a ``QknrGradArgs`` from tensors: q and k as the forward call got
+    them, dq, dk and dv the gradients of its outputs."""
+    a = QknrGradArgs()
+    load().qknr_grad_args_init(ctypes.byref(a))
+    acts = {"q": q, "k": k, "dq": dq, "dk": dk, "dv": dv, "dq_out": dq_out, "dk_out": dk_out, "dv_out": dv_out}
+    given = [t for t in acts.values() if t is not None]
+    if not given or given[0].dtype not in _ACT or any(t.dtype != given[0].dtype for t in given):
+        raise ValueError("q, k and the gradients must share one dtype: bfloat16 or float16")
+    a.dtype = _ACT[given[0].dtype]
+    for name, t in acts.items():
+        if t is None:
+            continue
+        heads = {"q": n_heads_q, "k": n_heads_k, "v": n_heads_v}[name.replace("_out", "")[-1]]
+        stride = _rows(t, name)
+        if t.shape != (tokens, heads * head_dim):
+            raise ValueError(f"{name} must be [{tokens}, {heads * head_dim}]")
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_stride", stride)
+    a.tokens = tokens
+    a.n_heads_q, a.n_heads_k, a.n_heads_v, a.head_dim = n_heads_q, n_heads_k, n_heads_v, head_dim
+    for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if g is not None:
+            setattr(a, name, _vector(g, head_dim, name).data_ptr())
+    a.eps = eps
+    if cos is not None:
+        if cos.dtype not in _TAB or sin is None or sin.dtype != cos.dtype or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be of one shape, both float32 or both bfloat16")
+        if not (cos.is_contiguous() and sin.is_contiguous() and cos.is_cuda and sin.is_cuda):
+            raise ValueError("cos and sin must be contiguous CUDA tensors")
+        a.cos_dtype = _TAB[cos.dtype]
+        a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
+        a.cos_rows = cos.shape[0] if cos_rows is None else cos_rows
+    a.cos_layout = COS_LAYOUT[cos_layout]
+    a.rope_style = ROPE[rope_style]
+    a.dev_status = _ptr(dev_status)
+    a.flags = flags
+    return a
+
+
+def _grad_launch(a, like, dgamma, workspace, stream):
+    lib = load()
+    for name, g in dgamma.items():
+        setattr(a, name, None if g is None else g.data_ptr())
+    workspace = _workspace(lib.qknr_grad_workspace_bytes, a, workspace, like, stream)
+    _call(lib.qknr_backward, a, stream)
+
+
+def qk_norm_rope_packed_backward(dout, qkv, n_heads_q, n_heads_k, n_heads_v, head_dim, gamma_q, gamma_k, cos, sin, *,
+                                 out=None, workspace=None, stream=None, status=True, **kw):
+    """Backward pass of ``qk_norm_rope_packed``: ``qkv`` is that call's input
+    (run it with ``out=``, so that the input survives), ``dout`` the gradient
+    of its output.  Returns (dqkv, dgamma_q, dgamma_k), the gains' gradients
+    float32 [head_dim].  In place of ``dout`` unless ``out`` is given, which
+    also receives a copy of V's gradient."""
+    D = head_dim
+    width = (n_heads_q + n_heads_k + n_heads_v) * D
+    if qkv.dim() != 2 or qkv.shape[1] != width:
+        raise ValueError(f"qkv must be [tokens, {width}]")
+    _match(dout, qkv, "dout")
+    _check_table(cos, D, kw.get("cos_layout", "shared_row"), n_heads_q or n_heads_k)
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(qkv.device)
+    q0, k0, v0, v1 = 0, n_heads_q * D, (n_heads_q + n_heads_k) * D, width
+
+    def cols(t, a, b):
+        return None if t is None or a == b else t[:, a:b]
+
+    if out is not None:
+        _match(out, qkv, "out")
+    a = grad_args(q=cols(qkv, q0, k0), k=cols(qkv, k0, v0), dq=cols(dout, q0, k0), dk=cols(dout, k0, v0),
+                  dv=cols(dout, v0, v1), dq_out=cols(out, q0, k0), dk_out=cols(out, k0, v0), dv_out=cols(out, v0, v1),
+                  n_heads_q=n_heads_q, n_heads_k=n_heads_k, n_heads_v=n_heads_v, head_dim=D,
+                  gamma_q=gamma_q if n_heads_q else None, gamma_k=gamma_k if n_heads_k else None, cos=cos, sin=sin,
+                  tokens=qkv.shape[0], **kw)
+    dgq = _empty((D,), torch.float32, qkv, stream) if n_heads_q else None
+    dgk = _empty((D,), torch.float32, qkv, stream) if n_heads_k else None
+    _grad_launch(a, qkv, {"dgamma_q": dgq, "dgamma_k": dgk}, workspace, stream)
+    return dout if out is None else out, dgq, dgk
+
+
+def qk_norm_rope_tensor_backward(dout, x, n_heads, head_dim, gamma, cos, sin, *, out=None, workspace=None, stream=None,
+                                 status=True, **kw):
+    """Backward pass of ``qk_norm_rope_tensor`` (one Q or K tensor [T, H*D]):
+    returns (dx, dgamma).  In place of ``dout`` unless ``out`` is given."""
+    if x.dim() != 2 or x.shape[1] != n_heads * head_dim:
+        raise ValueError("x must be [tokens, n_heads*head_dim]")
+    _check_table(cos, head_dim, kw.get("cos_layout", "shared_row"), n_heads)
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(x.device)
+    a = grad_args(q=x, dq=_match(dout, x, "dout"), dq_out=None if out is None else _match(out, x, "out"),
+                  n_heads_q=n_heads, head_dim=head_dim, gamma_q=gamma, cos=cos, sin=sin, tokens=x.shape[0], **kw)
+    dgamma = _empty((head_dim,), torch.float32, x, stream)
+    _grad_launch(a, x, {"dgamma_q": dgamma}, workspace, stream)
+    return dout if out is None else out, dgamma

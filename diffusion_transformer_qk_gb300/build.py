@@ -43,6 +43,7 @@ SOURCES = [
     "gn_api.cu",
     "ln_api.cu",
     "grad_api.cu",
+    "attn_api.cu",
 ]
 
 

@@ -1,0 +1,314 @@
+// C-ABI launchers of attention and its backward pass: validation, tensor
+// maps, launch planning and the launches.  No allocation, no synchronisation.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "../../include/qknr_attn.h"
+#include "attn_kernel.cuh"
+#include "qknr_host.h"
+
+namespace {
+
+using qknr_host::aligned16;
+using qknr_host::fail;
+using qknr_host::Span;
+using qknr_host::span_of;
+
+qknr::MemSpan msp(Span s) { return qknr::MemSpan{s.lo, s.hi}; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor map encoder, looked up once.
+qknr_status encoder(EncodeFn* out) {
+  static EncodeFn fn = nullptr;
+  if (!fn) {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return qknr_host::cuda_fail(e, "cudaGetDriverEntryPointByVersion");
+    if (found != cudaDriverEntryPointSuccess || !sym)
+      return fail(QKNR_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    fn = reinterpret_cast<EncodeFn>(sym);
+  }
+  *out = fn;
+  return QKNR_OK;
+}
+
+// Token rows as [batch][heads][D/64][rows][64], boxes of 128 rows of one
+// head.  Rows past the sequence read as zero.
+qknr_status make_map(CUtensorMap* map, const qknr_attn_args* a, const void* base, long long stride, int seq, int heads) {
+  EncodeFn enc;
+  const qknr_status st = encoder(&enc);
+  if (st != QKNR_OK) return st;
+  const cuuint64_t D = a->head_dim, row = static_cast<cuuint64_t>(stride) * 2;
+  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(seq), D / 64, static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(a->batch)};
+  const cuuint64_t strides[4] = {row, 128, D * 2, row * seq};
+  const cuuint32_t box[5] = {64, qknr::kTile, static_cast<cuuint32_t>(D / 64), 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(map, a->dtype == QKNR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         5, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QKNR_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
+  return QKNR_OK;
+}
+
+qknr_status check_shape(const qknr_attn_args* a) {
+  if (!a) return fail(QKNR_ERR_NULL, "args is NULL");
+  if (a->abi_version != QKNR_ABI_VERSION)
+    return fail(QKNR_ERR_ABI, "abi_version %u, library expects %d", a->abi_version, QKNR_ABI_VERSION);
+  if (a->dtype != QKNR_BF16 && a->dtype != QKNR_FP16)
+    return fail(QKNR_ERR_UNSUPPORTED, "activation dtype must be BF16 or FP16");
+  if (a->head_dim != 64 && a->head_dim != 128)
+    return fail(QKNR_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128)", a->head_dim);
+  if (a->batch < 0 || a->seq_q < 0 || a->seq_k < 0) return fail(QKNR_ERR_SHAPE, "negative batch or sequence");
+  if (a->n_heads_q < 1 || a->n_heads_k < 1 || a->n_heads_q % a->n_heads_k)
+    return fail(QKNR_ERR_SHAPE, "n_heads_q %d must be a positive multiple of n_heads_k %d", a->n_heads_q, a->n_heads_k);
+  if (a->scale != 0.0f && !(a->scale > 0.0f && std::isfinite(a->scale)))
+    return fail(QKNR_ERR_SHAPE, "scale must be positive (0: 1 / sqrt(head_dim))");
+  const long long q_tiles = (a->seq_q + 127LL) / 128, k_tiles = (a->seq_k + 127LL) / 128;
+  if (q_tiles * a->n_heads_q * a->batch > 0x7fffffffLL || k_tiles * a->n_heads_k * a->batch > 0x7fffffffLL ||
+      static_cast<long long>(a->seq_q) * a->batch > 0x7fffffffLL || static_cast<long long>(a->seq_k) * a->batch > 0x7fffffffLL)
+    return fail(QKNR_ERR_UNSUPPORTED, "more than 2^31 rows or tiles");
+  return QKNR_OK;
+}
+
+struct Rows {                 // a tensor of token rows
+  const char* name;
+  const void* base;
+  long long stride;           // elements
+  int seq, heads;
+  Span span;
+};
+
+// Fills in the default stride and checks one tensor.  A NULL base is an
+// error unless the tensor has no rows.
+qknr_status check_rows(const qknr_attn_args* a, Rows* r) {
+  const long long width = static_cast<long long>(r->heads) * a->head_dim, n = static_cast<long long>(a->batch) * r->seq;
+  if (r->stride == 0) r->stride = width;
+  if (r->stride < width) return fail(QKNR_ERR_SHAPE, "%s_stride is smaller than heads * head_dim", r->name);
+  if (r->stride >= (1LL << 31)) return fail(QKNR_ERR_UNSUPPORTED, "%s_stride of 2^31 elements or more", r->name);
+  if ((r->stride * 2) % 16 || !aligned16(r->base))
+    return fail(QKNR_ERR_ALIGN, "%s base or row stride not 16-byte aligned", r->name);
+  if (n > 0 && !r->base) return fail(QKNR_ERR_NULL, "%s is required", r->name);
+  r->span = span_of(r->base, n, r->stride * 2, width * 2);
+  return QKNR_OK;
+}
+
+// Checks `ins` against `outs`; outputs may interleave with each other
+// (column views of one packed buffer) but not with an input.
+qknr_status check_overlap(const Span* outs, int n_out, const Span* ins, int n_in) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = 0; j < n_in; ++j)
+      if (qknr_host::overlaps(outs[i], ins[j])) return fail(QKNR_ERR_OVERLAP, "an output overlaps an input");
+  return QKNR_OK;
+}
+
+// What both passes share, once the shapes are known to be good.
+qknr_status common(const qknr_attn_args* a, qknr::AttnParams* kp) {
+  if ((reinterpret_cast<uintptr_t>(a->lse) | reinterpret_cast<uintptr_t>(a->q_lens) | reinterpret_cast<uintptr_t>(a->k_lens)) & 3u)
+    return fail(QKNR_ERR_ALIGN, "lse, q_lens or k_lens not 4-byte aligned");
+  kp->batch = a->batch;
+  kp->seq_q = a->seq_q;
+  kp->seq_k = a->seq_k;
+  kp->heads_q = a->n_heads_q;
+  kp->heads_k = a->n_heads_k;
+  kp->group = a->n_heads_q / a->n_heads_k;
+  kp->causal = a->causal != 0;
+  kp->scale = a->scale != 0.0f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->head_dim));
+  kp->scale_log2 = kp->scale * qknr::kLog2e;
+  kp->lse = a->lse;
+  kp->q_lens = a->q_lens;
+  kp->k_lens = a->k_lens;
+  kp->flags = a->flags;
+  kp->status = a->dev_status;
+  kp->wait_limit_ns = a->wait_limit_ns ? a->wait_limit_ns : 2000000000ull;
+  const long long n_lse = static_cast<long long>(a->batch) * a->n_heads_q * a->seq_q;
+  kp->sp_lse = msp(span_of(a->lse, n_lse, 4, 4));
+  kp->sp_q_lens = msp(span_of(a->q_lens, a->batch, 4, 4));
+  kp->sp_k_lens = msp(span_of(a->k_lens, a->batch, 4, 4));
+  return QKNR_OK;
+}
+
+size_t delta_bytes(const qknr_attn_args* a) {
+  return (static_cast<size_t>(a->batch) * a->n_heads_q * a->seq_q * 4 + 15) / 16 * 16;
+}
+
+qknr_status launch(const void* fn, long long grid, int block, int smem, const qknr_attn_args* a, qknr::AttnParams* kp,
+                   int dev, const qknr_host::DeviceInfo& di, qknr_stream_t stream, const char* what) {
+  int regs = 0;
+  const qknr_status st = qknr_host::configure_kernel(fn, dev, di, &regs);
+  if (st != QKNR_OK) return st;
+  void* kargs[] = {kp};
+  return qknr_host::launch_kernel(fn, static_cast<int>(grid), block, smem, reinterpret_cast<cudaStream_t>(stream), kargs,
+                                  !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
+}
+
+struct Kernels {
+  const void *fwd, *delta, *dq, *dkv;
+  int fwd_smem, dq_smem, dkv_smem;
+};
+
+template <typename T, int D>
+Kernels kernels() {
+  return Kernels{reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_delta_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_dq_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_dkv_kernel<T, D>),
+                 qknr::fwd::kSmem<D>, qknr::dq::kSmem<D>, qknr::dkv::kSmem<D>};
+}
+
+Kernels kernels_for(const qknr_attn_args* a) {
+  if (a->dtype == QKNR_BF16) return a->head_dim == 64 ? kernels<__nv_bfloat16, 64>() : kernels<__nv_bfloat16, 128>();
+  return a->head_dim == 64 ? kernels<__half, 64>() : kernels<__half, 128>();
+}
+
+qknr_status device(int* dev, qknr_host::DeviceInfo* di) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return qknr_host::cuda_fail(e, "cudaGetDevice");
+  return qknr_host::device_info(*dev, di);
+}
+
+}  // namespace
+
+extern "C" {
+
+void qknr_attn_args_init(qknr_attn_args* a) {
+  if (!a) return;
+  memset(a, 0, sizeof(*a));
+  a->abi_version = QKNR_ABI_VERSION;
+  a->dtype = QKNR_BF16;
+}
+
+size_t qknr_attn_sizeof_args(void) { return sizeof(qknr_attn_args); }
+
+qknr_status qknr_attn_workspace_bytes(const qknr_attn_args* a, size_t* bytes) {
+  if (!bytes) return fail(QKNR_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  return check_shape(a);
+}
+
+qknr_status qknr_attn_backward_workspace_bytes(const qknr_attn_args* a, size_t* bytes) {
+  if (!bytes) return fail(QKNR_ERR_NULL, "bytes is NULL");
+  *bytes = 0;
+  const qknr_status st = check_shape(a);
+  if (st != QKNR_OK) return st;
+  *bytes = delta_bytes(a);
+  return QKNR_OK;
+}
+
+qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
+  qknr_status st = check_shape(a);
+  if (st != QKNR_OK) return st;
+  qknr::AttnParams kp;
+  memset(&kp, 0, sizeof(kp));
+  Rows q{"q", a->q, a->q_stride, a->seq_q, a->n_heads_q}, k{"k", a->k, a->k_stride, a->seq_k, a->n_heads_k},
+      v{"v", a->v, a->v_stride, a->seq_k, a->n_heads_k}, o{"o", a->o, a->o_stride, a->seq_q, a->n_heads_q};
+  for (Rows* r : {&q, &k, &v, &o})
+    if ((st = check_rows(a, r)) != QKNR_OK) return st;
+  if ((st = common(a, &kp)) != QKNR_OK) return st;
+  if (a->batch == 0 || a->seq_q == 0) return QKNR_OK;
+  if (!a->lse) return fail(QKNR_ERR_NULL, "lse is required");
+  const Span outs[] = {o.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)}};
+  const Span ins[] = {q.span, k.span, v.span, span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)};
+  if ((st = check_overlap(outs, 2, ins, 5)) != QKNR_OK) return st;
+  if (qknr_host::overlaps(outs[0], outs[1])) return fail(QKNR_ERR_OVERLAP, "o and lse overlap");
+  kp.o = static_cast<char*>(a->o);
+  kp.o_stride = o.stride * 2;
+  kp.sp_o = msp(o.span);
+  kp.tiles = (a->seq_q + 2 * qknr::kTile - 1) / (2 * qknr::kTile);
+
+  int dev = 0;
+  qknr_host::DeviceInfo di;
+  if ((st = device(&dev, &di)) != QKNR_OK) return st;
+  if ((st = make_map(&kp.map_q, a, a->q, q.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
+  if (a->seq_k > 0) {   // without keys the kernel loads nothing
+    if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
+    if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
+  }
+  const Kernels fn = kernels_for(a);
+  return launch(fn.fwd, static_cast<long long>(kp.tiles) * a->n_heads_q * a->batch, qknr::kAttnThreads, fn.fwd_smem, a,
+                &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
+}
+
+qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
+  qknr_status st = check_shape(a);
+  if (st != QKNR_OK) return st;
+  qknr::AttnParams kp;
+  memset(&kp, 0, sizeof(kp));
+  Rows q{"q", a->q, a->q_stride, a->seq_q, a->n_heads_q}, k{"k", a->k, a->k_stride, a->seq_k, a->n_heads_k},
+      v{"v", a->v, a->v_stride, a->seq_k, a->n_heads_k}, o{"o", a->o, a->o_stride, a->seq_q, a->n_heads_q},
+      g{"dout", a->dout, a->dout_stride, a->seq_q, a->n_heads_q}, dq{"dq", a->dq, a->dq_stride, a->seq_q, a->n_heads_q},
+      dk{"dk", a->dk, a->dk_stride, a->seq_k, a->n_heads_k}, dv{"dv", a->dv, a->dv_stride, a->seq_k, a->n_heads_k};
+  for (Rows* r : {&q, &k, &v, &o, &g, &dq, &dk, &dv})
+    if ((st = check_rows(a, r)) != QKNR_OK) return st;
+  if ((st = common(a, &kp)) != QKNR_OK) return st;
+  if (a->batch == 0 || (a->seq_q == 0 && a->seq_k == 0)) return QKNR_OK;
+  const size_t need = delta_bytes(a);
+  if (a->seq_q > 0 && !a->lse) return fail(QKNR_ERR_NULL, "lse is required");
+  if (need && !a->workspace) return fail(QKNR_ERR_NULL, "workspace is required");
+  if (a->workspace_bytes < need) return fail(QKNR_ERR_SHAPE, "workspace of %zu bytes, %zu needed", a->workspace_bytes, need);
+  if (!aligned16(a->workspace)) return fail(QKNR_ERR_ALIGN, "workspace not 16-byte aligned");
+  const Span ws = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
+  const Span outs[] = {dq.span, dk.span, dv.span, ws};
+  const Span ins[] = {q.span, k.span, v.span, o.span, g.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)},
+                      span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)};
+  if ((st = check_overlap(outs, 4, ins, 8)) != QKNR_OK) return st;
+  for (int i = 0; i < 3; ++i)
+    if (qknr_host::overlaps(ws, outs[i])) return fail(QKNR_ERR_OVERLAP, "the workspace overlaps a gradient");
+  kp.o_in = static_cast<const char*>(a->o);
+  kp.dout = static_cast<const char*>(a->dout);
+  kp.dq = static_cast<char*>(a->dq);
+  kp.dk = static_cast<char*>(a->dk);
+  kp.dv = static_cast<char*>(a->dv);
+  kp.o_stride = o.stride * 2;
+  kp.dout_stride = g.stride * 2;
+  kp.dq_stride = dq.stride * 2;
+  kp.dk_stride = dk.stride * 2;
+  kp.dv_stride = dv.stride * 2;
+  kp.delta = static_cast<float*>(a->workspace);
+  kp.sp_o = msp(o.span);
+  kp.sp_dout = msp(g.span);
+  kp.sp_dq = msp(dq.span);
+  kp.sp_dk = msp(dk.span);
+  kp.sp_dv = msp(dv.span);
+  kp.sp_delta = msp(ws);
+
+  int dev = 0;
+  qknr_host::DeviceInfo di;
+  if ((st = device(&dev, &di)) != QKNR_OK) return st;
+  // a map of no rows is never loaded from
+  if (a->seq_q > 0) {
+    if ((st = make_map(&kp.map_q, a, a->q, q.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
+    if ((st = make_map(&kp.map_do, a, a->dout, g.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
+  }
+  if (a->seq_k > 0) {
+    if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
+    if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
+  }
+  const Kernels fn = kernels_for(a);
+  if (a->seq_q > 0) {
+    const long long rows = static_cast<long long>(a->batch) * a->seq_q * a->n_heads_q, teams = 256 / (a->head_dim / 8);
+    long long grid = (rows + teams - 1) / teams;
+    if (grid > 8LL * di.num_sms) grid = 8LL * di.num_sms;
+    void* kargs[] = {&kp};
+    st = qknr_host::launch_kernel(fn.delta, static_cast<int>(grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
+                                  !(a->flags & QKNR_FLAG_NO_OVERLAP), "cudaLaunchKernelExC(attention delta)");
+    if (st != QKNR_OK) return st;
+    kp.tiles = (a->seq_q + qknr::kTile - 1) / qknr::kTile;
+    st = launch(fn.dq, static_cast<long long>(kp.tiles) * a->n_heads_q * a->batch, qknr::kAttnThreads, fn.dq_smem, a, &kp,
+                dev, di, stream, "cudaLaunchKernelExC(attention dq)");
+    if (st != QKNR_OK) return st;
+  }
+  if (a->seq_k == 0) return QKNR_OK;
+  kp.tiles = (a->seq_k + qknr::kTile - 1) / qknr::kTile;
+  return launch(fn.dkv, static_cast<long long>(kp.tiles) * a->n_heads_k * a->batch, qknr::kAttnThreads, fn.dkv_smem, a, &kp,
+                dev, di, stream, "cudaLaunchKernelExC(attention dk, dv)");
+}
+
+}  // extern "C"

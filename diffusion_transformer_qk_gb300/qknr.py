@@ -47,6 +47,8 @@ EXPORTS = (
     "qknr_host_plan_init", "qknr_host_buffer_bytes", "qknr_forward_host", "qknr_sizeof_host_plan",
     "qknr_ln_args_init", "qknr_ln_forward", "qknr_ln_workspace_bytes", "qknr_ln_backward", "qknr_ln_sizeof_args",
     "qknr_grad_args_init", "qknr_grad_workspace_bytes", "qknr_backward", "qknr_sizeof_grad_args",
+    "qknr_attn_args_init", "qknr_attn_workspace_bytes", "qknr_attn_backward_workspace_bytes", "qknr_attn_forward",
+    "qknr_attn_backward", "qknr_attn_sizeof_args",
 )
 GN_MODE = {"auto": 0, "fused": 1, "two_pass": 2, "cluster": 3}
 GN_FLAG_TEST_NO_RECORDS = 0x2
@@ -172,6 +174,23 @@ class QknrGradArgs(ctypes.Structure):
     ]
 
 
+class QknrAttnArgs(ctypes.Structure):
+    """Mirror of ``qknr_attn_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("o", c_void_p), ("lse", c_void_p),
+        ("q_stride", c_int64), ("k_stride", c_int64), ("v_stride", c_int64), ("o_stride", c_int64),
+        ("batch", c_int32), ("seq_q", c_int32), ("seq_k", c_int32),
+        ("n_heads_q", c_int32), ("n_heads_k", c_int32), ("head_dim", c_int32),
+        ("q_lens", c_void_p), ("k_lens", c_void_p), ("scale", c_float), ("causal", c_int32),
+        ("dout", c_void_p), ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p),
+        ("dout_stride", c_int64), ("dq_stride", c_int64), ("dk_stride", c_int64), ("dv_stride", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32), ("wait_limit_ns", c_uint64),
+    ]
+
+
 class QknrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -245,6 +264,13 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         for fn, struct in ((lib.qknr_ln_forward, QknrLnArgs), (lib.qknr_ln_backward, QknrLnArgs),
                            (lib.qknr_backward, QknrGradArgs)):
             fn.argtypes, fn.restype = [ctypes.POINTER(struct), c_void_p], c_int32
+        p_attn = ctypes.POINTER(QknrAttnArgs)
+        lib.qknr_attn_args_init.argtypes, lib.qknr_attn_args_init.restype = [p_attn], None
+        for fn in (lib.qknr_attn_workspace_bytes, lib.qknr_attn_backward_workspace_bytes):
+            fn.argtypes, fn.restype = [p_attn, ctypes.POINTER(c_size_t)], c_int32
+        for fn in (lib.qknr_attn_forward, lib.qknr_attn_backward):
+            fn.argtypes, fn.restype = [p_attn, c_void_p], c_int32
+        lib.qknr_attn_sizeof_args.restype = c_size_t
         lib.qknr_ln_sizeof_args.restype = c_size_t
         lib.qknr_sizeof_grad_args.restype = c_size_t
         if lib.qknr_abi_version() != ABI_VERSION:
@@ -255,6 +281,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 lib.qknr_gn_sizeof_args() != ctypes.sizeof(QknrGnArgs) or \
                 lib.qknr_ln_sizeof_args() != ctypes.sizeof(QknrLnArgs) or \
                 lib.qknr_sizeof_grad_args() != ctypes.sizeof(QknrGradArgs) or \
+                lib.qknr_attn_sizeof_args() != ctypes.sizeof(QknrAttnArgs) or \
                 lib.qknr_sizeof_host_plan() != ctypes.sizeof(QknrHostPlan):
             raise RuntimeError("libqknr.so struct layout differs from the binding")
         if path is None:
@@ -849,6 +876,12 @@ def _workspace(fn, a, workspace, like, stream):
     return workspace
 
 
+def _stride(t, name):
+    """Row stride of a 2-D view; 0 (the library's default) where it has no
+    elements, whose strides mean nothing."""
+    return _rows(t, name) if t.numel() else 0
+
+
 def _match(t, like, name):
     if t.dtype != like.dtype or t.shape != like.shape:
         raise ValueError(f"{name} must match {like.dtype} {tuple(like.shape)}")
@@ -876,7 +909,7 @@ def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False
     if x.dtype not in _ACT:
         raise ValueError("x must be bfloat16 or float16")
     a.dtype = _ACT[x.dtype]
-    a.x, a.x_stride = x.data_ptr(), _rows(x, "x")
+    a.x, a.x_stride = x.data_ptr(), _stride(x, "x")
     a.tokens, a.hidden = x.shape
     a.rows_per_batch = rows_per_batch or 0
     sets = -(-x.shape[0] // rows_per_batch) if rows_per_batch else 1
@@ -888,7 +921,7 @@ def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False
             raise ValueError(f"{name} must be [C] or [{sets}, C]")
         if t.dtype not in (torch.float32, x.dtype) or (weight is not None and t.dtype != weight.dtype):
             raise ValueError("weight and bias must both be float32 or both of x's dtype")
-        stride = _rows(rows, name)
+        stride = _stride(rows, name)
         if rows.shape[0] > 1 and a.param_stride and stride != a.param_stride:
             raise ValueError("weight and bias need the same row stride")
         if rows.shape[0] > 1:
@@ -917,7 +950,7 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
     out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
     mean = _empty((T,), torch.float32, x, stream) if mean is None else _vector(mean, T, "mean")
     rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd")
-    a.y, a.y_stride = out.data_ptr(), _rows(out, "out")
+    a.y, a.y_stride = out.data_ptr(), _stride(out, "out")
     a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
     _call(load().qknr_ln_forward, a, stream)
     return out, mean, rstd
@@ -934,8 +967,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
     T, C = x.shape
     sets = -(-T // rows_per_batch) if rows_per_batch else 1
     out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
-    a.dy, a.dy_stride = _match(dy, x, "dy").data_ptr(), _rows(dy, "dy")
-    a.dx, a.dx_stride = out.data_ptr(), _rows(out, "out")
+    a.dy, a.dy_stride = _match(dy, x, "dy").data_ptr(), _stride(dy, "dy")
+    a.dx, a.dx_stride = out.data_ptr(), _stride(out, "out")
     a.mean, a.rstd = _vector(mean, T, "mean").data_ptr(), _vector(rstd, T, "rstd").data_ptr()
     shape = ((sets, C) if rows_per_batch else (C,)) if weight is None else \
         (weight.shape if weight.dim() == 1 else (sets, C))
@@ -968,7 +1001,7 @@ def grad_args(*, head_dim, q=None, k=None, dq=None, dk=None, dv=None, dq_out=Non
         if t is None:
             continue
         heads = {"q": n_heads_q, "k": n_heads_k, "v": n_heads_v}[name.replace("_out", "")[-1]]
-        stride = _rows(t, name)
+        stride = _stride(t, name)
         if t.shape != (tokens, heads * head_dim):
             raise ValueError(f"{name} must be [{tokens}, {heads * head_dim}]")
         setattr(a, name, t.data_ptr())
@@ -1049,3 +1082,86 @@ def qk_norm_rope_tensor_backward(dout, x, n_heads, head_dim, gamma, cos, sin, *,
     dgamma = _empty((head_dim,), torch.float32, x, stream)
     _grad_launch(a, x, {"dgamma_q": dgamma}, workspace, stream)
     return dout if out is None else out, dgamma
+
+
+# ---------------------------------------------------------------------------
+# attention and its backward pass (include/qknr_attn.h)
+
+def attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False, q_lens=None, k_lens=None,
+              dev_status=None, flags=0, wait_limit_ns=0) -> QknrAttnArgs:
+    """The arguments both passes share: token rows q [batch * seq_q, Hq * D],
+    k and v [batch * seq_k, Hk * D] (views with any row stride, such as the
+    columns of a packed QKV activation)."""
+    a = QknrAttnArgs()
+    load().qknr_attn_args_init(ctypes.byref(a))
+    if q.dtype not in _ACT or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype: bfloat16 or float16")
+    a.dtype = _ACT[q.dtype]
+    for name, t, heads in (("q", q, n_heads_q), ("k", k, n_heads_k), ("v", v, n_heads_k)):
+        setattr(a, name + "_stride", _stride(t, name))
+        if t.dim() != 2 or t.shape[1] != heads * head_dim or batch < 1 or t.shape[0] % batch:
+            raise ValueError(f"{name} must be [batch * seq, {heads * head_dim}]")
+        setattr(a, name, t.data_ptr())
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v need the same number of rows")
+    a.batch, a.seq_q, a.seq_k = batch, q.shape[0] // batch, k.shape[0] // batch
+    a.n_heads_q, a.n_heads_k, a.head_dim = n_heads_q, n_heads_k, head_dim
+    for name, t in (("q_lens", q_lens), ("k_lens", k_lens)):
+        if t is not None:
+            if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != batch:
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {batch} values")
+            setattr(a, name, t.data_ptr())
+    if scale is not None:
+        if not scale > 0:
+            raise ValueError("scale must be positive")
+        a.scale = scale
+    a.causal = int(bool(causal))
+    a.dev_status = _ptr(dev_status)
+    a.flags, a.wait_limit_ns = flags, wait_limit_ns
+    return a
+
+
+def attention(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False, q_lens=None, k_lens=None,
+              out=None, lse=None, workspace=None, stream=None, status=True, **kw):
+    """Attention over token rows: returns (o [batch * seq_q, Hq * D], lse
+    float32 [batch, Hq, seq_q]).  ``q_lens``/``k_lens`` (int32 [batch] on the
+    device) end each sample's queries and keys, ``causal`` lines the diagonal
+    up with their last ones; a query that sees no key answers zero with lse
+    -inf.  ``out`` and ``lse`` receive the results (default: new tensors)."""
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(q.device)
+    a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
+                  k_lens=k_lens, **kw)
+    out = _empty(q.shape, q.dtype, q, stream) if out is None else _match(out, q, "out")
+    shape = (batch, n_heads_q, a.seq_q)
+    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, q.shape[0] * n_heads_q, "lse")
+    a.o, a.o_stride, a.lse = out.data_ptr(), _stride(out, "out"), lse.data_ptr()
+    lib = load()
+    workspace = _workspace(lib.qknr_attn_workspace_bytes, a, workspace, q, stream)
+    _call(lib.qknr_attn_forward, a, stream)
+    return out, lse
+
+
+def attention_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False,
+                       q_lens=None, k_lens=None, dq=None, dk=None, dv=None, workspace=None, stream=None, status=True,
+                       **kw):
+    """Gradients of ``attention`` from do, its inputs and its outputs o and
+    lse: returns (dq, dk, dv), new tensors unless given (column views of one
+    packed buffer are fine).  Rows past the lengths get zero."""
+    if status and "dev_status" not in kw:
+        kw["dev_status"] = status_buffer(q.device)
+    a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
+                  k_lens=k_lens, **kw)
+    a.o, a.o_stride = _match(o, q, "o").data_ptr(), _stride(o, "o")
+    a.dout, a.dout_stride = _match(do, q, "do").data_ptr(), _stride(do, "do")
+    a.lse = _vector(lse, q.shape[0] * n_heads_q, "lse").data_ptr()
+    dq = _empty(q.shape, q.dtype, q, stream) if dq is None else _match(dq, q, "dq")
+    dk = _empty(k.shape, q.dtype, q, stream) if dk is None else _match(dk, k, "dk")
+    dv = _empty(v.shape, q.dtype, q, stream) if dv is None else _match(dv, v, "dv")
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_stride", _stride(t, name))
+    lib = load()
+    workspace = _workspace(lib.qknr_attn_backward_workspace_bytes, a, workspace, q, stream)
+    _call(lib.qknr_attn_backward, a, stream)
+    return dq, dk, dv

@@ -845,6 +845,47 @@ def gn_launch_noalloc(a: QknrGnArgs, stream: Optional[torch.cuda.Stream] = None)
 
 # ---------------------------------------------------------------------------
 # training: helpers of the entry points below
+#
+# A training step makes the same few calls over and over, so what a call's
+# metadata decides (every check of shapes, strides and dtypes, the filled-in
+# argument struct, the workspace's size) is worked out once per combination
+# and kept; a call then copies the struct and puts its pointers in.  Nothing
+# is kept of the tensors themselves.
+
+_plans = {}
+_MOST_PLANS = 1024
+
+
+class _Plan:
+    __slots__ = ("struct", "args", "workspace", "info")
+
+    def __init__(self, a, workspace_fn=None, info=None):
+        n = c_size_t(0)
+        if workspace_fn is not None:
+            st = workspace_fn(ctypes.byref(a), ctypes.byref(n))
+            if st != OK:
+                raise QknrError(st, load().qknr_last_error().decode())
+        self.workspace = n.value
+        for name, kind in a._fields_:
+            if kind is c_void_p:
+                setattr(a, name, None)
+        self.struct, self.args, self.info = type(a), bytes(a), info
+
+    def new(self):
+        return self.struct.from_buffer_copy(self.args)
+
+
+def _keep(key, plan):
+    if len(_plans) >= _MOST_PLANS:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _meta(t):
+    """What a plan depends on of a tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
 
 def _empty(shape, dtype, like, stream):
     """A new tensor on like's device that belongs to the stream the call runs
@@ -855,25 +896,34 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _call(fn, a, stream) -> None:
+def _call(fn, a, stream, like) -> None:
     """One library call on ``stream`` (default: the current stream)."""
-    s = torch.cuda.current_stream() if stream is None else stream
-    st = fn(ctypes.byref(a), c_void_p(s.cuda_stream))
+    s = torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
+    st = fn(ctypes.byref(a), s)
     if st != OK:
         raise QknrError(st, load().qknr_last_error().decode())
 
 
-def _workspace(fn, a, workspace, like, stream):
-    """Put a workspace into ``a``: the caller's, or a new one of the size the
-    library asks for.  Returns the tensor (to be kept until the call)."""
+def _workspace(a, plan, workspace, like, stream):
+    """Put a workspace into ``a``: the caller's, or a new one.  Returns the
+    tensor (to be kept until the call)."""
     if workspace is None:
-        n = c_size_t(0)
-        st = fn(ctypes.byref(a), ctypes.byref(n))
-        if st != OK:
-            raise QknrError(st, load().qknr_last_error().decode())
-        workspace = _empty((max(n.value, 16),), torch.uint8, like, stream)
-    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if not plan.workspace:
+            return None
+        workspace = _empty((plan.workspace,), torch.uint8, like, stream)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), plan.workspace
+    else:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
+
+
+def _status(a, status, dev_status, like):
+    """The status word: the caller's, the device's, or none."""
+    if dev_status is not None:
+        a.dev_status = dev_status.data_ptr()
+    elif status:
+        word = _status_bufs.get(like.get_device())
+        a.dev_status = (status_buffer(like.device) if word is None else word).data_ptr()
 
 
 def _stride(t, name):
@@ -935,7 +985,7 @@ def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False
 
 
 def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False, out=None, mean=None, rstd=None,
-               eps=1e-6, stream=None, status=True, **kw):
+               eps=1e-6, stream=None, status=True, dev_status=None, flags=0):
     """Layer norm of token rows ``x`` [T, C] for training: returns (y, mean,
     rstd), the last two float32 [T] for the backward pass.
 
@@ -943,41 +993,58 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
     t // rows_per_batch; with ``unit_offset`` the gain is 1 + weight (the
     modulated norm of ``adaln_modulate``).  The result goes to ``out``, a new
     tensor by default (the backward pass needs x); ``out=x`` is in place."""
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(x.device)
-    a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, **kw)
+    key = ("ln", _meta(x), _meta(weight), _meta(bias), _meta(out), rows_per_batch, unit_offset, eps, flags)
+    plan = _plans.get(key)
+    if plan is None:
+        a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, flags=flags)
+        a.y_stride = x.shape[1] if out is None else _stride(_match(out, x, "out"), "out")
+        plan = _keep(key, _Plan(a))
     T = x.shape[0]
-    out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
     mean = _empty((T,), torch.float32, x, stream) if mean is None else _vector(mean, T, "mean")
     rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd")
-    a.y, a.y_stride = out.data_ptr(), _stride(out, "out")
-    a.mean, a.rstd = mean.data_ptr(), rstd.data_ptr()
-    _call(load().qknr_ln_forward, a, stream)
+    a = plan.new()
+    a.x, a.y, a.mean, a.rstd = x.data_ptr(), out.data_ptr(), mean.data_ptr(), rstd.data_ptr()
+    if weight is not None:
+        a.weight = weight.data_ptr()
+    if bias is not None:
+        a.bias = bias.data_ptr()
+    _status(a, status, dev_status, x)
+    _call((_lib or load()).qknr_ln_forward, a, stream, x)
     return out, mean, rstd
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_offset=False, out=None, dweight=None,
-                        dbias=None, workspace=None, stream=None, status=True, **kw):
+                        dbias=None, workspace=None, stream=None, status=True, dev_status=None, flags=0):
     """Gradients of ``layer_norm``: returns (dx, dweight, dbias), the last two
     float32, of weight's shape ([C] where weight is None).  ``out`` receives
     dx (default: a new tensor; ``out=dy`` is in place)."""
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(x.device)
-    a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, **kw)
+    key = ("ln_bwd", _meta(dy), _meta(x), _meta(weight), _meta(out), rows_per_batch, unit_offset, flags)
+    plan = _plans.get(key)
     T, C = x.shape
-    sets = -(-T // rows_per_batch) if rows_per_batch else 1
-    out = _empty(x.shape, x.dtype, x, stream) if out is None else _match(out, x, "out")
-    a.dy, a.dy_stride = _match(dy, x, "dy").data_ptr(), _stride(dy, "dy")
-    a.dx, a.dx_stride = out.data_ptr(), _stride(out, "out")
+    if plan is None:
+        a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags)
+        a.dy_stride = _stride(_match(dy, x, "dy"), "dy")
+        a.dx_stride = C if out is None else _stride(_match(out, x, "out"), "out")
+        sets = -(-T // rows_per_batch) if rows_per_batch else 1
+        shape = ((sets, C) if rows_per_batch else (C,)) if weight is None else \
+            (weight.shape if weight.dim() == 1 else (sets, C))
+        plan = _keep(key, _Plan(a, load().qknr_ln_workspace_bytes, (shape, sets * C)))
+    shape, n = plan.info
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
+    dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, n, "dweight")
+    dbias = _empty(shape, torch.float32, x, stream) if dbias is None else _vector(dbias, n, "dbias")
+    a = plan.new()
+    a.x, a.dy, a.dx = x.data_ptr(), dy.data_ptr(), out.data_ptr()
     a.mean, a.rstd = _vector(mean, T, "mean").data_ptr(), _vector(rstd, T, "rstd").data_ptr()
-    shape = ((sets, C) if rows_per_batch else (C,)) if weight is None else \
-        (weight.shape if weight.dim() == 1 else (sets, C))
-    dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, sets * C, "dweight")
-    dbias = _empty(shape, torch.float32, x, stream) if dbias is None else _vector(dbias, sets * C, "dbias")
     a.dweight, a.dbias = dweight.data_ptr(), dbias.data_ptr()
-    lib = load()
-    workspace = _workspace(lib.qknr_ln_workspace_bytes, a, workspace, x, stream)
-    _call(lib.qknr_ln_backward, a, stream)
+    if weight is not None:
+        a.weight = weight.data_ptr()
+    _status(a, status, dev_status, x)
+    workspace = _workspace(a, plan, workspace, x, stream)
+    _call((_lib or load()).qknr_ln_backward, a, stream, x)
     return out, dweight, dbias
 
 
@@ -1027,61 +1094,69 @@ def grad_args(*, head_dim, q=None, k=None, dq=None, dk=None, dv=None, dq_out=Non
     return a
 
 
-def _grad_launch(a, like, dgamma, workspace, stream):
-    lib = load()
-    for name, g in dgamma.items():
-        setattr(a, name, None if g is None else g.data_ptr())
-    workspace = _workspace(lib.qknr_grad_workspace_bytes, a, workspace, like, stream)
-    _call(lib.qknr_backward, a, stream)
-
-
 def qk_norm_rope_packed_backward(dout, qkv, n_heads_q, n_heads_k, n_heads_v, head_dim, gamma_q, gamma_k, cos, sin, *,
-                                 out=None, workspace=None, stream=None, status=True, **kw):
+                                 out=None, rope_style="interleaved", cos_layout="shared_row", cos_rows=None, eps=1e-6,
+                                 workspace=None, stream=None, status=True, dev_status=None, flags=0):
     """Backward pass of ``qk_norm_rope_packed``: ``qkv`` is that call's input
     (run it with ``out=``, so that the input survives), ``dout`` the gradient
     of its output.  Returns (dqkv, dgamma_q, dgamma_k), the gains' gradients
-    float32 [head_dim].  In place of ``dout`` unless ``out`` is given, which
-    also receives a copy of V's gradient."""
+    float32 [head_dim] (None for a tensor without heads).  In place of
+    ``dout`` unless ``out`` is given, which also receives a copy of V's
+    gradient."""
     D = head_dim
-    width = (n_heads_q + n_heads_k + n_heads_v) * D
-    if qkv.dim() != 2 or qkv.shape[1] != width:
-        raise ValueError(f"qkv must be [tokens, {width}]")
-    _match(dout, qkv, "dout")
-    _check_table(cos, D, kw.get("cos_layout", "shared_row"), n_heads_q or n_heads_k)
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(qkv.device)
-    q0, k0, v0, v1 = 0, n_heads_q * D, (n_heads_q + n_heads_k) * D, width
+    key = ("qk_bwd", _meta(dout), _meta(qkv), _meta(out), n_heads_q, n_heads_k, n_heads_v, D, _meta(gamma_q),
+           _meta(gamma_k), _meta(cos), _meta(sin), rope_style, cos_layout, cos_rows, eps, flags)
+    plan = _plans.get(key)
+    k0, v0 = n_heads_q * D * 2, (n_heads_q + n_heads_k) * D * 2   # bytes into a row
+    if plan is None:
+        width = (n_heads_q + n_heads_k + n_heads_v) * D
+        if qkv.dim() != 2 or qkv.shape[1] != width:
+            raise ValueError(f"qkv must be [tokens, {width}]")
+        _match(dout, qkv, "dout")
+        if out is not None:
+            _match(out, qkv, "out")
+        _check_table(cos, D, cos_layout, n_heads_q or n_heads_k)
 
-    def cols(t, a, b):
-        return None if t is None or a == b else t[:, a:b]
+        def cols(t, a, b):
+            return None if t is None or a == b else t[:, a // 2:b // 2]
 
-    if out is not None:
-        _match(out, qkv, "out")
-    a = grad_args(q=cols(qkv, q0, k0), k=cols(qkv, k0, v0), dq=cols(dout, q0, k0), dk=cols(dout, k0, v0),
-                  dv=cols(dout, v0, v1), dq_out=cols(out, q0, k0), dk_out=cols(out, k0, v0), dv_out=cols(out, v0, v1),
-                  n_heads_q=n_heads_q, n_heads_k=n_heads_k, n_heads_v=n_heads_v, head_dim=D,
-                  gamma_q=gamma_q if n_heads_q else None, gamma_k=gamma_k if n_heads_k else None, cos=cos, sin=sin,
-                  tokens=qkv.shape[0], **kw)
-    dgq = _empty((D,), torch.float32, qkv, stream) if n_heads_q else None
-    dgk = _empty((D,), torch.float32, qkv, stream) if n_heads_k else None
-    _grad_launch(a, qkv, {"dgamma_q": dgq, "dgamma_k": dgk}, workspace, stream)
+        end = width * 2
+        a = grad_args(q=cols(qkv, 0, k0), k=cols(qkv, k0, v0), dq=cols(dout, 0, k0), dk=cols(dout, k0, v0),
+                      dv=cols(dout, v0, end), dq_out=cols(out, 0, k0), dk_out=cols(out, k0, v0),
+                      dv_out=cols(out, v0, end), n_heads_q=n_heads_q, n_heads_k=n_heads_k, n_heads_v=n_heads_v,
+                      head_dim=D, gamma_q=gamma_q if n_heads_q else None, gamma_k=gamma_k if n_heads_k else None,
+                      cos=cos, sin=sin, rope_style=rope_style, cos_layout=cos_layout, cos_rows=cos_rows, eps=eps,
+                      tokens=qkv.shape[0], flags=flags)
+        plan = _keep(key, _Plan(a, load().qknr_grad_workspace_bytes))
+    a = plan.new()
+    x, d = qkv.data_ptr(), dout.data_ptr()
+    o = d if out is None else out.data_ptr()
+    dgq = dgk = None
+    if n_heads_q:
+        dgq = _empty((D,), torch.float32, qkv, stream)
+        a.q, a.dq, a.dq_out, a.gamma_q, a.dgamma_q = x, d, o, gamma_q.data_ptr(), dgq.data_ptr()
+    if n_heads_k:
+        dgk = _empty((D,), torch.float32, qkv, stream)
+        a.k, a.dk, a.dk_out, a.gamma_k, a.dgamma_k = x + k0, d + k0, o + k0, gamma_k.data_ptr(), dgk.data_ptr()
+    if n_heads_v and out is not None:
+        a.dv, a.dv_out = d + v0, o + v0
+    a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
+    _status(a, status, dev_status, qkv)
+    workspace = _workspace(a, plan, workspace, qkv, stream)
+    _call((_lib or load()).qknr_backward, a, stream, qkv)
     return dout if out is None else out, dgq, dgk
 
 
-def qk_norm_rope_tensor_backward(dout, x, n_heads, head_dim, gamma, cos, sin, *, out=None, workspace=None, stream=None,
-                                 status=True, **kw):
+def qk_norm_rope_tensor_backward(dout, x, n_heads, head_dim, gamma, cos, sin, *, out=None, rope_style="interleaved",
+                                 cos_layout="shared_row", cos_rows=None, eps=1e-6, workspace=None, stream=None,
+                                 status=True, dev_status=None, flags=0):
     """Backward pass of ``qk_norm_rope_tensor`` (one Q or K tensor [T, H*D]):
     returns (dx, dgamma).  In place of ``dout`` unless ``out`` is given."""
-    if x.dim() != 2 or x.shape[1] != n_heads * head_dim:
-        raise ValueError("x must be [tokens, n_heads*head_dim]")
-    _check_table(cos, head_dim, kw.get("cos_layout", "shared_row"), n_heads)
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(x.device)
-    a = grad_args(q=x, dq=_match(dout, x, "dout"), dq_out=None if out is None else _match(out, x, "out"),
-                  n_heads_q=n_heads, head_dim=head_dim, gamma_q=gamma, cos=cos, sin=sin, tokens=x.shape[0], **kw)
-    dgamma = _empty((head_dim,), torch.float32, x, stream)
-    _grad_launch(a, x, {"dgamma_q": dgamma}, workspace, stream)
-    return dout if out is None else out, dgamma
+    dx, dgamma, _ = qk_norm_rope_packed_backward(dout, x, n_heads, 0, 0, head_dim, gamma, None, cos, sin, out=out,
+                                                 rope_style=rope_style, cos_layout=cos_layout, cos_rows=cos_rows,
+                                                 eps=eps, workspace=workspace, stream=stream, status=status,
+                                                 dev_status=dev_status, flags=flags)
+    return dx, dgamma
 
 
 # ---------------------------------------------------------------------------
@@ -1122,46 +1197,68 @@ def attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, c
 
 
 def attention(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False, q_lens=None, k_lens=None,
-              out=None, lse=None, workspace=None, stream=None, status=True, **kw):
+              out=None, lse=None, workspace=None, stream=None, status=True, dev_status=None, flags=0, wait_limit_ns=0):
     """Attention over token rows: returns (o [batch * seq_q, Hq * D], lse
     float32 [batch, Hq, seq_q]).  ``q_lens``/``k_lens`` (int32 [batch] on the
     device) end each sample's queries and keys, ``causal`` lines the diagonal
     up with their last ones; a query that sees no key answers zero with lse
     -inf.  ``out`` and ``lse`` receive the results (default: new tensors)."""
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(q.device)
-    a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
-                  k_lens=k_lens, **kw)
-    out = _empty(q.shape, q.dtype, q, stream) if out is None else _match(out, q, "out")
-    shape = (batch, n_heads_q, a.seq_q)
-    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, q.shape[0] * n_heads_q, "lse")
-    a.o, a.o_stride, a.lse = out.data_ptr(), _stride(out, "out"), lse.data_ptr()
-    lib = load()
-    workspace = _workspace(lib.qknr_attn_workspace_bytes, a, workspace, q, stream)
-    _call(lib.qknr_attn_forward, a, stream)
+    key = ("attn", _meta(q), _meta(k), _meta(v), n_heads_q, n_heads_k, head_dim, batch, scale, causal, _meta(q_lens),
+           _meta(k_lens), _meta(out), flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
+                      k_lens=k_lens, flags=flags, wait_limit_ns=wait_limit_ns)
+        a.o_stride = 0 if out is None else _stride(_match(out, q, "out"), "out")
+        plan = _keep(key, _Plan(a, load().qknr_attn_workspace_bytes, ((batch, n_heads_q, a.seq_q), q.shape[0] * n_heads_q)))
+    shape, n = plan.info
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, n, "lse")
+    a = plan.new()
+    a.q, a.k, a.v, a.o, a.lse = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()
+    if q_lens is not None:
+        a.q_lens = q_lens.data_ptr()
+    if k_lens is not None:
+        a.k_lens = k_lens.data_ptr()
+    _status(a, status, dev_status, q)
+    workspace = _workspace(a, plan, workspace, q, stream)
+    _call((_lib or load()).qknr_attn_forward, a, stream, q)
     return out, lse
 
 
 def attention_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False,
                        q_lens=None, k_lens=None, dq=None, dk=None, dv=None, workspace=None, stream=None, status=True,
-                       **kw):
+                       dev_status=None, flags=0, wait_limit_ns=0):
     """Gradients of ``attention`` from do, its inputs and its outputs o and
     lse: returns (dq, dk, dv), new tensors unless given (column views of one
     packed buffer are fine).  Rows past the lengths get zero."""
-    if status and "dev_status" not in kw:
-        kw["dev_status"] = status_buffer(q.device)
-    a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
-                  k_lens=k_lens, **kw)
-    a.o, a.o_stride = _match(o, q, "o").data_ptr(), _stride(o, "o")
-    a.dout, a.dout_stride = _match(do, q, "do").data_ptr(), _stride(do, "do")
-    a.lse = _vector(lse, q.shape[0] * n_heads_q, "lse").data_ptr()
-    dq = _empty(q.shape, q.dtype, q, stream) if dq is None else _match(dq, q, "dq")
-    dk = _empty(k.shape, q.dtype, q, stream) if dk is None else _match(dk, k, "dk")
-    dv = _empty(v.shape, q.dtype, q, stream) if dv is None else _match(dv, v, "dv")
-    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-        setattr(a, name, t.data_ptr())
-        setattr(a, name + "_stride", _stride(t, name))
-    lib = load()
-    workspace = _workspace(lib.qknr_attn_backward_workspace_bytes, a, workspace, q, stream)
-    _call(lib.qknr_attn_backward, a, stream)
+    key = ("attn_bwd", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), n_heads_q, n_heads_k, head_dim, batch, scale,
+           causal, _meta(q_lens), _meta(k_lens), _meta(dq), _meta(dk), _meta(dv), flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
+                      k_lens=k_lens, flags=flags, wait_limit_ns=wait_limit_ns)
+        a.o_stride, a.dout_stride = _stride(_match(o, q, "o"), "o"), _stride(_match(do, q, "do"), "do")
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if t is not None:
+                setattr(a, name + "_stride", _stride(_match(t, like, name), name))
+        plan = _keep(key, _Plan(a, load().qknr_attn_backward_workspace_bytes, q.shape[0] * n_heads_q))
+    if dq is None:
+        dq = _empty(q.shape, q.dtype, q, stream)
+    if dk is None:
+        dk = _empty(k.shape, k.dtype, k, stream)
+    if dv is None:
+        dv = _empty(v.shape, v.dtype, v, stream)
+    a = plan.new()
+    a.q, a.k, a.v, a.o, a.dout = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr()
+    a.lse = _vector(lse, plan.info, "lse").data_ptr()
+    a.dq, a.dk, a.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+    if q_lens is not None:
+        a.q_lens = q_lens.data_ptr()
+    if k_lens is not None:
+        a.k_lens = k_lens.data_ptr()
+    _status(a, status, dev_status, q)
+    workspace = _workspace(a, plan, workspace, q, stream)
+    _call((_lib or load()).qknr_attn_backward, a, stream, q)
     return dq, dk, dv

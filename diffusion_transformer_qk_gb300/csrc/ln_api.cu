@@ -20,28 +20,48 @@ using qknr_host::span_of;
 constexpr long long kCtas = 152;
 constexpr int kMaxHidden = 32768;
 
+// the instances with the fewest chunks per thread that hold the row
+template <typename T>
+const void* direct_fn(int cpt) {
+  if (cpt <= 1) return reinterpret_cast<const void*>(qknr::ln_forward_direct_kernel<T, 1>);
+  if (cpt <= 2) return reinterpret_cast<const void*>(qknr::ln_forward_direct_kernel<T, 2>);
+  if (cpt <= 4) return reinterpret_cast<const void*>(qknr::ln_forward_direct_kernel<T, 4>);
+  return reinterpret_cast<const void*>(qknr::ln_forward_direct_kernel<T, 8>);
+}
+
 template <typename T>
 const void* forward_fn(int cpt) {
   switch (cpt) {
     case 1: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 1>);
     case 2: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 2>);
-    case 3: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 3>);
-    case 4: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 4>);
-    default: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 8>);
+    default: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 3>);
   }
 }
 
 template <typename T>
-const void* backward_fn(bool is_long) {
-  return is_long ? reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, true>)
-                 : reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, false>);
+const void* backward_fn(int cpt, bool is_long) {
+  if (is_long) return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, qknr::kLnBwdCpt, true>);
+  switch (cpt) {
+    case 1: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>);
+    case 2: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
+    case 3: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 3, false>);
+    default: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 4, false>);
+  }
+}
+
+// The smallest power of two of warps, up to `most`, that leaves a thread at
+// most `cpt` of a row's chunks.
+int warps_for(int n_chunks, int cpt, int most) {
+  int w = 1;
+  while (w < most && 32 * cpt * w < n_chunks) w *= 2;
+  return w;
 }
 
 qknr::MemSpan msp(Span s) { return qknr::MemSpan{s.lo, s.hi}; }
 
 // How the backward pass cuts the rows (nothing here needs a device).
 struct Cut {
-  int tiles, group_warps, groups;
+  int tiles, group_warps, groups, cpt;
   long long sets, units_per_set, unit_rows, rows_per_batch;
   size_t sums_bytes, parts_bytes;
 };
@@ -62,15 +82,25 @@ qknr_status check_shape(const qknr_ln_args* a) {
   return QKNR_OK;
 }
 
+// Ring depth of each of `groups` groups: 128 KB per SM in flight keep HBM
+// busy, and at least two stages that fit beside `other` bytes.
+int stages_for(const qknr_host::DeviceInfo& di, size_t stage_bytes, int groups, size_t other) {
+  const size_t room = (di.smem_optin - qknr::kLnOffStages - other) / (stage_bytes * groups);
+  size_t n = 128 * 1024 / (stage_bytes * groups);
+  if (n < 2) n = 2;
+  if (n > room) n = room;
+  if (n > static_cast<size_t>(qknr::kLnMaxStages / groups)) n = qknr::kLnMaxStages / groups;
+  return static_cast<int>(n);
+}
+
 Cut cut_rows(const qknr_ln_args* a) {
   Cut c;
   const long long T = a->tokens;
-  const int warps = (a->hidden / 8 + 31) / 32;
+  const int n_chunks = a->hidden / 8;
   c.tiles = (a->hidden + qknr::kLnTile - 1) / qknr::kLnTile;
-  c.group_warps = warps < qknr::kLnBwdWarps ? warps : qknr::kLnBwdWarps;
-  c.groups = qknr::kLnBwdWarps / c.group_warps;
-  // a group of several warps needs a named barrier, 1 .. 15
-  if (c.group_warps > 1 && c.groups > 15) c.groups = 15;
+  c.group_warps = warps_for(n_chunks, qknr::kLnBwdCpt, qknr::kLnBwdWarps);
+  c.groups = qknr::kLnBwdWarps / c.group_warps;   // groups of several warps: at most 4 named barriers
+  c.cpt = (n_chunks + 32 * c.group_warps - 1) / (32 * c.group_warps);
   c.rows_per_batch = a->rows_per_batch ? a->rows_per_batch : T;
   c.sets = T ? (T + c.rows_per_batch - 1) / c.rows_per_batch : 0;
   const long long rows = c.rows_per_batch < T ? c.rows_per_batch : T;
@@ -120,6 +150,9 @@ qknr_status common(const qknr_ln_args* a, qknr::LnParams* kp) {
   kp->eps = a->eps;
   kp->inv_c = 1.0f / static_cast<float>(C);
   kp->unit = a->flags & QKNR_LN_UNIT_OFFSET ? 1.0f : 0.0f;
+  kp->row_bytes = static_cast<unsigned>(C) * 2;
+  kp->flags = a->flags;
+  kp->wait_limit_ns = a->wait_limit_ns ? a->wait_limit_ns : 2000000000ull;
   kp->status = a->dev_status;
   kp->sp_x = msp(span_of(a->x, T, xs * es, (long long)C * es));
   kp->sp_weight = msp(span_of(a->weight, sets, ps * pes, (long long)C * pes));
@@ -193,23 +226,27 @@ qknr_status qknr_ln_forward(const qknr_ln_args* a, qknr_stream_t stream) {
   qknr_host::DeviceInfo di;
   st = device(&dev, &di);
   if (st != QKNR_OK) return st;
-  // A row takes enough warps for four chunks a thread (eight for the longest
-  // rows); short calls take one chunk a thread, which is the faster row.
-  const int n_chunks = C / 8, most = qknr::kLnFwdThreads / 32;
-  int cpt = T < 4LL * di.num_sms ? 1 : 4;
-  int warps = (n_chunks + 32 * cpt - 1) / (32 * cpt);
-  if (warps > most) warps = most;
-  cpt = (n_chunks + 32 * warps - 1) / (32 * warps);
+  // Calls of a few rows per SM have nothing to stream: a CTA per row, its
+  // chunks spread over as many warps as there are.  So do rows of more than
+  // 12288 values, whose parameters do not fit in registers.
+  const int n_chunks = C / 8, keep = 3;
+  const bool bf = a->dtype == QKNR_BF16;
+  if (T < 4LL * di.num_sms || n_chunks > 32 * keep * qknr::kLnWarps) {
+    const int warps = warps_for(n_chunks, 1, qknr::kLnWarps);
+    const int cpt = (n_chunks + 32 * warps - 1) / (32 * warps);
+    kp.group_warps = warps;
+    kp.groups = warps == 1 ? 4 : 1;               // rows of one warp: four to a CTA
+    return run(bf ? direct_fn<__nv_bfloat16>(cpt) : direct_fn<__half>(cpt), (T + kp.groups - 1) / kp.groups,
+               32 * warps * kp.groups, 0, a, &kp, dev, di, stream, "cudaLaunchKernelExC(layer norm)");
+  }
+  const int warps = warps_for(n_chunks, keep, qknr::kLnWarps);
+  const int cpt = (n_chunks + 32 * warps - 1) / (32 * warps);
   kp.group_warps = warps;
-  kp.groups = warps == 1 ? 4 : 1;                 // rows of one warp: four to a CTA
-  const void* fn = a->dtype == QKNR_BF16 ? forward_fn<__nv_bfloat16>(cpt) : forward_fn<__half>(cpt);
-  const int block = 32 * warps * kp.groups;
-  int occ = 0;
-  st = qknr_host::occupancy(fn, dev, block, 0, &occ);
-  if (st != QKNR_OK) return st;
-  long long grid = (T + kp.groups - 1) / kp.groups;
-  if (grid > (long long)di.num_sms * occ) grid = (long long)di.num_sms * occ;
-  return run(fn, grid, block, 0, a, &kp, dev, di, stream, "cudaLaunchKernelExC(layer norm)");
+  kp.groups = qknr::kLnWarps / warps;
+  kp.stages = stages_for(di, kp.row_bytes, kp.groups, 0);
+  return run(bf ? forward_fn<__nv_bfloat16>(cpt) : forward_fn<__half>(cpt), di.num_sms, qknr::kLnThreads,
+             qknr::kLnOffStages + static_cast<size_t>(kp.stages) * kp.groups * kp.row_bytes, a, &kp, dev, di, stream,
+             "cudaLaunchKernelExC(layer norm)");
 }
 
 qknr_status qknr_ln_workspace_bytes(const qknr_ln_args* a, size_t* bytes) {
@@ -297,13 +334,15 @@ qknr_status qknr_ln_backward(const qknr_ln_args* a, qknr_stream_t stream) {
     st = run(fn, grid, 256, 0, a, &kp, dev, di, stream, "cudaLaunchKernelExC(layer norm row sums)");
     if (st != QKNR_OK) return st;
   }
-  const void* fn = bf ? backward_fn<__nv_bfloat16>(c.tiles > 1) : backward_fn<__half>(c.tiles > 1);
+  const void* fn = bf ? backward_fn<__nv_bfloat16>(c.cpt, c.tiles > 1) : backward_fn<__half>(c.cpt, c.tiles > 1);
   const int cols = C < qknr::kLnTile ? C : qknr::kLnTile;
-  const size_t smem = qknr::kLnBwdRedBytes + (c.groups > 1 ? static_cast<size_t>(c.groups) * 2 * cols * 4 : 0);
+  const size_t sums = c.groups > 1 ? static_cast<size_t>(c.groups) * 2 * cols * 4 : 0;
+  const size_t stage = 4 * static_cast<size_t>(cols);
+  kp.stages = stages_for(di, stage, c.groups, sums);
   long long ctas = di.num_sms / c.tiles;
   if (ctas > c.sets * c.units_per_set) ctas = c.sets * c.units_per_set;
-  st = run(fn, ctas * c.tiles, 32 * c.group_warps * c.groups, smem, a, &kp, dev, di, stream,
-           "cudaLaunchKernelExC(layer norm backward)");
+  st = run(fn, ctas * c.tiles, qknr::kLnBwdThreads, qknr::kLnOffStages + kp.stages * c.groups * stage + sums, a, &kp,
+           dev, di, stream, "cudaLaunchKernelExC(layer norm backward)");
   if (st != QKNR_OK || !kp.parts || (!kp.dweight && !kp.dbias)) return st;
   qknr::PartsParams pp;
   memset(&pp, 0, sizeof(pp));

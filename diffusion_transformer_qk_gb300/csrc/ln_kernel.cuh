@@ -1,12 +1,20 @@
 // Layer norm, forward and backward, for sm_103a (formulas: qknr_ln.h).
 //
 // Both passes are bound by HBM: the forward reads x and writes y, the
-// backward reads x and dy and writes dx.  A row lives in the registers of
-// the warps that share it: thread l of a group of W warps holds the 16-byte
-// chunks l, l + 32 W, ... of the row, so the variance is a true second pass
-// (squared deviations from the finished mean) without a second read, and a
-// group asks for its next row before it reduces the one it holds, which keeps
-// the loads in flight across the reductions' latency.
+// backward reads x and dy and writes dx.  Persistent CTAs, one per SM; their
+// warps form groups that each take whole rows.  A group owns a ring of
+// shared-memory stages that bulk copies fill some rows ahead (128 KB per SM
+// in flight), reads a row into registers, and asks for the row after next
+// into the same stage as soon as the group's first barrier says that every
+// warp has its share.  Thread l of a group of W warps holds the 16-byte
+// chunks l, l + 32 W, ... of every row it sees, so the row is unpacked once,
+// the variance is a true second pass (squared deviations from the finished
+// mean) without a second read, and what belongs to a column (gain, bias, the
+// columns' sums) stays in registers from row to row.
+//
+// Every mbarrier wait is bounded.  A group decides together whether it goes
+// on: each warp posts whether its wait succeeded with its part of the row's
+// sums, so no warp is left at a named barrier for one that gave up.
 #pragma once
 
 #include "qknr_ptx.cuh"
@@ -38,12 +46,23 @@ struct LnParams {
   long long units_per_set;    // chunks of rows each parameter row's tokens are cut into
   long long unit_rows;        // rows per chunk
   int tiles;                  // column tiles a row is cut into
+  int stages;                 // ring depth of a group
+  unsigned row_bytes;         // hidden * 2
+  unsigned flags;
+  unsigned long long wait_limit_ns;
   float eps;
   float inv_c;
   float unit;                 // added to the weight
   int* status;
   MemSpan sp_x, sp_y, sp_dy, sp_dx, sp_weight, sp_bias, sp_mean, sp_rstd, sp_dweight, sp_dbias, sp_ws;
 };
+
+// the parameter row of a token row
+__device__ __forceinline__ long long ln_set(const LnParams& p, long long row) {
+  if (p.sets == 1) return 0;
+  if (p.tokens <= 0xffffffffLL) return static_cast<unsigned>(row) / static_cast<unsigned>(p.rows_per_batch);
+  return row / p.rows_per_batch;
+}
 
 // 16 bytes read once
 __device__ __forceinline__ uint4 ln_load16(const char* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
@@ -74,24 +93,46 @@ __device__ __forceinline__ void ln_gain8(const LnParams& p, long long set, int k
   for (int j = 0; j < 4; ++j) g[j] = __fadd2_rn(g[j], make_float2(p.unit, p.unit));
 }
 
+// the bias of chunk k, or 0
+template <typename T>
+__device__ __forceinline__ void ln_bias8(const LnParams& p, long long set, int k, float2 (&b)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = make_float2(0.0f, 0.0f);
+  const int bytes = p.param_fp32 ? 32 : 16;
+  const char* row = p.bias + set * p.param_stride;
+  if (p.bias && in_span(row + k * bytes, bytes, p.sp_bias, p.status)) ln_param8<T>(row, k, p.param_fp32, b);
+}
+
 __device__ __forceinline__ float ln_warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
 
-// The sum of `a` (and of `b`) over a group's W warps, the same in every
-// thread: a shuffle tree inside each warp, then the warps' sums added in
-// order from shared memory.  `red` alternates between two buffers, so the
-// one barrier also keeps a fast warp from overwriting sums a slow one reads.
-__device__ __forceinline__ float2 ln_group_sum(float2 v, int W, int gw, int lane, int bar_id, float2* red) {
+// The sum of v over a group's W warps, the same in every thread: a shuffle
+// tree inside each warp, then the warps' sums added in order from shared
+// memory.  `ok` becomes whether every warp's was true.  The caller uses two
+// buffers `red` in turn, so the one barrier also keeps a fast warp from
+// overwriting sums a slow one reads.
+struct LnPart {
+  float2 v;
+  int ok;
+  int pad;
+};
+
+__device__ __forceinline__ float2 ln_group_sum(float2 v, bool& ok, int W, int gw, int lane, int bar_id, LnPart* red) {
   v.x = ln_warp_sum(v.x);
   v.y = ln_warp_sum(v.y);
   if (W == 1) return v;
-  if (lane == 0) red[gw] = v;
+  if (lane == 0) red[gw] = LnPart{v, ok, 0};
   named_barrier_sync(bar_id, 32 * W);
-  float2 s = red[0];
-  for (int w = 1; w < W; ++w) s = __fadd2_rn(s, red[w]);
+  float2 s = red[0].v;
+  int all = red[0].ok;
+  for (int w = 1; w < W; ++w) {
+    s = __fadd2_rn(s, red[w].v);
+    all &= red[w].ok;
+  }
+  ok = all != 0;
   return s;
 }
 
@@ -100,111 +141,277 @@ __device__ __forceinline__ float ln_hsum(const float2 (&v)[4]) {
   return __fadd_rn(s.x, s.y);
 }
 
-constexpr int kLnFwdThreads = 512;
+// ---------------------------------------------------------------------------
+// the rings
+
+constexpr int kLnWarps = 16;                      // warps of the forward pass
+constexpr int kLnThreads = 32 * kLnWarps;
+constexpr int kLnMaxStages = 32;                  // all groups' together
+// dynamic shared memory map (bytes)
+constexpr int kLnOffBars = 0;                     // full[32]
+constexpr int kLnOffAbort = 256;
+constexpr int kLnOffRed = 512;                    // LnPart [2][kLnWarps]
+constexpr int kLnOffStages = kLnOffRed + 2 * kLnWarps * 16;   // 1024
+static_assert(sizeof(LnPart) == 16 && kLnOffStages % 128 == 0, "shared memory map");
+
+// One group's ring of `stages` stages.  Its rows come in the order in which
+// the group's first thread put them.
+struct LnRing {
+  uint32_t bars, stage0;
+  const unsigned char* ptr;
+  unsigned stage_bytes;
+  int stages;
+  volatile int* abort_flag;
+  int* status;
+  unsigned long long limit;
+  int s = 0;                  // next stage to read
+  uint32_t phase = 0;
+  int put_s = 0;              // next stage to fill (first thread)
+  int in_flight = 0;
+
+  __device__ __forceinline__ LnRing(unsigned char* smem, const LnParams& p, unsigned stage_bytes_, int grp)
+      : bars(smem_addr(smem) + kLnOffBars + 8 * grp * p.stages),
+        stage0(smem_addr(smem) + kLnOffStages + grp * p.stages * stage_bytes_),
+        ptr(smem + kLnOffStages + grp * p.stages * stage_bytes_),
+        stage_bytes(stage_bytes_),
+        stages(p.stages),
+        abort_flag(reinterpret_cast<volatile int*>(smem + kLnOffAbort)),
+        status(p.status),
+        limit(p.wait_limit_ns) {}
+
+  // Row `a` (and `b` behind it) into the next stage, which has been read.
+  __device__ __forceinline__ void put(const char* a, const MemSpan& sp_a, const char* b, const MemSpan& sp_b,
+                                      unsigned bytes) {
+    if (!in_span(a, bytes, sp_a, status) || (b && !in_span(b, bytes, sp_b, status))) {
+      *abort_flag = 1;
+      return;
+    }
+    const uint32_t dst = stage0 + put_s * stage_bytes, bar = bars + 8 * put_s;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the group's reads come before the copy
+    mbar_arrive_expect_tx(bar, b ? 2 * bytes : bytes);
+    bulk_load(dst, a, bytes, bar);
+    if (b) bulk_load(dst + bytes, b, bytes, bar);
+    if (++put_s == stages) put_s = 0;
+    ++in_flight;
+  }
+  // The next row has landed; the same answer in every lane.
+  __device__ __forceinline__ bool wait() const {
+    return __all_sync(0xffffffffu, mbar_try_wait(bars + 8 * s, phase) ||
+                                       bounded_wait(bars + 8 * s, phase, limit, abort_flag, status));
+  }
+  __device__ __forceinline__ const uint4* row() const { return reinterpret_cast<const uint4*>(ptr + s * stage_bytes); }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  // first thread, giving up: copies in flight end before the CTA leaves its shared memory
+  __device__ __forceinline__ void drain() {
+    const unsigned long long t0 = global_timer_ns();
+    for (; in_flight > 0; --in_flight) {
+      while (!mbar_try_wait(bars + 8 * s, phase) && global_timer_ns() - t0 < limit) {
+      }
+      next();
+    }
+  }
+};
+
+// one thread: all groups' barriers
+__device__ __forceinline__ void ln_init_rings(unsigned char* smem, int n) {
+  for (int i = 0; i < n; ++i) mbar_init(smem_addr(smem) + kLnOffBars + 8 * i, 1);
+  *reinterpret_cast<volatile int*>(smem + kLnOffAbort) = 0;
+  fence_barrier_init();
+}
+
+// ---------------------------------------------------------------------------
+// forward
+
+// Calls of a few rows per SM, and rows whose columns are too many for a
+// thread to keep their parameters: a row is loaded straight into registers
+// and held as read.
+template <typename T, int CPT>
+__device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&raw)[CPT], long long row, int W, int gw,
+                                               int lane, int bar, LnPart* red) {
+  const int l = gw * 32 + lane, step = 32 * W, n_chunks = p.hidden / 8;
+  bool ok = true;
+  // mean: chunks past the row hold zeros
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    float2 X[4];
+    Elem<T>::unpack(raw[i], X);
+    s = __fadd_rn(s, ln_hsum(X));
+  }
+  const float mean = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, bar, red).x, p.inv_c);
+  const float2 nm = make_float2(-mean, -mean);
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    if (l + i * step < n_chunks) {
+      float2 X[4];
+      Elem<T>::unpack(raw[i], X);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 d = __fadd2_rn(X[j], nm);
+        X[j] = __fmul2_rn(d, d);
+      }
+      s = __fadd_rn(s, ln_hsum(X));
+    }
+  }
+  const float var = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, bar, red + kLnWarps).x, p.inv_c);
+  const float rstd = rsqrtf(__fadd_rn(var, p.eps));
+  if (l == 0) {
+    if (p.mean && in_span(p.mean + row, 4, p.sp_mean, p.status)) p.mean[row] = mean;
+    if (p.rstd && in_span(p.rstd + row, 4, p.sp_rstd, p.status)) p.rstd[row] = rstd;
+  }
+  const long long set = ln_set(p, row);
+  char* dst = p.y + row * p.y_stride;
+  const bool fits = in_span(dst, p.row_bytes, p.sp_y, p.status);
+  const float2 R = make_float2(rstd, rstd);
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int k = l + i * step;
+    if (fits && k < n_chunks) {
+      float2 X[4], g[4], b[4];
+      Elem<T>::unpack(raw[i], X);
+      ln_gain8<T>(p, set, k, g);
+      ln_bias8<T>(p, set, k, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) X[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(X[j], nm), R), g[j], b[j]);
+      store16(dst + k * 16, Elem<T>::pack(X));
+    }
+  }
+}
 
 template <typename T, int CPT>
-__global__ void __launch_bounds__(kLnFwdThreads) ln_forward_kernel(const __grid_constant__ LnParams p) {
-  __shared__ float2 red[2][kLnFwdThreads / 32];
+__global__ void __launch_bounds__(kLnThreads) ln_forward_direct_kernel(const __grid_constant__ LnParams p) {
+  __shared__ LnPart red[2 * kLnWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.group_warps, grp = warp / W, gw = warp % W;
-  const int l = gw * 32 + lane, step = 32 * W, n_chunks = p.hidden / 8;
-  const long long stride = static_cast<long long>(gridDim.x) * p.groups;
-  const unsigned row_bytes = p.hidden * 2u;
+  const int l = gw * 32 + lane, n_chunks = p.hidden / 8;
   grid_dependency_wait();
-
-  uint4 next[CPT];
-  long long row = static_cast<long long>(blockIdx.x) * p.groups + grp;
-  auto fetch = [&](long long r) {
-    const char* src = p.x + r * p.x_stride;
-    const bool ok = r < p.tokens && in_span(src, row_bytes, p.sp_x, p.status);
-#pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const int k = l + i * step;
-      next[i] = make_uint4(0, 0, 0, 0);
-      if (ok && k < n_chunks) next[i] = ln_load16(src + k * 16);
-    }
-  };
-  fetch(row);
-  for (; row < p.tokens; row += stride) {
+  const long long row = static_cast<long long>(blockIdx.x) * p.groups + grp;
+  const char* src = p.x + row * p.x_stride;
+  if (row < p.tokens && in_span(src, p.row_bytes, p.sp_x, p.status)) {
     uint4 raw[CPT];
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) raw[i] = next[i];
-    fetch(row + stride);
-    // mean: chunks past the row hold zeros
+    for (int i = 0; i < CPT; ++i) {
+      const int k = l + i * 32 * W;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (k < n_chunks) raw[i] = ln_load16(src + k * 16);
+    }
+    ln_forward_row<T, CPT>(p, raw, row, W, gw, lane, 1 + grp, red);
+  }
+  grid_dependents_launch();
+}
+
+template <typename T, int CPT>
+__global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_constant__ LnParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = p.group_warps, grp = warp / W, gw = warp % W, l = gw * 32 + lane, n_chunks = p.hidden / 8;
+  LnRing ring(smem, p, p.row_bytes, grp);
+  if (threadIdx.x == 0) ln_init_rings(smem, p.stages * p.groups);
+  __syncthreads();
+  grid_dependency_wait();
+  const long long step = static_cast<long long>(gridDim.x) * p.groups;
+  long long row = static_cast<long long>(blockIdx.x) * p.groups + grp, ahead = row;
+  const bool leader = gw == 0 && lane == 0 && !(p.flags & 1u);   // test only: issue nothing
+  if (leader)
+    for (int i = 0; i < p.stages && ahead < p.tokens; ++i, ahead += step)
+      ring.put(p.x + ahead * p.x_stride, p.sp_x, nullptr, p.sp_x, p.row_bytes);
+  LnPart* red = reinterpret_cast<LnPart*>(smem + kLnOffRed) + grp * W;
+  bool mine[CPT];
+  float2 g[CPT][4], b[CPT][4];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
+  long long set = -1;
+  bool ok = true;
+  for (; row < p.tokens; row += step) {
+    if (ln_set(p, row) != set) {
+      set = ln_set(p, row);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        if (!mine[i]) continue;
+        ln_gain8<T>(p, set, l + i * 32 * W, g[i]);
+        ln_bias8<T>(p, set, l + i * 32 * W, b[i]);
+      }
+    }
+    ok = ring.wait();
+    float2 X[CPT][4];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      float2 X[4];
-      Elem<T>::unpack(raw[i], X);
-      s = __fadd_rn(s, ln_hsum(X));
+      const uint4 raw = mine[i] ? ring.row()[l + i * 32 * W] : make_uint4(0, 0, 0, 0);
+      Elem<T>::unpack(raw, X[i]);
+      s = __fadd_rn(s, ln_hsum(X[i]));
     }
-    const int bar = 1 + grp;
-    const float mean = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), W, gw, lane, bar, red[0]).x, p.inv_c);
+    const float mean = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, 1 + grp, red).x, p.inv_c);
+    if (!ok) break;
+    ring.next();
+    if (leader) {
+      --ring.in_flight;
+      if (ahead < p.tokens) ring.put(p.x + ahead * p.x_stride, p.sp_x, nullptr, p.sp_x, p.row_bytes);
+      ahead += step;
+    }
     const float2 nm = make_float2(-mean, -mean);
-    s = 0.0f;
+    float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      if (l + i * step < n_chunks) {
-        float2 X[4];
-        Elem<T>::unpack(raw[i], X);
+    for (int i = 0; i < CPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 d = __fadd2_rn(X[j], nm);
-          X[j] = __fmul2_rn(d, d);
-        }
-        s = __fadd_rn(s, ln_hsum(X));
+      for (int j = 0; j < 4; ++j) {
+        X[i][j] = __fadd2_rn(X[i][j], nm);
+        if (mine[i]) q = __ffma2_rn(X[i][j], X[i][j], q);
       }
-    }
-    const float var = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), W, gw, lane, bar, red[1]).x, p.inv_c);
+    const float var = __fmul_rn(
+        ln_group_sum(make_float2(__fadd_rn(q.x, q.y), 0.0f), ok, W, gw, lane, 1 + grp, red + kLnWarps).x, p.inv_c);
     const float rstd = rsqrtf(__fadd_rn(var, p.eps));
     if (l == 0) {
       if (p.mean && in_span(p.mean + row, 4, p.sp_mean, p.status)) p.mean[row] = mean;
       if (p.rstd && in_span(p.rstd + row, 4, p.sp_rstd, p.status)) p.rstd[row] = rstd;
     }
-    const long long set = row / p.rows_per_batch;
-    const char* brow = p.bias + set * p.param_stride;
-    char* dst = p.y + row * p.y_stride;
-    const bool ok = in_span(dst, row_bytes, p.sp_y, p.status) &&
-                    (!p.bias || in_span(brow, static_cast<unsigned long long>(p.hidden) * (p.param_fp32 ? 4 : 2),
-                                        p.sp_bias, p.status));
     const float2 R = make_float2(rstd, rstd);
+    char* dst = p.y + row * p.y_stride + l * 16;
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-      const int k = l + i * step;
-      if (ok && k < n_chunks) {
-        float2 X[4], g[4], b[4];
-        Elem<T>::unpack(raw[i], X);
-        ln_gain8<T>(p, set, k, g);
+      float2 o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = make_float2(0.0f, 0.0f);
-        if (p.bias) ln_param8<T>(brow, k, p.param_fp32, b);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) X[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(X[j], nm), R), g[j], b[j]);
-        store16(dst + k * 16, Elem<T>::pack(X));
-      }
+      for (int j = 0; j < 4; ++j) o[j] = __ffma2_rn(__fmul2_rn(X[i][j], R), g[i][j], b[i][j]);
+      if (mine[i] && in_span(dst + i * 512 * W, 16, p.sp_y, p.status)) store16(dst + i * 512 * W, Elem<T>::pack(o));
     }
   }
   grid_dependents_launch();
+  if (!ok && leader) ring.drain();
 }
 
 // ---------------------------------------------------------------------------
 // backward
 
-constexpr int kLnBwdWarps = 32;
+// Eight warps of up to four chunks a thread: with 255 registers a thread
+// holds its columns' sums, its gains and a row's xhat and dy, and the row's
+// fixed costs (two shuffle trees, a barrier) are paid by few warps.
+constexpr int kLnBwdWarps = 8;
 constexpr int kLnBwdThreads = 32 * kLnBwdWarps;
-constexpr int kLnTile = 8 * kLnBwdThreads;        // columns of one CTA: a chunk per thread
-constexpr int kLnBwdRedBytes = 2 * kLnBwdWarps * 8;
+constexpr int kLnBwdCpt = 4;
+constexpr int kLnTile = 8 * 32 * kLnBwdWarps * kLnBwdCpt;   // 8192 columns: the longest row one CTA takes
 
-// g * xhat and g of one chunk, summed into (sum g, sum g xhat)
+// xhat and dy of one chunk
 template <typename T>
-__device__ __forceinline__ void ln_grad_chunk(const uint4& xr, const uint4& dr, const float2 (&gain)[4], float2 nm,
-                                              float2 R, float2 (&xh)[4], float2 (&dy)[4], float2& s) {
+__device__ __forceinline__ void ln_grad_values(const uint4& xr, const uint4& dr, float2 nm, float2 R, float2 (&xh)[4],
+                                               float2 (&dy)[4]) {
   Elem<T>::unpack(xr, xh);
   Elem<T>::unpack(dr, dy);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) xh[j] = __fmul2_rn(__fadd2_rn(xh[j], nm), R);
+}
+
+// one chunk's part of (sum g, sum g xhat)
+__device__ __forceinline__ void ln_grad_sums(const float2 (&xh)[4], const float2 (&dy)[4], const float2 (&gain)[4],
+                                             float2& s) {
   float2 a = make_float2(0.0f, 0.0f), c = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    xh[j] = __fmul2_rn(__fadd2_rn(xh[j], nm), R);
     const float2 g = __fmul2_rn(dy[j], gain[j]);
     a = __fadd2_rn(a, g);
     c = __ffma2_rn(g, xh[j], c);
@@ -217,7 +424,7 @@ __device__ __forceinline__ void ln_grad_chunk(const uint4& xr, const uint4& dr, 
 // one CTA per row.
 template <typename T>
 __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant__ LnParams p) {
-  __shared__ float2 red[2][8];
+  __shared__ LnPart red[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_chunks = p.hidden / 8;
   grid_dependency_wait();
   int parity = 0;
@@ -225,18 +432,20 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
     const char* xs = p.x + row * p.x_stride;
     const char* ds = p.dy + row * p.dy_stride;
     float2 s = make_float2(0.0f, 0.0f);
-    if (in_span(xs, p.hidden * 2u, p.sp_x, p.status) && in_span(ds, p.hidden * 2u, p.sp_dy, p.status) &&
+    if (in_span(xs, p.row_bytes, p.sp_x, p.status) && in_span(ds, p.row_bytes, p.sp_dy, p.status) &&
         in_span(p.mean + row, 4, p.sp_mean, p.status) && in_span(p.rstd + row, 4, p.sp_rstd, p.status)) {
       const float2 nm = make_float2(-p.mean[row], -p.mean[row]), R = make_float2(p.rstd[row], p.rstd[row]);
-      const long long set = row / p.rows_per_batch;
+      const long long set = ln_set(p, row);
       for (int k = threadIdx.x; k < n_chunks; k += 256) {
         float2 gain[4], xh[4], dy[4];
         ln_gain8<T>(p, set, k, gain);
-        ln_grad_chunk<T>(*reinterpret_cast<const uint4*>(xs + k * 16), *reinterpret_cast<const uint4*>(ds + k * 16),
-                         gain, nm, R, xh, dy, s);
+        ln_grad_values<T>(*reinterpret_cast<const uint4*>(xs + k * 16), *reinterpret_cast<const uint4*>(ds + k * 16),
+                          nm, R, xh, dy);
+        ln_grad_sums(xh, dy, gain, s);
       }
     }
-    s = ln_group_sum(s, 8, warp, lane, 1, red[parity]);
+    bool ok = true;
+    s = ln_group_sum(s, ok, 8, warp, lane, 1, red[parity]);
     if (threadIdx.x == 0 && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status)) {
       p.row_sums[2 * row] = __fmul_rn(s.x, p.inv_c);
       p.row_sums[2 * row + 1] = __fmul_rn(s.y, p.inv_c);
@@ -245,128 +454,185 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
   grid_dependents_launch();
 }
 
-// dx, and the sums of dy and dy xhat over the rows.  A thread owns one chunk
-// of 8 columns for the whole launch, so those sums stay in its registers
-// over all the rows of a unit (a chunk of one sample's rows); the CTA's row
-// groups then add theirs in order through shared memory and write the unit's
-// partial sums, or the result where a sample is one unit.  LONG: the row
-// spans several CTAs (a column tile each) and its two sums come from
+// dx, and the sums of dy and dy xhat over the rows.  A thread owns the same
+// chunks of 8 columns for the whole launch, so those sums stay in its
+// registers over all the rows of a unit (a chunk of one sample's rows); the
+// CTA's row groups then add theirs in order through shared memory and write
+// the unit's partial sums, or the result where a sample is one unit.  LONG:
+// the row spans several CTAs (a column tile each) and its two sums come from
 // ln_row_sums_kernel.
-template <typename T, bool LONG>
-__global__ void __launch_bounds__(kLnBwdThreads) ln_backward_kernel(const __grid_constant__ LnParams p) {
-  extern __shared__ float2 red[];                 // [2][kLnBwdWarps], two buffers used in turn
-  float* acc = reinterpret_cast<float*>(red + 2 * kLnBwdWarps);   // [groups][2][columns of the tile]
+template <typename T, int CPT, bool LONG>
+__global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __grid_constant__ LnParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = p.group_warps, grp = warp / W, gw = warp % W;
-  const int tile = static_cast<int>(blockIdx.x % p.tiles);
-  const int k0 = tile * (kLnTile / 8), n_chunks = p.hidden / 8;
-  const int k = k0 + gw * 32 + lane;              // this thread's chunk
-  const int tile_cols = (n_chunks - k0 < kLnTile / 8 ? n_chunks - k0 : kLnTile / 8) * 8;
-  const bool mine = k < n_chunks;
-  const long long units = p.sets * p.units_per_set;
+  const int W = p.group_warps;
+  const int tile = static_cast<int>(blockIdx.x % p.tiles), k0 = tile * (kLnTile / 8);
+  const int n_chunks = p.hidden / 8 - k0 < kLnTile / 8 ? p.hidden / 8 - k0 : kLnTile / 8;   // of this tile
+  const unsigned bytes = n_chunks * 16u;
+  // two rows of the widest tile per stage
+  const unsigned stage_bytes = 2 * (p.tiles > 1 ? kLnTile * 2u : p.row_bytes);
+  const int grp = warp / W, gw = warp % W, l = gw * 32 + lane, cols = n_chunks * 8;
+  LnRing ring(smem, p, stage_bytes, grp);
+  volatile int* give_up = ring.abort_flag + 1;
+  if (threadIdx.x == 0) {
+    ln_init_rings(smem, p.stages * p.groups);
+    *give_up = 0;
+  }
+  __syncthreads();
   grid_dependency_wait();
-
-  for (long long u = blockIdx.x / p.tiles; u < units; u += gridDim.x / p.tiles) {
+  const long long units = p.sets * p.units_per_set, unit_step = gridDim.x / p.tiles;
+  // rows [first, last) of unit u
+  auto rows_of = [&](long long u, long long& first, long long& last) {
     const long long set = u / p.units_per_set;
-    const long long set_end = (set + 1) * p.rows_per_batch < p.tokens ? (set + 1) * p.rows_per_batch : p.tokens;
-    const long long first = set * p.rows_per_batch + (u % p.units_per_set) * p.unit_rows;
-    const long long last = first + p.unit_rows < set_end ? first + p.unit_rows : set_end;
-    float2 dw[4], db[4], gain[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dw[j] = db[j] = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) gain[j] = make_float2(0.0f, 0.0f);
-    if (mine) ln_gain8<T>(p, set, k, gain);
+    const long long end = (set + 1) * p.rows_per_batch < p.tokens ? (set + 1) * p.rows_per_batch : p.tokens;
+    first = set * p.rows_per_batch + (u - set * p.units_per_set) * p.unit_rows;
+    last = first + p.unit_rows < end ? first + p.unit_rows : end;
+    return set;
+  };
+  // the group's rows, some ahead of the one in work: unit, row, end of the unit
+  long long a_unit = blockIdx.x / p.tiles, a_row = 0, a_last = 0;
+  const bool leader = gw == 0 && lane == 0 && !(p.flags & 1u);   // test only: issue nothing
+  auto put = [&]() {
+    while (a_row >= a_last) {                     // the next unit with a row for this group
+      if (a_unit >= units) return;
+      rows_of(a_unit, a_row, a_last);
+      a_row += grp;
+      a_unit += unit_step;
+    }
+    ring.put(p.x + a_row * p.x_stride + k0 * 16, p.sp_x, p.dy + a_row * p.dy_stride + k0 * 16, p.sp_dy, bytes);
+    a_row += p.groups;
+  };
+  if (leader)
+    for (int i = 0; i < p.stages; ++i) put();
 
-    uint4 nx, nd;
-    float nmean, nrstd;
-    auto fetch = [&](long long r) {
-      nx = nd = make_uint4(0, 0, 0, 0);
-      nmean = nrstd = 0.0f;
-      const char* xs = p.x + r * p.x_stride + k * 16;
-      const char* ds = p.dy + r * p.dy_stride + k * 16;
-      if (r < last && mine && in_span(xs, 16, p.sp_x, p.status) && in_span(ds, 16, p.sp_dy, p.status)) {
-        nx = ln_load16(xs);
-        nd = ln_load16(ds);
-      }
+  float* acc = reinterpret_cast<float*>(smem + kLnOffStages + p.stages * p.groups * stage_bytes);   // [groups][2][columns]
+  LnPart* red = reinterpret_cast<LnPart*>(smem + kLnOffRed) + grp * W;
+  bool mine[CPT];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
+  bool ok = true;
+  for (long long u = blockIdx.x / p.tiles; u < units; u += unit_step) {
+    long long first, last;
+    const long long set = rows_of(u, first, last);
+    float2 dw[CPT][4], db[CPT][4], gain[CPT][4];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = gain[i][j] = make_float2(0.0f, 0.0f);
+      if (mine[i]) ln_gain8<T>(p, set, k0 + l + i * 32 * W, gain[i]);
+    }
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto stats = [&](long long r) {
       if (r < last && in_span(p.mean + r, 4, p.sp_mean, p.status) && in_span(p.rstd + r, 4, p.sp_rstd, p.status)) {
         nmean = p.mean[r];
         nrstd = p.rstd[r];
       }
     };
-    fetch(first + grp);
+    stats(first + grp);
     int parity = 0;
-    for (long long row = first + grp; row < last; row += p.groups, parity ^= 1) {
-      const uint4 xr = nx, dr = nd;
+    for (long long row = first + grp; ok && row < last; row += p.groups, parity ^= 1) {
       const float2 nm = make_float2(-nmean, -nmean), R = make_float2(nrstd, nrstd);
-      fetch(row + p.groups);
-      float2 xh[4], dy[4], s = make_float2(0.0f, 0.0f);
-      ln_grad_chunk<T>(xr, dr, gain, nm, R, xh, dy, s);
-      if (LONG) {
-        s = make_float2(0.0f, 0.0f);
-        if (in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status))
-          s = *reinterpret_cast<const float2*>(p.row_sums + 2 * row);
-      } else {
-        s = ln_group_sum(s, W, gw, lane, 1 + grp, red + parity * kLnBwdWarps + grp * W);
-        s = __fmul2_rn(s, make_float2(p.inv_c, p.inv_c));
-      }
-      const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
-      float2 o[4];
+      stats(row + p.groups);
+      ok = ring.wait();
+      float2 xh[CPT][4], dy[CPT][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        db[j] = __fadd2_rn(db[j], dy[j]);
-        dw[j] = __ffma2_rn(dy[j], xh[j], dw[j]);
-        o[j] = __fmul2_rn(__ffma2_rn(xh[j], c2, __ffma2_rn(dy[j], gain[j], c1)), R);
+      for (int i = 0; i < CPT; ++i) {
+        uint4 xr = make_uint4(0, 0, 0, 0), dr = xr;
+        if (mine[i]) {
+          xr = ring.row()[l + i * 32 * W];
+          dr = ring.row()[n_chunks + l + i * 32 * W];
+        }
+      // past the row: dy = 0 and gain = 0, so xhat's value does not count
+        ln_grad_values<T>(xr, dr, nm, R, xh[i], dy[i]);
       }
-      char* dst = p.dx + row * p.dx_stride + k * 16;
-      if (mine && in_span(dst, 16, p.sp_dx, p.status)) store16(dst, Elem<T>::pack(o));
-    }
-
-    // the groups' sums, added in order
-    const int c = (gw * 32 + lane) * 8;
-    if (p.groups > 1) {
-      float* slot = acc + grp * 2 * tile_cols;
-      __syncthreads();                            // the previous unit's sums have been read
-      if (mine) {
+      float2 s = make_float2(0.0f, 0.0f);
+      if (!LONG) {
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) ln_grad_sums(xh[i], dy[i], gain[i], s);
+      }
+      s = ln_group_sum(s, ok, W, gw, lane, 1 + grp, red + parity * kLnBwdWarps);
+      if (!ok) break;
+      ring.next();
+      if (leader) {
+        --ring.in_flight;
+        put();
+      }
+      if (!LONG)
+        s = __fmul2_rn(s, make_float2(p.inv_c, p.inv_c));
+      else if (in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status))
+        s = *reinterpret_cast<const float2*>(p.row_sums + 2 * row);
+      const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
+      char* dst = p.dx + row * p.dx_stride + (k0 + l) * 16;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        float2 o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          *reinterpret_cast<float2*>(slot + c + 2 * j) = dw[j];
-          *reinterpret_cast<float2*>(slot + tile_cols + c + 2 * j) = db[j];
+          db[i][j] = __fadd2_rn(db[i][j], dy[i][j]);
+          dw[i][j] = __ffma2_rn(dy[i][j], xh[i][j], dw[i][j]);
+          o[j] = __fmul2_rn(__ffma2_rn(xh[i][j], c2, __ffma2_rn(dy[i][j], gain[i][j], c1)), R);
         }
-      }
-      __syncthreads();
-      if (grp == 0 && mine) {
-        for (int g = 1; g < p.groups; ++g) {
-          const float* other = acc + g * 2 * tile_cols;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dw[j] = __fadd2_rn(dw[j], *reinterpret_cast<const float2*>(other + c + 2 * j));
-            db[j] = __fadd2_rn(db[j], *reinterpret_cast<const float2*>(other + tile_cols + c + 2 * j));
-          }
-        }
+        if (mine[i] && in_span(dst + i * 512 * W, 16, p.sp_dx, p.status)) store16(dst + i * 512 * W, Elem<T>::pack(o));
       }
     }
-    if (grp == 0 && mine) {
-      const bool whole = p.units_per_set == 1;
-      float* ow = whole ? p.dweight : p.parts;
-      float* ob = whole ? p.dbias : p.parts;
-      if (ow) {
-        ow += whole ? set * p.hidden + k * 8 : u * 2 * p.hidden + k * 8;
-        if (in_span(ow, 32, whole ? p.sp_dweight : p.sp_ws, p.status)) {
-          reinterpret_cast<float4*>(ow)[0] = make_float4(dw[0].x, dw[0].y, dw[1].x, dw[1].y);
-          reinterpret_cast<float4*>(ow)[1] = make_float4(dw[2].x, dw[2].y, dw[3].x, dw[3].y);
+    // the groups' sums, added in order
+    if (p.groups > 1) {
+      float* slot = acc + grp * 2 * cols;
+      named_barrier_sync(15, kLnBwdThreads);            // the previous unit's sums have been read
+#pragma unroll
+      for (int i = 0; i < CPT; ++i)
+        if (mine[i]) {
+          float2* a = reinterpret_cast<float2*>(slot + (l + i * 32 * W) * 8);
+          float2* b = reinterpret_cast<float2*>(slot + cols + (l + i * 32 * W) * 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            a[j] = dw[i][j];
+            b[j] = db[i][j];
+          }
         }
-      }
-      if (ob) {
-        ob += whole ? set * p.hidden + k * 8 : (u * 2 + 1) * p.hidden + k * 8;
-        if (in_span(ob, 32, whole ? p.sp_dbias : p.sp_ws, p.status)) {
-          reinterpret_cast<float4*>(ob)[0] = make_float4(db[0].x, db[0].y, db[1].x, db[1].y);
-          reinterpret_cast<float4*>(ob)[1] = make_float4(db[2].x, db[2].y, db[3].x, db[3].y);
+      // one thread's view of the abort flag, for all to leave together
+      if (threadIdx.x == 0) *give_up = *ring.abort_flag;
+      named_barrier_sync(15, kLnBwdThreads);
+      if (*give_up) break;
+      if (grp == 0)
+        for (int g = 1; g < p.groups; ++g)
+#pragma unroll
+          for (int i = 0; i < CPT; ++i)
+            if (mine[i]) {
+              const float2* a = reinterpret_cast<const float2*>(acc + g * 2 * cols + (l + i * 32 * W) * 8);
+              const float2* b = reinterpret_cast<const float2*>(acc + g * 2 * cols + cols + (l + i * 32 * W) * 8);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                dw[i][j] = __fadd2_rn(dw[i][j], a[j]);
+                db[i][j] = __fadd2_rn(db[i][j], b[j]);
+              }
+            }
+    } else if (!ok) {
+      break;                                      // the group left its rows together
+    }
+    if (grp == 0) {
+      const bool whole = p.units_per_set == 1;
+      auto write = [&](float* out, const MemSpan& sp, const float2 (&v)[4]) {
+        if (!in_span(out, 32, sp, p.status)) return;
+        reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+      };
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        if (!mine[i]) continue;
+        const int c = (k0 + l + i * 32 * W) * 8;
+        if (whole) {
+          if (p.dweight) write(p.dweight + set * p.hidden + c, p.sp_dweight, dw[i]);
+          if (p.dbias) write(p.dbias + set * p.hidden + c, p.sp_dbias, db[i]);
+        } else {
+          write(p.parts + u * 2 * p.hidden + c, p.sp_ws, dw[i]);
+          write(p.parts + (u * 2 + 1) * p.hidden + c, p.sp_ws, db[i]);
         }
       }
     }
   }
   grid_dependents_launch();
+  if (leader && (!ok || *ring.abort_flag)) ring.drain();
 }
 
 }  // namespace qknr

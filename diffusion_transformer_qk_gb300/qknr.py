@@ -149,7 +149,7 @@ class QknrLnArgs(ctypes.Structure):
         ("dy_stride", c_int64), ("dx_stride", c_int64),
         ("dweight", c_void_p), ("dbias", c_void_p),
         ("workspace", c_void_p), ("workspace_bytes", c_size_t),
-        ("dev_status", c_void_p), ("flags", c_uint32),
+        ("dev_status", c_void_p), ("flags", c_uint32), ("wait_limit_ns", c_uint64),
     ]
 
 
@@ -949,7 +949,7 @@ def _vector(t, n, name):
 # layer norm and its backward pass (include/qknr_ln.h)
 
 def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False, eps=1e-6, dev_status=None,
-            flags=0) -> QknrLnArgs:
+            flags=0, wait_limit_ns=0) -> QknrLnArgs:
     """The arguments both passes share: token rows ``x`` [T, C], ``weight``
     and ``bias`` [C] or [B, C] (float32 or x's dtype; either may be None) and
     which of their rows a token takes (t // rows_per_batch; default: one
@@ -980,12 +980,12 @@ def ln_args(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False
         setattr(a, name, t.data_ptr())
     a.eps = eps
     a.dev_status = _ptr(dev_status)
-    a.flags = flags | (LN_UNIT_OFFSET if unit_offset else 0)
+    a.flags, a.wait_limit_ns = flags | (LN_UNIT_OFFSET if unit_offset else 0), wait_limit_ns
     return a
 
 
 def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=False, out=None, mean=None, rstd=None,
-               eps=1e-6, stream=None, status=True, dev_status=None, flags=0):
+               eps=1e-6, stream=None, status=True, dev_status=None, flags=0, wait_limit_ns=0):
     """Layer norm of token rows ``x`` [T, C] for training: returns (y, mean,
     rstd), the last two float32 [T] for the backward pass.
 
@@ -993,10 +993,11 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
     t // rows_per_batch; with ``unit_offset`` the gain is 1 + weight (the
     modulated norm of ``adaln_modulate``).  The result goes to ``out``, a new
     tensor by default (the backward pass needs x); ``out=x`` is in place."""
-    key = ("ln", _meta(x), _meta(weight), _meta(bias), _meta(out), rows_per_batch, unit_offset, eps, flags)
+    key = ("ln", _meta(x), _meta(weight), _meta(bias), _meta(out), rows_per_batch, unit_offset, eps, flags, wait_limit_ns)
     plan = _plans.get(key)
     if plan is None:
-        a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, flags=flags)
+        a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, flags=flags,
+                    wait_limit_ns=wait_limit_ns)
         a.y_stride = x.shape[1] if out is None else _stride(_match(out, x, "out"), "out")
         plan = _keep(key, _Plan(a))
     T = x.shape[0]
@@ -1016,15 +1017,18 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_offset=False, out=None, dweight=None,
-                        dbias=None, workspace=None, stream=None, status=True, dev_status=None, flags=0):
+                        dbias=None, workspace=None, stream=None, status=True, dev_status=None, flags=0,
+                        wait_limit_ns=0):
     """Gradients of ``layer_norm``: returns (dx, dweight, dbias), the last two
     float32, of weight's shape ([C] where weight is None).  ``out`` receives
     dx (default: a new tensor; ``out=dy`` is in place)."""
-    key = ("ln_bwd", _meta(dy), _meta(x), _meta(weight), _meta(out), rows_per_batch, unit_offset, flags)
+    key = ("ln_bwd", _meta(dy), _meta(x), _meta(weight), _meta(out), rows_per_batch, unit_offset, flags,
+           wait_limit_ns)
     plan = _plans.get(key)
     T, C = x.shape
     if plan is None:
-        a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags)
+        a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags,
+                    wait_limit_ns=wait_limit_ns)
         a.dy_stride = _stride(_match(dy, x, "dy"), "dy")
         a.dx_stride = C if out is None else _stride(_match(out, x, "out"), "out")
         sets = -(-T // rows_per_batch) if rows_per_batch else 1

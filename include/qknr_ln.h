@@ -29,7 +29,9 @@
  *
  * Ownership and errors follow qknr.h: the caller owns every buffer
  * (the backward pass's workspace included), the library allocates nothing
- * and never synchronises; argument errors return before any CUDA call.
+ * and never synchronises; argument errors return before any CUDA call; a
+ * bounded in-kernel wait that runs out writes QKNR_ERR_TIMEOUT to
+ * *dev_status.
  */
 #ifndef QKNR_LN_H_
 #define QKNR_LN_H_
@@ -63,8 +65,9 @@ typedef struct qknr_ln_args {
   float *dweight, *dbias;     /* device [B, C], contiguous; either may be NULL */
   void *workspace;            /* device, 16-byte aligned, qknr_ln_workspace_bytes */
   size_t workspace_bytes;
-  int32_t *dev_status;        /* optional device int32, written by checked builds only */
-  uint32_t flags;             /* QKNR_FLAG_NO_OVERLAP, QKNR_LN_UNIT_OFFSET */
+  int32_t *dev_status;        /* optional device int32 (see qknr.h) */
+  uint32_t flags;             /* QKNR_FLAG_NO_OVERLAP, QKNR_FLAG_TEST_STALL, QKNR_LN_UNIT_OFFSET */
+  uint64_t wait_limit_ns;     /* 0 = 2 s */
 } qknr_ln_args;
 
 /* Defaults: bf16, fp32 parameters, eps 1e-6, everything else zero. */

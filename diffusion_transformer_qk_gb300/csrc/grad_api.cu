@@ -255,7 +255,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   pp.status = a->dev_status;
   void* pargs[] = {&pp};
   return qknr_host::launch_kernel(reinterpret_cast<const void*>(qknr::parts_kernel),
-                                  static_cast<int>(qknr::parts_grid(pp, 1)), qknr::kPartsCols * qknr::kPartsRows, 0, cs,
+                                  static_cast<int>(qknr::parts_grid(pp, 1)), 32 * qknr::kPartsRows, 0, cs,
                                   pargs, overlap, "cudaLaunchKernelExC(dgamma)");
 }
 

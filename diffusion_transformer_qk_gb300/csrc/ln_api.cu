@@ -41,20 +41,15 @@ const void* forward_fn(int cpt) {
 template <typename T>
 const void* backward_fn(int cpt, bool is_long) {
   if (is_long) return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, qknr::kLnBwdCpt, true>);
-  switch (cpt) {
-    case 1: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>);
-    case 2: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
-    case 3: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 3, false>);
-    default: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 4, false>);
-  }
+  return cpt == 1 ? reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>)
+                  : reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
 }
 
-// The smallest power of two of warps, up to `most`, that leaves a thread at
-// most `cpt` of a row's chunks.
+// The fewest warps, up to `most`, that leave a thread at most `cpt` of a
+// row's chunks.
 int warps_for(int n_chunks, int cpt, int most) {
-  int w = 1;
-  while (w < most && 32 * cpt * w < n_chunks) w *= 2;
-  return w;
+  const int w = (n_chunks + 32 * cpt - 1) / (32 * cpt);
+  return w < most ? w : most;
 }
 
 qknr::MemSpan msp(Span s) { return qknr::MemSpan{s.lo, s.hi}; }
@@ -99,7 +94,7 @@ Cut cut_rows(const qknr_ln_args* a) {
   const int n_chunks = a->hidden / 8;
   c.tiles = (a->hidden + qknr::kLnTile - 1) / qknr::kLnTile;
   c.group_warps = warps_for(n_chunks, qknr::kLnBwdCpt, qknr::kLnBwdWarps);
-  c.groups = qknr::kLnBwdWarps / c.group_warps;   // groups of several warps: at most 4 named barriers
+  c.groups = qknr::kLnBwdWarps / c.group_warps;   // groups of several warps: at most 8 named barriers
   c.cpt = (n_chunks + 32 * c.group_warps - 1) / (32 * c.group_warps);
   c.rows_per_batch = a->rows_per_batch ? a->rows_per_batch : T;
   c.sets = T ? (T + c.rows_per_batch - 1) / c.rows_per_batch : 0;
@@ -244,7 +239,7 @@ qknr_status qknr_ln_forward(const qknr_ln_args* a, qknr_stream_t stream) {
   kp.group_warps = warps;
   kp.groups = qknr::kLnWarps / warps;
   kp.stages = stages_for(di, kp.row_bytes, kp.groups, 0);
-  return run(bf ? forward_fn<__nv_bfloat16>(cpt) : forward_fn<__half>(cpt), di.num_sms, qknr::kLnThreads,
+  return run(bf ? forward_fn<__nv_bfloat16>(cpt) : forward_fn<__half>(cpt), di.num_sms, 32 * warps * kp.groups,
              qknr::kLnOffStages + static_cast<size_t>(kp.stages) * kp.groups * kp.row_bytes, a, &kp, dev, di, stream,
              "cudaLaunchKernelExC(layer norm)");
 }
@@ -341,7 +336,7 @@ qknr_status qknr_ln_backward(const qknr_ln_args* a, qknr_stream_t stream) {
   kp.stages = stages_for(di, stage, c.groups, sums);
   long long ctas = di.num_sms / c.tiles;
   if (ctas > c.sets * c.units_per_set) ctas = c.sets * c.units_per_set;
-  st = run(fn, ctas * c.tiles, qknr::kLnBwdThreads, qknr::kLnOffStages + kp.stages * c.groups * stage + sums, a, &kp,
+  st = run(fn, ctas * c.tiles, 32 * c.group_warps * c.groups, qknr::kLnOffStages + kp.stages * c.groups * stage + sums, a, &kp,
            dev, di, stream, "cudaLaunchKernelExC(layer norm backward)");
   if (st != QKNR_OK || !kp.parts || (!kp.dweight && !kp.dbias)) return st;
   qknr::PartsParams pp;
@@ -356,7 +351,7 @@ qknr_status qknr_ln_backward(const qknr_ln_args* a, qknr_stream_t stream) {
   pp.sp_out[1] = kp.sp_dbias;
   pp.status = a->dev_status;
   return run(reinterpret_cast<const void*>(qknr::parts_kernel), qknr::parts_grid(pp, c.sets),
-             qknr::kPartsCols * qknr::kPartsRows, 0, a, &pp, dev, di, stream,
+             32 * qknr::kPartsRows, 0, a, &pp, dev, di, stream,
              "cudaLaunchKernelExC(layer norm parameter sums)");
 }
 

@@ -103,37 +103,35 @@ __device__ __forceinline__ void ln_bias8(const LnParams& p, long long set, int k
   if (p.bias && in_span(row + k * bytes, bytes, p.sp_bias, p.status)) ln_param8<T>(row, k, p.param_fp32, b);
 }
 
-__device__ __forceinline__ float ln_warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
-
-// The sum of v over a group's W warps, the same in every thread: a shuffle
-// tree inside each warp, then the warps' sums added in order from shared
-// memory.  `ok` becomes whether every warp's was true.  The caller uses two
-// buffers `red` in turn, so the one barrier also keeps a fast warp from
-// overwriting sums a slow one reads.
+// The sum of each of v's N values over a group's W <= 16 warps, the same in
+// every thread: a shuffle tree inside each warp, then a tree over
+// the warps' sums in shared memory.  `ok` becomes whether every warp's was
+// true.  The caller uses two buffers `red` in turn, so the one barrier also
+// keeps a fast warp from overwriting sums a slow one reads.
 struct LnPart {
   float2 v;
   int ok;
   int pad;
 };
 
-__device__ __forceinline__ float2 ln_group_sum(float2 v, bool& ok, int W, int gw, int lane, int bar_id, LnPart* red) {
-  v.x = ln_warp_sum(v.x);
-  v.y = ln_warp_sum(v.y);
-  if (W == 1) return v;
-  if (lane == 0) red[gw] = LnPart{v, ok, 0};
+template <int N>
+__device__ __forceinline__ void ln_group_sum(float (&v)[N], bool& ok, int W, int gw, int lane, int bar_id, LnPart* red) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
+  if (W == 1) return;
+  if (lane == 0) red[gw] = LnPart{make_float2(v[0], v[N - 1]), ok, 0};
   named_barrier_sync(bar_id, 32 * W);
-  float2 s = red[0].v;
-  int all = red[0].ok;
-  for (int w = 1; w < W; ++w) {
-    s = __fadd2_rn(s, red[w].v);
-    all &= red[w].ok;
-  }
-  ok = all != 0;
-  return s;
+  LnPart part{make_float2(0.0f, 0.0f), 1, 0};
+  if ((lane & 15) < W) part = red[lane & 15];
+  v[0] = part.v.x;
+  if (N == 2) v[N - 1] = part.v.y;
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
+  ok = __all_sync(0xffffffffu, part.ok != 0);
 }
 
 __device__ __forceinline__ float ln_hsum(const float2 (&v)[4]) {
@@ -243,7 +241,9 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
     Elem<T>::unpack(raw[i], X);
     s = __fadd_rn(s, ln_hsum(X));
   }
-  const float mean = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, bar, red).x, p.inv_c);
+  float t[1] = {s};
+  ln_group_sum(t, ok, W, gw, lane, bar, red);
+  const float mean = __fmul_rn(t[0], p.inv_c);
   const float2 nm = make_float2(-mean, -mean);
   s = 0.0f;
 #pragma unroll
@@ -259,7 +259,9 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
       s = __fadd_rn(s, ln_hsum(X));
     }
   }
-  const float var = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, bar, red + kLnWarps).x, p.inv_c);
+  t[0] = s;
+  ln_group_sum(t, ok, W, gw, lane, bar, red + kLnWarps);
+  const float var = __fmul_rn(t[0], p.inv_c);
   const float rstd = rsqrtf(__fadd_rn(var, p.eps));
   if (l == 0) {
     if (p.mean && in_span(p.mean + row, 4, p.sp_mean, p.status)) p.mean[row] = mean;
@@ -326,11 +328,12 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
   float2 g[CPT][4], b[CPT][4];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
-  long long set = -1;
+  long long set_end = 0;                          // first row past the sample whose parameters are in g and b
   bool ok = true;
   for (; row < p.tokens; row += step) {
-    if (ln_set(p, row) != set) {
-      set = ln_set(p, row);
+    if (row >= set_end) {
+      const long long set = ln_set(p, row);
+      set_end = (set + 1) * p.rows_per_batch;
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         if (!mine[i]) continue;
@@ -347,7 +350,9 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
       Elem<T>::unpack(raw, X[i]);
       s = __fadd_rn(s, ln_hsum(X[i]));
     }
-    const float mean = __fmul_rn(ln_group_sum(make_float2(s, 0.0f), ok, W, gw, lane, 1 + grp, red).x, p.inv_c);
+    float t[1] = {s};
+    ln_group_sum(t, ok, W, gw, lane, 1 + grp, red);
+    const float mean = __fmul_rn(t[0], p.inv_c);
     if (!ok) break;
     ring.next();
     if (leader) {
@@ -364,8 +369,9 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
         X[i][j] = __fadd2_rn(X[i][j], nm);
         if (mine[i]) q = __ffma2_rn(X[i][j], X[i][j], q);
       }
-    const float var = __fmul_rn(
-        ln_group_sum(make_float2(__fadd_rn(q.x, q.y), 0.0f), ok, W, gw, lane, 1 + grp, red + kLnWarps).x, p.inv_c);
+    t[0] = __fadd_rn(q.x, q.y);
+    ln_group_sum(t, ok, W, gw, lane, 1 + grp, red + kLnWarps);
+    const float var = __fmul_rn(t[0], p.inv_c);
     const float rstd = rsqrtf(__fadd_rn(var, p.eps));
     if (l == 0) {
       if (p.mean && in_span(p.mean + row, 4, p.sp_mean, p.status)) p.mean[row] = mean;
@@ -388,12 +394,11 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // backward
 
-// Eight warps of up to four chunks a thread: with 255 registers a thread
-// holds its columns' sums, its gains and a row's xhat and dy, and the row's
-// fixed costs (two shuffle trees, a barrier) are paid by few warps.
-constexpr int kLnBwdWarps = 8;
+// Two chunks a thread: with 128 registers it holds its columns' sums, its
+// gains and a row's xhat and dy.
+constexpr int kLnBwdWarps = 16;
 constexpr int kLnBwdThreads = 32 * kLnBwdWarps;
-constexpr int kLnBwdCpt = 4;
+constexpr int kLnBwdCpt = 2;
 constexpr int kLnTile = 8 * 32 * kLnBwdWarps * kLnBwdCpt;   // 8192 columns: the longest row one CTA takes
 
 // xhat and dy of one chunk
@@ -445,10 +450,11 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
       }
     }
     bool ok = true;
-    s = ln_group_sum(s, ok, 8, warp, lane, 1, red[parity]);
+    float t[2] = {s.x, s.y};
+    ln_group_sum(t, ok, 8, warp, lane, 1, red[parity]);
     if (threadIdx.x == 0 && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status)) {
-      p.row_sums[2 * row] = __fmul_rn(s.x, p.inv_c);
-      p.row_sums[2 * row + 1] = __fmul_rn(s.y, p.inv_c);
+      p.row_sums[2 * row] = __fmul_rn(t[0], p.inv_c);
+      p.row_sums[2 * row + 1] = __fmul_rn(t[1], p.inv_c);
     }
   }
   grid_dependents_launch();
@@ -550,16 +556,16 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
 #pragma unroll
         for (int i = 0; i < CPT; ++i) ln_grad_sums(xh[i], dy[i], gain[i], s);
       }
-      s = ln_group_sum(s, ok, W, gw, lane, 1 + grp, red + parity * kLnBwdWarps);
+      float t[2] = {s.x, s.y};
+      ln_group_sum(t, ok, W, gw, lane, 1 + grp, red + parity * kLnBwdWarps);
       if (!ok) break;
       ring.next();
       if (leader) {
         --ring.in_flight;
         put();
       }
-      if (!LONG)
-        s = __fmul2_rn(s, make_float2(p.inv_c, p.inv_c));
-      else if (in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status))
+      s = make_float2(__fmul_rn(t[0], p.inv_c), __fmul_rn(t[1], p.inv_c));
+      if (LONG && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status))
         s = *reinterpret_cast<const float2*>(p.row_sums + 2 * row);
       const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
       char* dst = p.dx + row * p.dx_stride + (k0 + l) * 16;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
     // the groups' sums, added in order
     if (p.groups > 1) {
       float* slot = acc + grp * 2 * cols;
-      named_barrier_sync(15, kLnBwdThreads);            // the previous unit's sums have been read
+      named_barrier_sync(15, 32 * W * p.groups);            // the previous unit's sums have been read
 #pragma unroll
       for (int i = 0; i < CPT; ++i)
         if (mine[i]) {
@@ -592,7 +598,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
         }
       // one thread's view of the abort flag, for all to leave together
       if (threadIdx.x == 0) *give_up = *ring.abort_flag;
-      named_barrier_sync(15, kLnBwdThreads);
+      named_barrier_sync(15, 32 * W * p.groups);
       if (*give_up) break;
       if (grp == 0)
         for (int g = 1; g < p.groups; ++g)

@@ -41,8 +41,12 @@ const void* forward_fn(int cpt) {
 template <typename T>
 const void* backward_fn(int cpt, bool is_long) {
   if (is_long) return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, qknr::kLnBwdCpt, true>);
-  return cpt == 1 ? reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>)
-                  : reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
+  switch (cpt) {
+    case 1: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>);
+    case 2: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
+    case 3: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 3, false>);
+    default: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 4, false>);
+  }
 }
 
 // The fewest warps, up to `most`, that leave a thread at most `cpt` of a
@@ -234,10 +238,9 @@ qknr_status qknr_ln_forward(const qknr_ln_args* a, qknr_stream_t stream) {
     return run(bf ? direct_fn<__nv_bfloat16>(cpt) : direct_fn<__half>(cpt), (T + kp.groups - 1) / kp.groups,
                32 * warps * kp.groups, 0, a, &kp, dev, di, stream, "cudaLaunchKernelExC(layer norm)");
   }
-  const int warps = warps_for(n_chunks, keep, qknr::kLnWarps);
-  const int cpt = (n_chunks + 32 * warps - 1) / (32 * warps);
+  kp.groups = qknr::kLnWarps / warps_for(n_chunks, keep, qknr::kLnWarps);
+  const int warps = qknr::kLnWarps / kp.groups, cpt = (n_chunks + 32 * warps - 1) / (32 * warps);
   kp.group_warps = warps;
-  kp.groups = qknr::kLnWarps / warps;
   kp.stages = stages_for(di, kp.row_bytes, kp.groups, 0);
   return run(bf ? forward_fn<__nv_bfloat16>(cpt) : forward_fn<__half>(cpt), di.num_sms, 32 * warps * kp.groups,
              qknr::kLnOffStages + static_cast<size_t>(kp.stages) * kp.groups * kp.row_bytes, a, &kp, dev, di, stream,

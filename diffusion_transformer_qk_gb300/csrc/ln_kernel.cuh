@@ -103,35 +103,55 @@ __device__ __forceinline__ void ln_bias8(const LnParams& p, long long set, int k
   if (p.bias && in_span(row + k * bytes, bytes, p.sp_bias, p.status)) ln_param8<T>(row, k, p.param_fp32, b);
 }
 
-// The sum of each of v's N values over a group's W <= 16 warps, the same in
-// every thread: a shuffle tree inside each warp, then a tree over
-// the warps' sums in shared memory.  `ok` becomes whether every warp's was
-// true.  The caller uses two buffers `red` in turn, so the one barrier also
-// keeps a fast warp from overwriting sums a slow one reads.
-struct LnPart {
-  float2 v;
-  int ok;
-  int pad;
-};
+// The sum of each of v's N (1 or 2) values over a group's W warps, the same
+// in every thread: a shuffle tree inside each warp (two values share one
+// tree, a half of the lanes each), then the 16 / N slots of `red` that the
+// group's warps fill are added in order; slots of absent warps hold zero.
+// Returns whether every thread's `ok` was true (the barrier's own reduction).
+// The caller uses two buffers `red` in turn, so the one barrier also keeps a
+// fast warp from overwriting sums a slow one reads.
+constexpr int kLnRedFloats = 16;
 
 template <int N>
-__device__ __forceinline__ void ln_group_sum(float (&v)[N], bool& ok, int W, int gw, int lane, int bar_id, LnPart* red) {
+__device__ __forceinline__ bool ln_group_sum(float (&v)[N], bool ok, int W, int gw, int lane, int bar_id, float* red) {
+  float t = v[0];
+  if (N == 2) {
+    const bool upper = lane & 16;
+    t = __fadd_rn(upper ? v[N - 1] : v[0], __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[N - 1], 16));
+  } else {
+    t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 16));
+  }
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1)
+  for (int off = 8; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
+  if (W == 1) {
+    v[0] = __shfl_sync(0xffffffffu, t, 0);
+    if (N == 2) v[N - 1] = __shfl_sync(0xffffffffu, t, 16);
+    return __all_sync(0xffffffffu, ok);
+  }
+  if (N == 2 ? (lane & 15) == 0 : lane == 0) red[N == 2 ? 2 * gw + (lane >> 4) : gw] = t;
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u), "r"(bar_id), "r"(32 * W)
+      : "memory");
+  const float4* r = reinterpret_cast<const float4*>(red);
+  float2 lo = make_float2(0.0f, 0.0f), hi = lo;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
-  if (W == 1) return;
-  if (lane == 0) red[gw] = LnPart{make_float2(v[0], v[N - 1]), ok, 0};
-  named_barrier_sync(bar_id, 32 * W);
-  LnPart part{make_float2(0.0f, 0.0f), 1, 0};
-  if ((lane & 15) < W) part = red[lane & 15];
-  v[0] = part.v.x;
-  if (N == 2) v[N - 1] = part.v.y;
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __fadd_rn(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
-  ok = __all_sync(0xffffffffu, part.ok != 0);
+  for (int i = 0; i < kLnRedFloats / 4; ++i) {
+    const float4 part = r[i];
+    lo = __fadd2_rn(lo, make_float2(part.x, part.y));
+    hi = __fadd2_rn(hi, make_float2(part.z, part.w));
+  }
+  const float2 s = __fadd2_rn(lo, hi);
+  if (N == 2) {
+    v[0] = s.x;
+    v[N - 1] = s.y;
+  } else {
+    v[0] = __fadd_rn(s.x, s.y);
+  }
+  return all != 0;
 }
 
 __device__ __forceinline__ float ln_hsum(const float2 (&v)[4]) {
@@ -148,9 +168,9 @@ constexpr int kLnMaxStages = 32;                  // all groups' together
 // dynamic shared memory map (bytes)
 constexpr int kLnOffBars = 0;                     // full[32]
 constexpr int kLnOffAbort = 256;
-constexpr int kLnOffRed = 512;                    // LnPart [2][kLnWarps]
-constexpr int kLnOffStages = kLnOffRed + 2 * kLnWarps * 16;   // 1024
-static_assert(sizeof(LnPart) == 16 && kLnOffStages % 128 == 0, "shared memory map");
+constexpr int kLnOffRed = 512;                    // per group two buffers of kLnRedFloats
+constexpr int kLnOffStages = kLnOffRed + kLnWarps * 2 * kLnRedFloats * 4;   // 2560
+static_assert(kLnOffStages % 128 == 0, "shared memory map");
 
 // One group's ring of `stages` stages.  Its rows come in the order in which
 // the group's first thread put them.
@@ -192,10 +212,9 @@ struct LnRing {
     if (++put_s == stages) put_s = 0;
     ++in_flight;
   }
-  // The next row has landed; the same answer in every lane.
+  // The next row has landed (one thread's answer).
   __device__ __forceinline__ bool wait() const {
-    return __all_sync(0xffffffffu, mbar_try_wait(bars + 8 * s, phase) ||
-                                       bounded_wait(bars + 8 * s, phase, limit, abort_flag, status));
+    return mbar_try_wait(bars + 8 * s, phase) || bounded_wait(bars + 8 * s, phase, limit, abort_flag, status);
   }
   __device__ __forceinline__ const uint4* row() const { return reinterpret_cast<const uint4*>(ptr + s * stage_bytes); }
   __device__ __forceinline__ void next() {
@@ -215,11 +234,17 @@ struct LnRing {
   }
 };
 
-// one thread: all groups' barriers
+// the whole CTA: all groups' barriers and sum slots
 __device__ __forceinline__ void ln_init_rings(unsigned char* smem, int n) {
-  for (int i = 0; i < n; ++i) mbar_init(smem_addr(smem) + kLnOffBars + 8 * i, 1);
-  *reinterpret_cast<volatile int*>(smem + kLnOffAbort) = 0;
-  fence_barrier_init();
+  for (int i = threadIdx.x; i < kLnWarps * 2 * kLnRedFloats; i += blockDim.x)
+    reinterpret_cast<float*>(smem + kLnOffRed)[i] = 0.0f;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < n; ++i) mbar_init(smem_addr(smem) + kLnOffBars + 8 * i, 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + kLnOffAbort);
+    flags[0] = flags[1] = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
@@ -230,9 +255,8 @@ __device__ __forceinline__ void ln_init_rings(unsigned char* smem, int n) {
 // and held as read.
 template <typename T, int CPT>
 __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&raw)[CPT], long long row, int W, int gw,
-                                               int lane, int bar, LnPart* red) {
+                                               int lane, int bar, float* red) {
   const int l = gw * 32 + lane, step = 32 * W, n_chunks = p.hidden / 8;
-  bool ok = true;
   // mean: chunks past the row hold zeros
   float s = 0.0f;
 #pragma unroll
@@ -242,7 +266,7 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
     s = __fadd_rn(s, ln_hsum(X));
   }
   float t[1] = {s};
-  ln_group_sum(t, ok, W, gw, lane, bar, red);
+  ln_group_sum(t, true, W, gw, lane, bar, red);
   const float mean = __fmul_rn(t[0], p.inv_c);
   const float2 nm = make_float2(-mean, -mean);
   s = 0.0f;
@@ -260,7 +284,7 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
     }
   }
   t[0] = s;
-  ln_group_sum(t, ok, W, gw, lane, bar, red + kLnWarps);
+  ln_group_sum(t, true, W, gw, lane, bar, red + kLnRedFloats);
   const float var = __fmul_rn(t[0], p.inv_c);
   const float rstd = rsqrtf(__fadd_rn(var, p.eps));
   if (l == 0) {
@@ -288,10 +312,12 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
 
 template <typename T, int CPT>
 __global__ void __launch_bounds__(kLnThreads) ln_forward_direct_kernel(const __grid_constant__ LnParams p) {
-  __shared__ LnPart red[2 * kLnWarps];
+  __shared__ __align__(16) float red[2 * kLnRedFloats];   // a CTA of several groups has groups of one warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.group_warps, grp = warp / W, gw = warp % W;
   const int l = gw * 32 + lane, n_chunks = p.hidden / 8;
+  if (threadIdx.x < 2 * kLnRedFloats) red[threadIdx.x] = 0.0f;
+  __syncthreads();
   grid_dependency_wait();
   const long long row = static_cast<long long>(blockIdx.x) * p.groups + grp;
   const char* src = p.x + row * p.x_stride;
@@ -314,8 +340,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int W = p.group_warps, grp = warp / W, gw = warp % W, l = gw * 32 + lane, n_chunks = p.hidden / 8;
   LnRing ring(smem, p, p.row_bytes, grp);
-  if (threadIdx.x == 0) ln_init_rings(smem, p.stages * p.groups);
-  __syncthreads();
+  ln_init_rings(smem, p.stages * p.groups);
   grid_dependency_wait();
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
   long long row = static_cast<long long>(blockIdx.x) * p.groups + grp, ahead = row;
@@ -323,7 +348,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
   if (leader)
     for (int i = 0; i < p.stages && ahead < p.tokens; ++i, ahead += step)
       ring.put(p.x + ahead * p.x_stride, p.sp_x, nullptr, p.sp_x, p.row_bytes);
-  LnPart* red = reinterpret_cast<LnPart*>(smem + kLnOffRed) + grp * W;
+  float* red = reinterpret_cast<float*>(smem + kLnOffRed) + grp * 2 * kLnRedFloats;
   bool mine[CPT];
   float2 g[CPT][4], b[CPT][4];
 #pragma unroll
@@ -341,7 +366,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
         ln_bias8<T>(p, set, l + i * 32 * W, b[i]);
       }
     }
-    ok = ring.wait();
+    const bool landed = ring.wait();
     float2 X[CPT][4];
     float s = 0.0f;
 #pragma unroll
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
       s = __fadd_rn(s, ln_hsum(X[i]));
     }
     float t[1] = {s};
-    ln_group_sum(t, ok, W, gw, lane, 1 + grp, red);
+    ok = ln_group_sum(t, landed, W, gw, lane, 1 + grp, red);
     const float mean = __fmul_rn(t[0], p.inv_c);
     if (!ok) break;
     ring.next();
@@ -370,7 +395,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
         if (mine[i]) q = __ffma2_rn(X[i][j], X[i][j], q);
       }
     t[0] = __fadd_rn(q.x, q.y);
-    ln_group_sum(t, ok, W, gw, lane, 1 + grp, red + kLnWarps);
+    ln_group_sum(t, true, W, gw, lane, 1 + grp, red + kLnRedFloats);
     const float var = __fmul_rn(t[0], p.inv_c);
     const float rstd = rsqrtf(__fadd_rn(var, p.eps));
     if (l == 0) {
@@ -394,11 +419,12 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // backward
 
-// Two chunks a thread: with 128 registers it holds its columns' sums, its
-// gains and a row's xhat and dy.
-constexpr int kLnBwdWarps = 16;
+// Eight warps of up to four chunks a thread: with 255 registers a thread
+// holds its columns' sums, its gains and a row's xhat and dy, and the row's
+// fixed costs (a shuffle tree, a barrier) are paid by few warps.
+constexpr int kLnBwdWarps = 8;
 constexpr int kLnBwdThreads = 32 * kLnBwdWarps;
-constexpr int kLnBwdCpt = 2;
+constexpr int kLnBwdCpt = 4;
 constexpr int kLnTile = 8 * 32 * kLnBwdWarps * kLnBwdCpt;   // 8192 columns: the longest row one CTA takes
 
 // xhat and dy of one chunk
@@ -429,7 +455,7 @@ __device__ __forceinline__ void ln_grad_sums(const float2 (&xh)[4], const float2
 // one CTA per row.
 template <typename T>
 __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant__ LnParams p) {
-  __shared__ LnPart red[2][8];
+  __shared__ __align__(16) float red[2][kLnRedFloats];   // all sixteen written: eight warps, two values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_chunks = p.hidden / 8;
   grid_dependency_wait();
   int parity = 0;
@@ -449,9 +475,8 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
         ln_grad_sums(xh, dy, gain, s);
       }
     }
-    bool ok = true;
     float t[2] = {s.x, s.y};
-    ln_group_sum(t, ok, 8, warp, lane, 1, red[parity]);
+    ln_group_sum(t, true, 8, warp, lane, 1, red[parity]);
     if (threadIdx.x == 0 && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status)) {
       p.row_sums[2 * row] = __fmul_rn(t[0], p.inv_c);
       p.row_sums[2 * row + 1] = __fmul_rn(t[1], p.inv_c);
@@ -480,11 +505,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
   const int grp = warp / W, gw = warp % W, l = gw * 32 + lane, cols = n_chunks * 8;
   LnRing ring(smem, p, stage_bytes, grp);
   volatile int* give_up = ring.abort_flag + 1;
-  if (threadIdx.x == 0) {
-    ln_init_rings(smem, p.stages * p.groups);
-    *give_up = 0;
-  }
-  __syncthreads();
+  ln_init_rings(smem, p.stages * p.groups);
   grid_dependency_wait();
   const long long units = p.sets * p.units_per_set, unit_step = gridDim.x / p.tiles;
   // rows [first, last) of unit u
@@ -512,7 +533,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
     for (int i = 0; i < p.stages; ++i) put();
 
   float* acc = reinterpret_cast<float*>(smem + kLnOffStages + p.stages * p.groups * stage_bytes);   // [groups][2][columns]
-  LnPart* red = reinterpret_cast<LnPart*>(smem + kLnOffRed) + grp * W;
+  float* red = reinterpret_cast<float*>(smem + kLnOffRed) + grp * 2 * kLnRedFloats;
   bool mine[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
@@ -527,19 +548,27 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
       for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = gain[i][j] = make_float2(0.0f, 0.0f);
       if (mine[i]) ln_gain8<T>(p, set, k0 + l + i * 32 * W, gain[i]);
     }
+    // the statistics of the row after the one in work
+    const float *at_mean = p.mean + first + grp, *at_rstd = p.rstd + first + grp;
+    int left = last - first > grp ? static_cast<int>((last - first - grp + p.groups - 1) / p.groups) : 0;   // the group's rows
     float nmean = 0.0f, nrstd = 0.0f;
-    auto stats = [&](long long r) {
-      if (r < last && in_span(p.mean + r, 4, p.sp_mean, p.status) && in_span(p.rstd + r, 4, p.sp_rstd, p.status)) {
-        nmean = p.mean[r];
-        nrstd = p.rstd[r];
+    auto stats = [&]() {
+      if (left > 0 && in_span(at_mean, 4, p.sp_mean, p.status) && in_span(at_rstd, 4, p.sp_rstd, p.status)) {
+        nmean = *at_mean;
+        nrstd = *at_rstd;
       }
+      at_mean += p.groups;
+      at_rstd += p.groups;
     };
-    stats(first + grp);
-    int parity = 0;
-    for (long long row = first + grp; ok && row < last; row += p.groups, parity ^= 1) {
+    stats();
+    char* dst = p.dx + (first + grp) * p.dx_stride + (k0 + l) * 16;
+    const float2* sums = reinterpret_cast<const float2*>(p.row_sums) + first + grp;   // LONG
+    float* buf = red;
+    for (; left > 0; dst += p.groups * p.dx_stride, sums += p.groups, buf = buf == red ? red + kLnRedFloats : red) {
       const float2 nm = make_float2(-nmean, -nmean), R = make_float2(nrstd, nrstd);
-      stats(row + p.groups);
-      ok = ring.wait();
+      --left;
+      stats();
+      const bool landed = ring.wait();
       float2 xh[CPT][4], dy[CPT][4];
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
@@ -548,7 +577,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
           xr = ring.row()[l + i * 32 * W];
           dr = ring.row()[n_chunks + l + i * 32 * W];
         }
-      // past the row: dy = 0 and gain = 0, so xhat's value does not count
+        // past the row: dy = 0 and gain = 0, so xhat's value does not count
         ln_grad_values<T>(xr, dr, nm, R, xh[i], dy[i]);
       }
       float2 s = make_float2(0.0f, 0.0f);
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
         for (int i = 0; i < CPT; ++i) ln_grad_sums(xh[i], dy[i], gain[i], s);
       }
       float t[2] = {s.x, s.y};
-      ln_group_sum(t, ok, W, gw, lane, 1 + grp, red + parity * kLnBwdWarps);
+      ok = ln_group_sum(t, landed, W, gw, lane, 1 + grp, buf);
       if (!ok) break;
       ring.next();
       if (leader) {
@@ -565,10 +594,8 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
         put();
       }
       s = make_float2(__fmul_rn(t[0], p.inv_c), __fmul_rn(t[1], p.inv_c));
-      if (LONG && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status))
-        s = *reinterpret_cast<const float2*>(p.row_sums + 2 * row);
+      if (LONG && in_span(sums, 8, p.sp_ws, p.status)) s = *sums;
       const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
-      char* dst = p.dx + row * p.dx_stride + (k0 + l) * 16;
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         float2 o[4];
@@ -584,7 +611,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
     // the groups' sums, added in order
     if (p.groups > 1) {
       float* slot = acc + grp * 2 * cols;
-      named_barrier_sync(15, 32 * W * p.groups);            // the previous unit's sums have been read
+      named_barrier_sync(15, 32 * W * p.groups);   // the previous unit's sums have been read
 #pragma unroll
       for (int i = 0; i < CPT; ++i)
         if (mine[i]) {

@@ -32,20 +32,20 @@ const void* direct_fn(int cpt) {
 template <typename T>
 const void* forward_fn(int cpt) {
   switch (cpt) {
-    case 1: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 1>);
-    case 2: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 2>);
-    default: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 3>);
+    case 1: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 1, 2>);
+    case 2: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 2, 2>);
+    default: return reinterpret_cast<const void*>(qknr::ln_forward_kernel<T, 3, 1>);
   }
 }
 
 template <typename T>
 const void* backward_fn(int cpt, bool is_long) {
-  if (is_long) return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, qknr::kLnBwdCpt, true>);
+  if (is_long) return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, qknr::kLnBwdCpt, 1, true>);
   switch (cpt) {
-    case 1: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, false>);
-    case 2: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, false>);
-    case 3: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 3, false>);
-    default: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 4, false>);
+    case 1: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 1, 2, false>);
+    case 2: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 2, 2, false>);
+    case 3: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 3, 2, false>);
+    default: return reinterpret_cast<const void*>(qknr::ln_backward_kernel<T, 4, 1, false>);
   }
 }
 

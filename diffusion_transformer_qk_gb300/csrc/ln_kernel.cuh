@@ -103,32 +103,43 @@ __device__ __forceinline__ void ln_bias8(const LnParams& p, long long set, int k
   if (p.bias && in_span(row + k * bytes, bytes, p.sp_bias, p.status)) ln_param8<T>(row, k, p.param_fp32, b);
 }
 
-// The sum of each of v's N (1 or 2) values over a group's W warps, the same
-// in every thread: a shuffle tree inside each warp (two values share one
-// tree, a half of the lanes each), then the 16 / N slots of `red` that the
-// group's warps fill are added in order; slots of absent warps hold zero.
-// Returns whether every thread's `ok` was true (the barrier's own reduction).
-// The caller uses two buffers `red` in turn, so the one barrier also keeps a
-// fast warp from overwriting sums a slow one reads.
-constexpr int kLnRedFloats = 16;
+// The sum of each of v's N (1, 2 or 4) values over a group's W <= MOST warps,
+// the same in every thread: a shuffle tree inside each warp (the values share
+// one tree, 32 / N lanes each once they have been folded), then the N * MOST
+// slots of `red` that the group's warps fill are added in order; slots of
+// absent warps hold zero.  Returns whether every thread's `ok` was true (the
+// barrier's own reduction).  The caller uses two buffers `red` in turn, so
+// the one barrier also keeps a fast warp from overwriting sums a slow one
+// reads.
+constexpr int kLnRedFloats = 32;
 
-template <int N>
+template <int N, int MOST>
 __device__ __forceinline__ bool ln_group_sum(float (&v)[N], bool ok, int W, int gw, int lane, int bar_id, float* red) {
-  float t = v[0];
-  if (N == 2) {
-    const bool upper = lane & 16;
-    t = __fadd_rn(upper ? v[N - 1] : v[0], __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[N - 1], 16));
-  } else {
-    t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 16));
-  }
+  static_assert(N * MOST <= kLnRedFloats && (N * MOST) % 4 == 0 && (N == 1 || N == 2 || N == 4), "slots");
+  float t[N];
 #pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, off));
+  for (int i = 0; i < N; ++i) t[i] = v[i];
+#pragma unroll
+  for (int n = N, off = 16; off >= 1; off >>= 1) {
+    if (n > 1) {
+      // the lanes with bit `off` keep the second half of the values
+      const bool upper = lane & off;
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) {
+        const float keep = upper ? t[n / 2 + i] : t[i], give = upper ? t[i] : t[n / 2 + i];
+        t[i] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, off));
+      }
+      n /= 2;
+    } else {
+      t[0] = __fadd_rn(t[0], __shfl_xor_sync(0xffffffffu, t[0], off));
+    }
+  }
   if (W == 1) {
-    v[0] = __shfl_sync(0xffffffffu, t, 0);
-    if (N == 2) v[N - 1] = __shfl_sync(0xffffffffu, t, 16);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, t[0], i * (32 / N));
     return __all_sync(0xffffffffu, ok);
   }
-  if (N == 2 ? (lane & 15) == 0 : lane == 0) red[N == 2 ? 2 * gw + (lane >> 4) : gw] = t;
+  if (lane % (32 / N) == 0) red[N * gw + lane / (32 / N)] = t[0];
   uint32_t all;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
@@ -139,17 +150,20 @@ __device__ __forceinline__ bool ln_group_sum(float (&v)[N], bool ok, int W, int 
   const float4* r = reinterpret_cast<const float4*>(red);
   float2 lo = make_float2(0.0f, 0.0f), hi = lo;
 #pragma unroll
-  for (int i = 0; i < kLnRedFloats / 4; ++i) {
+  for (int i = 0; i < N * MOST / 4; ++i) {
     const float4 part = r[i];
     lo = __fadd2_rn(lo, make_float2(part.x, part.y));
     hi = __fadd2_rn(hi, make_float2(part.z, part.w));
   }
-  const float2 s = __fadd2_rn(lo, hi);
-  if (N == 2) {
-    v[0] = s.x;
-    v[N - 1] = s.y;
+  if (N == 4) {
+    v[0] = lo.x;
+    v[N / 4] = lo.y;
+    v[N / 2] = hi.x;
+    v[N - 1] = hi.y;
   } else {
-    v[0] = __fadd_rn(s.x, s.y);
+    const float2 s = __fadd2_rn(lo, hi);
+    v[0] = N == 1 ? __fadd_rn(s.x, s.y) : s.x;
+    if (N == 2) v[N - 1] = s.y;
   }
   return all != 0;
 }
@@ -266,7 +280,7 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
     s = __fadd_rn(s, ln_hsum(X));
   }
   float t[1] = {s};
-  ln_group_sum(t, true, W, gw, lane, bar, red);
+  ln_group_sum<1, kLnWarps>(t, true, W, gw, lane, bar, red);
   const float mean = __fmul_rn(t[0], p.inv_c);
   const float2 nm = make_float2(-mean, -mean);
   s = 0.0f;
@@ -284,7 +298,7 @@ __device__ __forceinline__ void ln_forward_row(const LnParams& p, const uint4 (&
     }
   }
   t[0] = s;
-  ln_group_sum(t, true, W, gw, lane, bar, red + kLnRedFloats);
+  ln_group_sum<1, kLnWarps>(t, true, W, gw, lane, bar, red + kLnRedFloats);
   const float var = __fmul_rn(t[0], p.inv_c);
   const float rstd = rsqrtf(__fadd_rn(var, p.eps));
   if (l == 0) {
@@ -334,7 +348,9 @@ __global__ void __launch_bounds__(kLnThreads) ln_forward_direct_kernel(const __g
   grid_dependents_launch();
 }
 
-template <typename T, int CPT>
+// A group takes NR of its rows at a time: their sums share the shuffle trees
+// and the barriers.
+template <typename T, int CPT, int NR>
 __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -342,6 +358,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
   LnRing ring(smem, p, p.row_bytes, grp);
   ln_init_rings(smem, p.stages * p.groups);
   grid_dependency_wait();
+  grid_dependents_launch();
   const long long step = static_cast<long long>(gridDim.x) * p.groups;
   long long row = static_cast<long long>(blockIdx.x) * p.groups + grp, ahead = row;
   const bool leader = gw == 0 && lane == 0 && !(p.flags & 1u);   // test only: issue nothing
@@ -355,7 +372,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
   for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
   long long set_end = 0;                          // first row past the sample whose parameters are in g and b
   bool ok = true;
-  for (; row < p.tokens; row += step) {
+  while (row < p.tokens) {
     if (row >= set_end) {
       const long long set = ln_set(p, row);
       set_end = (set + 1) * p.rows_per_batch;
@@ -366,53 +383,71 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
         ln_bias8<T>(p, set, l + i * 32 * W, b[i]);
       }
     }
-    const bool landed = ring.wait();
-    float2 X[CPT][4];
-    float s = 0.0f;
+    // NR rows of the same sample, or one
+    const long long most = set_end < p.tokens ? set_end : p.tokens;
+    const int n = NR > 1 && row + step < most ? 2 : 1;
+    float2 X[NR][CPT][4];
+    float t[NR];
+    bool landed = true;
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      const uint4 raw = mine[i] ? ring.row()[l + i * 32 * W] : make_uint4(0, 0, 0, 0);
-      Elem<T>::unpack(raw, X[i]);
-      s = __fadd_rn(s, ln_hsum(X[i]));
-    }
-    float t[1] = {s};
-    ok = ln_group_sum(t, landed, W, gw, lane, 1 + grp, red);
-    const float mean = __fmul_rn(t[0], p.inv_c);
-    if (!ok) break;
-    ring.next();
-    if (leader) {
-      --ring.in_flight;
-      if (ahead < p.tokens) ring.put(p.x + ahead * p.x_stride, p.sp_x, nullptr, p.sp_x, p.row_bytes);
-      ahead += step;
-    }
-    const float2 nm = make_float2(-mean, -mean);
-    float2 q = make_float2(0.0f, 0.0f);
+    for (int r = 0; r < NR; ++r) {
+      t[r] = 0.0f;
+      if (r < n) {
+        landed = ring.wait() && landed;
+        const uint4* st = ring.row();
 #pragma unroll
-    for (int i = 0; i < CPT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        X[i][j] = __fadd2_rn(X[i][j], nm);
-        if (mine[i]) q = __ffma2_rn(X[i][j], X[i][j], q);
+        for (int i = 0; i < CPT; ++i) {
+          Elem<T>::unpack(mine[i] ? st[l + i * 32 * W] : make_uint4(0, 0, 0, 0), X[r][i]);
+          t[r] = __fadd_rn(t[r], ln_hsum(X[r][i]));
+        }
+        ring.next();
       }
-    t[0] = __fadd_rn(q.x, q.y);
-    ln_group_sum(t, true, W, gw, lane, 1 + grp, red + kLnRedFloats);
-    const float var = __fmul_rn(t[0], p.inv_c);
-    const float rstd = rsqrtf(__fadd_rn(var, p.eps));
-    if (l == 0) {
-      if (p.mean && in_span(p.mean + row, 4, p.sp_mean, p.status)) p.mean[row] = mean;
-      if (p.rstd && in_span(p.rstd + row, 4, p.sp_rstd, p.status)) p.rstd[row] = rstd;
     }
-    const float2 R = make_float2(rstd, rstd);
-    char* dst = p.y + row * p.y_stride + l * 16;
+    ok = ln_group_sum<NR, kLnWarps>(t, landed, W, gw, lane, 1 + grp, red);
+    if (!ok) break;
+    if (leader)
+      for (int r = 0; r < n; ++r) {
+        --ring.in_flight;
+        if (ahead < p.tokens) ring.put(p.x + ahead * p.x_stride, p.sp_x, nullptr, p.sp_x, p.row_bytes);
+        ahead += step;
+      }
+    float mean[NR];
 #pragma unroll
-    for (int i = 0; i < CPT; ++i) {
-      float2 o[4];
+    for (int r = 0; r < NR; ++r) {
+      mean[r] = __fmul_rn(t[r], p.inv_c);
+      const float2 nm = make_float2(-mean[r], -mean[r]);
+      float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __ffma2_rn(__fmul2_rn(X[i][j], R), g[i][j], b[i][j]);
-      if (mine[i] && in_span(dst + i * 512 * W, 16, p.sp_y, p.status)) store16(dst + i * 512 * W, Elem<T>::pack(o));
+      for (int i = 0; i < CPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          X[r][i][j] = __fadd2_rn(X[r][i][j], nm);
+          if (mine[i]) q = __ffma2_rn(X[r][i][j], X[r][i][j], q);
+        }
+      t[r] = __fadd_rn(q.x, q.y);
     }
+    ln_group_sum<NR, kLnWarps>(t, true, W, gw, lane, 1 + grp, red + kLnRedFloats);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      if (r >= n) break;
+      const float rstd = rsqrtf(__fadd_rn(__fmul_rn(t[r], p.inv_c), p.eps));
+      const long long at = row + r * step;
+      if (l == 0) {
+        if (p.mean && in_span(p.mean + at, 4, p.sp_mean, p.status)) p.mean[at] = mean[r];
+        if (p.rstd && in_span(p.rstd + at, 4, p.sp_rstd, p.status)) p.rstd[at] = rstd;
+      }
+      const float2 R = make_float2(rstd, rstd);
+      char* dst = p.y + at * p.y_stride + l * 16;
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        float2 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __ffma2_rn(__fmul2_rn(X[r][i][j], R), g[i][j], b[i][j]);
+        if (mine[i] && in_span(dst + i * 512 * W, 16, p.sp_y, p.status)) store16(dst + i * 512 * W, Elem<T>::pack(o));
+      }
+    }
+    row += n * step;
   }
-  grid_dependents_launch();
   if (!ok && leader) ring.drain();
 }
 
@@ -455,7 +490,7 @@ __device__ __forceinline__ void ln_grad_sums(const float2 (&xh)[4], const float2
 // one CTA per row.
 template <typename T>
 __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant__ LnParams p) {
-  __shared__ __align__(16) float red[2][kLnRedFloats];   // all sixteen written: eight warps, two values
+  __shared__ __align__(16) float red[2][kLnRedFloats];   // the sixteen read are written: eight warps, two values
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_chunks = p.hidden / 8;
   grid_dependency_wait();
   int parity = 0;
@@ -476,7 +511,7 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
       }
     }
     float t[2] = {s.x, s.y};
-    ln_group_sum(t, true, 8, warp, lane, 1, red[parity]);
+    ln_group_sum<2, 8>(t, true, 8, warp, lane, 1, red[parity]);
     if (threadIdx.x == 0 && in_span(p.row_sums + 2 * row, 8, p.sp_ws, p.status)) {
       p.row_sums[2 * row] = __fmul_rn(t[0], p.inv_c);
       p.row_sums[2 * row + 1] = __fmul_rn(t[1], p.inv_c);
@@ -492,7 +527,11 @@ __global__ void __launch_bounds__(256) ln_row_sums_kernel(const __grid_constant_
 // the unit's partial sums, or the result where a sample is one unit.  LONG:
 // the row spans several CTAs (a column tile each) and its two sums come from
 // ln_row_sums_kernel.
-template <typename T, int CPT, bool LONG>
+//
+// NR rows go through the sums together (CPT <= 3: at four chunks a thread the
+// registers hold one), which halves the shuffles, barriers and exposed
+// latency per row.
+template <typename T, int CPT, int NR, bool LONG>
 __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __grid_constant__ LnParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -507,6 +546,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
   volatile int* give_up = ring.abort_flag + 1;
   ln_init_rings(smem, p.stages * p.groups);
   grid_dependency_wait();
+  grid_dependents_launch();
   const long long units = p.sets * p.units_per_set, unit_step = gridDim.x / p.tiles;
   // rows [first, last) of unit u
   auto rows_of = [&](long long u, long long& first, long long& last) {
@@ -548,64 +588,80 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
       for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = gain[i][j] = make_float2(0.0f, 0.0f);
       if (mine[i]) ln_gain8<T>(p, set, k0 + l + i * 32 * W, gain[i]);
     }
-    // the statistics of the row after the one in work
+    // the statistics of the rows after those in work
     const float *at_mean = p.mean + first + grp, *at_rstd = p.rstd + first + grp;
     int left = last - first > grp ? static_cast<int>((last - first - grp + p.groups - 1) / p.groups) : 0;   // the group's rows
-    float nmean = 0.0f, nrstd = 0.0f;
-    auto stats = [&]() {
-      if (left > 0 && in_span(at_mean, 4, p.sp_mean, p.status) && in_span(at_rstd, 4, p.sp_rstd, p.status)) {
-        nmean = *at_mean;
-        nrstd = *at_rstd;
+    float nmean[NR], nrstd[NR];
+    auto stats = [&](int rows) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        nmean[r] = nrstd[r] = 0.0f;
+        if (rows > r && in_span(at_mean, 4, p.sp_mean, p.status) && in_span(at_rstd, 4, p.sp_rstd, p.status)) {
+          nmean[r] = *at_mean;
+          nrstd[r] = *at_rstd;
+        }
+        at_mean += p.groups;
+        at_rstd += p.groups;
       }
-      at_mean += p.groups;
-      at_rstd += p.groups;
     };
-    stats();
+    stats(left);
     char* dst = p.dx + (first + grp) * p.dx_stride + (k0 + l) * 16;
     const float2* sums = reinterpret_cast<const float2*>(p.row_sums) + first + grp;   // LONG
     float* buf = red;
-    for (; left > 0; dst += p.groups * p.dx_stride, sums += p.groups, buf = buf == red ? red + kLnRedFloats : red) {
-      const float2 nm = make_float2(-nmean, -nmean), R = make_float2(nrstd, nrstd);
-      --left;
-      stats();
-      const bool landed = ring.wait();
-      float2 xh[CPT][4], dy[CPT][4];
+    for (; left > 0; left -= NR, buf = buf == red ? red + kLnRedFloats : red) {
+      float2 xh[NR][CPT][4], dy[NR][CPT][4], R[NR];
+      float t[2 * NR];
+      bool landed = true;
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        uint4 xr = make_uint4(0, 0, 0, 0), dr = xr;
-        if (mine[i]) {
-          xr = ring.row()[l + i * 32 * W];
-          dr = ring.row()[n_chunks + l + i * 32 * W];
+      for (int r = 0; r < NR; ++r) {
+        const float2 nm = make_float2(-nmean[r], -nmean[r]);
+        R[r] = make_float2(nrstd[r], nrstd[r]);
+        const bool some = r < left;               // an odd last row: its partner's dy is zero
+        if (some) landed = ring.wait() && landed;
+        const uint4* st = ring.row();
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          uint4 xr = make_uint4(0, 0, 0, 0), dr = xr;
+          if (some && mine[i]) {
+            xr = st[l + i * 32 * W];
+            dr = st[n_chunks + l + i * 32 * W];
+          }
+          // past the row: dy = 0 and gain = 0, so xhat's value does not count
+          ln_grad_values<T>(xr, dr, nm, R[r], xh[r][i], dy[r][i]);
+          if (!LONG) ln_grad_sums(xh[r][i], dy[r][i], gain[i], s);
         }
-        // past the row: dy = 0 and gain = 0, so xhat's value does not count
-        ln_grad_values<T>(xr, dr, nm, R, xh[i], dy[i]);
+        t[2 * r] = s.x;
+        t[2 * r + 1] = s.y;
+        if (some) ring.next();
       }
-      float2 s = make_float2(0.0f, 0.0f);
-      if (!LONG) {
-#pragma unroll
-        for (int i = 0; i < CPT; ++i) ln_grad_sums(xh[i], dy[i], gain[i], s);
-      }
-      float t[2] = {s.x, s.y};
-      ok = ln_group_sum(t, landed, W, gw, lane, 1 + grp, buf);
+      stats(left - NR);
+      ok = ln_group_sum<2 * NR, kLnBwdWarps>(t, landed, W, gw, lane, 1 + grp, buf);
       if (!ok) break;
-      ring.next();
-      if (leader) {
-        --ring.in_flight;
-        put();
-      }
-      s = make_float2(__fmul_rn(t[0], p.inv_c), __fmul_rn(t[1], p.inv_c));
-      if (LONG && in_span(sums, 8, p.sp_ws, p.status)) s = *sums;
-      const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
-#pragma unroll
-      for (int i = 0; i < CPT; ++i) {
-        float2 o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          db[i][j] = __fadd2_rn(db[i][j], dy[i][j]);
-          dw[i][j] = __ffma2_rn(dy[i][j], xh[i][j], dw[i][j]);
-          o[j] = __fmul2_rn(__ffma2_rn(xh[i][j], c2, __ffma2_rn(dy[i][j], gain[i][j], c1)), R);
+      if (leader)
+        for (int r = 0; r < NR && r < left; ++r) {
+          --ring.in_flight;
+          put();
         }
-        if (mine[i] && in_span(dst + i * 512 * W, 16, p.sp_dx, p.status)) store16(dst + i * 512 * W, Elem<T>::pack(o));
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float2 s = make_float2(__fmul_rn(t[2 * r], p.inv_c), __fmul_rn(t[2 * r + 1], p.inv_c));
+        if (LONG && r < left && in_span(sums, 8, p.sp_ws, p.status)) s = *sums;
+        const float2 c1 = make_float2(-s.x, -s.x), c2 = make_float2(-s.y, -s.y);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          float2 o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            db[i][j] = __fadd2_rn(db[i][j], dy[r][i][j]);
+            dw[i][j] = __ffma2_rn(dy[r][i][j], xh[r][i][j], dw[i][j]);
+            o[j] = __fmul2_rn(__ffma2_rn(xh[r][i][j], c2, __ffma2_rn(dy[r][i][j], gain[i][j], c1)), R[r]);
+          }
+          if (r < left && mine[i] && in_span(dst + i * 512 * W, 16, p.sp_dx, p.status))
+            store16(dst + i * 512 * W, Elem<T>::pack(o));
+        }
+        dst += p.groups * p.dx_stride;
+        sums += p.groups;
       }
     }
     // the groups' sums, added in order
@@ -664,7 +720,6 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
       }
     }
   }
-  grid_dependents_launch();
   if (leader && (!ok || *ring.abort_flag)) ring.drain();
 }
 

@@ -17,8 +17,8 @@ using qknr_host::fail;
 using qknr_host::Span;
 using qknr_host::span_of;
 
-// CTAs at most: four of 256 threads on each SM of a GB300.
-constexpr long long kMaxCtas = 4 * 152;
+// CTAs at most: the three of 256 threads that each SM of a GB300 holds.
+constexpr long long kMaxCtas = 3 * 152;
 
 template <typename T, typename CT>
 const void* kernel(int D, bool rh) {
@@ -239,7 +239,10 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   const bool overlap = !(a->flags & QKNR_FLAG_NO_OVERLAP);
   const long long n = ctas(a);
   void* kargs[] = {&kp};
-  st = qknr_host::launch_kernel(fn, static_cast<int>(n), qknr::kGradThreads, 0, cs, kargs, overlap,
+  int regs = 0;
+  st = qknr_host::configure_kernel(fn, dev, di, &regs);
+  if (st != QKNR_OK) return st;
+  st = qknr_host::launch_kernel(fn, static_cast<int>(n), qknr::kGradThreads, qknr::kGradSmem, cs, kargs, overlap,
                                 "cudaLaunchKernelExC(QK backward)");
   if (st != QKNR_OK || (!a->dgamma_q && !a->dgamma_k)) return st;
   qknr::PartsParams pp;

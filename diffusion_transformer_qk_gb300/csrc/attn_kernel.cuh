@@ -86,10 +86,12 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int first, int la
 template <typename T, int D>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t idesc = mma_desc<T>(kTile, kTile, false);
+  const uint32_t da = desc_k_major(a), db = desc_k_major(b);
+  mma_ss<false>(d, da, db, idesc);
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint32_t off = (k / 4) * (kTile * 128) + (k % 4) * 32;
-    mma_ss(d, desc_k_major(a + off), desc_k_major(b + off), idesc, k > 0);
+  for (int k = 1; k < D / 16; ++k) {
+    const uint32_t off = ((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4;
+    mma_ss<true>(d, da + off, db + off, idesc);
   }
 }
 
@@ -98,10 +100,10 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
 template <typename T, int D, bool SPLIT>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
   constexpr uint32_t idesc = mma_desc<T>(kTile, D, true);
+  const uint32_t db = desc_mn_major(b, kTile * 128);
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    mma_ts(d, a + (SPLIT ? (k / 4) * 64 + (k % 4) * 8 : k * 8), desc_mn_major(b + k * 2048, kTile * 128), idesc,
-           accumulate || k > 0);
+    mma_ts(d, a + (SPLIT ? (k / 4) * 64 + (k % 4) * 8 : k * 8), db + k * (2048 >> 4), idesc, accumulate || k > 0);
 }
 
 // The common part of the kernels: barriers, tensor memory, bounded waits.
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
   AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
+            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i >= P_FULL && i < O_DONE ? 4 : 1);
     *abort_flag = 0;
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       if (nb[t]) ok = c.wait(Q_FULL + t, 0);
     ok = ok && c.wait(KV_FULL, 0);
     tc_fence_after();
-    if (ok && c.lane == 0) {
+    if (ok && elect_one()) {
       for (int t = 0; t < 2; ++t)
         if (nb[t]) {
           mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, ring);
@@ -275,22 +277,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         if (ok && j < nb[t]) {
           ok = c.wait(P_FULL + t, j);
           tc_fence_after();
-          if (ok && c.lane == 0) {
+          if (ok && elect_one()) {
             mma_cols<T, D, false>(tmem + 2 * kTile + t * kTile, tmem + t * kTile, ring + sv * kTileBytes<D>, j > 0);
             mma_commit(c.bar(O_DONE + t));
           }
         }
-        if (t == 1 && ok && c.lane == 0) mma_commit(c.bar(KV_EMPTY + sv));
-        if (ok && c.lane == 0 && j + 1 < nb[t]) {
+        if (t == 1 && ok && elect_one()) mma_commit(c.bar(KV_EMPTY + sv));
+        if (ok && elect_one() && j + 1 < nb[t]) {
           mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, ring + sk * kTileBytes<D>);
           mma_commit(c.bar(S_FULL + t));
         }
       }
-      if (ok && c.lane == 0 && j + 1 < blocks) mma_commit(c.bar(KV_EMPTY + sk));
+      if (ok && elect_one() && j + 1 < blocks) mma_commit(c.bar(KV_EMPTY + sk));
     }
     if (!ok && blocks > 0) {
       // MMAs in flight end before tensor memory is given back
-      if (c.lane == 0) mma_commit(c.bar(DRAIN));
+      if (elect_one()) mma_commit(c.bar(DRAIN));
       const unsigned long long t0 = global_timer_ns();
       while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
       }
@@ -488,7 +490,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
   AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
+            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == DP_FREE || i == DS_FULL ? 8 : 1);
     *abort_flag = 0;
@@ -567,13 +569,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       return got;
     };
     auto scores = [&](int j) {
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_rows<T, D>(tmem + (j & 1) * kTile, sq, sk + (j % kK) * kTileBytes<D>);
         mma_commit(c.bar(S_FULL + (j & 1)));
       }
     };
     auto grads = [&](int j) {
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + (j % kV) * kTileBytes<D>);
         mma_commit(c.bar(DP_FULL));
         mma_commit(c.bar(V_EMPTY + j % kV));
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       ok = c.wait(DS_FULL, j);
       tc_fence_after();
       if (!ok) break;
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (j & 1) * kTile, sk + (j % kK) * kTileBytes<D>, j > 0);
         mma_commit(c.bar(K_EMPTY + j % kK));
       }
@@ -606,9 +608,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (ok) scores(j + 2);
       }
     }
-    if (ok && c.lane == 0) mma_commit(c.bar(DONE));
+    if (ok && elect_one()) mma_commit(c.bar(DONE));
     if (!ok && n > 0) {
-      if (c.lane == 0) mma_commit(c.bar(DRAIN));
+      if (elect_one()) mma_commit(c.bar(DRAIN));
       const unsigned long long t0 = global_timer_ns();
       while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
       }
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
   AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31)};
+            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == P_FULL || i == DS_FULL || i == ROWS ? 8 : 1);
     *abort_flag = 0;
@@ -808,13 +810,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       return got;
     };
     auto scores = [&](int i) {
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_rows<T, D>(tmem, sk, sq + (i % kQ) * kTileBytes<D>);
         mma_commit(c.bar(S_FULL));
       }
     };
     auto grads = [&](int i) {
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_rows<T, D>(tmem + kTile, sv, sdo + (i % kO) * kTileBytes<D>);
         mma_commit(c.bar(DP_FULL));
       }
@@ -827,7 +829,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       ok = c.wait(P_FULL, i);
       tc_fence_after();
       if (!ok) break;
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + (i % kO) * kTileBytes<D>, i > 0);
         mma_commit(c.bar(O_EMPTY + i % kO));
       }
@@ -839,7 +841,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       ok = c.wait(DS_FULL, i);
       tc_fence_after();
       if (!ok) break;
-      if (c.lane == 0) {
+      if (elect_one()) {
         mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + (i % kQ) * kTileBytes<D>, i > 0);
         mma_commit(c.bar(Q_EMPTY + i % kQ));
       }
@@ -849,9 +851,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         grads(i + 1);
       }
     }
-    if (ok && c.lane == 0) mma_commit(c.bar(DONE));
+    if (ok && elect_one()) mma_commit(c.bar(DONE));
     if (!ok && n > 0) {
-      if (c.lane == 0) mma_commit(c.bar(DRAIN));
+      if (elect_one()) mma_commit(c.bar(DRAIN));
       const unsigned long long t0 = global_timer_ns();
       while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
       }

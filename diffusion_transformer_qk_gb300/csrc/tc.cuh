@@ -20,17 +20,20 @@ namespace qknr {
 
 constexpr uint64_t kDescFixed = (uint64_t(1) << 46) /* descriptor version */ | (uint64_t(2) << 61) /* 128-byte swizzle */;
 
-// Contraction along the columns: 8-row groups 1024 bytes apart.  The k-th
-// slice of 16 columns starts 32 bytes further.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  return kDescFixed | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 16) | ((addr & 0x3ffff) >> 4);
-}
+// A descriptor is a constant upper half (row-group stride 1024 bytes, version,
+// swizzle) and a lower half of start address and, for MN-major tiles, the
+// distance of the next 64 columns; slices of the contraction differ by an
+// addition to the lower half.
+constexpr uint32_t kDescHigh = uint32_t(kDescFixed >> 32) | uint32_t(1024 >> 4);
 
-// Contraction along the rows: 8-row groups 1024 bytes apart, the next 64
-// columns `tile_bytes` away.  The k-th slice of 16 rows starts 2048 bytes
-// further.
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t tile_bytes) {
-  return kDescFixed | (uint64_t(1024 >> 4) << 32) | (uint64_t(tile_bytes >> 4) << 16) | ((addr & 0x3ffff) >> 4);
+// Contraction along the columns.  The k-th slice of 16 columns starts 32
+// bytes further.
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t addr) { return (1u << 16) | (addr >> 4); }
+
+// Contraction along the rows, the next 64 columns `tile_bytes` away.  The
+// k-th slice of 16 rows starts 2048 bytes further.
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t addr, uint32_t tile_bytes) {
+  return ((tile_bytes >> 4) << 16) | (addr >> 4);
 }
 
 template <typename T>
@@ -54,21 +57,30 @@ __host__ __device__ constexpr uint32_t mma_desc(int M, int N, bool b_mn_major) {
 // ---------------------------------------------------------------------------
 // MMA issue (one thread)
 
-// D[tmem] (+)= A[smem] B[smem], 16 of the contraction
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// True in one thread of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+
+// D[tmem] (+)= A[smem] B[smem], 16 of the contraction; a and b: lower halves
+// of the descriptors
+template <bool ACCUMULATE>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 da, {%1, %4};\n\t"
+      "mov.b64 db, {%2, %4};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "n"(ACCUMULATE ? 1 : 0)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 db, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
 

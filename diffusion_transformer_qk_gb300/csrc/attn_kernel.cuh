@@ -664,18 +664,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       tmem_loaded(d[1]);
       c.arrive(DP_FREE);
       const int seen = limit - j * kTile - half * 64;
-      const bool masked = __any_sync(0xffffffffu, seen < 64);
+      if (__any_sync(0xffffffffu, seen < 64)) {
+        // p = 0 and a finite dp - delta where the row does not see the key
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            s[i][e] = 32 * i + e < seen ? s[i][e] : 0.0f;
+            d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
+          }
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float2 x = __fmul2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]),
-                                __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), C, ND));
-          if (masked) {
-            x.x = 32 * i + 2 * e < seen ? x.x : 0.0f;
-            x.y = 32 * i + 2 * e + 1 < seen ? x.y : 0.0f;
-          }
+          const float2 x = __fmul2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]),
+                                      __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), C, ND));
           w[e] = pack2<T>(x.x, x.y);
         }
         tmem_store16(ts + 16 * i, w);
@@ -867,29 +872,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + half * 64 + lanes, tdp = tmem + kTile + half * 64 + lanes;
     const float2 SL = make_float2(p.scale_log2, p.scale_log2), C = make_float2(kGradC<T>, kGradC<T>);
-    // Threads 0-127 fetch kP - lse (log2) of a tile's queries, 128-255
-    // -delta kC, one block ahead.  A query past the length or with no key has lse = inf
-    // here: p = 0.
+    // Threads 0-127 hand round kP - lse (log2) of a tile's queries, 128-255
+    // -delta kC.  The values are fetched one block ahead, and only looked at
+    // when that block begins, so that nothing waits for them.  A query past
+    // the length or with no key gets -inf: p = 0.
     const int which = static_cast<int>(threadIdx.x) >> 7, col = static_cast<int>(threadIdx.x) & 127;
+    const float* source = which ? p.delta : p.lse;
+    const MemSpan& sp_source = which ? p.sp_delta : p.sp_lse;
     auto fetch = [&](int i) {
       const int h = hk * p.group + i / per_head, q = (first + i % per_head) * kTile + col;
-      const long long at = (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + q;
-      float v = which ? 0.0f : -INFINITY;
-      if (q < q_len) {
-        if (which == 0) {
-          if (in_span(p.lse + at, 4, p.sp_lse, p.status)) v = p.lse[at];
-          v = v == -INFINITY ? -INFINITY : __fmaf_rn(v, -kLog2e, GradScale<T>::kP);
-        } else if (in_span(p.delta + at, 4, p.sp_delta, p.status)) {
-          v = -p.delta[at] * kGradC<T>;
-        }
-      }
-      return v;
+      const float* at = source + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + q;
+      return q < q_len && in_span(at, 4, sp_source, p.status) ? *at : (which ? 0.0f : -INFINITY);
     };
     bool ok = true;
     float next = n > 0 ? fetch(0) : 0.0f;
     for (int i = 0; i < n; ++i) {
       float* mine = rows + (i & 1) * 2 * kTile;
-      mine[which * kTile + col] = next;
+      mine[which * kTile + col] = which ? -next * kGradC<T>
+                                        : (next == -INFINITY ? -INFINITY : __fmaf_rn(next, -kLog2e, GradScale<T>::kP));
       if (i + 1 < n) next = fetch(i + 1);
       __syncwarp();
       if (c.lane == 0) mbar_arrive(c.bar(ROWS));
@@ -907,8 +907,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       const int from = p.causal ? key - diag - (first + i % per_head) * kTile - half * 64 : 0;
       const bool masked = __any_sync(0xffffffffu, from > 0);
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        uint32_t w[16];
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 l4 = nl[a * 8 + e];
@@ -919,13 +918,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
           x[1] = exp2_approx(u.y);
           x[2] = exp2_approx(v.x);
           x[3] = exp2_approx(v.y);
-          if (masked) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) x[g] = 32 * a + 4 * e + g >= from ? x[g] : 0.0f;
-          }
-          w[2 * e] = pack2<T>(x[0], x[1]);
-          w[2 * e + 1] = pack2<T>(x[2], x[3]);
         }
+      if (masked) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[a][e] = 32 * a + e >= from ? s[a][e] : 0.0f;
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(s[a][2 * e], s[a][2 * e + 1]);
         tmem_store16(ts + 16 * a, w);
       }
       tmem_wait_store();
@@ -938,6 +942,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       tmem_load32(tdp + 32, d[1]);
       tmem_wait_load(d[0]);
       tmem_loaded(d[1]);
+      if (masked) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
+      }
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         uint32_t w[16];
@@ -945,16 +955,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         for (int e = 0; e < 8; ++e) {
           const float4 d4 = nd[a * 8 + e];
           const float* x = &s[a][4 * e];
-          float2 u = __fmul2_rn(make_float2(x[0], x[1]),
-                                __ffma2_rn(make_float2(d[a][4 * e], d[a][4 * e + 1]), C, make_float2(d4.x, d4.y)));
-          float2 v = __fmul2_rn(make_float2(x[2], x[3]),
-                                __ffma2_rn(make_float2(d[a][4 * e + 2], d[a][4 * e + 3]), C, make_float2(d4.z, d4.w)));
-          if (masked) {
-            u.x = 32 * a + 4 * e >= from ? u.x : 0.0f;
-            u.y = 32 * a + 4 * e + 1 >= from ? u.y : 0.0f;
-            v.x = 32 * a + 4 * e + 2 >= from ? v.x : 0.0f;
-            v.y = 32 * a + 4 * e + 3 >= from ? v.y : 0.0f;
-          }
+          const float2 u = __fmul2_rn(make_float2(x[0], x[1]),
+                                      __ffma2_rn(make_float2(d[a][4 * e], d[a][4 * e + 1]), C, make_float2(d4.x, d4.y)));
+          const float2 v = __fmul2_rn(make_float2(x[2], x[3]),
+                                      __ffma2_rn(make_float2(d[a][4 * e + 2], d[a][4 * e + 3]), C, make_float2(d4.z, d4.w)));
           w[2 * e] = pack2<T>(u.x, u.y);
           w[2 * e + 1] = pack2<T>(v.x, v.y);
         }

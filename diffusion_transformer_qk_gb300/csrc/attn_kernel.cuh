@@ -10,7 +10,8 @@
 // Roles of a CTA's 12 warps: 0-7 are two groups of four that each cover the
 // 128 lanes of tensor memory (a thread owns one row of a score tile), warp 8
 // issues the MMAs, warp 9 the TMA loads, warps 10 and 11 fill up the third
-// group, whose registers go to the first two.  Every wait is bounded; a role that
+// group, whose registers go to the first two (and hand round the queries'
+// statistics in the dk, dv kernel).  Every wait is bounded; a role that
 // gives up sets the CTA's abort flag, drains what it started and leaves.
 #pragma once
 
@@ -105,6 +106,20 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, uint32_t b, boo
   for (int k = 0; k < kTile / 16; ++k)
     mma_ts(d, a + (SPLIT ? (k / 4) * 64 + (k % 4) * 8 : k * 8), db + k * (2048 >> 4), idesc, accumulate || k > 0);
 }
+
+// A place in a ring of N stages, stepped without divisions: the issuing warp's
+// instructions between two products are time the tensor cores may stand still.
+template <int N>
+struct RingPos {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == N) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
 
 // The common part of the kernels: barriers, tensor memory, bounded waits.
 struct AttnCta {
@@ -526,16 +541,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         mbar_arrive_expect_tx(c.bar(Q_FULL), 2 * kTileBytes<D>);
         tma_load_tile(sq, &p.map_q, q0, h, b, c.bar(Q_FULL));
         tma_load_tile(sdo, &p.map_do, q0, h, b, c.bar(Q_FULL));
-        for (int j = 0; j < n; ++j) {
-          ok = c.wait1(K_EMPTY + j % kK, (j / kK + 1) & 1);
+        RingPos<kK> k;
+        RingPos<kV> v;
+        for (int j = 0; j < n; ++j, k.step(), v.step()) {
+          ok = c.wait1(K_EMPTY + k.s, k.phase ^ 1u);
           if (!ok) break;
-          mbar_arrive_expect_tx(c.bar(K_FULL + j % kK), kTileBytes<D>);
-          tma_load_tile(sk + (j % kK) * kTileBytes<D>, &p.map_k, j * kTile, hk, b, c.bar(K_FULL + j % kK));
+          mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
+          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, j * kTile, hk, b, c.bar(K_FULL + k.s));
           ++ik;
-          ok = c.wait1(V_EMPTY + j % kV, (j / kV + 1) & 1);
+          ok = c.wait1(V_EMPTY + v.s, v.phase ^ 1u);
           if (!ok) break;
-          mbar_arrive_expect_tx(c.bar(V_FULL + j % kV), kTileBytes<D>);
-          tma_load_tile(sv + (j % kV) * kTileBytes<D>, &p.map_v, j * kTile, hk, b, c.bar(V_FULL + j % kV));
+          mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
+          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, j * kTile, hk, b, c.bar(V_FULL + v.s));
           ++iv;
         }
       }
@@ -555,58 +572,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   } else if (c.warp == kAttnMmaWarp) {
     bool ok = n > 0;
     const bool ragged = k_len < p.seq_k;
-    // block j's K and V have landed, with nothing past the sample's keys
-    auto have_k = [&](int j) {
-      const bool got = c.wait(K_FULL + j % kK, j / kK);
+    // Blocks whose scores, dP and dQ products come next, and their stages.
+    RingPos<kK> ks, kd;
+    RingPos<kV> vs;
+    int js = 0, jv = 0;
+    // the block's K (V) has landed, with nothing past the sample's keys
+    auto have = [&](int full, int tile_at, uint32_t phase, int j) {
+      const bool got = c.wait(full, phase);
       if (got && ragged && (j + 1) * kTile > k_len)
-        zero_rows<D>(smem + (2 + j % kK) * kTileBytes<D>, k_len - j * kTile, c.lane);
+        zero_rows<D>(smem + tile_at * kTileBytes<D>, k_len - j * kTile, c.lane);
       return got;
     };
-    auto have_v = [&](int j) {
-      const bool got = c.wait(V_FULL + j % kV, j / kV);
-      if (got && ragged && (j + 1) * kTile > k_len)
-        zero_rows<D>(smem + (2 + kK + j % kV) * kTileBytes<D>, k_len - j * kTile, c.lane);
-      return got;
-    };
-    auto scores = [&](int j) {
+    auto scores = [&]() {
+      if (!have(K_FULL + ks.s, 2 + ks.s, ks.phase, js)) return false;
       if (elect_one()) {
-        mma_rows<T, D>(tmem + (j & 1) * kTile, sq, sk + (j % kK) * kTileBytes<D>);
-        mma_commit(c.bar(S_FULL + (j & 1)));
+        mma_rows<T, D>(tmem + (js & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
+        mma_commit(c.bar(S_FULL + (js & 1)));
       }
+      ks.step();
+      ++js;
+      return true;
     };
-    auto grads = [&](int j) {
+    auto grads = [&]() {
+      if (!have(V_FULL + vs.s, 2 + kK + vs.s, vs.phase, jv)) return false;
       if (elect_one()) {
-        mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + (j % kV) * kTileBytes<D>);
+        mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + vs.s * kTileBytes<D>);
         mma_commit(c.bar(DP_FULL));
-        mma_commit(c.bar(V_EMPTY + j % kV));
+        mma_commit(c.bar(V_EMPTY + vs.s));
       }
+      vs.step();
+      ++jv;
+      return true;
     };
-    ok = ok && c.wait(Q_FULL, 0) && have_k(0);
-    if (ok) scores(0);
-    ok = ok && have_v(0);
-    if (ok) grads(0);
-    if (ok && n > 1) {
-      ok = have_k(1);
-      if (ok) scores(1);
-    }
+    ok = ok && c.wait(Q_FULL, 0) && scores() && grads() && (n == 1 || scores());
     for (int j = 0; ok && j < n; ++j) {
       if (j + 1 < n) {
-        ok = have_v(j + 1) && c.wait(DP_FREE, j);
+        ok = c.wait(DP_FREE, j);
         tc_fence_after();
         if (!ok) break;
-        grads(j + 1);
+        ok = grads();
+        if (!ok) break;
       }
       ok = c.wait(DS_FULL, j);
       tc_fence_after();
       if (!ok) break;
       if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (j & 1) * kTile, sk + (j % kK) * kTileBytes<D>, j > 0);
-        mma_commit(c.bar(K_EMPTY + j % kK));
+        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (j & 1) * kTile, sk + kd.s * kTileBytes<D>, j > 0);
+        mma_commit(c.bar(K_EMPTY + kd.s));
       }
-      if (j + 2 < n) {
-        ok = have_k(j + 2);
-        if (ok) scores(j + 2);
-      }
+      kd.step();
+      if (j + 2 < n) ok = scores();
     }
     if (ok && elect_one()) mma_commit(c.bar(DONE));
     if (!ok && n > 0) {
@@ -720,7 +735,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
 namespace dkv {
 constexpr int kQ = 3, kO = 2;                     // Q and dO tiles in flight
 enum { KV_FULL = 0, Q_FULL = 1, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ, O_EMPTY = O_FULL + kO,
-       S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, DONE, DRAIN, BARS };
+       S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, ROWS_FREE = ROWS + 2,
+       DONE = ROWS_FREE + 2, DRAIN, BARS };
 constexpr int kRowBytes = 2 * 2 * kTile * 4;      // two buffers of (lse, delta) of a tile's queries
 template <int D>
 constexpr int kSmem = (2 + kQ + kO) * kTileBytes<D> + kRowBytes + 256;
@@ -737,7 +753,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
             __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == P_FULL || i == DS_FULL || i == ROWS ? 8 : 1);
+    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == P_FULL || i == DS_FULL || (i >= ROWS_FREE && i < DONE) ? 8 : (i >= ROWS && i < ROWS_FREE ? 2 : 1));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -770,18 +786,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         mbar_arrive_expect_tx(c.bar(KV_FULL), 2 * kTileBytes<D>);
         tma_load_tile(sk, &p.map_k, k0, hk, b, c.bar(KV_FULL));
         tma_load_tile(sv, &p.map_v, k0, hk, b, c.bar(KV_FULL));
-        for (int i = 0; i < n; ++i) {
-          const int h = hk * p.group + i / per_head, q0 = (first + i % per_head) * kTile;
-          ok = c.wait1(Q_EMPTY + i % kQ, (i / kQ + 1) & 1);
+        RingPos<kQ> q;
+        RingPos<kO> o;
+        int h = hk * p.group, t = first;
+        for (int i = 0; i < n; ++i, q.step(), o.step()) {
+          ok = c.wait1(Q_EMPTY + q.s, q.phase ^ 1u);
           if (!ok) break;
-          mbar_arrive_expect_tx(c.bar(Q_FULL + i % kQ), kTileBytes<D>);
-          tma_load_tile(sq + (i % kQ) * kTileBytes<D>, &p.map_q, q0, h, b, c.bar(Q_FULL + i % kQ));
+          mbar_arrive_expect_tx(c.bar(Q_FULL + q.s), kTileBytes<D>);
+          tma_load_tile(sq + q.s * kTileBytes<D>, &p.map_q, t * kTile, h, b, c.bar(Q_FULL + q.s));
           ++iq;
-          ok = c.wait1(O_EMPTY + i % kO, (i / kO + 1) & 1);
+          ok = c.wait1(O_EMPTY + o.s, o.phase ^ 1u);
           if (!ok) break;
-          mbar_arrive_expect_tx(c.bar(O_FULL + i % kO), kTileBytes<D>);
-          tma_load_tile(sdo + (i % kO) * kTileBytes<D>, &p.map_do, q0, h, b, c.bar(O_FULL + i % kO));
+          mbar_arrive_expect_tx(c.bar(O_FULL + o.s), kTileBytes<D>);
+          tma_load_tile(sdo + o.s * kTileBytes<D>, &p.map_do, t * kTile, h, b, c.bar(O_FULL + o.s));
           ++io;
+          if (++t == end) {
+            t = first;
+            ++h;
+          }
         }
       }
       if (!ok || *abort_flag) {
@@ -800,61 +822,58 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   } else if (c.warp == kAttnMmaWarp) {
     bool ok = n > 0;
     const bool ragged = q_len < p.seq_q;
-    auto clean = [&](unsigned char* t, int i) {
-      const int q0 = (first + i % per_head) * kTile;
-      if (ragged && q0 + kTile > q_len) zero_rows<D>(t, q_len - q0, c.lane);
-    };
-    auto have_q = [&](int i) {
-      const bool got = c.wait(Q_FULL + i % kQ, i / kQ);
-      if (got) clean(smem + (2 + i % kQ) * kTileBytes<D>, i);
+    // Blocks whose scores, dP, dV and dK products come next.
+    RingPos<kQ> qs, qd;
+    RingPos<kO> os, od;
+    int ts = first, to = first;                   // their query tiles
+    // the tile has landed, with nothing past the sample's queries
+    auto have = [&](int full, int tile_at, uint32_t phase, int& t) {
+      const bool got = c.wait(full, phase);
+      if (got && ragged && (t + 1) * kTile > q_len) zero_rows<D>(smem + tile_at * kTileBytes<D>, q_len - t * kTile, c.lane);
+      if (++t == end) t = first;
       return got;
     };
-    auto have_do = [&](int i) {
-      const bool got = c.wait(O_FULL + i % kO, i / kO);
-      if (got) clean(smem + (2 + kQ + i % kO) * kTileBytes<D>, i);
-      return got;
-    };
-    auto scores = [&](int i) {
+    auto scores = [&]() {
+      if (!have(Q_FULL + qs.s, 2 + qs.s, qs.phase, ts)) return false;
       if (elect_one()) {
-        mma_rows<T, D>(tmem, sk, sq + (i % kQ) * kTileBytes<D>);
+        mma_rows<T, D>(tmem, sk, sq + qs.s * kTileBytes<D>);
         mma_commit(c.bar(S_FULL));
       }
+      qs.step();
+      return true;
     };
-    auto grads = [&](int i) {
+    auto grads = [&]() {
+      if (!have(O_FULL + os.s, 2 + kQ + os.s, os.phase, to)) return false;
       if (elect_one()) {
-        mma_rows<T, D>(tmem + kTile, sv, sdo + (i % kO) * kTileBytes<D>);
+        mma_rows<T, D>(tmem + kTile, sv, sdo + os.s * kTileBytes<D>);
         mma_commit(c.bar(DP_FULL));
       }
+      os.step();
+      return true;
     };
-    ok = ok && c.wait(KV_FULL, 0) && have_q(0);
-    if (ok) scores(0);
-    ok = ok && have_do(0);
-    if (ok) grads(0);
+    ok = ok && c.wait(KV_FULL, 0) && scores() && grads();
     for (int i = 0; ok && i < n; ++i) {
       ok = c.wait(P_FULL, i);
       tc_fence_after();
       if (!ok) break;
       if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + (i % kO) * kTileBytes<D>, i > 0);
-        mma_commit(c.bar(O_EMPTY + i % kO));
+        mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + od.s * kTileBytes<D>, i > 0);
+        mma_commit(c.bar(O_EMPTY + od.s));
       }
+      od.step();
       if (i + 1 < n) {
-        ok = have_q(i + 1);
+        ok = scores();
         if (!ok) break;
-        scores(i + 1);
       }
       ok = c.wait(DS_FULL, i);
       tc_fence_after();
       if (!ok) break;
       if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + (i % kQ) * kTileBytes<D>, i > 0);
-        mma_commit(c.bar(Q_EMPTY + i % kQ));
+        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + qd.s * kTileBytes<D>, i > 0);
+        mma_commit(c.bar(Q_EMPTY + qd.s));
       }
-      if (i + 1 < n) {
-        ok = have_do(i + 1);
-        if (!ok) break;
-        grads(i + 1);
-      }
+      qd.step();
+      if (i + 1 < n) ok = grads();
     }
     if (ok && elect_one()) mma_commit(c.bar(DONE));
     if (!ok && n > 0) {
@@ -864,7 +883,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (c.warp < kAttnMmaWarp) {
+  } else if (c.warp >= kAttnMmaWarp) {
+    // Warps 10 and 11 hand round kP - lse (log2) and -delta kC of the blocks'
+    // queries, up to two blocks ahead.  A query past the length or with no
+    // key gets -inf: p = 0.
+    const bool second = c.warp == kAttnMmaWarp + 3;
+    const float* source = second ? p.delta : p.lse;
+    const MemSpan& sp_source = second ? p.sp_delta : p.sp_lse;
+    int h = hk * p.group, t = first;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const float* at = source + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int q = t * kTile + 32 * e + c.lane;
+        v[e] = second ? 0.0f : -INFINITY;
+        if (q < q_len && in_span(at + 32 * e, 4, sp_source, p.status)) v[e] = at[32 * e];
+      }
+      // the block before last has been read
+      ok = i < 2 || c.wait(ROWS_FREE + (i & 1), (i >> 1) - 1);
+      if (!ok) break;
+      float* out = rows + (i & 1) * 2 * kTile + (second ? kTile : 0) + c.lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        out[32 * e] = second ? -v[e] * kGradC<T> : (v[e] == -INFINITY ? -INFINITY : __fmaf_rn(v[e], -kLog2e, GradScale<T>::kP));
+      __syncwarp();
+      if (c.lane == 0) mbar_arrive(c.bar(ROWS + (i & 1)));
+      if (++t == end) {
+        t = first;
+        ++h;
+      }
+    }
+  } else {
     more_registers<kAttnWorkRegs>();
     // a thread per key and half of the block's queries
     const int half = c.warp >> 2;
@@ -872,30 +923,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + half * 64 + lanes, tdp = tmem + kTile + half * 64 + lanes;
     const float2 SL = make_float2(p.scale_log2, p.scale_log2), C = make_float2(kGradC<T>, kGradC<T>);
-    // Threads 0-127 hand round kP - lse (log2) of a tile's queries, 128-255
-    // -delta kC.  The values are fetched one block ahead, and only looked at
-    // when that block begins, so that nothing waits for them.  A query past
-    // the length or with no key gets -inf: p = 0.
-    const int which = static_cast<int>(threadIdx.x) >> 7, col = static_cast<int>(threadIdx.x) & 127;
-    const float* source = which ? p.delta : p.lse;
-    const MemSpan& sp_source = which ? p.sp_delta : p.sp_lse;
-    auto fetch = [&](int i) {
-      const int h = hk * p.group + i / per_head, q = (first + i % per_head) * kTile + col;
-      const float* at = source + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + q;
-      return q < q_len && in_span(at, 4, sp_source, p.status) ? *at : (which ? 0.0f : -INFINITY);
-    };
     bool ok = true;
-    float next = n > 0 ? fetch(0) : 0.0f;
+    int t = first;                                // the block's query tile
     for (int i = 0; i < n; ++i) {
-      float* mine = rows + (i & 1) * 2 * kTile;
-      mine[which * kTile + col] = which ? -next * kGradC<T>
-                                        : (next == -INFINITY ? -INFINITY : __fmaf_rn(next, -kLog2e, GradScale<T>::kP));
-      if (i + 1 < n) next = fetch(i + 1);
-      __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(ROWS));
+      const float* mine = rows + (i & 1) * 2 * kTile;
       const float4* nl = reinterpret_cast<const float4*>(mine + half * 64);
       const float4* nd = reinterpret_cast<const float4*>(mine + kTile + half * 64);
-      ok = c.wait(ROWS, i) && c.wait(S_FULL, i);
+      ok = c.wait(ROWS + (i & 1), i >> 1) && c.wait(S_FULL, i);
       if (!ok) break;
       tc_fence_after();
       float s[2][32];
@@ -904,7 +938,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       tmem_wait_load(s[0]);
       tmem_loaded(s[1]);
       // query q0 + c sees this key when c >= from
-      const int from = p.causal ? key - diag - (first + i % per_head) * kTile - half * 64 : 0;
+      const int from = p.causal ? key - diag - t * kTile - half * 64 : 0;
+      if (++t == end) t = first;
       const bool masked = __any_sync(0xffffffffu, from > 0);
 #pragma unroll
       for (int a = 0; a < 2; ++a)
@@ -966,6 +1001,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       }
       tmem_wait_store();
       c.arrive(DS_FULL);
+      if (c.lane == 0) mbar_arrive(c.bar(ROWS_FREE + (i & 1)));
     }
     if (ok && n > 0) ok = c.wait(DONE, 0);
     tc_fence_after();

@@ -109,6 +109,15 @@ qknr_status check_overlap(const Span* outs, int n_out, const Span* ins, int n_in
   return QKNR_OK;
 }
 
+qknr_status check_workspace(const qknr_attn_args* a, size_t need) {
+  if (need == 0) return QKNR_OK;
+  if (!a->workspace) return fail(QKNR_ERR_NULL, "workspace is required");
+  if (a->workspace_bytes < need)
+    return fail(QKNR_ERR_SHAPE, "workspace of %zu bytes, %zu needed", a->workspace_bytes, need);
+  if (!aligned16(a->workspace)) return fail(QKNR_ERR_ALIGN, "workspace not 16-byte aligned");
+  return QKNR_OK;
+}
+
 // What both passes share, once the shapes are known to be good.
 qknr_status common(const qknr_attn_args* a, qknr::AttnParams* kp) {
   if ((reinterpret_cast<uintptr_t>(a->lse) | reinterpret_cast<uintptr_t>(a->q_lens) | reinterpret_cast<uintptr_t>(a->k_lens)) & 3u)
@@ -139,6 +148,77 @@ size_t delta_bytes(const qknr_attn_args* a) {
   return (static_cast<size_t>(a->batch) * a->n_heads_q * a->seq_q * 4 + 15) / 16 * 16;
 }
 
+// How a kernel's tiles go to the CTAs, one on each SM of a GB300 (nothing here
+// needs a device; on fewer SMs CTAs queue up, none waits for another).
+constexpr int kCtas = 152;
+
+struct Cut {
+  int tiles = 0, total = 0, ctas = 0, waves = 0, rem = 0;
+  size_t part_bytes = 0, stats_bytes = 0;
+};
+
+// `rows`: rows of a tile; `blocks`: its iterations at most; `slot_rows`: fp32
+// rows of a partial result.
+Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long long blocks, int slot_rows, bool stats) {
+  Cut c;
+  c.tiles = (seq + rows - 1) / rows;
+  const long long total = static_cast<long long>(c.tiles) * heads * a->batch;
+  c.total = static_cast<int>(total);
+  c.ctas = kCtas;
+  c.waves = static_cast<int>(total / c.ctas);
+  c.rem = static_cast<int>(total % c.ctas);
+  if (c.rem == 0) return c;
+  // Sharing the last tiles out saves most of a tile's time and costs the
+  // partial results and a kernel that joins them, about as much as six
+  // iterations at head_dim 128, twelve at 64.
+  const long long cost = a->head_dim == 128 ? 6 : 12;
+  if (blocks * (c.ctas - c.rem) > cost * c.ctas) {
+    if (c.waves == 0) {
+      // no smaller shares than two iterations
+      const long long most = c.rem * blocks / 2;
+      if (most < c.ctas) c.ctas = static_cast<int>(most > c.rem ? most : c.rem);
+    }
+    if (c.ctas > c.rem) {
+      c.part_bytes = static_cast<size_t>(2 * c.ctas) * slot_rows * a->head_dim * 4;
+      c.stats_bytes = stats ? static_cast<size_t>(2 * c.ctas) * slot_rows * 8 : 0;
+      return c;
+    }
+  }
+  if (c.waves == 0) c.ctas = c.rem;
+  ++c.waves;
+  c.rem = 0;
+  return c;
+}
+
+long long blocks_of(int seq) { return (static_cast<long long>(seq) + qknr::kTile - 1) / qknr::kTile; }
+
+Cut cut_forward(const qknr_attn_args* a) {
+  return cut_tiles(a, a->seq_q, a->n_heads_q, qknr::fwd::kRows, blocks_of(a->seq_k), qknr::fwd::kRows, true);
+}
+Cut cut_dq(const qknr_attn_args* a) {
+  return cut_tiles(a, a->seq_q, a->n_heads_q, qknr::kTile, blocks_of(a->seq_k), qknr::kTile, false);
+}
+Cut cut_dkv(const qknr_attn_args* a) {
+  return cut_tiles(a, a->seq_k, a->n_heads_k, qknr::kTile, blocks_of(a->seq_q) * (a->n_heads_q / a->n_heads_k),
+                   2 * qknr::kTile, false);
+}
+
+size_t backward_bytes(const qknr_attn_args* a) {
+  const size_t q = cut_dq(a).part_bytes, kv = cut_dkv(a).part_bytes;
+  return delta_bytes(a) + (q > kv ? q : kv);      // one after the other in the same place
+}
+
+void apply(const Cut& c, qknr::AttnParams* kp, void* part) {
+  kp->tiles = c.tiles;
+  kp->total = c.total;
+  kp->waves = c.waves;
+  kp->rem = c.rem;
+  kp->part = static_cast<float*>(part);
+  kp->stats = reinterpret_cast<float*>(static_cast<char*>(part) + c.part_bytes);
+  kp->sp_part = msp(span_of(part, 1, 0, static_cast<long long>(c.part_bytes)));
+  kp->sp_stats = msp(span_of(kp->stats, 1, 0, static_cast<long long>(c.stats_bytes)));
+}
+
 qknr_status launch(const void* fn, long long grid, int block, int smem, const qknr_attn_args* a, qknr::AttnParams* kp,
                    int dev, const qknr_host::DeviceInfo& di, qknr_stream_t stream, const char* what) {
   int regs = 0;
@@ -149,8 +229,18 @@ qknr_status launch(const void* fn, long long grid, int block, int smem, const qk
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
 }
 
+// The kernel that joins partial results: a warp per row of the tiles shared out.
+qknr_status join(const void* fn, const Cut& c, int rows, const qknr_attn_args* a, qknr::AttnParams* kp, qknr_stream_t stream,
+                 const char* what) {
+  if (c.rem == 0) return QKNR_OK;
+  int ctas = c.ctas;
+  void* kargs[] = {kp, &ctas};
+  return qknr_host::launch_kernel(fn, c.rem * rows / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
+                                  !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
+}
+
 struct Kernels {
-  const void *fwd, *delta, *dq, *dkv;
+  const void *fwd, *delta, *dq, *dkv, *join_fwd, *join_dq, *join_dkv;
   int fwd_smem, dq_smem, dkv_smem;
 };
 
@@ -160,6 +250,9 @@ Kernels kernels() {
                  reinterpret_cast<const void*>(qknr::attn_delta_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dq_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dkv_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_join_forward_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_join_grad_kernel<T, D, false>),
+                 reinterpret_cast<const void*>(qknr::attn_join_grad_kernel<T, D, true>),
                  qknr::fwd::kSmem<D>, qknr::dq::kSmem<D>, qknr::dkv::kSmem<D>};
 }
 
@@ -190,7 +283,11 @@ size_t qknr_attn_sizeof_args(void) { return sizeof(qknr_attn_args); }
 qknr_status qknr_attn_workspace_bytes(const qknr_attn_args* a, size_t* bytes) {
   if (!bytes) return fail(QKNR_ERR_NULL, "bytes is NULL");
   *bytes = 0;
-  return check_shape(a);
+  const qknr_status st = check_shape(a);
+  if (st != QKNR_OK) return st;
+  const Cut c = cut_forward(a);
+  *bytes = c.part_bytes + c.stats_bytes;
+  return QKNR_OK;
 }
 
 qknr_status qknr_attn_backward_workspace_bytes(const qknr_attn_args* a, size_t* bytes) {
@@ -198,7 +295,7 @@ qknr_status qknr_attn_backward_workspace_bytes(const qknr_attn_args* a, size_t* 
   *bytes = 0;
   const qknr_status st = check_shape(a);
   if (st != QKNR_OK) return st;
-  *bytes = delta_bytes(a);
+  *bytes = backward_bytes(a);
   return QKNR_OK;
 }
 
@@ -214,14 +311,19 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
   if ((st = common(a, &kp)) != QKNR_OK) return st;
   if (a->batch == 0 || a->seq_q == 0) return QKNR_OK;
   if (!a->lse) return fail(QKNR_ERR_NULL, "lse is required");
-  const Span outs[] = {o.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)}};
+  const Cut cut = cut_forward(a);
+  const size_t need = cut.part_bytes + cut.stats_bytes;
+  if ((st = check_workspace(a, need)) != QKNR_OK) return st;
+  const Span ws = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
+  const Span outs[] = {o.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)}, ws};
   const Span ins[] = {q.span, k.span, v.span, span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)};
-  if ((st = check_overlap(outs, 2, ins, 5)) != QKNR_OK) return st;
-  if (qknr_host::overlaps(outs[0], outs[1])) return fail(QKNR_ERR_OVERLAP, "o and lse overlap");
+  if ((st = check_overlap(outs, 3, ins, 5)) != QKNR_OK) return st;
+  if (qknr_host::overlaps(outs[0], outs[1]) || qknr_host::overlaps(outs[0], ws) || qknr_host::overlaps(outs[1], ws))
+    return fail(QKNR_ERR_OVERLAP, "o, lse and the workspace overlap");
   kp.o = static_cast<char*>(a->o);
   kp.o_stride = o.stride * 2;
   kp.sp_o = msp(o.span);
-  kp.tiles = (a->seq_q + 2 * qknr::kTile - 1) / (2 * qknr::kTile);
+  apply(cut, &kp, a->workspace);
 
   int dev = 0;
   qknr_host::DeviceInfo di;
@@ -232,8 +334,9 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(a);
-  return launch(fn.fwd, static_cast<long long>(kp.tiles) * a->n_heads_q * a->batch, qknr::kAttnThreads, fn.fwd_smem, a,
-                &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
+  st = launch(fn.fwd, cut.ctas, qknr::kAttnThreads, fn.fwd_smem, a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
+  if (st != QKNR_OK) return st;
+  return join(fn.join_fwd, cut, qknr::fwd::kRows, a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
 }
 
 qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
@@ -249,11 +352,9 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
     if ((st = check_rows(a, r)) != QKNR_OK) return st;
   if ((st = common(a, &kp)) != QKNR_OK) return st;
   if (a->batch == 0 || (a->seq_q == 0 && a->seq_k == 0)) return QKNR_OK;
-  const size_t need = delta_bytes(a);
+  const size_t need = backward_bytes(a);
   if (a->seq_q > 0 && !a->lse) return fail(QKNR_ERR_NULL, "lse is required");
-  if (need && !a->workspace) return fail(QKNR_ERR_NULL, "workspace is required");
-  if (a->workspace_bytes < need) return fail(QKNR_ERR_SHAPE, "workspace of %zu bytes, %zu needed", a->workspace_bytes, need);
-  if (!aligned16(a->workspace)) return fail(QKNR_ERR_ALIGN, "workspace not 16-byte aligned");
+  if ((st = check_workspace(a, need)) != QKNR_OK) return st;
   const Span ws = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
   const Span outs[] = {dq.span, dk.span, dv.span, ws};
   const Span ins[] = {q.span, k.span, v.span, o.span, g.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)},
@@ -277,7 +378,8 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   kp.sp_dq = msp(dq.span);
   kp.sp_dk = msp(dk.span);
   kp.sp_dv = msp(dv.span);
-  kp.sp_delta = msp(ws);
+  kp.sp_delta = msp(span_of(kp.delta, 1, 0, static_cast<long long>(delta_bytes(a))));
+  void* part = static_cast<char*>(a->workspace) + delta_bytes(a);
 
   int dev = 0;
   qknr_host::DeviceInfo di;
@@ -300,15 +402,19 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
     st = qknr_host::launch_kernel(fn.delta, static_cast<int>(grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), "cudaLaunchKernelExC(attention delta)");
     if (st != QKNR_OK) return st;
-    kp.tiles = (a->seq_q + qknr::kTile - 1) / qknr::kTile;
-    st = launch(fn.dq, static_cast<long long>(kp.tiles) * a->n_heads_q * a->batch, qknr::kAttnThreads, fn.dq_smem, a, &kp,
-                dev, di, stream, "cudaLaunchKernelExC(attention dq)");
+    const Cut cut = cut_dq(a);
+    apply(cut, &kp, part);
+    st = launch(fn.dq, cut.ctas, qknr::kAttnThreads, fn.dq_smem, a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention dq)");
+    if (st != QKNR_OK) return st;
+    st = join(fn.join_dq, cut, qknr::kTile, a, &kp, stream, "cudaLaunchKernelExC(attention dq, joining)");
     if (st != QKNR_OK) return st;
   }
   if (a->seq_k == 0) return QKNR_OK;
-  kp.tiles = (a->seq_k + qknr::kTile - 1) / qknr::kTile;
-  return launch(fn.dkv, static_cast<long long>(kp.tiles) * a->n_heads_k * a->batch, qknr::kAttnThreads, fn.dkv_smem, a, &kp,
-                dev, di, stream, "cudaLaunchKernelExC(attention dk, dv)");
+  const Cut cut = cut_dkv(a);
+  apply(cut, &kp, part);
+  st = launch(fn.dkv, cut.ctas, qknr::kAttnThreads, fn.dkv_smem, a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention dk, dv)");
+  if (st != QKNR_OK) return st;
+  return join(fn.join_dkv, cut, 2 * qknr::kTile, a, &kp, stream, "cudaLaunchKernelExC(attention dk, dv, joining)");
 }
 
 }  // extern "C"

@@ -11,7 +11,14 @@
 // 128 lanes of tensor memory (a thread owns one row of a score tile), warp 8
 // issues the MMAs, warp 9 the TMA loads, warps 10 and 11 fill up the third
 // group, whose registers go to the first two (and hand round the queries'
-// statistics in the dk, dv kernel).  Every wait is bounded; a role that
+// statistics in the dk, dv kernel).
+//
+// Persistent CTAs, one per SM.  Tile w of CTA c is tile w * CTAs + c, so that
+// CTAs next to each other read the same keys; the tiles left over after the
+// last full wave are cut along their contraction into as many equal parts as
+// there are CTAs, whose fp32 partial results attn_join_*_kernel adds in a
+// fixed order.  A tile's loads, its first products and the previous tile's
+// epilogue overlap.  Every wait is bounded; a role that
 // gives up sets the CTA's abort flag, drains what it started and leaves.
 #pragma once
 
@@ -36,10 +43,15 @@ struct AttnParams {
   int causal;
   float scale, scale_log2;
   int tiles;                  // row tiles of a head
+  int total;                  // tiles in all
+  int waves;                  // whole tiles per CTA
+  int rem;                    // tiles after those, shared out among all CTAs
+  float* part;                // their partial results, two slots per CTA
+  float* stats;               // forward: (maximum, sum) of the slots' rows
   unsigned flags;
   int* status;
   unsigned long long wait_limit_ns;
-  MemSpan sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens;
+  MemSpan sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
 };
 
 constexpr int kAttnThreads = 384;
@@ -151,6 +163,22 @@ struct AttnCta {
   __device__ __forceinline__ bool wait(int i, uint32_t phase) const {
     return __all_sync(0xffffffffu, wait1(i, phase));
   }
+  // One thread, giving up: the last `n` of `issued` copies into a ring of n
+  // stages end before the CTA leaves its shared memory.
+  __device__ __forceinline__ void drain(int full, int n, int issued) const {
+    const unsigned long long t0 = global_timer_ns();
+    for (int i = issued > n ? issued - n : 0; i < issued; ++i)
+      while (!mbar_try_wait(bar(full + i % n), static_cast<uint32_t>(i / n) & 1u) && global_timer_ns() - t0 < limit) {
+      }
+  }
+  // Whole warp, giving up: the MMAs in flight end before tensor memory is given back.
+  __device__ __forceinline__ void drain_mma(int i) const {
+    if (elect_one()) mma_commit(bar(i));
+    const unsigned long long t0 = global_timer_ns();
+    while (!mbar_try_wait(bar(i), 0) && global_timer_ns() - t0 < limit) {
+    }
+    __syncwarp();
+  }
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
   // a warp's arrival after its tensor memory accesses
   __device__ __forceinline__ void arrive(int i) const {
@@ -159,6 +187,57 @@ struct AttnCta {
     if (lane == 0) mbar_arrive(bar(i));
   }
 };
+
+// One piece of a CTA's work: a tile and which part of its contraction, in
+// 1024ths; `slot` is where a partial result goes (-1: the tile is whole).
+constexpr int kUnits = 1024;
+struct AttnWork {
+  int tile, u0, u1, slot;
+};
+
+// first unit of CTA c's share of the tiles left over
+__device__ __forceinline__ long long attn_share(const AttnParams& p, long long c, int ctas) {
+  return c * p.rem * kUnits / ctas;
+}
+
+__device__ __forceinline__ bool attn_work(const AttnParams& p, int s, AttnWork& w) {
+  const int n = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+  if (s < p.waves) {
+    w = AttnWork{s * n + c, 0, kUnits, -1};
+    return w.tile < p.total;
+  }
+  const int k = s - p.waves;
+  if (p.rem == 0 || k > 1) return false;
+  const long long v0 = attn_share(p, c, n), v1 = attn_share(p, c + 1, n);
+  const int r = static_cast<int>(v0 / kUnits) + k;
+  const long long lo = v0 > static_cast<long long>(r) * kUnits ? v0 : static_cast<long long>(r) * kUnits;
+  const long long hi = v1 < static_cast<long long>(r + 1) * kUnits ? v1 : static_cast<long long>(r + 1) * kUnits;
+  if (lo >= hi) return false;
+  w = AttnWork{p.waves * n + r, static_cast<int>(lo - static_cast<long long>(r) * kUnits),
+               static_cast<int>(hi - static_cast<long long>(r) * kUnits), 2 * c + k};
+  return true;
+}
+
+// The tile's place.  Without a causal mask the tiles of a head follow each
+// other; with one, tiles of the same cost do (`heavy_last`: the later rows
+// cost more), the costly ones first.
+struct AttnPlace {
+  int t, h, b;
+};
+__device__ __forceinline__ AttnPlace attn_place(const AttnParams& p, int tile, int heads, bool heavy_last) {
+  if (p.causal) {
+    const int per = heads * p.batch, t = tile / per, r = tile - t * per;
+    return AttnPlace{heavy_last ? p.tiles - 1 - t : t, r % heads, r / heads};
+  }
+  const int r = tile / p.tiles;
+  return AttnPlace{tile - r * p.tiles, r % heads, r / heads};
+}
+
+// iterations [begin, end) of n that a piece takes
+__device__ __forceinline__ void attn_cut(const AttnWork& w, int n, int& begin, int& end) {
+  begin = static_cast<int>(static_cast<long long>(n) * w.u0 / kUnits);
+  end = static_cast<int>(static_cast<long long>(n) * w.u1 / kUnits);
+}
 
 // 16 bytes of a row at a time: 32 accumulator values from tensor memory to
 // their place in a row of the output, times f (zero where the row has no value)
@@ -175,33 +254,55 @@ __device__ __forceinline__ void store_cols(char* dst, const float (&v)[32], floa
   }
 }
 
+// the same values as a partial result
+__device__ __forceinline__ void store_part(float* dst, const float (&v)[32], bool some) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    reinterpret_cast<float4*>(dst)[c] =
+        some ? make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+
 // ---------------------------------------------------------------------------
-// forward: a CTA takes 256 queries of one head as two tiles whose softmaxes
+// forward: a tile is 256 queries of one head, two halves whose softmaxes
 // alternate with each other's products.
 
 namespace fwd {
-constexpr int kStages = 4;                        // K and V tiles in flight, in turn
-enum { Q_FULL = 0, KV_FULL = 2, KV_EMPTY = KV_FULL + kStages, S_FULL = KV_EMPTY + kStages, P_FULL = S_FULL + 2,
-       O_DONE = P_FULL + 2, DRAIN = O_DONE + 2, BARS = DRAIN + 1 };
+constexpr int kRows = 2 * kTile;
+constexpr int kK = 2, kV = 2;                     // K and V tiles in flight
+enum { Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
+       S_FULL = V_EMPTY + kV, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, O_FREE = O_DONE + 2, DRAIN = O_FREE + 2, BARS };
+__device__ __forceinline__ int arrivals(int i) {
+  return (i >= P_FULL && i < O_DONE) || (i >= O_FREE && i < DRAIN) ? 4 : 1;
+}
 template <int D>
-constexpr int kSmem = (2 + kStages) * kTileBytes<D> + 256;
+constexpr int kCtl = (2 + kK + kV) * kTileBytes<D>;
+template <int D>
+constexpr int kSmem = kCtl<D> + 256;
 // The running maximum is only raised, and the accumulator rescaled, when the
 // new one is more than 2^8 above: p stays below 2^8, which 16-bit floats and
 // the fp32 sums hold as exactly as values below one.
 constexpr float kSlack = 8.0f;
+
+struct Seg {
+  int b, h, q0, slot;
+  int q_len, k_len, diag;     // causal: query i sees keys up to i + diag
+  int begin;                  // first key block
+  int nb[2];                  // key blocks of each half
+  int blocks;
+};
 }  // namespace fwd
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __grid_constant__ AttnParams p) {
   using namespace fwd;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* ctl = smem + (2 + kStages) * kTileBytes<D>;
+  unsigned char* ctl = smem + kCtl<D>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
-  AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
+  const AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
+                  __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i >= P_FULL && i < O_DONE ? 4 : 1);
+    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), arrivals(i));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -211,204 +312,259 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
+  grid_dependents_launch();
 
-  const int tile = p.causal ? p.tiles - 1 - static_cast<int>(blockIdx.x % p.tiles) : static_cast<int>(blockIdx.x % p.tiles);
-  const int h = static_cast<int>(blockIdx.x / p.tiles % p.heads_q), b = static_cast<int>(blockIdx.x / p.tiles / p.heads_q);
-  const int q0 = tile * 2 * kTile;
-  const int q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
-  const int k_len = clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
-  const int diag = k_len - q_len;                 // causal: query i sees keys up to i + diag
-  int nb[2];                                      // key blocks of each query tile
+  auto segment = [&](int s, Seg& g) {
+    AttnWork w;
+    if (!attn_work(p, s, w)) return false;
+    const AttnPlace at = attn_place(p, w.tile, p.heads_q, true);
+    g.b = at.b;
+    g.h = at.h;
+    g.q0 = at.t * kRows;
+    g.slot = w.slot;
+    g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
+    g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    g.diag = g.k_len - g.q_len;
+    int nb[2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int first = q0 + t * kTile;
-    int last = first + kTile < q_len ? first + kTile : q_len;
-    int keys = first >= q_len ? 0 : (p.causal ? last + diag : k_len);
-    keys = keys < 0 ? 0 : (keys > k_len ? k_len : keys);
-    nb[t] = (keys + kTile - 1) / kTile;
-  }
-  const int blocks = nb[0] > nb[1] ? nb[0] : nb[1];
-  const uint32_t ring = c.base + 2 * kTileBytes<D>;
+    for (int t = 0; t < 2; ++t) {
+      const int first = g.q0 + t * kTile, last = first + kTile < g.q_len ? first + kTile : g.q_len;
+      int keys = first >= g.q_len ? 0 : (p.causal ? last + g.diag : g.k_len);
+      keys = keys < 0 ? 0 : (keys > g.k_len ? g.k_len : keys);
+      nb[t] = (keys + kTile - 1) / kTile;
+    }
+    int end;
+    attn_cut(w, nb[0] > nb[1] ? nb[0] : nb[1], g.begin, end);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int last = nb[t] < end ? nb[t] : end;
+      g.nb[t] = last > g.begin ? last - g.begin : 0;
+    }
+    g.blocks = g.nb[0] > g.nb[1] ? g.nb[0] : g.nb[1];
+    return true;
+  };
+  const uint32_t sk = c.base + 2 * kTileBytes<D>, sv = c.base + (2 + kK) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
   if (c.warp == kAttnLoadWarp) {
-    if (c.lane == 0 && blocks > 0) {
-      const int hk = h / p.group;
-      int issued = 0;
-      bool ok = !(p.flags & 1u);                  // test only: issue nothing
-      if (ok) {
-        for (int t = 0; t < 2; ++t) {
-          if (nb[t] == 0) continue;
+    if (c.lane == 0 && !(p.flags & 1u)) {         // test only: issue nothing
+      RingPos<kK> k;
+      RingPos<kV> v;
+      int uses[2] = {0, 0}, ik = 0, iv = 0;
+      bool ok = true;
+      Seg g;
+      for (int s = 0; ok && segment(s, g); ++s) {
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (g.nb[t] == 0) continue;
+          ok = c.wait1(Q_EMPTY + t, uses[t] + 1);
+          if (!ok) break;
           mbar_arrive_expect_tx(c.bar(Q_FULL + t), kTileBytes<D>);
-          tma_load_tile(c.base + t * kTileBytes<D>, &p.map_q, q0 + t * kTile, h, b, c.bar(Q_FULL + t));
+          tma_load_tile(c.base + t * kTileBytes<D>, &p.map_q, g.q0 + t * kTile, g.h, g.b, c.bar(Q_FULL + t));
+          ++uses[t];
         }
-        for (int i = 0; i < 2 * blocks; ++i) {
-          const int s = i % kStages;
-          if (!c.wait1(KV_EMPTY + s, (i / kStages + 1) & 1)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(c.bar(KV_FULL + s), kTileBytes<D>);
-          tma_load_tile(ring + s * kTileBytes<D>, i & 1 ? &p.map_v : &p.map_k, (i / 2) * kTile, hk, b, c.bar(KV_FULL + s));
-          ++issued;
+        const int hk = g.h / p.group;
+        for (int j = 0; ok && j < g.blocks; ++j, k.step(), v.step()) {
+          ok = c.wait1(K_EMPTY + k.s, k.phase ^ 1u);
+          if (!ok) break;
+          mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
+          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
+          ++ik;
+          ok = c.wait1(V_EMPTY + v.s, v.phase ^ 1u);
+          if (!ok) break;
+          mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
+          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
+          ++iv;
         }
       }
       if (!ok || *abort_flag) {
-        // copies in flight end before the CTA leaves its shared memory
-        const unsigned long long t0 = global_timer_ns();
-        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          while (!mbar_try_wait(c.bar(KV_FULL + i % kStages), (i / kStages) & 1) && global_timer_ns() - t0 < c.limit) {
-          }
-        for (int t = 0; t < 2; ++t)
-          while (!(p.flags & 1u) && nb[t] && !mbar_try_wait(c.bar(Q_FULL + t), 0) && global_timer_ns() - t0 < c.limit) {
-          }
+        c.drain(K_FULL, kK, ik);
+        c.drain(V_FULL, kV, iv);
+        c.drain(Q_FULL, 1, uses[0]);
+        c.drain(Q_FULL + 1, 1, uses[1]);
       }
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
     // S_t(0), then per block: O_t += P_t V, S_t(next)
-    bool ok = blocks > 0;
-    for (int t = 0; t < 2 && ok; ++t)
-      if (nb[t]) ok = c.wait(Q_FULL + t, 0);
-    ok = ok && c.wait(KV_FULL, 0);
-    tc_fence_after();
-    if (ok && elect_one()) {
-      for (int t = 0; t < 2; ++t)
-        if (nb[t]) {
-          mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, ring);
-          mma_commit(c.bar(S_FULL + t));
-        }
-      mma_commit(c.bar(KV_EMPTY));
-    }
-    for (int j = 0; ok && j < blocks; ++j) {
-      const int iv = 2 * j + 1, ik = 2 * j + 2, sv = iv % kStages, sk = ik % kStages;
-      ok = c.wait(KV_FULL + sv, iv / kStages);
+    RingPos<kK> k;
+    RingPos<kV> v;
+    int uses[2] = {0, 0}, done[2] = {0, 0};       // tiles, blocks of each half so far
+    bool ok = true;
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      if (g.blocks == 0) continue;
+      for (int t = 0; t < 2 && ok; ++t)
+        if (g.nb[t]) ok = c.wait(Q_FULL + t, uses[t]);
+      ok = ok && c.wait(K_FULL + k.s, k.phase);
       if (!ok) break;
-      if (k_len < p.seq_k && (j + 1) * kTile > k_len)
-        zero_rows<D>(smem + (2 + sv) * kTileBytes<D>, k_len - j * kTile, c.lane);
-      if (j + 1 < blocks) ok = c.wait(KV_FULL + sk, ik / kStages);
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (ok && j < nb[t]) {
-          ok = c.wait(P_FULL + t, j);
-          tc_fence_after();
-          if (ok && elect_one()) {
-            mma_cols<T, D, false>(tmem + 2 * kTile + t * kTile, tmem + t * kTile, ring + sv * kTileBytes<D>, j > 0);
-            mma_commit(c.bar(O_DONE + t));
+        for (int t = 0; t < 2; ++t)
+          if (g.nb[t]) {
+            mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
+            mma_commit(c.bar(S_FULL + t));
+            if (g.nb[t] == 1) mma_commit(c.bar(Q_EMPTY + t));
+          }
+        mma_commit(c.bar(K_EMPTY + k.s));
+      }
+      k.step();
+      for (int j = 0; ok && j < g.blocks; ++j) {
+        ok = c.wait(V_FULL + v.s, v.phase);
+        if (!ok) break;
+        if (g.k_len < p.seq_k && (g.begin + j + 1) * kTile > g.k_len)
+          zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+        if (j + 1 < g.blocks) ok = c.wait(K_FULL + k.s, k.phase);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && j < g.nb[t]) {
+            // the accumulator has been read for the tile before
+            if (j == 0 && uses[t] > 0) ok = c.wait(O_FREE + t, uses[t] - 1);
+            ok = ok && c.wait(P_FULL + t, done[t]);
+            ++done[t];
+            tc_fence_after();
+            if (ok && elect_one()) {
+              mma_cols<T, D, false>(tmem + 2 * kTile + t * kTile, tmem + t * kTile, sv + v.s * kTileBytes<D>, j > 0);
+              mma_commit(c.bar(O_DONE + t));
+            }
+          }
+          if (t == 1 && ok && elect_one()) mma_commit(c.bar(V_EMPTY + v.s));
+          if (ok && j + 1 < g.nb[t] && elect_one()) {
+            mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
+            mma_commit(c.bar(S_FULL + t));
+            if (j + 2 == g.nb[t]) mma_commit(c.bar(Q_EMPTY + t));
           }
         }
-        if (t == 1 && ok && elect_one()) mma_commit(c.bar(KV_EMPTY + sv));
-        if (ok && elect_one() && j + 1 < nb[t]) {
-          mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, ring + sk * kTileBytes<D>);
-          mma_commit(c.bar(S_FULL + t));
+        v.step();
+        if (j + 1 < g.blocks) {
+          if (ok && elect_one()) mma_commit(c.bar(K_EMPTY + k.s));
+          k.step();
         }
       }
-      if (ok && elect_one() && j + 1 < blocks) mma_commit(c.bar(KV_EMPTY + sk));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) uses[t] += g.nb[t] > 0;
     }
-    if (!ok && blocks > 0) {
-      // MMAs in flight end before tensor memory is given back
-      if (elect_one()) mma_commit(c.bar(DRAIN));
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
-      }
-    }
-    __syncwarp();
+    if (!ok) c.drain_mma(DRAIN);
   } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // softmax: a thread per query
-    const int t = c.warp >> 2, n = nb[t];
-    const int row = q0 + t * kTile + (c.warp & 3) * 32 + c.lane;
+    const int t = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * kTile + lanes;
-    int limit = row < q_len ? (p.causal ? row + diag + 1 : k_len) : 0;   // keys this query sees
-    limit = limit < 0 ? 0 : (limit > k_len ? k_len : limit);
     const float sl = p.scale_log2, slack = kSlack / sl;
-    float m = -INFINITY;
-    float2 sum = make_float2(0.0f, 0.0f);
+    int done = 0;                                 // blocks so far
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = c.wait(S_FULL + t, j);
-      if (!ok) break;
-      tc_fence_after();
-      float s[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_load32(ts + 32 * i, s[i]);
-      tmem_wait_load(s[0]);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) tmem_loaded(s[i]);
-      const int seen = limit - j * kTile;
-      if (__any_sync(0xffffffffu, seen < kTile)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[i][e] = 32 * i + e < seen ? s[i][e] : -INFINITY;
+    Seg g;
+    for (int sg = 0; ok && segment(sg, g); ++sg) {
+      const int n = t ? g.nb[1] : g.nb[0];
+      int limit;                                  // keys from the first block on that this query sees
+      {
+        const int row = g.q0 + t * kTile + r;
+        limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
+        limit = (limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit)) - g.begin * kTile;
       }
-      float mx[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mx[i] = fmaxf(s[i][0], s[i][1]);
-#pragma unroll
-        for (int e = 2; e < 32; e += 2) mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = top;
-      } else if (__any_sync(0xffffffffu, top > m + slack)) {
-        const float raised = fmaxf(m, top);
-        const float f = raised == m ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(m, raised), sl));
-        m = raised;
-        sum = __fmul2_rn(sum, make_float2(f, f));
-        ok = c.wait(O_DONE + t, j - 1);
+      float m = -INFINITY;
+      float2 sum = make_float2(0.0f, 0.0f);
+      for (int j = 0; j < n; ++j, ++done) {
+        ok = c.wait(S_FULL + t, done);
         if (!ok) break;
         tc_fence_after();
+        float s[4][32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float o[32];
-          tmem_load32(to + 32 * i, o);
-          tmem_wait_load(o);
+        for (int i = 0; i < 4; ++i) tmem_load32(ts + 32 * i, s[i]);
+        tmem_wait_load(s[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __fmul_rn(o[e], f);
-          tmem_store32(to + 32 * i, o);
+        for (int i = 1; i < 4; ++i) tmem_loaded(s[i]);
+        const int seen = limit - j * kTile;
+        if (__any_sync(0xffffffffu, seen < kTile)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[i][e] = 32 * i + e < seen ? s[i][e] : -INFINITY;
         }
-      }
-      // a row that has seen nothing yet: exp2(-inf - 0) = 0
-      const float shift = m == -INFINITY ? 0.0f : __fmul_rn(-m, sl);
-      const float2 SL = make_float2(sl, sl), SH = make_float2(shift, shift);
+        float mx[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[16];
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = fmaxf(s[i][0], s[i][1]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = __ffma2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]), SL, SH);
-          const float2 y = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-          sum = __fadd2_rn(sum, y);
-          w[e] = pack2<T>(y.x, y.y);
+          for (int e = 2; e < 32; e += 2) mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
         }
-        tmem_store16(ts + 16 * i, w);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (j == 0) {
+          m = top;
+        } else if (__any_sync(0xffffffffu, top > m + slack)) {
+          const float raised = fmaxf(m, top);
+          const float f = raised == m ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(m, raised), sl));
+          m = raised;
+          sum = __fmul2_rn(sum, make_float2(f, f));
+          ok = c.wait(O_DONE + t, done - 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t o[16];
+            tmem_fetch16(to + 16 * i, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__fmul_rn(__uint_as_float(o[e]), f));
+            tmem_store16(to + 16 * i, o);
+          }
+        }
+        // a row that has seen nothing yet: exp2(-inf - 0) = 0
+        const float shift = m == -INFINITY ? 0.0f : __fmul_rn(-m, sl);
+        const float2 SL = make_float2(sl, sl), SH = make_float2(shift, shift);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]), SL, SH);
+            const float2 y = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum = __fadd2_rn(sum, y);
+            w[e] = pack2<T>(y.x, y.y);
+          }
+          tmem_store16(ts + 16 * i, w);
+        }
+        tmem_wait_store();
+        c.arrive(P_FULL + t);
       }
-      tmem_wait_store();
-      c.arrive(P_FULL + t);
-    }
-    if (ok && n > 0) ok = c.wait(O_DONE + t, n - 1);
-    tc_fence_after();
-    const float total = __fadd_rn(sum.x, sum.y);
-    const bool some = total != 0.0f;
-    const float inv = some ? __frcp_rn(total) : 0.0f;
-    const bool mine = row < p.seq_q;
-    if (ok) {
-      const long long at = (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + row;
-      if (mine && in_span(p.lse + at, 4, p.sp_lse, p.status))
-        p.lse[at] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
-      char* dst = p.o + (static_cast<long long>(b) * p.seq_q + row) * p.o_stride + h * (D * 2);
-      const bool fits = mine && in_span(dst, D * 2, p.sp_o, p.status);
+      if (!ok) break;
+      if (n > 0) {
+        ok = c.wait(O_DONE + t, done - 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const float total = __fadd_rn(sum.x, sum.y);
+      const bool some = total != 0.0f;
+      const float inv = some ? __frcp_rn(total) : 0.0f;
+      segment(sg, g);                             // again: the loop above has no registers to keep it in
+      const int row = g.q0 + t * kTile + r;
+      char* dst = p.o + (static_cast<long long>(g.b) * p.seq_q + row) * p.o_stride + g.h * (D * 2);
+      const long long at = static_cast<long long>(g.slot) * kRows + t * kTile + r;   // a part's row
+      bool fits;
+      if (g.slot >= 0) {
+        // a part of the keys: unnormalised, with its maximum and sum
+        if (in_span(p.stats + 2 * at, 8, p.sp_stats, p.status))
+          *reinterpret_cast<float2*>(p.stats + 2 * at) = make_float2(m, total);
+        fits = in_span(p.part + at * D, 4 * D, p.sp_part, p.status);
+      } else {
+        const long long l = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
+        if (row < p.seq_q && in_span(p.lse + l, 4, p.sp_lse, p.status))
+          p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
+        fits = row < p.seq_q && in_span(dst, D * 2, p.sp_o, p.status);
+      }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
         if (n > 0) {
           tmem_load32(to + 32 * i, o);
           tmem_wait_load(o);
+          if (i == D / 32 - 1) c.arrive(O_FREE + t);
         }
-        if (fits) store_cols<T>(dst + 64 * i, o, inv, some);
+        if (!fits) continue;
+        if (g.slot >= 0)
+          store_part(p.part + at * D + 32 * i, o, n > 0);
+        else
+          store_cols<T>(dst + 64 * i, o, inv, some);
       }
     }
     tc_fence_before();
@@ -418,7 +574,73 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     tc_fence_after();
     tmem_free(tmem, 512);
   }
-  grid_dependents_launch();
+}
+
+// The parts of tile r that was shared out: the first CTA with one, and how
+// many there are; part i's slot is slot(i).
+struct AttnParts {
+  int first, count, r;
+  long long unit0;
+  __device__ __forceinline__ AttnParts(const AttnParams& p, int r_, int ctas) : r(r_) {
+    unit0 = static_cast<long long>(r) * kUnits;
+    int c = static_cast<int>(static_cast<long long>(r) * ctas / p.rem);
+    while (c > 0 && attn_share(p, c, ctas) > unit0) --c;
+    while (attn_share(p, c + 1, ctas) <= unit0) ++c;
+    first = c;
+    while (c < ctas && attn_share(p, c, ctas) < unit0 + kUnits) ++c;
+    count = c - first;
+  }
+  __device__ __forceinline__ int slot(const AttnParams& p, int i, int ctas) const {
+    const int c = first + i;
+    return 2 * c + (r - static_cast<int>(attn_share(p, c, ctas) / kUnits));
+  }
+};
+
+// Joins the parts of the tiles that were shared out: a warp per query row.
+//   o = sum_i w_i o_i / sum_i w_i l_i,  w_i = exp2((m_i - max m) scale)
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int kRows = fwd::kRows;
+  const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  if (item >= p.rem * kRows) return;
+  const int r = item / kRows, q = item % kRows;
+  const AttnPlace at = attn_place(p, p.waves * ctas + r, p.heads_q, true);
+  const int row = at.t * kRows + q;
+  if (row >= p.seq_q) return;
+  const AttnParts parts(p, r, ctas);
+  float m = -INFINITY;
+  for (int i = 0; i < parts.count; ++i) {
+    const float* st = p.stats + (static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q) * 2;
+    if (in_span(st, 8, p.sp_stats, p.status)) m = fmaxf(m, *st);
+  }
+  float total = 0.0f;
+  float2 acc[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < parts.count; ++i) {
+    const long long k = static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q;
+    if (!in_span(p.stats + 2 * k, 8, p.sp_stats, p.status) || !in_span(p.part + k * D, 4 * D, p.sp_part, p.status)) continue;
+    const float2 st = *reinterpret_cast<const float2*>(p.stats + 2 * k);
+    // a part that saw no key has sum 0 and maximum -inf
+    const float w = st.x == m ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(st.x, m), p.scale_log2));
+    if (st.y == 0.0f) continue;
+    total = __fmaf_rn(w, st.y, total);
+    const float2* src = reinterpret_cast<const float2*>(p.part + k * D) + lane;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) acc[e] = __ffma2_rn(make_float2(w, w), src[32 * e], acc[e]);
+  }
+  const bool some = total != 0.0f;
+  const float inv = some ? __frcp_rn(total) : 0.0f;
+  const long long l = (static_cast<long long>(at.b) * p.heads_q + at.h) * p.seq_q + row;
+  if (lane == 0 && in_span(p.lse + l, 4, p.sp_lse, p.status))
+    p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
+  char* dst = p.o + (static_cast<long long>(at.b) * p.seq_q + row) * p.o_stride + at.h * (D * 2);
+  if (!in_span(dst, D * 2, p.sp_o, p.status)) return;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    reinterpret_cast<uint32_t*>(dst)[lane + 32 * e] =
+        some ? pack2<T>(__fmul_rn(acc[e].x, inv), __fmul_rn(acc[e].y, inv)) : 0u;
 }
 
 // ---------------------------------------------------------------------------
@@ -485,29 +707,40 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------------------
-// backward, dq: a CTA takes 128 queries of one head and walks their keys.
-// Per block S = Q K^T, dP = dO V^T, dQ += dS K.  The scores have two buffers,
-// so the next block's S is there when this block's dS is done.
+// backward, dq: a tile is 128 queries of one head, its iterations blocks of
+// 128 keys.  Per block S = Q K^T, dP = dO V^T, dQ += dS K.  The scores have
+// two buffers, so the next block's S is there when this block's dS is done.
 
 namespace dq {
 constexpr int kK = 3, kV = 2;                     // K and V tiles in flight
-enum { Q_FULL = 0, K_FULL = 1, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
-       S_FULL = V_EMPTY + kV, DP_FULL = S_FULL + 2, DP_FREE, DS_FULL, DONE, DRAIN, BARS };
+enum { Q_FULL = 0, Q_EMPTY, O_FULL, O_EMPTY, K_FULL, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK,
+       V_EMPTY = V_FULL + kV, S_FULL = V_EMPTY + kV, DP_FULL = S_FULL + 2, DP_FREE, DS_FULL, DONE = DS_FULL + 2, ACC_FREE, DRAIN, BARS };
+// DS_FULL has a barrier per score buffer: the next block's dS can be there
+// before the issuing warp has looked for this block's.
+__device__ __forceinline__ int arrivals(int i) { return (i >= DP_FREE && i < DONE) || i == ACC_FREE ? 8 : 1; }
 template <int D>
-constexpr int kSmem = (2 + kK + kV) * kTileBytes<D> + 256;
+constexpr int kCtl = (2 + kK + kV) * kTileBytes<D>;
+template <int D>
+constexpr int kSmem = kCtl<D> + 256;
+
+struct Seg {
+  int b, h, q0, slot;
+  int q_len, k_len, diag;
+  int begin, n;               // key blocks [begin, begin + n)
+};
 }  // namespace dq
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_constant__ AttnParams p) {
   using namespace dq;
   extern __shared__ __align__(1024) unsigned char smem[];
-  unsigned char* ctl = smem + (2 + kK + kV) * kTileBytes<D>;
+  unsigned char* ctl = smem + kCtl<D>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
-  AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
+  const AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
+                  __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == DP_FREE || i == DS_FULL ? 8 : 1);
+    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), arrivals(i));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -517,204 +750,239 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
+  grid_dependents_launch();
 
-  const int tile = p.causal ? p.tiles - 1 - static_cast<int>(blockIdx.x % p.tiles) : static_cast<int>(blockIdx.x % p.tiles);
-  const int h = static_cast<int>(blockIdx.x / p.tiles % p.heads_q), b = static_cast<int>(blockIdx.x / p.tiles / p.heads_q);
-  const int q0 = tile * kTile;
-  const int q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
-  const int k_len = clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
-  const int diag = k_len - q_len;
-  const int last = q0 + kTile < q_len ? q0 + kTile : q_len;
-  int keys = q0 >= q_len ? 0 : (p.causal ? last + diag : k_len);
-  keys = keys < 0 ? 0 : (keys > k_len ? k_len : keys);
-  const int n = (keys + kTile - 1) / kTile;
+  auto segment = [&](int s, Seg& g) {
+    AttnWork w;
+    if (!attn_work(p, s, w)) return false;
+    const AttnPlace at = attn_place(p, w.tile, p.heads_q, true);
+    g.b = at.b;
+    g.h = at.h;
+    g.q0 = at.t * kTile;
+    g.slot = w.slot;
+    g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
+    g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    g.diag = g.k_len - g.q_len;
+    const int last = g.q0 + kTile < g.q_len ? g.q0 + kTile : g.q_len;
+    int keys = g.q0 >= g.q_len ? 0 : (p.causal ? last + g.diag : g.k_len);
+    keys = keys < 0 ? 0 : (keys > g.k_len ? g.k_len : keys);
+    int end;
+    attn_cut(w, (keys + kTile - 1) / kTile, g.begin, end);
+    g.n = end - g.begin;
+    return true;
+  };
   const uint32_t sq = c.base, sdo = c.base + kTileBytes<D>, sk = c.base + 2 * kTileBytes<D>,
                  sv = c.base + (2 + kK) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
   if (c.warp == kAttnLoadWarp) {
-    if (c.lane == 0 && n > 0) {
-      const int hk = h / p.group;
-      int ik = 0, iv = 0;
-      bool ok = !(p.flags & 1u);
-      if (ok) {
-        mbar_arrive_expect_tx(c.bar(Q_FULL), 2 * kTileBytes<D>);
-        tma_load_tile(sq, &p.map_q, q0, h, b, c.bar(Q_FULL));
-        tma_load_tile(sdo, &p.map_do, q0, h, b, c.bar(Q_FULL));
-        RingPos<kK> k;
-        RingPos<kV> v;
-        for (int j = 0; j < n; ++j, k.step(), v.step()) {
+    if (c.lane == 0 && !(p.flags & 1u)) {         // test only: issue nothing
+      RingPos<kK> k;
+      RingPos<kV> v;
+      int uses = 0, ik = 0, iv = 0, io = 0;
+      bool ok = true;
+      Seg g;
+      for (int s = 0; ok && segment(s, g); ++s) {
+        if (g.n == 0) continue;
+        ok = c.wait1(Q_EMPTY, uses + 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(c.bar(Q_FULL), kTileBytes<D>);
+        tma_load_tile(sq, &p.map_q, g.q0, g.h, g.b, c.bar(Q_FULL));
+        ++uses;
+        const int hk = g.h / p.group;
+        for (int j = 0; ok && j < g.n; ++j, k.step(), v.step()) {
           ok = c.wait1(K_EMPTY + k.s, k.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
-          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, j * kTile, hk, b, c.bar(K_FULL + k.s));
+          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
           ++ik;
+          if (j == 0) {
+            ok = c.wait1(O_EMPTY, uses);
+            if (!ok) break;
+            mbar_arrive_expect_tx(c.bar(O_FULL), kTileBytes<D>);
+            tma_load_tile(sdo, &p.map_do, g.q0, g.h, g.b, c.bar(O_FULL));
+            ++io;
+          }
           ok = c.wait1(V_EMPTY + v.s, v.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
-          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, j * kTile, hk, b, c.bar(V_FULL + v.s));
+          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
           ++iv;
         }
       }
       if (!ok || *abort_flag) {
-        const unsigned long long t0 = global_timer_ns();
-        for (int i = ik > kK ? ik - kK : 0; i < ik; ++i)
-          while (!mbar_try_wait(c.bar(K_FULL + i % kK), (i / kK) & 1) && global_timer_ns() - t0 < c.limit) {
-          }
-        for (int i = iv > kV ? iv - kV : 0; i < iv; ++i)
-          while (!mbar_try_wait(c.bar(V_FULL + i % kV), (i / kV) & 1) && global_timer_ns() - t0 < c.limit) {
-          }
-        while (!(p.flags & 1u) && !mbar_try_wait(c.bar(Q_FULL), 0) && global_timer_ns() - t0 < c.limit) {
-        }
+        c.drain(K_FULL, kK, ik);
+        c.drain(V_FULL, kV, iv);
+        c.drain(Q_FULL, 1, uses);
+        c.drain(O_FULL, 1, io);
       }
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
-    bool ok = n > 0;
-    const bool ragged = k_len < p.seq_k;
     // Blocks whose scores, dP and dQ products come next, and their stages.
     RingPos<kK> ks, kd;
     RingPos<kV> vs;
-    int js = 0, jv = 0;
-    // the block's K (V) has landed, with nothing past the sample's keys
-    auto have = [&](int full, int tile_at, uint32_t phase, int j) {
-      const bool got = c.wait(full, phase);
-      if (got && ragged && (j + 1) * kTile > k_len)
-        zero_rows<D>(smem + tile_at * kTileBytes<D>, k_len - j * kTile, c.lane);
-      return got;
-    };
-    auto scores = [&]() {
-      if (!have(K_FULL + ks.s, 2 + ks.s, ks.phase, js)) return false;
-      if (elect_one()) {
-        mma_rows<T, D>(tmem + (js & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
-        mma_commit(c.bar(S_FULL + (js & 1)));
-      }
-      ks.step();
-      ++js;
-      return true;
-    };
-    auto grads = [&]() {
-      if (!have(V_FULL + vs.s, 2 + kK + vs.s, vs.phase, jv)) return false;
-      if (elect_one()) {
-        mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + vs.s * kTileBytes<D>);
-        mma_commit(c.bar(DP_FULL));
-        mma_commit(c.bar(V_EMPTY + vs.s));
-      }
-      vs.step();
-      ++jv;
-      return true;
-    };
-    ok = ok && c.wait(Q_FULL, 0) && scores() && grads() && (n == 1 || scores());
-    for (int j = 0; ok && j < n; ++j) {
-      if (j + 1 < n) {
-        ok = c.wait(DP_FREE, j);
+    int gs = 0, done = 0, live = 0;               // blocks with scores, with dQ; tiles
+    bool ok = true;
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      if (g.n == 0) continue;
+      const bool ragged = g.k_len < p.seq_k;
+      int js = 0, jv = 0;
+      // the block's K (V) has landed, with nothing past the sample's keys
+      auto have = [&](int full, int tile_at, uint32_t phase, int j) {
+        const bool got = c.wait(full, phase);
+        if (got && ragged && (g.begin + j + 1) * kTile > g.k_len)
+          zero_rows<D>(smem + tile_at * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+        return got;
+      };
+      auto scores = [&]() {
+        if (!have(K_FULL + ks.s, 2 + ks.s, ks.phase, js)) return false;
+        ++js;
+        if (elect_one()) {
+          mma_rows<T, D>(tmem + (gs & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
+          mma_commit(c.bar(S_FULL + (gs & 1)));
+          if (js == g.n) mma_commit(c.bar(Q_EMPTY));
+        }
+        ks.step();
+        ++gs;
+        return true;
+      };
+      auto grads = [&]() {
+        if (!have(V_FULL + vs.s, 2 + kK + vs.s, vs.phase, jv)) return false;
+        ++jv;
+        if (elect_one()) {
+          mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + vs.s * kTileBytes<D>);
+          mma_commit(c.bar(DP_FULL));
+          mma_commit(c.bar(V_EMPTY + vs.s));
+          if (jv == g.n) mma_commit(c.bar(O_EMPTY));
+        }
+        vs.step();
+        return true;
+      };
+      ok = c.wait(Q_FULL, live) && scores() && c.wait(O_FULL, live) && grads() && (g.n == 1 || scores());
+      for (int j = 0; ok && j < g.n; ++j, ++done) {
+        if (j + 1 < g.n) {
+          ok = c.wait(DP_FREE, done);
+          tc_fence_after();
+          ok = ok && grads();
+          if (!ok) break;
+        }
+        // the accumulator has been read for the tile before
+        if (j == 0 && live > 0) ok = c.wait(ACC_FREE, live - 1);
+        ok = ok && c.wait(DS_FULL + (done & 1), done >> 1);
         tc_fence_after();
         if (!ok) break;
-        ok = grads();
-        if (!ok) break;
+        if (elect_one()) {
+          mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (done & 1) * kTile, sk + kd.s * kTileBytes<D>, j > 0);
+          mma_commit(c.bar(K_EMPTY + kd.s));
+          if (j + 1 == g.n) mma_commit(c.bar(DONE));
+        }
+        kd.step();
+        if (j + 2 < g.n) ok = scores();
       }
-      ok = c.wait(DS_FULL, j);
-      tc_fence_after();
-      if (!ok) break;
-      if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (j & 1) * kTile, sk + kd.s * kTileBytes<D>, j > 0);
-        mma_commit(c.bar(K_EMPTY + kd.s));
-      }
-      kd.step();
-      if (j + 2 < n) ok = scores();
+      ++live;
     }
-    if (ok && elect_one()) mma_commit(c.bar(DONE));
-    if (!ok && n > 0) {
-      if (elect_one()) mma_commit(c.bar(DRAIN));
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
-      }
-    }
-    __syncwarp();
+    if (!ok) c.drain_mma(DRAIN);
   } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // a thread per query and half of the block's keys
-    const int half = c.warp >> 2;
-    const int row = q0 + (c.warp & 3) * 32 + c.lane;
+    const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
-    const bool valid = row < q_len;
-    int limit = valid ? (p.causal ? row + diag + 1 : k_len) : 0;
-    limit = limit < 0 ? 0 : (limit > k_len ? k_len : limit);
-    float lse2 = INFINITY, delta = 0.0f;          // p = 0 for a row that sees nothing
-    const long long at = (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + row;
-    if (limit > 0 && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
-      const float v = p.lse[at];
-      lse2 = v == -INFINITY ? INFINITY : __fmul_rn(v, kLog2e);
-      delta = p.delta[at];
-    }
-    const float nl = GradScale<T>::kP - lse2, nd = -delta * kGradC<T>;
-    const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
-                 C = make_float2(kGradC<T>, kGradC<T>);
+    int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t ts = tmem + (j & 1) * kTile + half * 64 + lanes, tdp = tmem + 2 * kTile + half * 64 + lanes;
-      ok = c.wait(S_FULL + (j & 1), j >> 1);
-      if (!ok) break;
-      tc_fence_after();
-      float s[2][32];
-      tmem_load32(ts, s[0]);
-      tmem_load32(ts + 32, s[1]);
-      tmem_wait_load(s[0]);
-      tmem_loaded(s[1]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 x = __ffma2_rn(make_float2(s[i][e], s[i][e + 1]), SL, NL);
-          s[i][e] = exp2_approx(x.x);
-          s[i][e + 1] = exp2_approx(x.y);
-        }
-      ok = c.wait(DP_FULL, j);
-      if (!ok) break;
-      tc_fence_after();
-      float d[2][32];
-      tmem_load32(tdp, d[0]);
-      tmem_load32(tdp + 32, d[1]);
-      tmem_wait_load(d[0]);
-      tmem_loaded(d[1]);
-      c.arrive(DP_FREE);
-      const int seen = limit - j * kTile - half * 64;
-      if (__any_sync(0xffffffffu, seen < 64)) {
-        // p = 0 and a finite dp - delta where the row does not see the key
+    Seg g;
+    for (int sg = 0; ok && segment(sg, g); ++sg) {
+      const int row = g.q0 + r;
+      int limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
+      limit = limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit);
+      float lse2 = INFINITY, delta = 0.0f;        // p = 0 for a row that sees nothing
+      const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
+      if (limit > 0 && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
+        const float v = p.lse[at];
+        lse2 = v == -INFINITY ? INFINITY : __fmul_rn(v, kLog2e);
+        delta = p.delta[at];
+      }
+      const float nl = GradScale<T>::kP - lse2, nd = -delta * kGradC<T>;
+      const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
+                   C = make_float2(kGradC<T>, kGradC<T>);
+      for (int j = 0; j < g.n; ++j, ++done) {
+        const uint32_t ts = tmem + (done & 1) * kTile + half * 64 + lanes, tdp = tmem + 2 * kTile + half * 64 + lanes;
+        ok = c.wait(S_FULL + (done & 1), done >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        float s[2][32];
+        tmem_load32(ts, s[0]);
+        tmem_load32(ts + 32, s[1]);
+        tmem_wait_load(s[0]);
+        tmem_loaded(s[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            s[i][e] = 32 * i + e < seen ? s[i][e] : 0.0f;
-            d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = __ffma2_rn(make_float2(s[i][e], s[i][e + 1]), SL, NL);
+            s[i][e] = exp2_approx(x.x);
+            s[i][e + 1] = exp2_approx(x.y);
           }
-      }
+        ok = c.wait(DP_FULL, done);
+        if (!ok) break;
+        tc_fence_after();
+        float d[2][32];
+        tmem_load32(tdp, d[0]);
+        tmem_load32(tdp + 32, d[1]);
+        tmem_wait_load(d[0]);
+        tmem_loaded(d[1]);
+        c.arrive(DP_FREE);
+        const int seen = limit - (g.begin + j) * kTile - half * 64;
+        if (__any_sync(0xffffffffu, seen < 64)) {
+          // p = 0 and a finite dp - delta where the row does not see the key
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[16];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = __fmul2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]),
-                                      __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), C, ND));
-          w[e] = pack2<T>(x.x, x.y);
+            for (int e = 0; e < 32; ++e) {
+              s[i][e] = 32 * i + e < seen ? s[i][e] : 0.0f;
+              d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
+            }
         }
-        tmem_store16(ts + 16 * i, w);
-      }
-      tmem_wait_store();
-      c.arrive(DS_FULL);
-    }
-    if (ok && n > 0) ok = c.wait(DONE, 0);
-    tc_fence_after();
-    char* dst = p.dq + (static_cast<long long>(b) * p.seq_q + row) * p.dq_stride + h * (D * 2) + half * D;
-    const bool fits = ok && row < p.seq_q && in_span(dst, D, p.sp_dq, p.status);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      float v[32];
-      if (ok && n > 0) {
-        tmem_load32(tmem + 3 * kTile + half * (D / 2) + 32 * i + lanes, v);
-        tmem_wait_load(v);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __fmul2_rn(make_float2(s[i][2 * e], s[i][2 * e + 1]),
+                                        __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), C, ND));
+            w[e] = pack2<T>(x.x, x.y);
+          }
+          tmem_store16(ts + 16 * i, w);
+        }
+        tmem_wait_store();
+        c.arrive(DS_FULL + (done & 1));
       }
-      if (fits) store_cols<T>(dst + 64 * i, v, p.scale * grad_scale_down(GradScale<T>::kS), n > 0 && limit > 0);
+      if (!ok) break;
+      if (g.n > 0) {
+        ok = c.wait(DONE, live++);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool some = g.n > 0 && limit > 0;
+      float* part = p.part + (static_cast<long long>(g.slot) * kTile + r) * D + half * (D / 2);
+      char* dst = p.dq + (static_cast<long long>(g.b) * p.seq_q + row) * p.dq_stride + g.h * (D * 2) + half * D;
+      const bool fits = g.slot >= 0 ? in_span(part, 2 * D, p.sp_part, p.status)
+                                    : row < p.seq_q && in_span(dst, D, p.sp_dq, p.status);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        float v[32];
+        if (g.n > 0) {
+          tmem_load32(tmem + 3 * kTile + half * (D / 2) + 32 * i + lanes, v);
+          tmem_wait_load(v);
+          if (i == D / 64 - 1) c.arrive(ACC_FREE);
+        }
+        if (!fits) continue;
+        if (g.slot >= 0)
+          store_part(part + 32 * i, v, some);
+        else
+          store_cols<T>(dst + 64 * i, v, p.scale * grad_scale_down(GradScale<T>::kS), some);
+      }
     }
     tc_fence_before();
   }
@@ -723,37 +991,82 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     tc_fence_after();
     tmem_free(tmem, 512);
   }
-  grid_dependents_launch();
+}
+
+// Adds the parts of the tiles that were shared out, KV: of dk and dv (side by
+// side in a slot, dv first), else of dq; a warp per row.
+template <typename T, int D, bool KV>
+__global__ void __launch_bounds__(256) attn_join_grad_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int kRows = (KV ? 2 : 1) * kTile;     // rows of a slot
+  const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  if (item >= p.rem * kRows) return;
+  const int r = item / kRows, q = item % kRows, which = q / kTile;
+  const AttnPlace at = attn_place(p, p.waves * ctas + r, KV ? p.heads_k : p.heads_q, !KV);
+  const int row = at.t * kTile + q % kTile, seq = KV ? p.seq_k : p.seq_q;
+  if (row >= seq) return;
+  const AttnParts parts(p, r, ctas);
+  float2 acc[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);
+  for (int i = 0; i < parts.count; ++i) {
+    const float* src = p.part + (static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q) * D;
+    if (!in_span(src, 4 * D, p.sp_part, p.status)) continue;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) acc[e] = __fadd2_rn(acc[e], reinterpret_cast<const float2*>(src)[lane + 32 * e]);
+  }
+  const bool dv = KV && which == 0;
+  const float f = dv ? grad_scale_down(GradScale<T>::kP) : p.scale * grad_scale_down(GradScale<T>::kS);
+  char* base = KV ? (dv ? p.dv : p.dk) : p.dq;
+  const long long stride = KV ? (dv ? p.dv_stride : p.dk_stride) : p.dq_stride;
+  char* dst = base + (static_cast<long long>(at.b) * seq + row) * stride + at.h * (D * 2);
+  if (!in_span(dst, D * 2, KV ? (dv ? p.sp_dv : p.sp_dk) : p.sp_dq, p.status)) return;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    reinterpret_cast<uint32_t*>(dst)[lane + 32 * e] = pack2<T>(__fmul_rn(acc[e].x, f), __fmul_rn(acc[e].y, f));
 }
 
 // ---------------------------------------------------------------------------
-// backward, dk and dv: a CTA takes 128 keys of one key head and walks the
-// queries of every head that shares it.  Per block, transposed so that P and
-// dS come out as left operands: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO,
-// dK += dS^T Q.
+// backward, dk and dv: a tile is 128 keys of one key head, its iterations
+// blocks of 128 queries of every head that shares it.  Per block, transposed
+// so that P and dS come out as left operands: S^T = K Q^T, dP^T = V dO^T, dV
+// += P^T dO, dK += dS^T Q.
 
 namespace dkv {
 constexpr int kQ = 3, kO = 2;                     // Q and dO tiles in flight
-enum { KV_FULL = 0, Q_FULL = 1, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ, O_EMPTY = O_FULL + kO,
-       S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, ROWS_FREE = ROWS + 2,
-       DONE = ROWS_FREE + 2, DRAIN, BARS };
+enum { K_FULL = 0, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ,
+       O_EMPTY = O_FULL + kO, S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, ROWS_FREE = ROWS + 2,
+       DONE = ROWS_FREE + 2, ACC_FREE, DRAIN, BARS };
+__device__ __forceinline__ int arrivals(int i) {
+  return i == P_FULL || i == DS_FULL || i == ACC_FREE || (i >= ROWS_FREE && i < DONE) ? 8
+                                                                                     : (i >= ROWS && i < ROWS_FREE ? 2 : 1);
+}
 constexpr int kRowBytes = 2 * 2 * kTile * 4;      // two buffers of (lse, delta) of a tile's queries
 template <int D>
-constexpr int kSmem = (2 + kQ + kO) * kTileBytes<D> + kRowBytes + 256;
+constexpr int kCtl = (2 + kQ + kO) * kTileBytes<D> + kRowBytes;
+template <int D>
+constexpr int kSmem = kCtl<D> + 256;
+
+struct Seg {
+  int b, h, k0, slot;         // h: key head
+  int q_len, k_len, diag;
+  int first, end;             // query tiles [first, end) see one of these keys
+  int n;                      // blocks
+  int h0, t0;                 // head and query tile of the first
+};
 }  // namespace dkv
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p) {
   using namespace dkv;
   extern __shared__ __align__(1024) unsigned char smem[];
-  float* rows = reinterpret_cast<float*>(smem + (2 + kQ + kO) * kTileBytes<D>);   // [2][2][128]
-  unsigned char* ctl = smem + (2 + kQ + kO) * kTileBytes<D> + kRowBytes;
+  unsigned char* ctl = smem + kCtl<D>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
   volatile uint32_t* tmem_word = reinterpret_cast<volatile uint32_t*>(ctl + 8 * BARS + 4);
-  AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
-            __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
+  const AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
+                  __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), i == P_FULL || i == DS_FULL || (i >= ROWS_FREE && i < DONE) ? 8 : (i >= ROWS && i < ROWS_FREE ? 2 : 1));
+    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), arrivals(i));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -763,126 +1076,154 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
+  grid_dependents_launch();
+  float* rows = reinterpret_cast<float*>(smem + (2 + kQ + kO) * kTileBytes<D>);   // [2][2][128]
 
-  const int hk = static_cast<int>(blockIdx.x / p.tiles % p.heads_k), b = static_cast<int>(blockIdx.x / p.tiles / p.heads_k);
-  const int k0 = static_cast<int>(blockIdx.x % p.tiles) * kTile;
-  const int q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
-  const int k_len = clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
-  const int diag = k_len - q_len;
-  // query tiles [first, end) see one of these keys
-  int first = 0, end = (q_len + kTile - 1) / kTile;
-  if (p.causal && k0 - diag > 0) first = (k0 - diag) / kTile;
-  if (k0 >= k_len || first > end) first = end;
-  const int per_head = end - first, n = per_head * p.group;
+  auto segment = [&](int s, Seg& g) {
+    AttnWork w;
+    if (!attn_work(p, s, w)) return false;
+    const AttnPlace at = attn_place(p, w.tile, p.heads_k, false);
+    g.b = at.b;
+    g.h = at.h;
+    g.k0 = at.t * kTile;
+    g.slot = w.slot;
+    g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
+    g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    g.diag = g.k_len - g.q_len;
+    g.first = 0;
+    g.end = (g.q_len + kTile - 1) / kTile;
+    if (p.causal && g.k0 - g.diag > 0) g.first = (g.k0 - g.diag) / kTile;
+    if (g.k0 >= g.k_len || g.first > g.end) g.first = g.end;
+    const int per_head = g.end - g.first;
+    int begin, end;
+    attn_cut(w, per_head * p.group, begin, end);
+    g.n = end - begin;
+    g.h0 = g.h * p.group + (per_head ? begin / per_head : 0);
+    g.t0 = g.first + (per_head ? begin % per_head : 0);
+    return true;
+  };
   const uint32_t sk = c.base, sv = c.base + kTileBytes<D>, sq = c.base + 2 * kTileBytes<D>,
                  sdo = c.base + (2 + kQ) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
   if (c.warp == kAttnLoadWarp) {
-    if (c.lane == 0 && n > 0) {
-      int iq = 0, io = 0;
-      bool ok = !(p.flags & 1u);
-      if (ok) {
-        mbar_arrive_expect_tx(c.bar(KV_FULL), 2 * kTileBytes<D>);
-        tma_load_tile(sk, &p.map_k, k0, hk, b, c.bar(KV_FULL));
-        tma_load_tile(sv, &p.map_v, k0, hk, b, c.bar(KV_FULL));
-        RingPos<kQ> q;
-        RingPos<kO> o;
-        int h = hk * p.group, t = first;
-        for (int i = 0; i < n; ++i, q.step(), o.step()) {
+    if (c.lane == 0 && !(p.flags & 1u)) {         // test only: issue nothing
+      RingPos<kQ> q;
+      RingPos<kO> o;
+      int uses = 0, vuses = 0, iq = 0, io = 0;
+      bool ok = true;
+      Seg g;
+      for (int s = 0; ok && segment(s, g); ++s) {
+        if (g.n == 0) continue;
+        ok = c.wait1(K_EMPTY, uses + 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(c.bar(K_FULL), kTileBytes<D>);
+        tma_load_tile(sk, &p.map_k, g.k0, g.h, g.b, c.bar(K_FULL));
+        ++uses;
+        int h = g.h0, t = g.t0;
+        for (int i = 0; i < g.n; ++i, q.step(), o.step()) {
           ok = c.wait1(Q_EMPTY + q.s, q.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(Q_FULL + q.s), kTileBytes<D>);
-          tma_load_tile(sq + q.s * kTileBytes<D>, &p.map_q, t * kTile, h, b, c.bar(Q_FULL + q.s));
+          tma_load_tile(sq + q.s * kTileBytes<D>, &p.map_q, t * kTile, h, g.b, c.bar(Q_FULL + q.s));
           ++iq;
+          if (i == 0) {
+            ok = c.wait1(V_EMPTY, uses);
+            if (!ok) break;
+            mbar_arrive_expect_tx(c.bar(V_FULL), kTileBytes<D>);
+            tma_load_tile(sv, &p.map_v, g.k0, g.h, g.b, c.bar(V_FULL));
+            ++vuses;
+          }
           ok = c.wait1(O_EMPTY + o.s, o.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(O_FULL + o.s), kTileBytes<D>);
-          tma_load_tile(sdo + o.s * kTileBytes<D>, &p.map_do, t * kTile, h, b, c.bar(O_FULL + o.s));
+          tma_load_tile(sdo + o.s * kTileBytes<D>, &p.map_do, t * kTile, h, g.b, c.bar(O_FULL + o.s));
           ++io;
-          if (++t == end) {
-            t = first;
+          if (++t == g.end) {
+            t = g.first;
             ++h;
           }
         }
       }
       if (!ok || *abort_flag) {
-        const unsigned long long t0 = global_timer_ns();
-        for (int i = iq > kQ ? iq - kQ : 0; i < iq; ++i)
-          while (!mbar_try_wait(c.bar(Q_FULL + i % kQ), (i / kQ) & 1) && global_timer_ns() - t0 < c.limit) {
-          }
-        for (int i = io > kO ? io - kO : 0; i < io; ++i)
-          while (!mbar_try_wait(c.bar(O_FULL + i % kO), (i / kO) & 1) && global_timer_ns() - t0 < c.limit) {
-          }
-        while (!(p.flags & 1u) && !mbar_try_wait(c.bar(KV_FULL), 0) && global_timer_ns() - t0 < c.limit) {
-        }
+        c.drain(Q_FULL, kQ, iq);
+        c.drain(O_FULL, kO, io);
+        c.drain(K_FULL, 1, uses);
+        c.drain(V_FULL, 1, vuses);
       }
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
-    bool ok = n > 0;
-    const bool ragged = q_len < p.seq_q;
     // Blocks whose scores, dP, dV and dK products come next.
     RingPos<kQ> qs, qd;
     RingPos<kO> os, od;
-    int ts = first, to = first;                   // their query tiles
-    // the tile has landed, with nothing past the sample's queries
-    auto have = [&](int full, int tile_at, uint32_t phase, int& t) {
-      const bool got = c.wait(full, phase);
-      if (got && ragged && (t + 1) * kTile > q_len) zero_rows<D>(smem + tile_at * kTileBytes<D>, q_len - t * kTile, c.lane);
-      if (++t == end) t = first;
-      return got;
-    };
-    auto scores = [&]() {
-      if (!have(Q_FULL + qs.s, 2 + qs.s, qs.phase, ts)) return false;
-      if (elect_one()) {
-        mma_rows<T, D>(tmem, sk, sq + qs.s * kTileBytes<D>);
-        mma_commit(c.bar(S_FULL));
-      }
-      qs.step();
-      return true;
-    };
-    auto grads = [&]() {
-      if (!have(O_FULL + os.s, 2 + kQ + os.s, os.phase, to)) return false;
-      if (elect_one()) {
-        mma_rows<T, D>(tmem + kTile, sv, sdo + os.s * kTileBytes<D>);
-        mma_commit(c.bar(DP_FULL));
-      }
-      os.step();
-      return true;
-    };
-    ok = ok && c.wait(KV_FULL, 0) && scores() && grads();
-    for (int i = 0; ok && i < n; ++i) {
-      ok = c.wait(P_FULL, i);
-      tc_fence_after();
-      if (!ok) break;
-      if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + od.s * kTileBytes<D>, i > 0);
-        mma_commit(c.bar(O_EMPTY + od.s));
-      }
-      od.step();
-      if (i + 1 < n) {
-        ok = scores();
+    int done = 0, live = 0;                       // blocks and tiles so far
+    bool ok = true;
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      if (g.n == 0) continue;
+      const bool ragged = g.q_len < p.seq_q;
+      int ts = g.t0, to = g.t0, is = 0, ig = 0;   // query tiles and blocks of the scores, of dP
+      // the tile has landed, with nothing past the sample's queries
+      auto have = [&](int full, int tile_at, uint32_t phase, int& t) {
+        const bool got = c.wait(full, phase);
+        if (got && ragged && (t + 1) * kTile > g.q_len)
+          zero_rows<D>(smem + tile_at * kTileBytes<D>, g.q_len - t * kTile, c.lane);
+        if (++t == g.end) t = g.first;
+        return got;
+      };
+      auto scores = [&]() {
+        if (!have(Q_FULL + qs.s, 2 + qs.s, qs.phase, ts)) return false;
+        ++is;
+        if (elect_one()) {
+          mma_rows<T, D>(tmem, sk, sq + qs.s * kTileBytes<D>);
+          mma_commit(c.bar(S_FULL));
+          if (is == g.n) mma_commit(c.bar(K_EMPTY));
+        }
+        qs.step();
+        return true;
+      };
+      auto grads = [&]() {
+        if (!have(O_FULL + os.s, 2 + kQ + os.s, os.phase, to)) return false;
+        ++ig;
+        if (elect_one()) {
+          mma_rows<T, D>(tmem + kTile, sv, sdo + os.s * kTileBytes<D>);
+          mma_commit(c.bar(DP_FULL));
+          if (ig == g.n) mma_commit(c.bar(V_EMPTY));
+        }
+        os.step();
+        return true;
+      };
+      ok = c.wait(K_FULL, live) && scores() && c.wait(V_FULL, live) && grads();
+      for (int i = 0; ok && i < g.n; ++i, ++done) {
+        // the accumulators have been read for the tile before
+        if (i == 0 && live > 0) ok = c.wait(ACC_FREE, live - 1);
+        ok = ok && c.wait(P_FULL, done);
+        tc_fence_after();
         if (!ok) break;
+        if (elect_one()) {
+          mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + od.s * kTileBytes<D>, i > 0);
+          mma_commit(c.bar(O_EMPTY + od.s));
+        }
+        od.step();
+        if (i + 1 < g.n) {
+          ok = scores();
+          if (!ok) break;
+        }
+        ok = c.wait(DS_FULL, done);
+        tc_fence_after();
+        if (!ok) break;
+        if (elect_one()) {
+          mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + qd.s * kTileBytes<D>, i > 0);
+          mma_commit(c.bar(Q_EMPTY + qd.s));
+          if (i + 1 == g.n) mma_commit(c.bar(DONE));
+        }
+        qd.step();
+        if (i + 1 < g.n) ok = grads();
       }
-      ok = c.wait(DS_FULL, i);
-      tc_fence_after();
-      if (!ok) break;
-      if (elect_one()) {
-        mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + qd.s * kTileBytes<D>, i > 0);
-        mma_commit(c.bar(Q_EMPTY + qd.s));
-      }
-      qd.step();
-      if (i + 1 < n) ok = grads();
+      ++live;
     }
-    if (ok && elect_one()) mma_commit(c.bar(DONE));
-    if (!ok && n > 0) {
-      if (elect_one()) mma_commit(c.bar(DRAIN));
-      const unsigned long long t0 = global_timer_ns();
-      while (!mbar_try_wait(c.bar(DRAIN), 0) && global_timer_ns() - t0 < c.limit) {
-      }
-    }
-    __syncwarp();
+    if (!ok) c.drain_mma(DRAIN);
   } else if (c.warp >= kAttnMmaWarp) {
     // Warps 10 and 11 hand round kP - lse (log2) and -delta kC of the blocks'
     // queries, up to two blocks ahead.  A query past the length or with no
@@ -890,134 +1231,155 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     const bool second = c.warp == kAttnMmaWarp + 3;
     const float* source = second ? p.delta : p.lse;
     const MemSpan& sp_source = second ? p.sp_delta : p.sp_lse;
-    int h = hk * p.group, t = first;
+    int done = 0;
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const float* at = source + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
-      float v[4];
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      int h = g.h0, t = g.t0;
+      for (int i = 0; i < g.n; ++i, ++done) {
+        const float* at = source + (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
+        float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int q = t * kTile + 32 * e + c.lane;
-        v[e] = second ? 0.0f : -INFINITY;
-        if (q < q_len && in_span(at + 32 * e, 4, sp_source, p.status)) v[e] = at[32 * e];
-      }
-      // the block before last has been read
-      ok = i < 2 || c.wait(ROWS_FREE + (i & 1), (i >> 1) - 1);
-      if (!ok) break;
-      float* out = rows + (i & 1) * 2 * kTile + (second ? kTile : 0) + c.lane;
+        for (int e = 0; e < 4; ++e) {
+          const int q = t * kTile + 32 * e + c.lane;
+          v[e] = second ? 0.0f : -INFINITY;
+          if (q < g.q_len && in_span(at + 32 * e, 4, sp_source, p.status)) v[e] = at[32 * e];
+        }
+        // the block before last has been read
+        ok = done < 2 || c.wait(ROWS_FREE + (done & 1), (done >> 1) - 1);
+        if (!ok) break;
+        float* out = rows + (done & 1) * 2 * kTile + (second ? kTile : 0) + c.lane;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        out[32 * e] = second ? -v[e] * kGradC<T> : (v[e] == -INFINITY ? -INFINITY : __fmaf_rn(v[e], -kLog2e, GradScale<T>::kP));
-      __syncwarp();
-      if (c.lane == 0) mbar_arrive(c.bar(ROWS + (i & 1)));
-      if (++t == end) {
-        t = first;
-        ++h;
+        for (int e = 0; e < 4; ++e)
+          out[32 * e] = second ? -v[e] * kGradC<T>
+                               : (v[e] == -INFINITY ? -INFINITY : __fmaf_rn(v[e], -kLog2e, GradScale<T>::kP));
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(c.bar(ROWS + (done & 1)));
+        if (++t == g.end) {
+          t = g.first;
+          ++h;
+        }
       }
     }
   } else {
     more_registers<kAttnWorkRegs>();
     // a thread per key and half of the block's queries
-    const int half = c.warp >> 2;
-    const int key = k0 + (c.warp & 3) * 32 + c.lane;
+    const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + half * 64 + lanes, tdp = tmem + kTile + half * 64 + lanes;
     const float2 SL = make_float2(p.scale_log2, p.scale_log2), C = make_float2(kGradC<T>, kGradC<T>);
+    int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
-    int t = first;                                // the block's query tile
-    for (int i = 0; i < n; ++i) {
-      const float* mine = rows + (i & 1) * 2 * kTile;
-      const float4* nl = reinterpret_cast<const float4*>(mine + half * 64);
-      const float4* nd = reinterpret_cast<const float4*>(mine + kTile + half * 64);
-      ok = c.wait(ROWS + (i & 1), i >> 1) && c.wait(S_FULL, i);
-      if (!ok) break;
-      tc_fence_after();
-      float s[2][32];
-      tmem_load32(ts, s[0]);
-      tmem_load32(ts + 32, s[1]);
-      tmem_wait_load(s[0]);
-      tmem_loaded(s[1]);
-      // query q0 + c sees this key when c >= from
-      const int from = p.causal ? key - diag - t * kTile - half * 64 : 0;
-      if (++t == end) t = first;
-      const bool masked = __any_sync(0xffffffffu, from > 0);
-#pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 l4 = nl[a * 8 + e];
-          float* x = &s[a][4 * e];
-          const float2 u = __ffma2_rn(make_float2(x[0], x[1]), SL, make_float2(l4.x, l4.y));
-          const float2 v = __ffma2_rn(make_float2(x[2], x[3]), SL, make_float2(l4.z, l4.w));
-          x[0] = exp2_approx(u.x);
-          x[1] = exp2_approx(u.y);
-          x[2] = exp2_approx(v.x);
-          x[3] = exp2_approx(v.y);
-        }
-      if (masked) {
+    Seg g;
+    for (int sg = 0; ok && segment(sg, g); ++sg) {
+      const int key = g.k0 + r;
+      int t = g.t0;                               // the block's query tile
+      for (int i = 0; i < g.n; ++i, ++done) {
+        const float* mine = rows + (done & 1) * 2 * kTile;
+        const float4* nl = reinterpret_cast<const float4*>(mine + half * 64);
+        const float4* nd = reinterpret_cast<const float4*>(mine + kTile + half * 64);
+        ok = c.wait(ROWS + (done & 1), done >> 1) && c.wait(S_FULL, done);
+        if (!ok) break;
+        tc_fence_after();
+        float s[2][32];
+        tmem_load32(ts, s[0]);
+        tmem_load32(ts + 32, s[1]);
+        tmem_wait_load(s[0]);
+        tmem_loaded(s[1]);
+        // query q0 + c sees this key when c >= from
+        const int from = p.causal ? key - g.diag - t * kTile - half * 64 : 0;
+        if (++t == g.end) t = g.first;
+        const bool masked = __any_sync(0xffffffffu, from > 0);
 #pragma unroll
         for (int a = 0; a < 2; ++a)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[a][e] = 32 * a + e >= from ? s[a][e] : 0.0f;
-      }
+          for (int e = 0; e < 8; ++e) {
+            const float4 l4 = nl[a * 8 + e];
+            float* x = &s[a][4 * e];
+            const float2 u = __ffma2_rn(make_float2(x[0], x[1]), SL, make_float2(l4.x, l4.y));
+            const float2 v = __ffma2_rn(make_float2(x[2], x[3]), SL, make_float2(l4.z, l4.w));
+            x[0] = exp2_approx(u.x);
+            x[1] = exp2_approx(u.y);
+            x[2] = exp2_approx(v.x);
+            x[3] = exp2_approx(v.y);
+          }
+        if (masked) {
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        uint32_t w[16];
+          for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack2<T>(s[a][2 * e], s[a][2 * e + 1]);
-        tmem_store16(ts + 16 * a, w);
-      }
-      tmem_wait_store();
-      c.arrive(P_FULL);
-      ok = c.wait(DP_FULL, i);
-      if (!ok) break;
-      tc_fence_after();
-      float d[2][32];
-      tmem_load32(tdp, d[0]);
-      tmem_load32(tdp + 32, d[1]);
-      tmem_wait_load(d[0]);
-      tmem_loaded(d[1]);
-      if (masked) {
-#pragma unroll
-        for (int a = 0; a < 2; ++a)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 d4 = nd[a * 8 + e];
-          const float* x = &s[a][4 * e];
-          const float2 u = __fmul2_rn(make_float2(x[0], x[1]),
-                                      __ffma2_rn(make_float2(d[a][4 * e], d[a][4 * e + 1]), C, make_float2(d4.x, d4.y)));
-          const float2 v = __fmul2_rn(make_float2(x[2], x[3]),
-                                      __ffma2_rn(make_float2(d[a][4 * e + 2], d[a][4 * e + 3]), C, make_float2(d4.z, d4.w)));
-          w[2 * e] = pack2<T>(u.x, u.y);
-          w[2 * e + 1] = pack2<T>(v.x, v.y);
+            for (int e = 0; e < 32; ++e) s[a][e] = 32 * a + e >= from ? s[a][e] : 0.0f;
         }
-        tmem_store16(tdp + 16 * a, w);
-      }
-      tmem_wait_store();
-      c.arrive(DS_FULL);
-      if (c.lane == 0) mbar_arrive(c.bar(ROWS_FREE + (i & 1)));
-    }
-    if (ok && n > 0) ok = c.wait(DONE, 0);
-    tc_fence_after();
-    // the first group writes dv, the second dk
-    const float f = half ? p.scale * grad_scale_down(GradScale<T>::kS) : grad_scale_down(GradScale<T>::kP);
-    char* dst = half ? p.dk + (static_cast<long long>(b) * p.seq_k + key) * p.dk_stride + hk * (D * 2)
-                     : p.dv + (static_cast<long long>(b) * p.seq_k + key) * p.dv_stride + hk * (D * 2);
-    const bool fits = ok && key < p.seq_k && in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      float v[32];
-      if (ok && n > 0) {
-        tmem_load32(tmem + (2 + half) * kTile + 32 * i + lanes, v);
-        tmem_wait_load(v);
+        for (int a = 0; a < 2; ++a) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = pack2<T>(s[a][2 * e], s[a][2 * e + 1]);
+          tmem_store16(ts + 16 * a, w);
+        }
+        tmem_wait_store();
+        c.arrive(P_FULL);
+        ok = c.wait(DP_FULL, done);
+        if (!ok) break;
+        tc_fence_after();
+        float d[2][32];
+        tmem_load32(tdp, d[0]);
+        tmem_load32(tdp + 32, d[1]);
+        tmem_wait_load(d[0]);
+        tmem_loaded(d[1]);
+        if (masked) {
+#pragma unroll
+          for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 d4 = nd[a * 8 + e];
+            const float* x = &s[a][4 * e];
+            const float2 u = __fmul2_rn(make_float2(x[0], x[1]),
+                                        __ffma2_rn(make_float2(d[a][4 * e], d[a][4 * e + 1]), C, make_float2(d4.x, d4.y)));
+            const float2 v = __fmul2_rn(make_float2(x[2], x[3]),
+                                        __ffma2_rn(make_float2(d[a][4 * e + 2], d[a][4 * e + 3]), C, make_float2(d4.z, d4.w)));
+            w[2 * e] = pack2<T>(u.x, u.y);
+            w[2 * e + 1] = pack2<T>(v.x, v.y);
+          }
+          tmem_store16(tdp + 16 * a, w);
+        }
+        tmem_wait_store();
+        c.arrive(DS_FULL);
+        if (c.lane == 0) mbar_arrive(c.bar(ROWS_FREE + (done & 1)));
       }
-      if (fits) store_cols<T>(dst + 64 * i, v, f, n > 0 && key < k_len);
+      if (!ok) break;
+      // the first group writes dv, the second dk
+      if (g.n > 0) {
+        ok = c.wait(DONE, live++);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const bool some = g.n > 0 && key < g.k_len;
+      const float f = half ? p.scale * grad_scale_down(GradScale<T>::kS) : grad_scale_down(GradScale<T>::kP);
+      float* part = p.part + ((static_cast<long long>(g.slot) * 2 + half) * kTile + r) * D;
+      char* dst = half ? p.dk + (static_cast<long long>(g.b) * p.seq_k + key) * p.dk_stride + g.h * (D * 2)
+                       : p.dv + (static_cast<long long>(g.b) * p.seq_k + key) * p.dv_stride + g.h * (D * 2);
+      const bool fits = g.slot >= 0 ? in_span(part, 4 * D, p.sp_part, p.status)
+                                    : key < p.seq_k && in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        float v[32];
+        if (g.n > 0) {
+          tmem_load32(tmem + (2 + half) * kTile + 32 * i + lanes, v);
+          tmem_wait_load(v);
+          if (i == D / 32 - 1) c.arrive(ACC_FREE);
+        }
+        if (!fits) continue;
+        if (g.slot >= 0)
+          store_part(part + 32 * i, v, some);
+        else
+          store_cols<T>(dst + 64 * i, v, f, some);
+      }
     }
     tc_fence_before();
   }
@@ -1026,7 +1388,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     tc_fence_after();
     tmem_free(tmem, 512);
   }
-  grid_dependents_launch();
 }
 
 }  // namespace qknr

@@ -3,15 +3,18 @@
 // All four kernels' products run on tcgen05 with operands that TMA leaves in
 // shared memory and accumulators in tensor memory; the probabilities (and the
 // score gradients) go back to tensor memory as 16-bit left operands of the
-// second product, in the columns whose scores they replace.  One thread
-// issues every MMA; MMAs of one thread run in order, so a product that
-// overwrites an operand of an earlier one needs no wait in between.
+// second product, in the columns whose scores they replace.  MMAs of
+// one thread run in order, so a product that overwrites an operand of an
+// earlier one needs no wait in between.  Two threads issue them, each one of
+// the two chains of products that do not depend on each other: what a thread
+// spends on waits between its products, the other's products fill (one thread
+// for both: 745 against 577 us forward at 2 x 4608 x 48 x 128).
 //
 // Roles of a CTA's 12 warps: 0-7 are two groups of four that each cover the
-// 128 lanes of tensor memory (a thread owns one row of a score tile), warp 8
-// issues the MMAs, warp 9 the TMA loads, warps 10 and 11 fill up the third
-// group, whose registers go to the first two (and hand round the queries'
-// statistics in the dk, dv kernel).
+// 128 lanes of tensor memory (a thread owns one row of a score tile), warps 8
+// and 10 issue the MMAs, warp 9 the TMA loads; warp 11 hands round the
+// queries' statistics in the dk, dv kernel.  The third group's registers go
+// to the first two.
 //
 // Persistent CTAs, one per SM.  Tile w of CTA c is tile w * CTAs + c, so that
 // CTAs next to each other read the same keys; the tiles left over after the
@@ -55,7 +58,7 @@ struct AttnParams {
 };
 
 constexpr int kAttnThreads = 384;
-constexpr int kAttnMmaWarp = 8, kAttnLoadWarp = 9;
+constexpr int kAttnMmaWarp = 8, kAttnLoadWarp = 9, kAttnMma2Warp = 10, kAttnRowWarp = 11;
 constexpr int kTile = 128;                        // rows of a tile, both ways
 // Registers: 384 threads start with 168 each; 2 x 128 x 208 + 128 x 80 fit in
 // the 384 x 168 that the block was launched with.
@@ -163,6 +166,16 @@ struct AttnCta {
   __device__ __forceinline__ bool wait(int i, uint32_t phase) const {
     return __all_sync(0xffffffffu, wait1(i, phase));
   }
+  // Whole warp, three barriers that are likely to be complete: lane 0 looks at
+  // the first, lane 1 at the second, the others at the third.  Shared memory
+  // answers slowly while the tensor cores read it: one look after the other
+  // costs 100 to 150 cycles each.
+  __device__ __forceinline__ bool wait(int i, uint32_t pi, int j, uint32_t pj, int k, uint32_t pk) const {
+    const int mine = lane == 0 ? i : (lane == 1 ? j : k);
+    const uint32_t phase = lane == 0 ? pi : (lane == 1 ? pj : pk);
+    if (__all_sync(0xffffffffu, mbar_test(bar(mine), phase & 1u))) return true;
+    return wait(i, pi) && wait(j, pj) && wait(k, pk);
+  }
   // One thread, giving up: the last `n` of `issued` copies into a ring of n
   // stages end before the CTA leaves its shared memory.
   __device__ __forceinline__ void drain(int full, int n, int issued) const {
@@ -239,27 +252,69 @@ __device__ __forceinline__ void attn_cut(const AttnWork& w, int n, int& begin, i
   end = static_cast<int>(static_cast<long long>(n) * w.u1 / kUnits);
 }
 
-// 16 bytes of a row at a time: 32 accumulator values from tensor memory to
-// their place in a row of the output, times f (zero where the row has no value)
-template <typename T>
-__device__ __forceinline__ void store_cols(char* dst, const float (&v)[32], float f, bool some) {
+// Epilogue stores.  A thread holds pieces of its own row; stored as they are,
+// every store instruction touches 32 rows, a cache line each (6000 cycles for
+// a 128 x 128 tile).  So the four lanes of a quad first swap 16-byte chunks:
+// afterwards v[k] is chunk (lane & 3) of the quad's k-th row, and an
+// instruction writes 64 bytes of each of eight rows.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint4 w;
-    uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+  for (int step = 1; step <= 2; step <<= 1) {
+    const bool upper = lane & step;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ww[i] = some ? pack2<T>(__fmul_rn(v[c * 8 + 2 * i], f), __fmul_rn(v[c * 8 + 2 * i + 1], f)) : 0u;
-    reinterpret_cast<uint4*>(dst)[c] = w;
+    for (int k = 0; k < 4; ++k) {
+      if (k & step) continue;
+      uint4& lo = v[k];
+      uint4& hi = v[k + step];
+      uint4 give = upper ? lo : hi;
+      give.x = __shfl_xor_sync(0xffffffffu, give.x, step);
+      give.y = __shfl_xor_sync(0xffffffffu, give.y, step);
+      give.z = __shfl_xor_sync(0xffffffffu, give.z, step);
+      give.w = __shfl_xor_sync(0xffffffffu, give.w, step);
+      if (upper) lo = give;
+      else hi = give;
+    }
   }
 }
 
-// the same values as a partial result
-__device__ __forceinline__ void store_part(float* dst, const float (&v)[32], bool some) {
+// 32 accumulator values of each row of a warp, times f (zero where the row has
+// no value), in the output's type.  `dst`: this thread's place in its own row;
+// rows are `stride` bytes apart, the warp's first `rows` of them are there.
+template <typename T>
+__device__ __forceinline__ void store_cols(char* dst, long long stride, int rows, const float (&v)[32], float f, bool some,
+                                           int lane) {
+  uint4 w[4];
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    reinterpret_cast<float4*>(dst)[c] =
-        some ? make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int c = 0; c < 4; ++c) {
+    uint32_t* ww = reinterpret_cast<uint32_t*>(&w[c]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ww[i] = some ? pack2<T>(__fmul_rn(v[c * 8 + 2 * i], f), __fmul_rn(v[c * 8 + 2 * i + 1], f)) : 0u;
+  }
+  quad_transpose(w, lane);
+  char* at = dst - (lane & 3) * stride + (lane & 3) * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if ((lane & ~3) + k < rows) *reinterpret_cast<uint4*>(at + k * stride) = w[k];
+}
+
+// the same values as a partial result: fp32 rows of D values
+template <int D>
+__device__ __forceinline__ void store_part(float* dst, const float (&v)[32], bool some, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float* x = &v[16 * h + 4 * c];
+      w[c] = some ? make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]))
+                  : make_uint4(0, 0, 0, 0);
+    }
+    quad_transpose(w, lane);
+    float* at = dst - (lane & 3) * D + (lane & 3) * 4 + 16 * h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(at + k * D) = w[k];
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -385,7 +440,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
-    // S_t(0), then per block: O_t += P_t V, S_t(next)
+    // S_t(0), then per block and half in turn: O_t += P_t V, S_t(next)
     RingPos<kK> k;
     RingPos<kV> v;
     int uses[2] = {0, 0}, done[2] = {0, 0};       // tiles, blocks of each half so far
@@ -393,56 +448,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.blocks == 0) continue;
-      for (int t = 0; t < 2 && ok; ++t)
-        if (g.nb[t]) ok = c.wait(Q_FULL + t, uses[t]);
-      ok = ok && c.wait(K_FULL + k.s, k.phase);
+      const int n0 = g.nb[0], n1 = g.nb[1], blocks = g.blocks;
+      // the block whose V has rows past the sample's keys
+      const int ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : blocks;
+      ok = (n0 == 0 || c.wait(Q_FULL, uses[0])) && (n1 == 0 || c.wait(Q_FULL + 1, uses[1])) && c.wait(K_FULL + k.s, k.phase);
       if (!ok) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (g.nb[t]) {
-            mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
-            mma_commit(c.bar(S_FULL + t));
-            if (g.nb[t] == 1) mma_commit(c.bar(Q_EMPTY + t));
-          }
+        for (int t = 0; t < 2; ++t) {
+          const int n = t ? n1 : n0;
+          if (n == 0) continue;
+          mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
+          mma_commit(c.bar(S_FULL + t));
+          if (n == 1) mma_commit(c.bar(Q_EMPTY + t));
+        }
         mma_commit(c.bar(K_EMPTY + k.s));
       }
       k.step();
-      for (int j = 0; ok && j < g.blocks; ++j) {
-        ok = c.wait(V_FULL + v.s, v.phase);
-        if (!ok) break;
-        if (g.k_len < p.seq_k && (g.begin + j + 1) * kTile > g.k_len)
-          zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
-        if (j + 1 < g.blocks) ok = c.wait(K_FULL + k.s, k.phase);
+      for (int j = 0; ok && j < blocks; ++j) {
+        const bool more = j + 1 < blocks;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (ok && j < g.nb[t]) {
-            // the accumulator has been read for the tile before
-            if (j == 0 && uses[t] > 0) ok = c.wait(O_FREE + t, uses[t] - 1);
-            ok = ok && c.wait(P_FULL + t, done[t]);
+          const int n = t ? n1 : n0;
+          const uint32_t ts = tmem + t * kTile, to = tmem + 2 * kTile + t * kTile;
+          // this block's V, the next one's K, the half's P
+          const int bv = V_FULL + v.s, bk = more ? K_FULL + k.s : bv, bp = j < n ? P_FULL + t : bv;
+          const uint32_t pv = v.phase, pk = more ? k.phase : pv, pp = j < n ? done[t] : pv;
+          if (t == 0) {
+            ok = c.wait(bv, pv, bk, pk, bp, pp);
+            if (!ok) break;
+            if (j >= ragged) zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+          } else if (j < n) {
+            ok = c.wait(bp, pp);
+            if (!ok) break;
+          }
+          if (j < n) {
             ++done[t];
-            tc_fence_after();
-            if (ok && elect_one()) {
-              mma_cols<T, D, false>(tmem + 2 * kTile + t * kTile, tmem + t * kTile, sv + v.s * kTileBytes<D>, j > 0);
+            // the accumulator has been read for the tile before
+            ok = j > 0 || uses[t] == 0 || c.wait(O_FREE + t, uses[t] - 1);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            if (j < n) {
+              mma_cols<T, D, false>(to, ts, sv + v.s * kTileBytes<D>, j > 0);
               mma_commit(c.bar(O_DONE + t));
             }
-          }
-          if (t == 1 && ok && elect_one()) mma_commit(c.bar(V_EMPTY + v.s));
-          if (ok && j + 1 < g.nb[t] && elect_one()) {
-            mma_rows<T, D>(tmem + t * kTile, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
-            mma_commit(c.bar(S_FULL + t));
-            if (j + 2 == g.nb[t]) mma_commit(c.bar(Q_EMPTY + t));
+            if (t == 1) mma_commit(c.bar(V_EMPTY + v.s));
+            if (j + 1 < n) {
+              mma_rows<T, D>(ts, c.base + t * kTileBytes<D>, sk + k.s * kTileBytes<D>);
+              mma_commit(c.bar(S_FULL + t));
+              if (j + 2 == n) mma_commit(c.bar(Q_EMPTY + t));
+            }
+            if (t == 1 && more) mma_commit(c.bar(K_EMPTY + k.s));
           }
         }
         v.step();
-        if (j + 1 < g.blocks) {
-          if (ok && elect_one()) mma_commit(c.bar(K_EMPTY + k.s));
-          k.step();
-        }
+        if (more) k.step();
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) uses[t] += g.nb[t] > 0;
+      uses[0] += n0 > 0;
+      uses[1] += n1 > 0;
     }
     if (!ok) c.drain_mma(DRAIN);
   } else if (c.warp < kAttnMmaWarp) {
@@ -487,9 +553,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         for (int i = 0; i < 4; ++i) {
           mx[i] = fmaxf(s[i][0], s[i][1]);
 #pragma unroll
-          for (int e = 2; e < 32; e += 2) mx[i] = fmaxf(mx[i], fmaxf(s[i][e], s[i][e + 1]));
+          for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], s[i][e], s[i][e + 1]);
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         if (j == 0) {
           m = top;
         } else if (__any_sync(0xffffffffu, top > m + slack)) {
@@ -540,18 +606,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       const int row = g.q0 + t * kTile + r;
       char* dst = p.o + (static_cast<long long>(g.b) * p.seq_q + row) * p.o_stride + g.h * (D * 2);
       const long long at = static_cast<long long>(g.slot) * kRows + t * kTile + r;   // a part's row
-      bool fits;
+      const int there = p.seq_q - (row - c.lane);   // rows from the warp's first on
       if (g.slot >= 0) {
         // a part of the keys: unnormalised, with its maximum and sum
         if (in_span(p.stats + 2 * at, 8, p.sp_stats, p.status))
           *reinterpret_cast<float2*>(p.stats + 2 * at) = make_float2(m, total);
-        fits = in_span(p.part + at * D, 4 * D, p.sp_part, p.status);
       } else {
         const long long l = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
         if (row < p.seq_q && in_span(p.lse + l, 4, p.sp_lse, p.status))
           p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
-        fits = row < p.seq_q && in_span(dst, D * 2, p.sp_o, p.status);
       }
+      // checked builds: the rows this warp writes
+      const bool fits = __all_sync(0xffffffffu, g.slot >= 0 ? in_span(p.part + at * D, 4 * D, p.sp_part, p.status)
+                                                            : row >= p.seq_q || in_span(dst, D * 2, p.sp_o, p.status));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
@@ -562,9 +629,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         }
         if (!fits) continue;
         if (g.slot >= 0)
-          store_part(p.part + at * D + 32 * i, o, n > 0);
+          store_part<D>(p.part + at * D + 32 * i, o, n > 0, c.lane);
         else
-          store_cols<T>(dst + 64 * i, o, inv, some);
+          store_cols<T>(dst + 64 * i, p.o_stride, there, o, inv, some, c.lane);
       }
     }
     tc_fence_before();
@@ -576,24 +643,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   }
 }
 
-// The parts of tile r that was shared out: the first CTA with one, and how
-// many there are; part i's slot is slot(i).
+// The parts of tile r that was shared out: count of them, CTAs first, first +
+// 1, ...; part i's slot is slot(i).
 struct AttnParts {
-  int first, count, r;
-  long long unit0;
-  __device__ __forceinline__ AttnParts(const AttnParams& p, int r_, int ctas) : r(r_) {
-    unit0 = static_cast<long long>(r) * kUnits;
+  int first, count, late;
+  __device__ __forceinline__ AttnParts(const AttnParams& p, int r, int ctas) {
+    const long long unit0 = static_cast<long long>(r) * kUnits;
     int c = static_cast<int>(static_cast<long long>(r) * ctas / p.rem);
     while (c > 0 && attn_share(p, c, ctas) > unit0) --c;
     while (attn_share(p, c + 1, ctas) <= unit0) ++c;
     first = c;
+    late = attn_share(p, c, ctas) < unit0;        // its share began in the tile before
     while (c < ctas && attn_share(p, c, ctas) < unit0 + kUnits) ++c;
     count = c - first;
   }
-  __device__ __forceinline__ int slot(const AttnParams& p, int i, int ctas) const {
-    const int c = first + i;
-    return 2 * c + (r - static_cast<int>(attn_share(p, c, ctas) / kUnits));
-  }
+  __device__ __forceinline__ int slot(int i) const { return 2 * (first + i) + (i == 0 ? late : 0); }
 };
 
 // Joins the parts of the tiles that were shared out: a warp per query row.
@@ -610,21 +674,22 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
   if (row >= p.seq_q) return;
   const AttnParts parts(p, r, ctas);
   float m = -INFINITY;
+#pragma unroll 4
   for (int i = 0; i < parts.count; ++i) {
-    const float* st = p.stats + (static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q) * 2;
+    const float* st = p.stats + (static_cast<long long>(parts.slot(i)) * kRows + q) * 2;
     if (in_span(st, 8, p.sp_stats, p.status)) m = fmaxf(m, *st);
   }
   float total = 0.0f;
   float2 acc[D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
   for (int i = 0; i < parts.count; ++i) {
-    const long long k = static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q;
+    const long long k = static_cast<long long>(parts.slot(i)) * kRows + q;
     if (!in_span(p.stats + 2 * k, 8, p.sp_stats, p.status) || !in_span(p.part + k * D, 4 * D, p.sp_part, p.status)) continue;
     const float2 st = *reinterpret_cast<const float2*>(p.stats + 2 * k);
-    // a part that saw no key has sum 0 and maximum -inf
+    // a part that saw no key has sum 0, maximum -inf and zeros
     const float w = st.x == m ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(st.x, m), p.scale_log2));
-    if (st.y == 0.0f) continue;
     total = __fmaf_rn(w, st.y, total);
     const float2* src = reinterpret_cast<const float2*>(p.part + k * D) + lane;
 #pragma unroll
@@ -714,7 +779,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 namespace dq {
 constexpr int kK = 3, kV = 2;                     // K and V tiles in flight
 enum { Q_FULL = 0, Q_EMPTY, O_FULL, O_EMPTY, K_FULL, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK,
-       V_EMPTY = V_FULL + kV, S_FULL = V_EMPTY + kV, DP_FULL = S_FULL + 2, DP_FREE, DS_FULL, DONE = DS_FULL + 2, ACC_FREE, DRAIN, BARS };
+       V_EMPTY = V_FULL + kV, S_FULL = V_EMPTY + kV, DP_FULL = S_FULL + 2, DP_FREE, DS_FULL, DONE = DS_FULL + 2, ACC_FREE, DRAIN, BARS = DRAIN + 2 };
 // DS_FULL has a barrier per score buffer: the next block's dS can be there
 // before the issuing warp has looked for this block's.
 __device__ __forceinline__ int arrivals(int i) { return (i >= DP_FREE && i < DONE) || i == ACC_FREE ? 8 : 1; }
@@ -819,71 +884,85 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
-    // Blocks whose scores, dP and dQ products come next, and their stages.
-    RingPos<kK> ks, kd;
-    RingPos<kV> vs;
+    // S(0), S(1), then per block dQ, S(two on): a block's S takes the place of
+    // the dS that dQ has just read
+    RingPos<kK> ks, kd;                           // stages of the next S and dQ
     int gs = 0, done = 0, live = 0;               // blocks with scores, with dQ; tiles
     bool ok = true;
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
-      const bool ragged = g.k_len < p.seq_k;
-      int js = 0, jv = 0;
-      // the block's K (V) has landed, with nothing past the sample's keys
-      auto have = [&](int full, int tile_at, uint32_t phase, int j) {
-        const bool got = c.wait(full, phase);
-        if (got && ragged && (g.begin + j + 1) * kTile > g.k_len)
-          zero_rows<D>(smem + tile_at * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
-        return got;
+      const int n = g.n, ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
+      // block j's K: nothing past the sample's keys
+      auto clean = [&](int j) {
+        if (j >= ragged) zero_rows<D>(smem + (2 + ks.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
       };
-      auto scores = [&]() {
-        if (!have(K_FULL + ks.s, 2 + ks.s, ks.phase, js)) return false;
-        ++js;
-        if (elect_one()) {
-          mma_rows<T, D>(tmem + (gs & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
-          mma_commit(c.bar(S_FULL + (gs & 1)));
-          if (js == g.n) mma_commit(c.bar(Q_EMPTY));
-        }
+      auto scores = [&](int j) {                  // the elected thread
+        mma_rows<T, D>(tmem + (gs & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
+        mma_commit(c.bar(S_FULL + (gs & 1)));
+        if (j + 1 == n) mma_commit(c.bar(Q_EMPTY));
+      };
+      ok = c.wait(Q_FULL, live);
+      for (int j = 0; ok && j < 2 && j < n; ++j) {
+        ok = c.wait(K_FULL + ks.s, ks.phase);
+        if (!ok) break;
+        clean(j);
+        if (elect_one()) scores(j);
         ks.step();
         ++gs;
-        return true;
-      };
-      auto grads = [&]() {
-        if (!have(V_FULL + vs.s, 2 + kK + vs.s, vs.phase, jv)) return false;
-        ++jv;
-        if (elect_one()) {
-          mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + vs.s * kTileBytes<D>);
-          mma_commit(c.bar(DP_FULL));
-          mma_commit(c.bar(V_EMPTY + vs.s));
-          if (jv == g.n) mma_commit(c.bar(O_EMPTY));
-        }
-        vs.step();
-        return true;
-      };
-      ok = c.wait(Q_FULL, live) && scores() && c.wait(O_FULL, live) && grads() && (g.n == 1 || scores());
-      for (int j = 0; ok && j < g.n; ++j, ++done) {
-        if (j + 1 < g.n) {
-          ok = c.wait(DP_FREE, done);
-          tc_fence_after();
-          ok = ok && grads();
-          if (!ok) break;
-        }
+      }
+      for (int j = 0; ok && j < n; ++j, ++done) {
+        const bool more = j + 2 < n;
         // the accumulator has been read for the tile before
-        if (j == 0 && live > 0) ok = c.wait(ACC_FREE, live - 1);
-        ok = ok && c.wait(DS_FULL + (done & 1), done >> 1);
-        tc_fence_after();
+        ok = !more || c.wait(K_FULL + ks.s, ks.phase);
         if (!ok) break;
+        if (more) clean(j + 2);
+        ok = (j > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) && c.wait(DS_FULL + (done & 1), done >> 1);
+        if (!ok) break;
+        tc_fence_after();
         if (elect_one()) {
           mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (done & 1) * kTile, sk + kd.s * kTileBytes<D>, j > 0);
           mma_commit(c.bar(K_EMPTY + kd.s));
-          if (j + 1 == g.n) mma_commit(c.bar(DONE));
+          if (j + 1 == n) mma_commit(c.bar(DONE));
+          if (more) scores(j + 2);
         }
         kd.step();
-        if (j + 2 < g.n) ok = scores();
+        if (more) {
+          ks.step();
+          ++gs;
+        }
       }
       ++live;
     }
     if (!ok) c.drain_mma(DRAIN);
+  } else if (c.warp == kAttnMma2Warp) {
+    // dP of each block, when the block's before has been read
+    RingPos<kV> v;
+    int done = 0, live = 0;
+    bool ok = true;
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      if (g.n == 0) continue;
+      const int n = g.n, ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
+      ok = c.wait(O_FULL, live);
+      for (int j = 0; ok && j < n; ++j, ++done) {
+        ok = c.wait(V_FULL + v.s, v.phase);
+        if (!ok) break;
+        if (j >= ragged) zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+        ok = done == 0 || c.wait(DP_FREE, done - 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + v.s * kTileBytes<D>);
+          mma_commit(c.bar(DP_FULL));
+          mma_commit(c.bar(V_EMPTY + v.s));
+          if (j + 1 == n) mma_commit(c.bar(O_EMPTY));
+        }
+        v.step();
+      }
+      ++live;
+    }
+    if (!ok) c.drain_mma(DRAIN + 1);
   } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // a thread per query and half of the block's keys
@@ -967,8 +1046,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       const bool some = g.n > 0 && limit > 0;
       float* part = p.part + (static_cast<long long>(g.slot) * kTile + r) * D + half * (D / 2);
       char* dst = p.dq + (static_cast<long long>(g.b) * p.seq_q + row) * p.dq_stride + g.h * (D * 2) + half * D;
-      const bool fits = g.slot >= 0 ? in_span(part, 2 * D, p.sp_part, p.status)
-                                    : row < p.seq_q && in_span(dst, D, p.sp_dq, p.status);
+      const int there = p.seq_q - (row - c.lane);   // rows from the warp's first on
+      const bool fits = __all_sync(0xffffffffu, g.slot >= 0 ? in_span(part, 2 * D, p.sp_part, p.status)
+                                                            : row >= p.seq_q || in_span(dst, D, p.sp_dq, p.status));
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         float v[32];
@@ -979,9 +1059,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         }
         if (!fits) continue;
         if (g.slot >= 0)
-          store_part(part + 32 * i, v, some);
+          store_part<D>(part + 32 * i, v, some, c.lane);
         else
-          store_cols<T>(dst + 64 * i, v, p.scale * grad_scale_down(GradScale<T>::kS), some);
+          store_cols<T>(dst + 64 * i, p.dq_stride, there, v, p.scale * grad_scale_down(GradScale<T>::kS), some, c.lane);
       }
     }
     tc_fence_before();
@@ -1009,8 +1089,9 @@ __global__ void __launch_bounds__(256) attn_join_grad_kernel(const __grid_consta
   float2 acc[D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
   for (int i = 0; i < parts.count; ++i) {
-    const float* src = p.part + (static_cast<long long>(parts.slot(p, i, ctas)) * kRows + q) * D;
+    const float* src = p.part + (static_cast<long long>(parts.slot(i)) * kRows + q) * D;
     if (!in_span(src, 4 * D, p.sp_part, p.status)) continue;
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) acc[e] = __fadd2_rn(acc[e], reinterpret_cast<const float2*>(src)[lane + 32 * e]);
@@ -1036,10 +1117,11 @@ namespace dkv {
 constexpr int kQ = 3, kO = 2;                     // Q and dO tiles in flight
 enum { K_FULL = 0, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ,
        O_EMPTY = O_FULL + kO, S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, ROWS_FREE = ROWS + 2,
-       DONE = ROWS_FREE + 2, ACC_FREE, DRAIN, BARS };
+       DONE = ROWS_FREE + 2, ACC_FREE, DRAIN, BARS = DRAIN + 2 };
 __device__ __forceinline__ int arrivals(int i) {
-  return i == P_FULL || i == DS_FULL || i == ACC_FREE || (i >= ROWS_FREE && i < DONE) ? 8
-                                                                                     : (i >= ROWS && i < ROWS_FREE ? 2 : 1);
+  if (i == P_FULL || i == DS_FULL || i == ACC_FREE || (i >= ROWS_FREE && i < DONE)) return 8;
+  // both chains are done with a tile, with the accumulators
+  return (i >= Q_EMPTY && i < O_FULL) || (i >= O_EMPTY && i < S_FULL) || i == DONE ? 2 : 1;
 }
 constexpr int kRowBytes = 2 * 2 * kTile * 4;      // two buffers of (lse, delta) of a tile's queries
 template <int D>
@@ -1153,106 +1235,136 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (c.warp == kAttnMmaWarp) {
-    // Blocks whose scores, dP, dV and dK products come next.
-    RingPos<kQ> qs, qd;
-    RingPos<kO> os, od;
+  } else if (c.warp == kAttnMmaWarp || c.warp == kAttnMma2Warp) {
+    // Two chains of the same form: S(0), then per block dV += P^T dO, S(next);
+    // dP(0), then per block dK += dS^T Q, dP(next).  (`a`: the tile of the
+    // chain's first product, `b`: of its second.)
+    const bool first_chain = c.warp == kAttnMmaWarp;
+    RingPos<kQ> q;
+    RingPos<kO> o;
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
+      const int n = g.n;
       const bool ragged = g.q_len < p.seq_q;
-      int ts = g.t0, to = g.t0, is = 0, ig = 0;   // query tiles and blocks of the scores, of dP
-      // the tile has landed, with nothing past the sample's queries
-      auto have = [&](int full, int tile_at, uint32_t phase, int& t) {
-        const bool got = c.wait(full, phase);
-        if (got && ragged && (t + 1) * kTile > g.q_len)
-          zero_rows<D>(smem + tile_at * kTileBytes<D>, g.q_len - t * kTile, c.lane);
-        if (++t == g.end) t = g.first;
-        return got;
+      int t = g.t0;                               // the block's query tile
+      // A tile that has landed: nothing past the sample's queries.  (Both
+      // chains write the zeros: the same ones, before either gives the tile
+      // back.)
+      auto clean_q = [&](int tile) {
+        if (ragged && (tile + 1) * kTile > g.q_len)
+          zero_rows<D>(smem + (2 + q.s) * kTileBytes<D>, g.q_len - tile * kTile, c.lane);
       };
-      auto scores = [&]() {
-        if (!have(Q_FULL + qs.s, 2 + qs.s, qs.phase, ts)) return false;
-        ++is;
+      auto clean_o = [&](int tile) {
+        if (ragged && (tile + 1) * kTile > g.q_len)
+          zero_rows<D>(smem + (2 + kQ + o.s) * kTileBytes<D>, g.q_len - tile * kTile, c.lane);
+      };
+      if (first_chain) {
+        ok = c.wait(K_FULL, live) && c.wait(Q_FULL + q.s, q.phase);
+        if (!ok) break;
+        clean_q(t);
         if (elect_one()) {
-          mma_rows<T, D>(tmem, sk, sq + qs.s * kTileBytes<D>);
+          mma_rows<T, D>(tmem, sk, sq + q.s * kTileBytes<D>);
           mma_commit(c.bar(S_FULL));
-          if (is == g.n) mma_commit(c.bar(K_EMPTY));
+          mma_commit(c.bar(Q_EMPTY + q.s));
+          if (n == 1) mma_commit(c.bar(K_EMPTY));
         }
-        qs.step();
-        return true;
-      };
-      auto grads = [&]() {
-        if (!have(O_FULL + os.s, 2 + kQ + os.s, os.phase, to)) return false;
-        ++ig;
-        if (elect_one()) {
-          mma_rows<T, D>(tmem + kTile, sv, sdo + os.s * kTileBytes<D>);
-          mma_commit(c.bar(DP_FULL));
-          if (ig == g.n) mma_commit(c.bar(V_EMPTY));
-        }
-        os.step();
-        return true;
-      };
-      ok = c.wait(K_FULL, live) && scores() && c.wait(V_FULL, live) && grads();
-      for (int i = 0; ok && i < g.n; ++i, ++done) {
-        // the accumulators have been read for the tile before
-        if (i == 0 && live > 0) ok = c.wait(ACC_FREE, live - 1);
-        ok = ok && c.wait(P_FULL, done);
-        tc_fence_after();
-        if (!ok) break;
-        if (elect_one()) {
-          mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + od.s * kTileBytes<D>, i > 0);
-          mma_commit(c.bar(O_EMPTY + od.s));
-        }
-        od.step();
-        if (i + 1 < g.n) {
-          ok = scores();
+        q.step();
+        for (int i = 0; i < n; ++i, ++done) {
+          const bool more = i + 1 < n;
+          const int next = t + 1 == g.end ? g.first : t + 1;
+          // the accumulators have been read for the tile before
+          ok = c.wait(O_FULL + o.s, o.phase) && (!more || c.wait(Q_FULL + q.s, q.phase));
           if (!ok) break;
+          clean_o(t);
+          if (more) clean_q(next);
+          ok = (i > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) && c.wait(P_FULL, done);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_cols<T, D, true>(tmem + 2 * kTile, tmem, sdo + o.s * kTileBytes<D>, i > 0);
+            mma_commit(c.bar(O_EMPTY + o.s));
+            if (!more) mma_commit(c.bar(DONE));
+            if (more) {
+              mma_rows<T, D>(tmem, sk, sq + q.s * kTileBytes<D>);
+              mma_commit(c.bar(S_FULL));
+              mma_commit(c.bar(Q_EMPTY + q.s));
+              if (i + 2 == n) mma_commit(c.bar(K_EMPTY));
+            }
+          }
+          o.step();
+          if (more) q.step();
+          t = next;
         }
-        ok = c.wait(DS_FULL, done);
-        tc_fence_after();
+      } else {
+        ok = c.wait(V_FULL, live) && c.wait(O_FULL + o.s, o.phase);
         if (!ok) break;
+        clean_o(t);
         if (elect_one()) {
-          mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + qd.s * kTileBytes<D>, i > 0);
-          mma_commit(c.bar(Q_EMPTY + qd.s));
-          if (i + 1 == g.n) mma_commit(c.bar(DONE));
+          mma_rows<T, D>(tmem + kTile, sv, sdo + o.s * kTileBytes<D>);
+          mma_commit(c.bar(DP_FULL));
+          mma_commit(c.bar(O_EMPTY + o.s));
+          if (n == 1) mma_commit(c.bar(V_EMPTY));
         }
-        qd.step();
-        if (i + 1 < g.n) ok = grads();
+        o.step();
+        for (int i = 0; i < n; ++i, ++done) {
+          const bool more = i + 1 < n;
+          const int next = t + 1 == g.end ? g.first : t + 1;
+          ok = c.wait(Q_FULL + q.s, q.phase) && (!more || c.wait(O_FULL + o.s, o.phase));
+          if (!ok) break;
+          clean_q(t);
+          if (more) clean_o(next);
+          ok = (i > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) && c.wait(DS_FULL, done);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_cols<T, D, true>(tmem + 3 * kTile, tmem + kTile, sq + q.s * kTileBytes<D>, i > 0);
+            mma_commit(c.bar(Q_EMPTY + q.s));
+            if (!more) mma_commit(c.bar(DONE));
+            if (more) {
+              mma_rows<T, D>(tmem + kTile, sv, sdo + o.s * kTileBytes<D>);
+              mma_commit(c.bar(DP_FULL));
+              mma_commit(c.bar(O_EMPTY + o.s));
+              if (i + 2 == n) mma_commit(c.bar(V_EMPTY));
+            }
+          }
+          q.step();
+          if (more) o.step();
+          t = next;
+        }
       }
       ++live;
     }
-    if (!ok) c.drain_mma(DRAIN);
-  } else if (c.warp >= kAttnMmaWarp) {
-    // Warps 10 and 11 hand round kP - lse (log2) and -delta kC of the blocks'
+    if (!ok) c.drain_mma(DRAIN + (first_chain ? 0 : 1));
+  } else if (c.warp == kAttnRowWarp) {
+    // Warp 11 hands round kP - lse (log2) and -delta kC of the blocks'
     // queries, up to two blocks ahead.  A query past the length or with no
     // key gets -inf: p = 0.
-    const bool second = c.warp == kAttnMmaWarp + 3;
-    const float* source = second ? p.delta : p.lse;
-    const MemSpan& sp_source = second ? p.sp_delta : p.sp_lse;
     int done = 0;
     bool ok = true;
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       int h = g.h0, t = g.t0;
       for (int i = 0; i < g.n; ++i, ++done) {
-        const float* at = source + (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
-        float v[4];
+        const long long at = (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
+        float l[4], d[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int q = t * kTile + 32 * e + c.lane;
-          v[e] = second ? 0.0f : -INFINITY;
-          if (q < g.q_len && in_span(at + 32 * e, 4, sp_source, p.status)) v[e] = at[32 * e];
+          const bool valid = t * kTile + 32 * e + c.lane < g.q_len;
+          l[e] = valid && in_span(p.lse + at + 32 * e, 4, p.sp_lse, p.status) ? p.lse[at + 32 * e] : -INFINITY;
+          d[e] = valid && in_span(p.delta + at + 32 * e, 4, p.sp_delta, p.status) ? p.delta[at + 32 * e] : 0.0f;
         }
         // the block before last has been read
         ok = done < 2 || c.wait(ROWS_FREE + (done & 1), (done >> 1) - 1);
         if (!ok) break;
-        float* out = rows + (done & 1) * 2 * kTile + (second ? kTile : 0) + c.lane;
+        float* out = rows + (done & 1) * 2 * kTile + c.lane;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          out[32 * e] = second ? -v[e] * kGradC<T>
-                               : (v[e] == -INFINITY ? -INFINITY : __fmaf_rn(v[e], -kLog2e, GradScale<T>::kP));
+        for (int e = 0; e < 4; ++e) {
+          out[32 * e] = l[e] == -INFINITY ? -INFINITY : __fmaf_rn(l[e], -kLog2e, GradScale<T>::kP);
+          out[kTile + 32 * e] = -d[e] * kGradC<T>;
+        }
         __syncwarp();
         if (c.lane == 0) mbar_arrive(c.bar(ROWS + (done & 1)));
         if (++t == g.end) {
@@ -1261,7 +1373,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         }
       }
     }
-  } else {
+  } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // a thread per key and half of the block's queries
     const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
@@ -1364,8 +1476,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       float* part = p.part + ((static_cast<long long>(g.slot) * 2 + half) * kTile + r) * D;
       char* dst = half ? p.dk + (static_cast<long long>(g.b) * p.seq_k + key) * p.dk_stride + g.h * (D * 2)
                        : p.dv + (static_cast<long long>(g.b) * p.seq_k + key) * p.dv_stride + g.h * (D * 2);
-      const bool fits = g.slot >= 0 ? in_span(part, 4 * D, p.sp_part, p.status)
-                                    : key < p.seq_k && in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status);
+      const int there = p.seq_k - (key - c.lane);   // rows from the warp's first on
+      const bool fits =
+          __all_sync(0xffffffffu, g.slot >= 0 ? in_span(part, 4 * D, p.sp_part, p.status)
+                                              : key >= p.seq_k || in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float v[32];
@@ -1376,9 +1490,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         }
         if (!fits) continue;
         if (g.slot >= 0)
-          store_part(part + 32 * i, v, some);
+          store_part<D>(part + 32 * i, v, some, c.lane);
         else
-          store_cols<T>(dst + 64 * i, v, f, some);
+          store_cols<T>(dst + 64 * i, half ? p.dk_stride : p.dv_stride, there, v, f, some, c.lane);
       }
     }
     tc_fence_before();

@@ -39,9 +39,11 @@ qknr_status encoder(EncodeFn* out) {
   return QKNR_OK;
 }
 
-// Token rows as [batch][heads][D/64][rows][64], boxes of 128 rows of one
-// head.  Rows past the sequence read as zero.
-qknr_status make_map(CUtensorMap* map, const qknr_attn_args* a, const void* base, long long stride, int seq, int heads) {
+// Token rows as [batch][heads][D/64][rows][64], boxes of `box_rows` rows of
+// one head, all its columns or `cols` of 64.  Rows past the sequence read as
+// zero and are not written.
+qknr_status make_map(CUtensorMap* map, const qknr_attn_args* a, const void* base, long long stride, int seq, int heads,
+                     int box_rows = qknr::kTile, int cols = 0) {
   EncodeFn enc;
   const qknr_status st = encoder(&enc);
   if (st != QKNR_OK) return st;
@@ -49,11 +51,13 @@ qknr_status make_map(CUtensorMap* map, const qknr_attn_args* a, const void* base
   const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(seq), D / 64, static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(a->batch)};
   const cuuint64_t strides[4] = {row, 128, D * 2, row * seq};
-  const cuuint32_t box[5] = {64, qknr::kTile, static_cast<cuuint32_t>(D / 64), 1, 1}, ones[5] = {1, 1, 1, 1, 1};
+  const cuuint32_t box[5] = {cols ? static_cast<cuuint32_t>(cols) : 64, static_cast<cuuint32_t>(box_rows),
+                             cols ? 1 : static_cast<cuuint32_t>(D / 64), 1, 1},
+                   ones[5] = {1, 1, 1, 1, 1};
   const CUresult r = enc(map, a->dtype == QKNR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                          5, const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(QKNR_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
   return QKNR_OK;
 }
@@ -333,6 +337,7 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
     if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
   }
+  if ((st = make_map(&kp.map_out, a, a->o, o.stride, a->seq_q, a->n_heads_q, qknr::kOutRows, 64)) != QKNR_OK) return st;
   const Kernels fn = kernels_for(a);
   st = launch(fn.fwd, cut.ctas, qknr::kAttnThreads, fn.fwd_smem, a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
   if (st != QKNR_OK) return st;
@@ -388,6 +393,8 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   if (a->seq_q > 0) {
     if ((st = make_map(&kp.map_q, a, a->q, q.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
     if ((st = make_map(&kp.map_do, a, a->dout, g.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
+    if ((st = make_map(&kp.map_out, a, a->dq, dq.stride, a->seq_q, a->n_heads_q, qknr::kOutRows, a->head_dim / 2)) != QKNR_OK)
+      return st;
   }
   if (a->seq_k > 0) {
     if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;

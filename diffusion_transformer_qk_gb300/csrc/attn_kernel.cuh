@@ -31,6 +31,7 @@ namespace qknr {
 
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
+  CUtensorMap map_out;        // o or dq: boxes of kOutRows rows of a warp
   const char* o_in;           // backward: the forward's output
   const char* dout;
   char* o;
@@ -111,6 +112,16 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   }
 }
 
+// the same with A 16-bit in tensor memory
+template <typename T, int D>
+__device__ __forceinline__ void mma_rows_ts(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = mma_desc<T>(kTile, kTile, false);
+  const uint32_t db = desc_k_major(b);
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k)
+    mma_ts(d, a + k * 8, db + (((k / 4) * (kTile * 128) + (k % 4) * 32) >> 4), idesc, k > 0);
+}
+
 // D[128 x D] (+)= A[128 x 128] B[128 x D]: A 16-bit in tensor memory (SPLIT:
 // its second 64 columns start 64 columns on), B contracted over its rows
 template <typename T, int D, bool SPLIT>
@@ -133,6 +144,11 @@ struct RingPos {
       s = 0;
       phase ^= 1u;
     }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    s += n;
+    phase ^= static_cast<uint32_t>(s / N) & 1u;
+    s %= N;
   }
 };
 
@@ -254,9 +270,30 @@ __device__ __forceinline__ void attn_cut(const AttnWork& w, int n, int& begin, i
 
 // Epilogue stores.  A thread holds pieces of its own row; stored as they are,
 // every store instruction touches 32 rows, a cache line each (6000 cycles for
-// a 128 x 128 tile).  So the four lanes of a quad first swap 16-byte chunks:
-// afterwards v[k] is chunk (lane & 3) of the quad's k-th row, and an
-// instruction writes 64 bytes of each of eight rows.
+// a 128 x 128 tile).  Where shared memory is left, a warp stages its rows
+// there and one TMA store writes them.
+constexpr int kOutRows = 32;
+
+// 32 accumulator values of each row of a warp, times f (zero where the row has
+// no value), in the output's type: chunks [first, first + 4) of the staged
+// rows, COLS values each, where the map's swizzle expects them.
+template <typename T, int COLS>
+__device__ __forceinline__ void stage_cols(unsigned char* stage, int first, const float (&v)[32], float f, bool some, int lane) {
+  const int flip = COLS == 64 ? lane & 7 : (lane >> 1) & 3;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint4 w;
+    uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      ww[i] = some ? pack2<T>(__fmul_rn(v[c * 8 + 2 * i], f), __fmul_rn(v[c * 8 + 2 * i + 1], f)) : 0u;
+    *reinterpret_cast<uint4*>(stage + lane * (COLS * 2) + (((first + c) ^ flip) << 4)) = w;
+  }
+}
+
+// Elsewhere the four lanes of a quad first swap 16-byte chunks: afterwards
+// v[k] is chunk (lane & 3) of the quad's k-th row, and an instruction writes 64
+// bytes of each of eight rows (3700 cycles).
 __device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int lane) {
 #pragma unroll
   for (int step = 1; step <= 2; step <<= 1) {
@@ -329,8 +366,9 @@ enum { Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = K_FULL + kK, V_FULL = K_EM
 __device__ __forceinline__ int arrivals(int i) {
   return (i >= P_FULL && i < O_DONE) || (i >= O_FREE && i < DRAIN) ? 4 : 1;
 }
+constexpr int kStage = kOutRows * 128;            // a warp's staged rows: 64 columns
 template <int D>
-constexpr int kCtl = (2 + kK + kV) * kTileBytes<D>;
+constexpr int kCtl = (2 + kK + kV) * kTileBytes<D> + 8 * kStage;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
 // The running maximum is only raised, and the accumulator rescaled, when the
@@ -409,6 +447,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       bool ok = true;
       Seg g;
       for (int s = 0; ok && segment(s, g); ++s) {
+        {
+          // the next tile's queries come from HBM: on their way while this one's keys come from L2
+          Seg next;
+          if (segment(s + 1, next))
+            for (int t = 0; t < 2; ++t)
+              if (next.nb[t]) tma_prefetch_tile(&p.map_q, next.q0 + t * kTile, next.h, next.b);
+        }
         for (int t = 0; t < 2 && ok; ++t) {
           if (g.nb[t] == 0) continue;
           ok = c.wait1(Q_EMPTY + t, uses[t] + 1);
@@ -517,6 +562,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     const int t = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * kTile + lanes;
+    unsigned char* stage = smem + (2 + kK + kV) * kTileBytes<D> + c.warp * kStage;
     const float sl = p.scale_log2, slack = kSlack / sl;
     int done = 0;                                 // blocks so far
     bool ok = true;
@@ -604,9 +650,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       const float inv = some ? __frcp_rn(total) : 0.0f;
       segment(sg, g);                             // again: the loop above has no registers to keep it in
       const int row = g.q0 + t * kTile + r;
-      char* dst = p.o + (static_cast<long long>(g.b) * p.seq_q + row) * p.o_stride + g.h * (D * 2);
       const long long at = static_cast<long long>(g.slot) * kRows + t * kTile + r;   // a part's row
-      const int there = p.seq_q - (row - c.lane);   // rows from the warp's first on
       if (g.slot >= 0) {
         // a part of the keys: unnormalised, with its maximum and sum
         if (in_span(p.stats + 2 * at, 8, p.sp_stats, p.status))
@@ -616,9 +660,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         if (row < p.seq_q && in_span(p.lse + l, 4, p.sp_lse, p.status))
           p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
       }
-      // checked builds: the rows this warp writes
-      const bool fits = __all_sync(0xffffffffu, g.slot >= 0 ? in_span(p.part + at * D, 4 * D, p.sp_part, p.status)
-                                                            : row >= p.seq_q || in_span(dst, D * 2, p.sp_o, p.status));
+      // checked builds: the rows of a part that this warp writes (a store by TMA stays inside its map)
+      const bool fits = __all_sync(0xffffffffu, g.slot < 0 || in_span(p.part + at * D, 4 * D, p.sp_part, p.status));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
@@ -628,12 +671,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           if (i == D / 32 - 1) c.arrive(O_FREE + t);
         }
         if (!fits) continue;
-        if (g.slot >= 0)
+        if (g.slot >= 0) {
           store_part<D>(p.part + at * D + 32 * i, o, n > 0, c.lane);
-        else
-          store_cols<T>(dst + 64 * i, p.o_stride, there, o, inv, some, c.lane);
+          continue;
+        }
+        if (i % 2 == 0) {
+          // the store before has read the stage
+          if (c.lane == 0) tma_store_wait_read();
+          __syncwarp();
+        }
+        stage_cols<T, 64>(stage, 4 * (i % 2), o, inv, some, c.lane);
+        if (i % 2 == 1) {
+          fence_async_shared();
+          __syncwarp();
+          if (c.lane == 0 && row < p.seq_q) tma_store_box(&p.map_out, smem_addr(stage), 0, row, i / 2, g.h, g.b);
+        }
       }
     }
+    if (c.lane == 0) tma_store_wait();
     tc_fence_before();
   }
   __syncthreads();
@@ -773,18 +828,28 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------------------
 // backward, dq: a tile is 128 queries of one head, its iterations blocks of
-// 128 keys.  Per block S = Q K^T, dP = dO V^T, dQ += dS K.  The scores have
-// two buffers, so the next block's S is there when this block's dS is done.
+// 128 keys.  Per block S = Q K^T, dP = dO V^T, dQ += dS K.
+//
+// Tensor memory holds S, dP, dQ, dS and Q (columns 0, 128, 256, 384, 448).  Q
+// as a left operand in tensor memory takes 32 KB off the shared memory that a
+// block's products read (160 KB, a quarter more than the tensor cores' time
+// for it) and leaves room for a third V tile in flight; it comes through the
+// K ring as the tile's first item, and the threads that own its rows copy it.
+// S is free for the next block as soon as it has been read into registers.
 
 namespace dq {
-constexpr int kK = 3, kV = 2;                     // K and V tiles in flight
-enum { Q_FULL = 0, Q_EMPTY, O_FULL, O_EMPTY, K_FULL, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK,
-       V_EMPTY = V_FULL + kV, S_FULL = V_EMPTY + kV, DP_FULL = S_FULL + 2, DP_FREE, DS_FULL, DONE = DS_FULL + 2, ACC_FREE, DRAIN, BARS = DRAIN + 2 };
-// DS_FULL has a barrier per score buffer: the next block's dS can be there
-// before the issuing warp has looked for this block's.
-__device__ __forceinline__ int arrivals(int i) { return (i >= DP_FREE && i < DONE) || i == ACC_FREE ? 8 : 1; }
+constexpr int kK = 3, kV = 2;                     // K (and Q) and V tiles in flight
+constexpr int kColS = 0, kColDp = kTile, kColDq = 2 * kTile, kColDs = 3 * kTile, kColQ = 3 * kTile + 64;
+enum { O_FULL = 0, O_EMPTY, K_FULL, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
+       Q_READY = V_EMPTY + kV, S_FULL, S_FREE, DP_FULL, DP_FREE, DS_FULL, DS_FREE, DONE, ACC_FREE, DRAIN,
+       BARS = DRAIN + 2 };
+__device__ __forceinline__ int arrivals(int i) {
+  return i == Q_READY || i == S_FREE || i == DP_FREE || i == DS_FULL || i == ACC_FREE ? 8 : 1;
+}
 template <int D>
-constexpr int kCtl = (2 + kK + kV) * kTileBytes<D>;
+constexpr int kStage = kOutRows * D;              // a warp's staged rows: D / 2 columns
+template <int D>
+constexpr int kCtl = (1 + kK + kV) * kTileBytes<D> + 8 * kStage<D>;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
 
@@ -836,33 +901,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.n = end - g.begin;
     return true;
   };
-  const uint32_t sq = c.base, sdo = c.base + kTileBytes<D>, sk = c.base + 2 * kTileBytes<D>,
-                 sv = c.base + (2 + kK) * kTileBytes<D>;
+  const uint32_t sdo = c.base, sk = c.base + kTileBytes<D>, sv = c.base + (1 + kK) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
   if (c.warp == kAttnLoadWarp) {
     if (c.lane == 0 && !(p.flags & 1u)) {         // test only: issue nothing
       RingPos<kK> k;
       RingPos<kV> v;
-      int uses = 0, ik = 0, iv = 0, io = 0;
+      int ik = 0, iv = 0, io = 0;
       bool ok = true;
       Seg g;
       for (int s = 0; ok && segment(s, g); ++s) {
+        {
+          // the next tile's queries come from HBM: on their way while this one's keys come from L2
+          Seg next;
+          if (segment(s + 1, next) && next.n > 0) {
+            tma_prefetch_tile(&p.map_q, next.q0, next.h, next.b);
+            tma_prefetch_tile(&p.map_do, next.q0, next.h, next.b);
+          }
+        }
         if (g.n == 0) continue;
-        ok = c.wait1(Q_EMPTY, uses + 1);
-        if (!ok) break;
-        mbar_arrive_expect_tx(c.bar(Q_FULL), kTileBytes<D>);
-        tma_load_tile(sq, &p.map_q, g.q0, g.h, g.b, c.bar(Q_FULL));
-        ++uses;
         const int hk = g.h / p.group;
-        for (int j = 0; ok && j < g.n; ++j, k.step(), v.step()) {
+        for (int j = -1; j < g.n; ++j) {
+          // Q, then K blocks
           ok = c.wait1(K_EMPTY + k.s, k.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
-          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
+          if (j < 0)
+            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_q, g.q0, g.h, g.b, c.bar(K_FULL + k.s));
+          else
+            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
           ++ik;
+          k.step();
+          if (j < 0) continue;
           if (j == 0) {
-            ok = c.wait1(O_EMPTY, uses);
+            ok = c.wait1(O_EMPTY, io + 1);
             if (!ok) break;
             mbar_arrive_expect_tx(c.bar(O_FULL), kTileBytes<D>);
             tma_load_tile(sdo, &p.map_do, g.q0, g.h, g.b, c.bar(O_FULL));
@@ -873,65 +946,62 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
           mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
           tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
           ++iv;
+          v.step();
         }
       }
       if (!ok || *abort_flag) {
         c.drain(K_FULL, kK, ik);
         c.drain(V_FULL, kV, iv);
-        c.drain(Q_FULL, 1, uses);
         c.drain(O_FULL, 1, io);
       }
     }
     __syncwarp();
   } else if (c.warp == kAttnMmaWarp) {
-    // S(0), S(1), then per block dQ, S(two on): a block's S takes the place of
-    // the dS that dQ has just read
+    // S(0), then per block S(next), when S has been read, and dQ
     RingPos<kK> ks, kd;                           // stages of the next S and dQ
-    int gs = 0, done = 0, live = 0;               // blocks with scores, with dQ; tiles
+    int done = 0, live = 0;                       // blocks of the tiles before, tiles
     bool ok = true;
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
       const int n = g.n, ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
-      // block j's K: nothing past the sample's keys
-      auto clean = [&](int j) {
-        if (j >= ragged) zero_rows<D>(smem + (2 + ks.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
-      };
-      auto scores = [&](int j) {                  // the elected thread
-        mma_rows<T, D>(tmem + (gs & 1) * kTile, sq, sk + ks.s * kTileBytes<D>);
-        mma_commit(c.bar(S_FULL + (gs & 1)));
-        if (j + 1 == n) mma_commit(c.bar(Q_EMPTY));
-      };
-      ok = c.wait(Q_FULL, live);
-      for (int j = 0; ok && j < 2 && j < n; ++j) {
-        ok = c.wait(K_FULL + ks.s, ks.phase);
-        if (!ok) break;
-        clean(j);
-        if (elect_one()) scores(j);
+      // block j's S: its K has landed, with nothing past the sample's keys
+      auto scores = [&](int j) {
+        if (!c.wait(K_FULL + ks.s, ks.phase)) return false;
+        if (j >= ragged) zero_rows<D>(smem + (1 + ks.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+        if (j > 0 && !c.wait(S_FREE, done + j - 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_rows_ts<T, D>(tmem + kColS, tmem + kColQ, sk + ks.s * kTileBytes<D>);
+          mma_commit(c.bar(S_FULL));
+        }
         ks.step();
-        ++gs;
-      }
-      for (int j = 0; ok && j < n; ++j, ++done) {
-        const bool more = j + 2 < n;
+        return true;
+      };
+      // Q has been copied: its place in the ring is free
+      ok = c.wait(Q_READY, live);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) mbar_arrive(c.bar(K_EMPTY + ks.s));
+      __syncwarp();
+      ks.step();
+      kd.step();
+      ok = scores(0);
+      for (int j = 0; ok && j < n; ++j) {
+        if (j + 1 < n) ok = scores(j + 1);
         // the accumulator has been read for the tile before
-        ok = !more || c.wait(K_FULL + ks.s, ks.phase);
-        if (!ok) break;
-        if (more) clean(j + 2);
-        ok = (j > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) && c.wait(DS_FULL + (done & 1), done >> 1);
+        ok = ok && (j > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) && c.wait(DS_FULL, done + j);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_cols<T, D, true>(tmem + 3 * kTile, tmem + (done & 1) * kTile, sk + kd.s * kTileBytes<D>, j > 0);
+          mma_cols<T, D, false>(tmem + kColDq, tmem + kColDs, sk + kd.s * kTileBytes<D>, j > 0);
           mma_commit(c.bar(K_EMPTY + kd.s));
+          mma_commit(c.bar(DS_FREE));
           if (j + 1 == n) mma_commit(c.bar(DONE));
-          if (more) scores(j + 2);
         }
         kd.step();
-        if (more) {
-          ks.step();
-          ++gs;
-        }
       }
+      done += n;
       ++live;
     }
     if (!ok) c.drain_mma(DRAIN);
@@ -948,12 +1018,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       for (int j = 0; ok && j < n; ++j, ++done) {
         ok = c.wait(V_FULL + v.s, v.phase);
         if (!ok) break;
-        if (j >= ragged) zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+        if (j >= ragged) zero_rows<D>(smem + (1 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
         ok = done == 0 || c.wait(DP_FREE, done - 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          mma_rows<T, D>(tmem + 2 * kTile, sdo, sv + v.s * kTileBytes<D>);
+          mma_rows<T, D>(tmem + kColDp, sdo, sv + v.s * kTileBytes<D>);
           mma_commit(c.bar(DP_FULL));
           mma_commit(c.bar(V_EMPTY + v.s));
           if (j + 1 == n) mma_commit(c.bar(O_EMPTY));
@@ -968,6 +1038,44 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     // a thread per query and half of the block's keys
     const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
+    RingPos<kK> k;                                // the K ring's place of the next tile's Q
+    bool ready = false;                           // it has been copied
+    // the next tile's Q: this thread's half of its row, to tensor memory
+    auto copy_q = [&]() {
+      if (!c.wait(K_FULL + k.s, k.phase)) return false;
+      const unsigned char* row_q = smem + (1 + k.s) * kTileBytes<D> + r * 128;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        // 32 values: four chunks of the row, where the swizzle has put them
+        const int first = half * (D / 16) + 4 * i;
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int chunk = first + e;
+          const uint4 x =
+              *reinterpret_cast<const uint4*>(row_q + (chunk >> 3) * (kTile * 128) + (((chunk & 7) ^ (r & 7)) << 4));
+          w[4 * e] = x.x;
+          w[4 * e + 1] = x.y;
+          w[4 * e + 2] = x.z;
+          w[4 * e + 3] = x.w;
+        }
+        tmem_store16(tmem + kColQ + first * 4 + lanes, w);
+      }
+      tmem_wait_store();
+      c.arrive(Q_READY);
+      return true;
+    };
+    // a tile's row: log-sum and delta
+    auto row_stats = [&](const Seg& g, float& lse, float& delta) {
+      const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + g.q0 + r;
+      lse = delta = 0.0f;
+      if (g.q0 + r < p.seq_q && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
+        lse = p.lse[at];
+        delta = p.delta[at];
+      }
+    };
+    unsigned char* stage = smem + (1 + kK + kV) * kTileBytes<D> + c.warp * kStage<D>;
+    float lse = 0.0f, delta = 0.0f;
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
     Seg g;
@@ -975,19 +1083,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       const int row = g.q0 + r;
       int limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
       limit = limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit);
-      float lse2 = INFINITY, delta = 0.0f;        // p = 0 for a row that sees nothing
-      const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
-      if (limit > 0 && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
-        const float v = p.lse[at];
-        lse2 = v == -INFINITY ? INFINITY : __fmul_rn(v, kLog2e);
-        delta = p.delta[at];
-      }
+      if (!ready) row_stats(g, lse, delta);
+      // p = 0 for a row that sees nothing
+      const float lse2 = limit == 0 || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
       const float nl = GradScale<T>::kP - lse2, nd = -delta * kGradC<T>;
       const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
                    C = make_float2(kGradC<T>, kGradC<T>);
+      if (g.n > 0) {
+        if (!ready) ok = copy_q();
+        if (!ok) break;
+        k.skip(g.n + 1);
+        ready = false;
+      }
       for (int j = 0; j < g.n; ++j, ++done) {
-        const uint32_t ts = tmem + (done & 1) * kTile + half * 64 + lanes, tdp = tmem + 2 * kTile + half * 64 + lanes;
-        ok = c.wait(S_FULL + (done & 1), done >> 1);
+        const uint32_t ts = tmem + kColS + half * 64 + lanes, tdp = tmem + kColDp + half * 64 + lanes;
+        ok = c.wait(S_FULL, done);
         if (!ok) break;
         tc_fence_after();
         float s[2][32];
@@ -995,6 +1105,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         tmem_load32(ts + 32, s[1]);
         tmem_wait_load(s[0]);
         tmem_loaded(s[1]);
+        c.arrive(S_FREE);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -1023,6 +1134,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
               d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
             }
         }
+        if (done > 0) {
+          // dQ has read the dS of the block before
+          ok = c.wait(DS_FREE, done - 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t w[16];
@@ -1032,28 +1149,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
                                         __ffma2_rn(make_float2(d[i][2 * e], d[i][2 * e + 1]), C, ND));
             w[e] = pack2<T>(x.x, x.y);
           }
-          tmem_store16(ts + 16 * i, w);
+          tmem_store16(tmem + kColDs + half * 32 + 16 * i + lanes, w);
         }
         tmem_wait_store();
-        c.arrive(DS_FULL + (done & 1));
+        c.arrive(DS_FULL);
       }
       if (!ok) break;
       if (g.n > 0) {
+        // Every S of this tile is done: the next one's Q can take Q's place,
+        // and its first products run under this one's epilogue.
+        ready = segment(sg + 1, g) && g.n > 0;
+        if (ready) {
+          row_stats(g, lse, delta);
+          ok = copy_q();
+        }
+        if (!ok) break;
+        segment(sg, g);
         ok = c.wait(DONE, live++);
         if (!ok) break;
         tc_fence_after();
       }
       const bool some = g.n > 0 && limit > 0;
       float* part = p.part + (static_cast<long long>(g.slot) * kTile + r) * D + half * (D / 2);
-      char* dst = p.dq + (static_cast<long long>(g.b) * p.seq_q + row) * p.dq_stride + g.h * (D * 2) + half * D;
-      const int there = p.seq_q - (row - c.lane);   // rows from the warp's first on
-      const bool fits = __all_sync(0xffffffffu, g.slot >= 0 ? in_span(part, 2 * D, p.sp_part, p.status)
-                                                            : row >= p.seq_q || in_span(dst, D, p.sp_dq, p.status));
+      // checked builds: the rows of a part that this warp writes (a store by TMA stays inside its map)
+      const bool fits = __all_sync(0xffffffffu, g.slot < 0 || in_span(part, 2 * D, p.sp_part, p.status));
+      if (g.slot < 0) {
+        // the store before has read the stage
+        if (c.lane == 0) tma_store_wait_read();
+        __syncwarp();
+      }
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
         float v[32];
         if (g.n > 0) {
-          tmem_load32(tmem + 3 * kTile + half * (D / 2) + 32 * i + lanes, v);
+          tmem_load32(tmem + kColDq + half * (D / 2) + 32 * i + lanes, v);
           tmem_wait_load(v);
           if (i == D / 64 - 1) c.arrive(ACC_FREE);
         }
@@ -1061,9 +1190,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (g.slot >= 0)
           store_part<D>(part + 32 * i, v, some, c.lane);
         else
-          store_cols<T>(dst + 64 * i, p.dq_stride, there, v, p.scale * grad_scale_down(GradScale<T>::kS), some, c.lane);
+          stage_cols<T, D / 2>(stage, 4 * i, v, p.scale * grad_scale_down(GradScale<T>::kS), some, c.lane);
+      }
+      if (g.slot < 0) {
+        fence_async_shared();
+        __syncwarp();
+        // half of the columns: the second 64 of 128, or 32 of 64
+        if (c.lane == 0 && row < p.seq_q)
+          tma_store_box(&p.map_out, smem_addr(stage), D == 128 ? 0 : half * 32, row, D == 128 ? half : 0, g.h, g.b);
       }
     }
+    if (c.lane == 0) tma_store_wait();
     tc_fence_before();
   }
   __syncthreads();
@@ -1196,6 +1333,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       bool ok = true;
       Seg g;
       for (int s = 0; ok && segment(s, g); ++s) {
+        {
+          Seg next;
+          if (segment(s + 1, next) && next.n > 0) {
+            tma_prefetch_tile(&p.map_k, next.k0, next.h, next.b);
+            tma_prefetch_tile(&p.map_v, next.k0, next.h, next.b);
+          }
+        }
         if (g.n == 0) continue;
         ok = c.wait1(K_EMPTY, uses + 1);
         if (!ok) break;

@@ -178,9 +178,25 @@ __device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+// the same box into L2 only
+__device__ __forceinline__ void tma_prefetch_tile(const CUtensorMap* map, int row, int head, int batch) {
+  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(map), "r"(0), "r"(row),
+               "r"(0), "r"(head), "r"(batch)
+               : "memory");
 }
+
+// A box of an output from shared memory; rows past the sequence are not
+// written.  Reads and writes of this thread's stores so far: tma_store_wait.
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* map, uint32_t src, int col, int row, int part, int head,
+                                              int batch) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4, %5}], [%6];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(col), "r"(row), "r"(part), "r"(head), "r"(batch), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Whether phase `parity` of `bar` is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {

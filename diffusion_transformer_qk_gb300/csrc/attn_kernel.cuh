@@ -5,24 +5,24 @@
 // score gradients) go back to tensor memory as 16-bit left operands of the
 // second product, in the columns whose scores they replace.  MMAs of
 // one thread run in order, so a product that overwrites an operand of an
-// earlier one needs no wait in between.  Two threads issue them, each one of
-// the two chains of products that do not depend on each other: what a thread
-// spends on waits between its products, the other's products fill (one thread
-// for both: 745 against 577 us forward at 2 x 4608 x 48 x 128).
+// earlier one needs no wait in between.
 //
 // Roles of a CTA's 12 warps: 0-7 are two groups of four that each cover the
-// 128 lanes of tensor memory (a thread owns one row of a score tile), warps 8
-// and 10 issue the MMAs, warp 9 the TMA loads; warp 11 hands round the
-// queries' statistics in the dk, dv kernel.  The third group's registers go
-// to the first two.
+// 128 lanes of tensor memory (a thread owns one row of a score tile), warp 8
+// issues the MMAs, warp 9 the TMA loads.  In the backward kernels warp 10
+// issues a second chain of products that does not depend on the first one's
+// order, so that what one warp spends on waits the other's products fill; in
+// the dk, dv kernel warp 11 hands round the queries' statistics.  The third
+// group's registers go to the first two.
 //
 // Persistent CTAs, one per SM.  Tile w of CTA c is tile w * CTAs + c, so that
 // CTAs next to each other read the same keys; the tiles left over after the
 // last full wave are cut along their contraction into as many equal parts as
 // there are CTAs, whose fp32 partial results attn_join_*_kernel adds in a
-// fixed order.  A tile's loads, its first products and the previous tile's
-// epilogue overlap.  Every wait is bounded; a role that
-// gives up sets the CTA's abort flag, drains what it started and leaves.
+// fixed order.  A causal mask's tiles are not cut once there is a full wave.
+// A tile's loads, its first products and the previous tile's epilogue overlap.
+// Every wait is bounded; a role that gives up sets the CTA's abort flag,
+// drains what it started and leaves.
 #pragma once
 
 #include "tc.cuh"
@@ -232,7 +232,9 @@ __device__ __forceinline__ long long attn_share(const AttnParams& p, long long c
 __device__ __forceinline__ bool attn_work(const AttnParams& p, int s, AttnWork& w) {
   const int n = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   if (s < p.waves) {
-    w = AttnWork{s * n + c, 0, kUnits, -1};
+    // with a causal mask a wave's tiles cost less and less: every other wave
+    // goes round the other way
+    w = AttnWork{s * n + (p.causal && (s & 1) ? n - 1 - c : c), 0, kUnits, -1};
     return w.tile < p.total;
   }
   const int k = s - p.waves;

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -25,7 +26,8 @@ using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, voi
 
 // The driver's tensor map encoder, looked up once.
 qknr_status encoder(EncodeFn* out) {
-  static EncodeFn fn = nullptr;
+  static std::atomic<EncodeFn> known{nullptr};
+  EncodeFn fn = known.load(std::memory_order_relaxed);
   if (!fn) {
     void* sym = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -34,6 +36,7 @@ qknr_status encoder(EncodeFn* out) {
     if (found != cudaDriverEntryPointSuccess || !sym)
       return fail(QKNR_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
     fn = reinterpret_cast<EncodeFn>(sym);
+    known.store(fn, std::memory_order_relaxed);
   }
   *out = fn;
   return QKNR_OK;
@@ -372,6 +375,12 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   if ((st = check_overlap(outs, 4, ins, 8)) != QKNR_OK) return st;
   for (int i = 0; i < 3; ++i)
     if (qknr_host::overlaps(ws, outs[i])) return fail(QKNR_ERR_OVERLAP, "the workspace overlaps a gradient");
+  const Rows* grads[] = {&dq, &dk, &dv};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if (qknr_host::rows_overlap(grads[i]->span, grads[i]->stride * 2, 2LL * grads[i]->heads * a->head_dim, grads[j]->span,
+                                  grads[j]->stride * 2, 2LL * grads[j]->heads * a->head_dim))
+        return fail(QKNR_ERR_OVERLAP, "%s overlaps %s", grads[i]->name, grads[j]->name);
   kp.o_in = static_cast<const char*>(a->o);
   kp.dout = static_cast<const char*>(a->dout);
   kp.dq = static_cast<char*>(a->dq);

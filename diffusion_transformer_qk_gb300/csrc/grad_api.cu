@@ -136,6 +136,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   int n_in = 0, n_out = 0;
   struct {
     Span out, own;
+    long long out_stride, own_stride, row;
     bool same;
   } grads[3];
   int n_grads = 0;
@@ -158,7 +159,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
                        ds * es, os * es, s.gamma, s.heads, msp(sx), msp(sd), msp(so), msp(sg)};
     ins[n_in++] = sx;
     ins[n_in++] = sg;
-    grads[n_grads++] = {so, sd, dx == s.dy && os == ds};
+    grads[n_grads++] = {so, sd, os * es, ds * es, row * es, dx == s.dy && os == ds};
     if (s.dgamma) outs[n_out++] = span_of(s.dgamma, 1, 0, (long long)D * 4);
   }
   const long long vrow = (long long)a->n_heads_v * D;
@@ -177,7 +178,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
     kp.v_chunks = static_cast<int>(vrow * es / 16);
     kp.sp_dv = msp(si);
     kp.sp_dv_out = msp(so);
-    grads[n_grads++] = {so, si, false};
+    grads[n_grads++] = {so, si, vos * es, vs * es, vrow * es, false};
   }
   const size_t need = workspace(a);
   const Span sk = span_of(a->workspace, 1, 0, static_cast<long long>(need));
@@ -200,6 +201,13 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
       for (int j = 0; j < n_grads; ++j)
         if (qknr_host::overlaps(grads[i].out, grads[j].own))
           return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps an incoming gradient without being in place");
+    for (int j = 0; j < n_grads; ++j) {
+      if (j == i) continue;
+      const auto &x = grads[i], &y = grads[j];
+      if (qknr_host::rows_overlap(x.out, x.out_stride, x.row, y.out, y.out_stride, y.row) ||
+          qknr_host::rows_overlap(x.out, x.out_stride, x.row, y.own, y.own_stride, y.row))
+        return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps another gradient");
+    }
   }
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j)

@@ -913,6 +913,8 @@ def _workspace(a, plan, workspace, like, stream):
         workspace = _empty((plan.workspace,), torch.uint8, like, stream)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), plan.workspace
     else:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
 
@@ -920,6 +922,8 @@ def _workspace(a, plan, workspace, like, stream):
 def _status(a, status, dev_status, like):
     """The status word: the caller's, the device's, or none."""
     if dev_status is not None:
+        if dev_status.dtype != torch.int32 or not dev_status.is_cuda or not dev_status.numel():
+            raise ValueError("dev_status must be an int32 CUDA tensor")
         a.dev_status = dev_status.data_ptr()
     elif status:
         word = _status_bufs.get(like.get_device())
@@ -1091,6 +1095,8 @@ def grad_args(*, head_dim, q=None, k=None, dq=None, dk=None, dv=None, dq_out=Non
         a.cos_dtype = _TAB[cos.dtype]
         a.cos, a.sin = cos.data_ptr(), sin.data_ptr()
         a.cos_rows = cos.shape[0] if cos_rows is None else cos_rows
+        if tokens and not 0 < a.cos_rows <= cos.shape[0]:
+            raise ValueError("cos_rows must be between 1 and cos's rows")
     a.cos_layout = COS_LAYOUT[cos_layout]
     a.rope_style = ROPE[rope_style]
     a.dev_status = _ptr(dev_status)
@@ -1191,9 +1197,9 @@ def attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, c
                 raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {batch} values")
             setattr(a, name, t.data_ptr())
     if scale is not None:
-        if not scale > 0:
-            raise ValueError("scale must be positive")
         a.scale = scale
+        if not 0 < a.scale < float("inf"):                  # as fp32
+            raise ValueError("scale must be positive and finite")
     a.causal = int(bool(causal))
     a.dev_status = _ptr(dev_status)
     a.flags, a.wait_limit_ns = flags, wait_limit_ns

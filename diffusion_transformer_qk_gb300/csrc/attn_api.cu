@@ -6,6 +6,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/qknr_attn.h"
 #include "attn_kernel.cuh"
@@ -107,12 +108,33 @@ qknr_status check_rows(const qknr_attn_args* a, Rows* r) {
   return QKNR_OK;
 }
 
-// Checks `ins` against `outs`; outputs may interleave with each other
-// (column views of one packed buffer) but not with an input.
-qknr_status check_overlap(const Span* outs, int n_out, const Span* ins, int n_in) {
-  for (int i = 0; i < n_out; ++i)
-    for (int j = 0; j < n_in; ++j)
-      if (qknr_host::overlaps(outs[i], ins[j])) return fail(QKNR_ERR_OVERLAP, "an output overlaps an input");
+qknr_host::RowSpan row_span(const qknr_attn_args* a, const Rows& r) {
+  return qknr_host::RowSpan{r.span, r.stride * 2, 2LL * r.heads * a->head_dim};
+}
+
+// Outputs may interleave with inputs and with each other (column views of one
+// packed buffer); `flat_outs` and `flat_ins` are the spans of what has no rows.
+qknr_status check_overlap(const qknr_attn_args* a, std::initializer_list<const Rows*> outs,
+                          std::initializer_list<const Rows*> ins, std::initializer_list<Span> flat_outs,
+                          std::initializer_list<Span> flat_ins) {
+  for (const Rows* o : outs) {
+    for (const Rows* i : ins)
+      if (qknr_host::rows_overlap(row_span(a, *o), row_span(a, *i)))
+        return fail(QKNR_ERR_OVERLAP, "%s overlaps %s", o->name, i->name);
+    for (const Rows* p : outs)
+      if (p != o && qknr_host::rows_overlap(row_span(a, *o), row_span(a, *p)))
+        return fail(QKNR_ERR_OVERLAP, "%s overlaps %s", o->name, p->name);
+    for (const Span& s : flat_ins)
+      if (qknr_host::overlaps(o->span, s)) return fail(QKNR_ERR_OVERLAP, "%s overlaps lse or the lengths", o->name);
+  }
+  for (const Span& f : flat_outs) {
+    for (const Rows* r : ins)
+      if (qknr_host::overlaps(f, r->span)) return fail(QKNR_ERR_OVERLAP, "%s overlaps lse or the workspace", r->name);
+    for (const Rows* r : outs)
+      if (qknr_host::overlaps(f, r->span)) return fail(QKNR_ERR_OVERLAP, "%s overlaps lse or the workspace", r->name);
+    for (const Span& s : flat_ins)
+      if (qknr_host::overlaps(f, s)) return fail(QKNR_ERR_OVERLAP, "lse, the lengths and the workspace overlap");
+  }
   return QKNR_OK;
 }
 
@@ -327,11 +349,10 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
   const size_t need = cut.part_bytes + cut.stats_bytes;
   if ((st = check_workspace(a, need)) != QKNR_OK) return st;
   const Span ws = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
-  const Span outs[] = {o.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)}, ws};
-  const Span ins[] = {q.span, k.span, v.span, span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)};
-  if ((st = check_overlap(outs, 3, ins, 5)) != QKNR_OK) return st;
-  if (qknr_host::overlaps(outs[0], outs[1]) || qknr_host::overlaps(outs[0], ws) || qknr_host::overlaps(outs[1], ws))
-    return fail(QKNR_ERR_OVERLAP, "o, lse and the workspace overlap");
+  const Span lse{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)};
+  st = check_overlap(a, {&o}, {&q, &k, &v}, {lse, ws}, {span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)});
+  if (st != QKNR_OK) return st;
+  if (qknr_host::overlaps(lse, ws)) return fail(QKNR_ERR_OVERLAP, "lse and the workspace overlap");
   kp.o = static_cast<char*>(a->o);
   kp.o_stride = o.stride * 2;
   kp.sp_o = msp(o.span);
@@ -369,18 +390,10 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   if (a->seq_q > 0 && !a->lse) return fail(QKNR_ERR_NULL, "lse is required");
   if ((st = check_workspace(a, need)) != QKNR_OK) return st;
   const Span ws = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
-  const Span outs[] = {dq.span, dk.span, dv.span, ws};
-  const Span ins[] = {q.span, k.span, v.span, o.span, g.span, Span{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)},
-                      span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)};
-  if ((st = check_overlap(outs, 4, ins, 8)) != QKNR_OK) return st;
-  for (int i = 0; i < 3; ++i)
-    if (qknr_host::overlaps(ws, outs[i])) return fail(QKNR_ERR_OVERLAP, "the workspace overlaps a gradient");
-  const Rows* grads[] = {&dq, &dk, &dv};
-  for (int i = 0; i < 3; ++i)
-    for (int j = 0; j < i; ++j)
-      if (qknr_host::rows_overlap(grads[i]->span, grads[i]->stride * 2, 2LL * grads[i]->heads * a->head_dim, grads[j]->span,
-                                  grads[j]->stride * 2, 2LL * grads[j]->heads * a->head_dim))
-        return fail(QKNR_ERR_OVERLAP, "%s overlaps %s", grads[i]->name, grads[j]->name);
+  const Span lse{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)};
+  st = check_overlap(a, {&dq, &dk, &dv}, {&q, &k, &v, &o, &g}, {ws},
+                     {lse, span_of(a->q_lens, a->batch, 4, 4), span_of(a->k_lens, a->batch, 4, 4)});
+  if (st != QKNR_OK) return st;
   kp.o_in = static_cast<const char*>(a->o);
   kp.dout = static_cast<const char*>(a->dout);
   kp.dq = static_cast<char*>(a->dq);

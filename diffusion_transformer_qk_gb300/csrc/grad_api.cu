@@ -14,6 +14,8 @@ namespace {
 
 using qknr_host::aligned16;
 using qknr_host::fail;
+using qknr_host::rows_overlap;
+using qknr_host::RowSpan;
 using qknr_host::Span;
 using qknr_host::span_of;
 
@@ -132,14 +134,15 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   if (heads > 0 && (!a->cos || !a->sin)) return fail(QKNR_ERR_NULL, "cos and sin are required");
   if (heads > 0 && (!aligned16(a->cos) || !aligned16(a->sin)))
     return fail(QKNR_ERR_ALIGN, "cos / sin not 16-byte aligned");
-  Span ins[10], outs[6];
+  RowSpan ins[8];
+  Span outs[3];
   int n_in = 0, n_out = 0;
   struct {
-    Span out, own;
-    long long out_stride, own_stride, row;
+    RowSpan out, own;
     bool same;
   } grads[3];
   int n_grads = 0;
+  auto flat = [](Span s) { return RowSpan{s, 0, 0}; };   // meets whatever its span meets
   for (int i = 0; i < 2; ++i) {
     Side& s = sides[i];
     qknr::GradSide& k = kp.side[i];
@@ -157,9 +160,9 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
     const Span so = span_of(dx, T, os * es, row * es), sg = span_of(s.gamma, 1, 0, (long long)D * 4);
     k = qknr::GradSide{static_cast<const char*>(s.x), static_cast<const char*>(s.dy), static_cast<char*>(dx), xs * es,
                        ds * es, os * es, s.gamma, s.heads, msp(sx), msp(sd), msp(so), msp(sg)};
-    ins[n_in++] = sx;
-    ins[n_in++] = sg;
-    grads[n_grads++] = {so, sd, os * es, ds * es, row * es, dx == s.dy && os == ds};
+    ins[n_in++] = RowSpan{sx, xs * es, row * es};
+    ins[n_in++] = flat(sg);
+    grads[n_grads++] = {RowSpan{so, os * es, row * es}, RowSpan{sd, ds * es, row * es}, dx == s.dy && os == ds};
     if (s.dgamma) outs[n_out++] = span_of(s.dgamma, 1, 0, (long long)D * 4);
   }
   const long long vrow = (long long)a->n_heads_v * D;
@@ -178,7 +181,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
     kp.v_chunks = static_cast<int>(vrow * es / 16);
     kp.sp_dv = msp(si);
     kp.sp_dv_out = msp(so);
-    grads[n_grads++] = {so, si, vos * es, vs * es, vrow * es, false};
+    grads[n_grads++] = {RowSpan{so, vos * es, vrow * es}, RowSpan{si, vs * es, vrow * es}, false};
   }
   const size_t need = workspace(a);
   const Span sk = span_of(a->workspace, 1, 0, static_cast<long long>(need));
@@ -188,32 +191,24 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   if (a->workspace_bytes < need)
     return fail(QKNR_ERR_SHAPE, "workspace of %zu bytes, %zu needed", a->workspace_bytes, need);
   if (!aligned16(a->workspace)) return fail(QKNR_ERR_ALIGN, "workspace not 16-byte aligned");
-  ins[n_in++] = sc;
-  ins[n_in++] = ss;
+  ins[n_in++] = flat(sc);
+  ins[n_in++] = flat(ss);
   outs[n_out++] = sk;
-  // Packed gradients interleave row by row, so their address spans overlap
-  // without sharing an element: an output is held against the inputs it must
-  // not touch, and against another gradient only where the rows are its own.
   for (int i = 0; i < n_grads; ++i) {
     for (int j = 0; j < n_in; ++j)
-      if (qknr_host::overlaps(grads[i].out, ins[j])) return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps an input");
-    if (!grads[i].same)
-      for (int j = 0; j < n_grads; ++j)
-        if (qknr_host::overlaps(grads[i].out, grads[j].own))
-          return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps an incoming gradient without being in place");
+      if (rows_overlap(grads[i].out, ins[j])) return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps an input");
     for (int j = 0; j < n_grads; ++j) {
-      if (j == i) continue;
-      const auto &x = grads[i], &y = grads[j];
-      if (qknr_host::rows_overlap(x.out, x.out_stride, x.row, y.out, y.out_stride, y.row) ||
-          qknr_host::rows_overlap(x.out, x.out_stride, x.row, y.own, y.own_stride, y.row))
-        return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps another gradient");
+      if ((j != i || !grads[i].same) && rows_overlap(grads[i].out, grads[j].own))
+        return fail(QKNR_ERR_OVERLAP, "a gradient output overlaps an incoming gradient without being in place");
+      if (j < i && rows_overlap(grads[i].out, grads[j].out)) return fail(QKNR_ERR_OVERLAP, "two gradient outputs overlap");
     }
   }
   for (int i = 0; i < n_out; ++i) {
+    const RowSpan out = flat(outs[i]);
     for (int j = 0; j < n_in; ++j)
-      if (qknr_host::overlaps(outs[i], ins[j])) return fail(QKNR_ERR_OVERLAP, "dgamma or the workspace overlaps an input");
+      if (rows_overlap(out, ins[j])) return fail(QKNR_ERR_OVERLAP, "dgamma or the workspace overlaps an input");
     for (int j = 0; j < n_grads; ++j)
-      if (qknr_host::overlaps(outs[i], grads[j].out) || qknr_host::overlaps(outs[i], grads[j].own))
+      if (rows_overlap(out, grads[j].out) || rows_overlap(out, grads[j].own))
         return fail(QKNR_ERR_OVERLAP, "dgamma or the workspace overlaps a gradient");
     for (int j = 0; j < i; ++j)
       if (qknr_host::overlaps(outs[i], outs[j])) return fail(QKNR_ERR_OVERLAP, "two outputs overlap");

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
+#include <initializer_list>
 
 #include "../../include/qknr_ln.h"
 #include "ln_kernel.cuh"
@@ -13,6 +14,8 @@ namespace {
 
 using qknr_host::aligned16;
 using qknr_host::fail;
+using qknr_host::rows_overlap;
+using qknr_host::RowSpan;
 using qknr_host::Span;
 using qknr_host::span_of;
 
@@ -161,6 +164,10 @@ qknr_status common(const qknr_ln_args* a, qknr::LnParams* kp) {
   return QKNR_OK;
 }
 
+RowSpan rows_of(const qknr::MemSpan& s, long long stride, const qknr_ln_args* a) {
+  return RowSpan{Span{static_cast<uintptr_t>(s.lo), static_cast<uintptr_t>(s.hi)}, stride, 2LL * a->hidden};
+}
+
 bool hits(Span out, std::initializer_list<qknr::MemSpan> ins) {
   for (const qknr::MemSpan& s : ins)
     if (qknr_host::overlaps(out, Span{static_cast<uintptr_t>(s.lo), static_cast<uintptr_t>(s.hi)})) return true;
@@ -214,7 +221,8 @@ qknr_status qknr_ln_forward(const qknr_ln_args* a, qknr_stream_t stream) {
   if (!aligned16(y) || (ys * 2) % 16) return fail(QKNR_ERR_ALIGN, "y base or stride not 16-byte aligned");
   const Span so = span_of(y, T, ys * 2, 2LL * C);
   const bool in_place = y == a->x && ys == xs;
-  if (!in_place && hits(so, {kp.sp_x})) return fail(QKNR_ERR_OVERLAP, "y overlaps x without being in place");
+  if (!in_place && rows_overlap(rows_of(msp(so), ys * 2, a), rows_of(kp.sp_x, kp.x_stride, a)))
+    return fail(QKNR_ERR_OVERLAP, "y overlaps x without being in place");
   if (hits(so, {kp.sp_weight, kp.sp_bias, kp.sp_mean, kp.sp_rstd}))
     return fail(QKNR_ERR_OVERLAP, "y overlaps a parameter, mean or rstd");
   kp.y = static_cast<char*>(y);
@@ -294,10 +302,13 @@ qknr_status qknr_ln_backward(const qknr_ln_args* a, qknr_stream_t stream) {
   const Span sw = span_of(a->dweight, c.sets, 4LL * C, 4LL * C), sb = span_of(a->dbias, c.sets, 4LL * C, 4LL * C);
   const Span sk = span_of(need ? a->workspace : nullptr, 1, 0, static_cast<long long>(need));
   const bool in_place = dx == a->dy && os == ds;
-  if (!in_place && hits(so, {kp.sp_dy})) return fail(QKNR_ERR_OVERLAP, "dx overlaps dy without being in place");
+  const RowSpan out = rows_of(msp(so), os * 2, a);
+  if (!in_place && rows_overlap(out, rows_of(kp.sp_dy, ds * 2, a)))
+    return fail(QKNR_ERR_OVERLAP, "dx overlaps dy without being in place");
+  if (rows_overlap(out, rows_of(kp.sp_x, kp.x_stride, a))) return fail(QKNR_ERR_OVERLAP, "dx overlaps x");
   const Span outs[] = {so, sw, sb, sk};
   for (int i = 0; i < 4; ++i) {
-    if (hits(outs[i], {kp.sp_x, kp.sp_weight, kp.sp_mean, kp.sp_rstd}) || (i && hits(outs[i], {kp.sp_dy})))
+    if (hits(outs[i], {kp.sp_weight, kp.sp_mean, kp.sp_rstd}) || (i && hits(outs[i], {kp.sp_x, kp.sp_dy})))
       return fail(QKNR_ERR_OVERLAP, "an output overlaps an input");
     for (int j = 0; j < i; ++j)
       if (qknr_host::overlaps(outs[i], outs[j])) return fail(QKNR_ERR_OVERLAP, "two outputs overlap");

@@ -237,9 +237,15 @@ struct LnRing {
       phase ^= 1u;
     }
   }
-  // first thread, giving up: copies in flight end before the CTA leaves its shared memory
-  __device__ __forceinline__ void drain() {
+  // first thread, giving up: copies in flight end before the CTA leaves its
+  // shared memory, those of the `given_up` rows before the next one included
+  __device__ __forceinline__ void drain(int given_up) {
     const unsigned long long t0 = global_timer_ns();
+    for (; given_up > 0; --given_up)
+      if (--s < 0) {
+        s = stages - 1;
+        phase ^= 1u;
+      }
     for (; in_flight > 0; --in_flight) {
       while (!mbar_try_wait(bars + 8 * s, phase) && global_timer_ns() - t0 < limit) {
       }
@@ -404,7 +410,10 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
       }
     }
     ok = ln_group_sum<NR, kLnWarps>(t, landed, W, gw, lane, 1 + grp, red);
-    if (!ok) break;
+    if (!ok) {
+      if (leader) ring.drain(n);
+      break;
+    }
     if (leader)
       for (int r = 0; r < n; ++r) {
         --ring.in_flight;
@@ -448,7 +457,6 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
     }
     row += n * step;
   }
-  if (!ok && leader) ring.drain();
 }
 
 // ---------------------------------------------------------------------------
@@ -578,6 +586,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
 #pragma unroll
   for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
   bool ok = true;
+  int given_up = 0;
   for (long long u = blockIdx.x / p.tiles; u < units; u += unit_step) {
     long long first, last;
     const long long set = rows_of(u, first, last);
@@ -637,7 +646,10 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
       }
       stats(left - NR);
       ok = ln_group_sum<2 * NR, kLnBwdWarps>(t, landed, W, gw, lane, 1 + grp, buf);
-      if (!ok) break;
+      if (!ok) {
+        given_up = left < NR ? left : NR;
+        break;
+      }
       if (leader)
         for (int r = 0; r < NR && r < left; ++r) {
           --ring.in_flight;
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
       }
     }
   }
-  if (leader && (!ok || *ring.abort_flag)) ring.drain();
+  if (leader && *ring.abort_flag) ring.drain(given_up);   // this group or another gave up
 }
 
 }  // namespace qknr

@@ -49,16 +49,20 @@ struct Span {
 Span span_of(const void* base, long long rows, long long stride_bytes, long long row_bytes);
 bool overlaps(Span a, Span b);
 
-// Two tensors of `a_row`, `b_row` bytes per row, rows `a_stride`, `b_stride`
-// bytes apart, whose spans are given: whether they may share an element.
-// Column views of one buffer interleave without sharing one.
-inline bool rows_overlap(Span a, long long a_stride, long long a_row, Span b, long long b_stride, long long b_row) {
-  if (!overlaps(a, b)) return false;
-  if (a_stride != b_stride) return true;
-  const bool b_later = b.lo >= a.lo;
-  const uintptr_t off = (b_later ? b.lo - a.lo : a.lo - b.lo) % static_cast<uintptr_t>(a_stride);
-  const long long first = b_later ? a_row : b_row, second = b_later ? b_row : a_row;
-  return static_cast<long long>(off) < first || static_cast<long long>(off) + second > a_stride;
+// Token rows: a span, the bytes between its rows (0: not rows) and those of a row.
+struct RowSpan {
+  Span span;
+  long long stride = 0, row = 0;
+};
+
+// Whether two tensors of token rows may share an element.  Column views of
+// one buffer interleave without sharing one.
+inline bool rows_overlap(const RowSpan& a, const RowSpan& b) {
+  if (!overlaps(a.span, b.span)) return false;
+  if (a.stride != b.stride || a.stride == 0) return true;
+  const RowSpan &lo = a.span.lo <= b.span.lo ? a : b, &hi = a.span.lo <= b.span.lo ? b : a;
+  const long long off = static_cast<long long>((hi.span.lo - lo.span.lo) % static_cast<uintptr_t>(a.stride));
+  return off < lo.row || off + hi.row > a.stride;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -77,7 +77,8 @@ qknr_status qknr_attn_backward_workspace_bytes(const qknr_attn_args *args, size_
 
 /* Validate and launch on `stream` (asynchronous).  Base addresses and row
    strides must be 16-byte aligned (lse and the lengths: 4-byte); an output
-   must not overlap an input. */
+   must not share an element with an input or another output (columns of one
+   buffer may interleave). */
 qknr_status qknr_attn_forward(const qknr_attn_args *args, qknr_stream_t stream);
 qknr_status qknr_attn_backward(const qknr_attn_args *args, qknr_stream_t stream);
 

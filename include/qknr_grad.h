@@ -65,8 +65,8 @@ qknr_status qknr_grad_workspace_bytes(const qknr_grad_args *args, size_t *bytes)
 /* Validate and launch on `stream` (asynchronous): one kernel that writes the
    gradients and partial sums of dgamma, and one that adds those.  Base
    addresses and row strides must be 16-byte aligned.  A gradient output may
-   be its own incoming gradient; it must not otherwise overlap an input or
-   another output. */
+   be its own incoming gradient; it must not otherwise share an element
+   with an input or another output (columns of one buffer may interleave). */
 qknr_status qknr_backward(const qknr_grad_args *args, qknr_stream_t stream);
 
 /* sizeof(qknr_grad_args) as compiled into the library. */

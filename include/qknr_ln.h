@@ -75,7 +75,8 @@ void qknr_ln_args_init(qknr_ln_args *a);
 
 /* Validate and launch the forward pass on `stream` (asynchronous, one
    kernel).  Base addresses and row strides must be 16-byte aligned (mean
-   and rstd: 4-byte); `y` must not partially overlap an input. */
+   and rstd: 4-byte); `y` must not share an element with an input
+   unless it is x. */
 qknr_status qknr_ln_forward(const qknr_ln_args *args, qknr_stream_t stream);
 
 /* Device bytes qknr_ln_backward needs at `workspace` for these arguments
@@ -85,8 +86,8 @@ qknr_status qknr_ln_workspace_bytes(const qknr_ln_args *args, size_t *bytes);
 /* Validate and launch the backward pass on `stream` (asynchronous): one
    kernel that writes dx and partial sums of dweight and dbias, and one that
    adds the partial sums; rows of more than 8192 values take a third that
-   sums each row first.  dx may be dy; it must not otherwise overlap an
-   input. */
+   sums each row first.  dx may be dy; outputs must not otherwise share
+   an element with an input (columns of one buffer may interleave). */
 qknr_status qknr_ln_backward(const qknr_ln_args *args, qknr_stream_t stream);
 
 /* sizeof(qknr_ln_args) as compiled into the library. */

@@ -9,6 +9,7 @@
 #include <initializer_list>
 
 #include "../../include/qknr_attn.h"
+#include "attn_few.cuh"
 #include "attn_kernel.cuh"
 #include "qknr_host.h"
 
@@ -226,7 +227,41 @@ Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long long b
 
 long long blocks_of(int seq) { return (static_cast<long long>(seq) + qknr::kTile - 1) / qknr::kTile; }
 
+// Few queries of a key head go without the tensor cores' tiles (us at 8 x 4096
+// keys of 24 heads x 128, few against tiles: 1 query 65 / 92, 2 heads sharing
+// a key head 79 / 159, 4 heads 132 / 298; but 4 queries of one head 132 / 92).
+bool few(const qknr_attn_args* a) {
+  const int group = a->n_heads_q / a->n_heads_k;
+  return a->seq_q <= 2 && a->seq_q * static_cast<long long>(group) <= qknr::kFewRows;
+}
+
+// Their key heads go round to the CTAs, the last ones (or all, where they are
+// fewer) cut along the keys.  A share is at least 256 keys, a step of all a
+// CTA's warps; below 1024 keys the second launch costs more than it saves.
+Cut cut_few(const qknr_attn_args* a) {
+  Cut c;
+  const long long total = static_cast<long long>(a->n_heads_k) * a->batch;
+  const long long rows = static_cast<long long>(a->seq_q) * (a->n_heads_q / a->n_heads_k);
+  c.tiles = 1;
+  c.total = static_cast<int>(total);
+  c.ctas = qknr::few_ctas(static_cast<int>(rows)) * kCtas;
+  const long long steps = a->seq_k < 1024 ? 1 : (static_cast<long long>(a->seq_k) + 255) / 256;
+  if (total * steps < c.ctas) c.ctas = total * steps > 0 ? static_cast<int>(total * steps) : 1;
+  c.waves = static_cast<int>(total / c.ctas);
+  c.rem = static_cast<int>(total % c.ctas);
+  if (c.rem > 0 && steps == 1) {
+    ++c.waves;
+    c.rem = 0;
+  }
+  if (c.rem > 0) {
+    c.part_bytes = static_cast<size_t>(2 * c.ctas) * rows * a->head_dim * 4;
+    c.stats_bytes = static_cast<size_t>(2 * c.ctas) * rows * 8;
+  }
+  return c;
+}
+
 Cut cut_forward(const qknr_attn_args* a) {
+  if (few(a)) return cut_few(a);
   return cut_tiles(a, a->seq_q, a->n_heads_q, qknr::fwd::kRows, blocks_of(a->seq_k), qknr::fwd::kRows, true);
 }
 Cut cut_dq(const qknr_attn_args* a) {
@@ -269,22 +304,26 @@ qknr_status join(const void* fn, const Cut& c, int rows, const qknr_attn_args* a
   if (c.rem == 0) return QKNR_OK;
   int ctas = c.ctas;
   void* kargs[] = {kp, &ctas};
-  return qknr_host::launch_kernel(fn, c.rem * rows / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
+  return qknr_host::launch_kernel(fn, (c.rem * rows + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
 }
 
 struct Kernels {
-  const void *fwd, *delta, *dq, *dkv, *join_fwd, *join_dq, *join_dkv;
+  const void *fwd, *few[3], *delta, *dq, *dkv, *join_fwd, *join_few, *join_dq, *join_dkv;
   int fwd_smem, dq_smem, dkv_smem;
 };
 
 template <typename T, int D>
 Kernels kernels() {
   return Kernels{reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D>),
+                 {reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 1>),
+                  reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 2>),
+                  reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 4>)},
                  reinterpret_cast<const void*>(qknr::attn_delta_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dq_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dkv_kernel<T, D>),
-                 reinterpret_cast<const void*>(qknr::attn_join_forward_kernel<T, D>),
+                 reinterpret_cast<const void*>(qknr::attn_join_forward_kernel<T, D, false>),
+                 reinterpret_cast<const void*>(qknr::attn_join_forward_kernel<T, D, true>),
                  reinterpret_cast<const void*>(qknr::attn_join_grad_kernel<T, D, false>),
                  reinterpret_cast<const void*>(qknr::attn_join_grad_kernel<T, D, true>),
                  qknr::fwd::kSmem<D>, qknr::dq::kSmem<D>, qknr::dkv::kSmem<D>};
@@ -361,13 +400,31 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
   int dev = 0;
   qknr_host::DeviceInfo di;
   if ((st = device(&dev, &di)) != QKNR_OK) return st;
+  const Kernels fn = kernels_for(a);
+  if (few(a)) {
+    kp.q_in = static_cast<const char*>(a->q);
+    kp.k_in = static_cast<const char*>(a->k);
+    kp.v_in = static_cast<const char*>(a->v);
+    kp.q_stride = q.stride * 2;
+    kp.k_stride = k.stride * 2;
+    kp.v_stride = v.stride * 2;
+    kp.sp_q = msp(q.span);
+    kp.sp_k = msp(k.span);
+    kp.sp_v = msp(v.span);
+    const int rows = a->seq_q * kp.group;
+    void* kargs[] = {&kp};
+    st = qknr_host::launch_kernel(fn.few[rows <= 1 ? 0 : (rows <= 2 ? 1 : 2)], cut.ctas, qknr::few_threads(rows), 0,
+                                  reinterpret_cast<cudaStream_t>(stream), kargs, !(a->flags & QKNR_FLAG_NO_OVERLAP),
+                                  "cudaLaunchKernelExC(attention, few queries)");
+    if (st != QKNR_OK) return st;
+    return join(fn.join_few, cut, rows, a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
+  }
   if ((st = make_map(&kp.map_q, a, a->q, q.stride, a->seq_q, a->n_heads_q)) != QKNR_OK) return st;
   if (a->seq_k > 0) {   // without keys the kernel loads nothing
     if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
     if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k)) != QKNR_OK) return st;
   }
   if ((st = make_map(&kp.map_out, a, a->o, o.stride, a->seq_q, a->n_heads_q, qknr::kOutRows, 64)) != QKNR_OK) return st;
-  const Kernels fn = kernels_for(a);
   st = launch(fn.fwd, cut.ctas, qknr::kAttnThreads, fn.fwd_smem, a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
   if (st != QKNR_OK) return st;
   return join(fn.join_fwd, cut, qknr::fwd::kRows, a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");

@@ -32,6 +32,8 @@ namespace qknr {
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
   CUtensorMap map_out;        // o or dq: boxes of kOutRows rows of a warp
+  const char *q_in, *k_in, *v_in;   // few queries: read without maps
+  long long q_stride, k_stride, v_stride;
   const char* o_in;           // backward: the forward's output
   const char* dout;
   char* o;
@@ -55,7 +57,7 @@ struct AttnParams {
   unsigned flags;
   int* status;
   unsigned long long wait_limit_ns;
-  MemSpan sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
+  MemSpan sp_q, sp_k, sp_v, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
 };
 
 constexpr int kAttnThreads = 384;
@@ -718,17 +720,29 @@ struct AttnParts {
 };
 
 // Joins the parts of the tiles that were shared out: a warp per query row.
+// FEW: the parts are those of a few queries (attn_few.cuh), a tile is a key
+// head's `group * seq_q` rows.
 //   o = sum_i w_i o_i / sum_i w_i l_i,  w_i = exp2((m_i - max m) scale)
-template <typename T, int D>
+template <typename T, int D, bool FEW>
 __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_constant__ AttnParams p, int ctas) {
-  constexpr int kRows = fwd::kRows;
+  const int kRows = FEW ? p.group * p.seq_q : fwd::kRows;
   const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   grid_dependency_wait();
   if (item >= p.rem * kRows) return;
   const int r = item / kRows, q = item % kRows;
-  const AttnPlace at = attn_place(p, p.waves * ctas + r, p.heads_q, true);
-  const int row = at.t * kRows + q;
-  if (row >= p.seq_q) return;
+  int b, h, row;
+  if (FEW) {
+    const int tile = p.waves * ctas + r, hk = tile % p.heads_k;
+    b = tile / p.heads_k;
+    h = hk * p.group + q / p.seq_q;
+    row = q % p.seq_q;
+  } else {
+    const AttnPlace at = attn_place(p, p.waves * ctas + r, p.heads_q, true);
+    b = at.b;
+    h = at.h;
+    row = at.t * kRows + q;
+    if (row >= p.seq_q) return;
+  }
   const AttnParts parts(p, r, ctas);
   float m = -INFINITY;
 #pragma unroll 4
@@ -754,10 +768,10 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
   }
   const bool some = total != 0.0f;
   const float inv = some ? __frcp_rn(total) : 0.0f;
-  const long long l = (static_cast<long long>(at.b) * p.heads_q + at.h) * p.seq_q + row;
+  const long long l = (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + row;
   if (lane == 0 && in_span(p.lse + l, 4, p.sp_lse, p.status))
     p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
-  char* dst = p.o + (static_cast<long long>(at.b) * p.seq_q + row) * p.o_stride + at.h * (D * 2);
+  char* dst = p.o + (static_cast<long long>(b) * p.seq_q + row) * p.o_stride + h * (D * 2);
   if (!in_span(dst, D * 2, p.sp_o, p.status)) return;
 #pragma unroll
   for (int e = 0; e < D / 64; ++e)

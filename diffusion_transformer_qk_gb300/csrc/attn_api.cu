@@ -227,24 +227,24 @@ Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long long b
 
 long long blocks_of(int seq) { return (static_cast<long long>(seq) + qknr::kTile - 1) / qknr::kTile; }
 
-// Few queries of a key head go without the tensor cores' tiles (us at 8 x 4096
-// keys of 24 heads x 128, few against tiles: 1 query 65 / 92, 2 heads sharing
-// a key head 79 / 159, 4 heads 132 / 298; but 4 queries of one head 132 / 92).
-bool few(const qknr_attn_args* a) {
-  const int group = a->n_heads_q / a->n_heads_k;
-  return a->seq_q <= 2 && a->seq_q * static_cast<long long>(group) <= qknr::kFewRows;
-}
+// A few queries go without the 256-row tiles, which read a key head's keys for
+// each of its query heads (us at 8 x 4096 keys of 24 heads x 128, few against
+// tiles: 1 query 70 / 92, 16 queries 72 / 92, 1 query of 4 heads on a key head
+// 72 / 298, of 16 heads 72 / 1115).
+bool few(const qknr_attn_args* a) { return a->seq_q <= qknr::kFewRows; }
 
-// Their key heads go round to the CTAs, the last ones (or all, where they are
-// fewer) cut along the keys.  A share is at least 256 keys, a step of all a
-// CTA's warps; below 1024 keys the second launch costs more than it saves.
+// Their tiles are up to kFewRows rows of a key head.  They go round to the
+// CTAs, the last ones (or all, where they are fewer) cut along the keys.  A
+// share is at least 256 keys, a step of all a CTA's warps; below 1024 keys the
+// second launch costs more than it saves.
 Cut cut_few(const qknr_attn_args* a) {
   Cut c;
-  const long long total = static_cast<long long>(a->n_heads_k) * a->batch;
-  const long long rows = static_cast<long long>(a->seq_q) * (a->n_heads_q / a->n_heads_k);
-  c.tiles = 1;
+  const long long all = static_cast<long long>(a->seq_q) * (a->n_heads_q / a->n_heads_k);
+  const long long rows = all < qknr::kFewRows ? all : qknr::kFewRows;
+  c.tiles = static_cast<int>((all + qknr::kFewRows - 1) / qknr::kFewRows);
+  const long long total = static_cast<long long>(a->n_heads_k) * a->batch * c.tiles;
   c.total = static_cast<int>(total);
-  c.ctas = qknr::few_ctas(static_cast<int>(rows)) * kCtas;
+  c.ctas = kCtas;
   const long long steps = a->seq_k < 1024 ? 1 : (static_cast<long long>(a->seq_k) + 255) / 256;
   if (total * steps < c.ctas) c.ctas = total * steps > 0 ? static_cast<int>(total * steps) : 1;
   c.waves = static_cast<int>(total / c.ctas);
@@ -309,7 +309,7 @@ qknr_status join(const void* fn, const Cut& c, int rows, const qknr_attn_args* a
 }
 
 struct Kernels {
-  const void *fwd, *few[3], *delta, *dq, *dkv, *join_fwd, *join_few, *join_dq, *join_dkv;
+  const void *fwd, *few[2], *delta, *dq, *dkv, *join_fwd, *join_few, *join_dq, *join_dkv;
   int fwd_smem, dq_smem, dkv_smem;
 };
 
@@ -317,8 +317,7 @@ template <typename T, int D>
 Kernels kernels() {
   return Kernels{reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D>),
                  {reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 1>),
-                  reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 2>),
-                  reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 4>)},
+                  reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 2>)},
                  reinterpret_cast<const void*>(qknr::attn_delta_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dq_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_dkv_kernel<T, D>),
@@ -403,19 +402,15 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
   const Kernels fn = kernels_for(a);
   if (few(a)) {
     kp.q_in = static_cast<const char*>(a->q);
-    kp.k_in = static_cast<const char*>(a->k);
-    kp.v_in = static_cast<const char*>(a->v);
     kp.q_stride = q.stride * 2;
-    kp.k_stride = k.stride * 2;
-    kp.v_stride = v.stride * 2;
     kp.sp_q = msp(q.span);
-    kp.sp_k = msp(k.span);
-    kp.sp_v = msp(v.span);
-    const int rows = a->seq_q * kp.group;
-    void* kargs[] = {&kp};
-    st = qknr_host::launch_kernel(fn.few[rows <= 1 ? 0 : (rows <= 2 ? 1 : 2)], cut.ctas, qknr::few_threads(rows), 0,
-                                  reinterpret_cast<cudaStream_t>(stream), kargs, !(a->flags & QKNR_FLAG_NO_OVERLAP),
-                                  "cudaLaunchKernelExC(attention, few queries)");
+    if (a->seq_k > 0) {
+      if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k, qknr::kFewKeys)) != QKNR_OK) return st;
+      if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k, qknr::kFewKeys)) != QKNR_OK) return st;
+    }
+    const int rows = a->seq_q * kp.group < qknr::kFewRows ? a->seq_q * kp.group : qknr::kFewRows, most = rows <= 8 ? 8 : 16;
+    st = launch(fn.few[most / 16], cut.ctas, 32 * qknr::few_warps(most), qknr::few_smem(most, a->head_dim), a, &kp, dev, di, stream,
+                "cudaLaunchKernelExC(attention, few queries)");
     if (st != QKNR_OK) return st;
     return join(fn.join_few, cut, rows, a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
   }

@@ -32,8 +32,8 @@ namespace qknr {
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
   CUtensorMap map_out;        // o or dq: boxes of kOutRows rows of a warp
-  const char *q_in, *k_in, *v_in;   // few queries: read without maps
-  long long q_stride, k_stride, v_stride;
+  const char* q_in;           // few queries: read without a map
+  long long q_stride;
   const char* o_in;           // backward: the forward's output
   const char* dout;
   char* o;
@@ -57,12 +57,13 @@ struct AttnParams {
   unsigned flags;
   int* status;
   unsigned long long wait_limit_ns;
-  MemSpan sp_q, sp_k, sp_v, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
+  MemSpan sp_q, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
 };
 
 constexpr int kAttnThreads = 384;
 constexpr int kAttnMmaWarp = 8, kAttnLoadWarp = 9, kAttnMma2Warp = 10, kAttnRowWarp = 11;
 constexpr int kTile = 128;                        // rows of a tile, both ways
+constexpr int kFewRows = 16;                      // rows of a tile of a few queries (attn_few.cuh)
 // Registers: 384 threads start with 168 each; 2 x 128 x 208 + 128 x 80 fit in
 // the 384 x 168 that the block was launched with.
 constexpr int kAttnWorkRegs = 208, kAttnIssueRegs = 80;
@@ -720,22 +721,23 @@ struct AttnParts {
 };
 
 // Joins the parts of the tiles that were shared out: a warp per query row.
-// FEW: the parts are those of a few queries (attn_few.cuh), a tile is a key
-// head's `group * seq_q` rows.
+// FEW: the parts are those of a few queries (attn_few.cuh), a tile up to
+// kFewRows of a key head's group * seq_q rows.
 //   o = sum_i w_i o_i / sum_i w_i l_i,  w_i = exp2((m_i - max m) scale)
 template <typename T, int D, bool FEW>
 __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_constant__ AttnParams p, int ctas) {
-  const int kRows = FEW ? p.group * p.seq_q : fwd::kRows;
+  const int kRows = FEW ? min(p.group * p.seq_q, kFewRows) : fwd::kRows;
   const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   grid_dependency_wait();
   if (item >= p.rem * kRows) return;
   const int r = item / kRows, q = item % kRows;
   int b, h, row;
   if (FEW) {
-    const int tile = p.waves * ctas + r, hk = tile % p.heads_k;
-    b = tile / p.heads_k;
-    h = hk * p.group + q / p.seq_q;
-    row = q % p.seq_q;
+    const int tile = p.waves * ctas + r, key_head = tile / p.tiles, x = (tile - key_head * p.tiles) * kFewRows + q;
+    if (x >= p.group * p.seq_q) return;
+    b = key_head / p.heads_k;
+    h = (key_head - b * p.heads_k) * p.group + x / p.seq_q;
+    row = x % p.seq_q;
   } else {
     const AttnPlace at = attn_place(p, p.waves * ctas + r, p.heads_q, true);
     b = at.b;

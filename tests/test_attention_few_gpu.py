@@ -19,16 +19,16 @@ def _lib(built_lib, cuda_device):
     assert Q.read_status() == 0
 
 
-# (queries, query heads, key heads): 1 to 4 rows of a key head, and 5 for the other kernel
+# (queries, query heads, key heads): 1 to 16 queries, up to 16 rows of a key head and more; 17 for the other kernel
 @pytest.mark.parametrize("Sq,Hq,Hk", [(1, 1, 1), (1, 3, 3), (1, 4, 2), (1, 3, 1), (1, 8, 2), (2, 3, 3), (2, 4, 2), (3, 2, 2),
-                                      (4, 1, 1), (1, 5, 1)])
+                                      (4, 1, 1), (1, 5, 1), (1, 18, 2), (8, 2, 2), (5, 3, 1), (16, 2, 2), (1, 20, 1), (16, 6, 2), (7, 5, 1), (17, 1, 1)])
 @pytest.mark.parametrize("Sk", [1, 2, 7, 8, 9, 63, 128, 129, 255, 257, 384, 511, 1000])
 @pytest.mark.parametrize("D,dtype", [(64, "fp16"), (128, "bf16")])
 def test_sizes(Sq, Hq, Hk, Sk, D, dtype):
     TA.both(2, Sq, Sk, Hq, Hk, D, dtype=dtype, seed=Sk + Sq)
 
 
-@pytest.mark.parametrize("Sq,Sk,Hq,Hk", [(1, 5000, 1, 1), (4, 3001, 1, 1), (1, 2999, 4, 1), (2, 2000, 2, 1)])
+@pytest.mark.parametrize("Sq,Sk,Hq,Hk", [(1, 5000, 1, 1), (4, 3001, 1, 1), (1, 2999, 4, 1), (2, 2000, 2, 1), (11, 3003, 2, 2), (9, 2500, 4, 1)])
 @pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "fp16")])
 def test_keys_shared_out_over_many_ctas(Sq, Sk, Hq, Hk, D, dtype):
     TA.both(1, Sq, Sk, Hq, Hk, D, dtype=dtype, seed=3)
@@ -39,7 +39,7 @@ def test_more_heads_than_ctas(batch, heads):
     TA.both(batch, 1, 600, heads, heads, 64, seed=4)
 
 
-@pytest.mark.parametrize("Sq,Sk", [(1, 300), (3, 300), (4, 2), (4, 1), (3, 1500)])
+@pytest.mark.parametrize("Sq,Sk", [(1, 300), (3, 300), (4, 2), (4, 1), (3, 1500), (16, 300), (13, 5)])
 def test_causal(Sq, Sk):
     TA.both(2, Sq, Sk, 2, 2, 64, causal=True, seed=5)
 
@@ -94,10 +94,22 @@ def test_decoding_a_sequence_matches_the_causal_pass():
         assert (o.float() - whole[t:t + 1].float()).abs().max().item() <= 4 * torch.finfo(torch.bfloat16).eps, t
 
 
+def test_a_wait_that_runs_out_is_reported():
+    s = TA.make(2, 1, 3000, 4, 2, 64, seed=16)
+    o, lse = TA.forward(s)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    TA.forward(s, flags=Q.FLAG_TEST_STALL, wait_limit_ns=2_000_000, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == Q.ERR_TIMEOUT
+    # the context is whole: the next call is right
+    assert same_bits(TA.forward(s)[0], o)
+
+
 def test_checked_build(libs_checked):
     TA.both(2, 1, 1000, 4, 2, 128, seed=12)
     TA.both(1, 3, 5000, 1, 1, 64, causal=True, seed=13)
     TA.both(160, 1, 300, 2, 2, 64, seed=14)
+    TA.both(1, 12, 3000, 1, 1, 128, seed=15)
 
 
 @pytest.fixture

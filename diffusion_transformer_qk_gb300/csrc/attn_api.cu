@@ -183,7 +183,7 @@ size_t delta_bytes(const qknr_attn_args* a) {
 constexpr int kCtas = 152;
 
 struct Cut {
-  int tiles = 0, total = 0, ctas = 0, waves = 0, rem = 0;
+  int tiles = 0, total = 0, ctas = 0, halves = 0, waves = 0, rem = 0;
   size_t part_bytes = 0, stats_bytes = 0;
 };
 
@@ -197,15 +197,33 @@ Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long long b
   c.ctas = kCtas;
   c.waves = static_cast<int>(total / c.ctas);
   c.rem = static_cast<int>(total % c.ctas);
+  auto buffers = [&](long long slots) {
+    c.part_bytes = static_cast<size_t>(slots) * slot_rows * a->head_dim * 4;
+    c.stats_bytes = stats ? static_cast<size_t>(slots) * slot_rows * 8 : 0;
+  };
+  // A causal mask's tiles cost 1 to `blocks` iterations, so that equal shares
+  // of the cheap ones left over gain nothing.  They go out whole, the costly
+  // ones first, every other wave the other way round (backward of 3 x 1999 x 16
+  // on 4 heads x 64: 147 us, 189 with the rest shared out); or all as two
+  // halves, where a costly one alone takes longer than an even spread would:
+  // by more than the 32 iterations that partial results of all tiles cost
+  // (backward of 8192 x 24 on 3 heads x 128: 189 more, 980 against 1136 us;
+  // forward of 8192 x 6 x 128: 24 more, 101 against 98), or by any where fewer
+  // tiles than CTAs are cut anyway (backward of 4096 x 4 x 128: 81 against 91).
+  const long long spread = total * blocks / (2 * c.ctas), half = blocks / 2 > spread ? blocks / 2 : spread;
+  const long long other = c.waves > 0 ? blocks : blocks * total / c.ctas;
+  if (a->causal && other - half > (c.waves > 0 ? 32 : 2)) {
+    c.halves = 1;
+    c.waves = static_cast<int>((2 * total + c.ctas - 1) / c.ctas);
+    c.rem = 0;
+    buffers(2 * total);
+    return c;
+  }
   if (c.rem == 0) return c;
   // Sharing the last tiles out saves most of a tile's time and costs the
   // partial results and a kernel that joins them, about as much as six
   // iterations at head_dim 128, twelve at 64.
   const long long cost = a->head_dim == 128 ? 6 : 12;
-  // A causal mask's tiles differ in cost, so that equal shares of the cheap
-  // ones left over gain nothing: whole tiles, the costly ones first, every
-  // other wave the other way round (backward of 3 x 1999 x 16 on 4 heads x 64:
-  // 148 us, 189 with the rest shared out).
   const bool even = !(a->causal && c.waves > 0);
   if (even && blocks * (c.ctas - c.rem) > cost * c.ctas) {
     if (c.waves == 0) {
@@ -214,8 +232,7 @@ Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long long b
       if (most < c.ctas) c.ctas = static_cast<int>(most > c.rem ? most : c.rem);
     }
     if (c.ctas > c.rem) {
-      c.part_bytes = static_cast<size_t>(2 * c.ctas) * slot_rows * a->head_dim * 4;
-      c.stats_bytes = stats ? static_cast<size_t>(2 * c.ctas) * slot_rows * 8 : 0;
+      buffers(2 * c.ctas);
       return c;
     }
   }
@@ -280,6 +297,7 @@ size_t backward_bytes(const qknr_attn_args* a) {
 void apply(const Cut& c, qknr::AttnParams* kp, void* part) {
   kp->tiles = c.tiles;
   kp->total = c.total;
+  kp->halves = c.halves;
   kp->waves = c.waves;
   kp->rem = c.rem;
   kp->part = static_cast<float*>(part);
@@ -301,10 +319,11 @@ qknr_status launch(const void* fn, long long grid, int block, int smem, const qk
 // The kernel that joins partial results: a warp per row of the tiles shared out.
 qknr_status join(const void* fn, const Cut& c, int rows, const qknr_attn_args* a, qknr::AttnParams* kp, qknr_stream_t stream,
                  const char* what) {
-  if (c.rem == 0) return QKNR_OK;
+  const long long cut = c.halves ? c.total : c.rem;
+  if (cut == 0) return QKNR_OK;
   int ctas = c.ctas;
   void* kargs[] = {kp, &ctas};
-  return qknr_host::launch_kernel(fn, (c.rem * rows + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
+  return qknr_host::launch_kernel(fn, static_cast<int>((cut * rows + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
 }
 

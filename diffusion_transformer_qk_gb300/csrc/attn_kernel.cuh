@@ -19,7 +19,8 @@
 // CTAs next to each other read the same keys; the tiles left over after the
 // last full wave are cut along their contraction into as many equal parts as
 // there are CTAs, whose fp32 partial results attn_join_*_kernel adds in a
-// fixed order.  A causal mask's tiles are not cut once there is a full wave.
+// fixed order.  A causal mask's tiles go out whole, or all of them as two
+// halves, costly ones first.
 // A tile's loads, its first products and the previous tile's epilogue overlap.
 // Every wait is bounded; a role that gives up sets the CTA's abort flag,
 // drains what it started and leaves.
@@ -50,7 +51,8 @@ struct AttnParams {
   float scale, scale_log2;
   int tiles;                  // row tiles of a head
   int total;                  // tiles in all
-  int waves;                  // whole tiles per CTA
+  int halves;                 // every tile goes out as two halves of its contraction
+  int waves;                  // whole tiles (or halves) per CTA
   int rem;                    // tiles after those, shared out among all CTAs
   float* part;                // their partial results, two slots per CTA
   float* stats;               // forward: (maximum, sum) of the slots' rows
@@ -237,7 +239,8 @@ __device__ __forceinline__ bool attn_work(const AttnParams& p, int s, AttnWork& 
   if (s < p.waves) {
     // with a causal mask a wave's tiles cost less and less: every other wave
     // goes round the other way
-    w = AttnWork{s * n + (p.causal && (s & 1) ? n - 1 - c : c), 0, kUnits, -1};
+    const int item = s * n + (p.causal && (s & 1) ? n - 1 - c : c), second = item & 1;
+    w = p.halves ? AttnWork{item >> 1, second * (kUnits / 2), (second + 1) * (kUnits / 2), item} : AttnWork{item, 0, kUnits, -1};
     return w.tile < p.total;
   }
   const int k = s - p.waves;
@@ -707,11 +710,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   }
 }
 
-// The parts of tile r that was shared out: count of them, CTAs first, first +
-// 1, ...; part i's slot is slot(i).
+// The parts of the r-th tile that was cut, `tile`: count of them; where it was
+// shared out they belong to CTAs first, first + 1, ...  Part i's slot is slot(i).
 struct AttnParts {
-  int first, count, late;
-  __device__ __forceinline__ AttnParts(const AttnParams& p, int r, int ctas) {
+  int tile, first, count, late;
+  bool halves;
+  __device__ __forceinline__ AttnParts(const AttnParams& p, int r, int ctas) : halves(p.halves) {
+    if (halves) {
+      tile = first = r;
+      count = 2;
+      late = 0;
+      return;
+    }
+    tile = p.waves * ctas + r;
     const long long unit0 = static_cast<long long>(r) * kUnits;
     int c = static_cast<int>(static_cast<long long>(r) * ctas / p.rem);
     while (c > 0 && attn_share(p, c, ctas) > unit0) --c;
@@ -721,8 +732,11 @@ struct AttnParts {
     while (c < ctas && attn_share(p, c, ctas) < unit0 + kUnits) ++c;
     count = c - first;
   }
-  __device__ __forceinline__ int slot(int i) const { return 2 * (first + i) + (i == 0 ? late : 0); }
+  __device__ __forceinline__ int slot(int i) const { return halves ? 2 * first + i : 2 * (first + i) + (i == 0 ? late : 0); }
 };
+
+// tiles that were cut
+__device__ __forceinline__ int attn_cut_tiles(const AttnParams& p) { return p.halves ? p.total : p.rem; }
 
 // Joins the parts of the tiles that were shared out: a warp per query row.
 // FEW: the parts are those of a few queries (attn_few.cuh), a tile up to
@@ -733,23 +747,23 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
   const int kRows = FEW ? min(p.group * p.seq_q, kFewRows) : fwd::kRows;
   const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   grid_dependency_wait();
-  if (item >= p.rem * kRows) return;
+  if (item >= attn_cut_tiles(p) * kRows) return;
   const int r = item / kRows, q = item % kRows;
+  const AttnParts parts(p, r, ctas);
   int b, h, row;
   if (FEW) {
-    const int tile = p.waves * ctas + r, key_head = tile / p.tiles, x = (tile - key_head * p.tiles) * kFewRows + q;
+    const int key_head = parts.tile / p.tiles, x = (parts.tile - key_head * p.tiles) * kFewRows + q;
     if (x >= p.group * p.seq_q) return;
     b = key_head / p.heads_k;
     h = (key_head - b * p.heads_k) * p.group + x / p.seq_q;
     row = x % p.seq_q;
   } else {
-    const AttnPlace at = attn_place(p, p.waves * ctas + r, p.heads_q, true);
+    const AttnPlace at = attn_place(p, parts.tile, p.heads_q, true);
     b = at.b;
     h = at.h;
     row = at.t * kRows + q;
     if (row >= p.seq_q) return;
   }
-  const AttnParts parts(p, r, ctas);
   float m = -INFINITY;
 #pragma unroll 4
   for (int i = 0; i < parts.count; ++i) {
@@ -1241,12 +1255,12 @@ __global__ void __launch_bounds__(256) attn_join_grad_kernel(const __grid_consta
   constexpr int kRows = (KV ? 2 : 1) * kTile;     // rows of a slot
   const int item = static_cast<int>(blockIdx.x) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   grid_dependency_wait();
-  if (item >= p.rem * kRows) return;
+  if (item >= attn_cut_tiles(p) * kRows) return;
   const int r = item / kRows, q = item % kRows, which = q / kTile;
-  const AttnPlace at = attn_place(p, p.waves * ctas + r, KV ? p.heads_k : p.heads_q, !KV);
+  const AttnParts parts(p, r, ctas);
+  const AttnPlace at = attn_place(p, parts.tile, KV ? p.heads_k : p.heads_q, !KV);
   const int row = at.t * kTile + q % kTile, seq = KV ? p.seq_k : p.seq_q;
   if (row >= seq) return;
-  const AttnParts parts(p, r, ctas);
   float2 acc[D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);

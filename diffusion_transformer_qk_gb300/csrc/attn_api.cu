@@ -424,8 +424,8 @@ qknr_status qknr_attn_forward(const qknr_attn_args* a, qknr_stream_t stream) {
     kp.q_stride = q.stride * 2;
     kp.sp_q = msp(q.span);
     if (a->seq_k > 0) {
-      if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k, qknr::kFewKeys)) != QKNR_OK) return st;
-      if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k, qknr::kFewKeys)) != QKNR_OK) return st;
+      if ((st = make_map(&kp.map_k, a, a->k, k.stride, a->seq_k, a->n_heads_k, qknr::few_keys(a->head_dim))) != QKNR_OK) return st;
+      if ((st = make_map(&kp.map_v, a, a->v, v.stride, a->seq_k, a->n_heads_k, qknr::few_keys(a->head_dim))) != QKNR_OK) return st;
     }
     const int rows = a->seq_q * kp.group < qknr::kFewRows ? a->seq_q * kp.group : qknr::kFewRows, most = rows <= 8 ? 8 : 16;
     st = launch(fn.few[most / 16], cut.ctas, 32 * qknr::few_warps(most), qknr::few_smem(most, a->head_dim), a, &kp, dev, di, stream,

@@ -2,28 +2,33 @@
 // keys for sm_103a (formulas: qknr_attn.h).
 //
 // Bound by HBM: every key and value is read once, for up to 16 of the group *
-// seq_q queries of a key head together.  A 128-row tile of attn_kernel.cuh would be
-// almost empty and its CTA waits for its own softmax between two loads; here
-// the warps run independently, each over 16 keys at a time, which TMA brings to
-// a ring of its own.  The products are warp-wide MMAs of 16 rows: the
-// contraction's order is free, so a lane's 16 bytes of a key serve as two
-// k-steps of Q K^T; and a lane's 16 bytes of four values, pairs of keys swapped
-// together, as eight column tiles of P V.  (Plain FMAs are as fast for one query, 65 us at 8 x 4096 keys
-// of 24 heads x 128, but take 79 for two and 132 for four.)  A warp keeps the
-// running maximum, sum and accumulator of each row; a CTA's warps join in
-// order through shared memory, and CTAs share a key head's keys like the
-// tiles' contraction in attn_kernel.cuh.
+// seq_q queries of a key head together.  A 256-row tile of attn_kernel.cuh
+// would be almost empty and its CTA waits for its own softmax between two
+// loads; here the warps run independently, each over 16 (head_dim 64: 32) keys
+// at a time, which TMA brings to a ring of its own.  The products are warp-wide
+// MMAs of 16 rows: the contraction's order is free, so a lane's 16 bytes of a
+// key serve as two k-steps of Q K^T; and a lane's 16 bytes of four values,
+// pairs of keys swapped together, as eight column tiles of P V.  A warp keeps
+// the running maximum, sum and accumulator of each row; a CTA's warps join in
+// order through shared memory, and CTAs share a key head's keys like the tiles'
+// contraction in attn_kernel.cuh.
+//
+// 8 x 4096 keys of 24 heads x 128: 70 us for 1 to 8 rows (5.8 TB/s), 72 for 16;
+// head_dim 64: 41 and 43.  Plain FMAs take 65 us for one row, but 79 for two
+// and 132 for four; the same MMAs fed by loads to registers 75 us, by 16-byte
+// asynchronous copies 85.
 #pragma once
 
 #include "attn_kernel.cuh"
 
 namespace qknr {
 
-constexpr int kFewKeys = 16;  // keys of a warp's step
+// Keys of a warp's step: 8 KB of keys and values.
+__host__ __device__ constexpr int few_keys(int d) { return 2048 / d; }
 // Up to 8 rows: 12 warps with 168 registers a thread; up to 16: 8 with 255.
 __host__ __device__ constexpr int few_warps(int rows) { return rows <= 8 ? 12 : 8; }
 // Steps in flight: 192 KB of keys and values per SM.
-__host__ __device__ constexpr int few_step_bytes(int d) { return 2 * kFewKeys * d * 2; }
+__host__ __device__ constexpr int few_step_bytes(int d) { return 2 * few_keys(d) * d * 2; }
 __host__ __device__ constexpr int few_stages(int rows, int d) { return 196608 / (few_warps(rows) * few_step_bytes(d)); }
 // [warps][stages] steps, in whose place [warps] [rows][D] sums come after a
 // key head's last step; [warps][rows] (maximum, sum); [warps][stages] barriers
@@ -54,6 +59,7 @@ __device__ __forceinline__ void few_mma<__half>(float (&c)[4], const uint32_t (&
 template <typename T, int D, int H>
 __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(const __grid_constant__ AttnParams p) {
   constexpr int ROWS = 8 * H, WARPS = few_warps(ROWS), KC = D / 32, VC = D / 64, STAGES = few_stages(ROWS, D);
+  constexpr int kKeys = few_keys(D), KT = kKeys / 8;
   constexpr int kRing = few_ring_bytes(ROWS, D), kStep = few_step_bytes(D);
   static_assert(STAGES >= 2 && ROWS * D * 4 <= kRing, "a warp's share of shared memory");
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -112,8 +118,8 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     int begin, end;
     attn_cut(w, n, begin, end);
     // lane 0: the next step's keys and values into the stage after those in flight
-    constexpr int kHop = WARPS * kFewKeys;
-    int ahead = begin + warp * kFewKeys, in_flight = 0;
+    constexpr int kHop = WARPS * kKeys;
+    int ahead = begin + warp * kKeys, in_flight = 0;
     int put = at.s;
     auto fetch = [&]() {
       if (ahead >= end || (p.flags & 1u)) return;             // test only: issue nothing
@@ -128,14 +134,14 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     if (lane == 0)
       for (int i = 0; i < STAGES; ++i) fetch();
 #pragma unroll 1
-    for (int k0 = begin + warp * kFewKeys; k0 < end; k0 += kHop) {
+    for (int k0 = begin + warp * kKeys; k0 < end; k0 += kHop) {
       ok = cta.wait(at.s, at.phase);
       if (!ok) break;
       const unsigned char* in = ring + at.s * kStep;
       // scores of keys k0 + 8 i + 2t, + 1: [0], [1] of row g, [2], [3] of row g + 8
-      float sc[2][4];
+      float sc[KT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < KT; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[i][e] = 0.0f;
 #pragma unroll
@@ -143,20 +149,20 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
           const uint4 other = H > 1 ? q[H - 1][c] : make_uint4(0, 0, 0, 0);
           const uint32_t lo[4] = {q[0][c].x, other.x, q[0][c].y, other.y}, hi[4] = {q[0][c].z, other.z, q[0][c].w, other.w};
           // row 8 i + g, chunk 2 t + (c & 1) of its half
-          const uint4 kr = *reinterpret_cast<const uint4*>(in + (c >> 1) * (kFewKeys * 128) + (8 * i + g) * 128 +
+          const uint4 kr = *reinterpret_cast<const uint4*>(in + (c >> 1) * (kKeys * 128) + (8 * i + g) * 128 +
                                                            (((2 * t + (c & 1)) ^ g) << 4));
           few_mma<T>(sc[i], lo, kr.x, kr.y);
           few_mma<T>(sc[i], hi, kr.z, kr.w);
         }
       }
-      uint32_t pr[4] = {0, 0, 0, 0};
+      uint32_t pr[KT / 2][4] = {};
       float old[H];
       bool raised = false;
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         float top = m[h];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < KT; ++i)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float& x = sc[i][2 * h + e];
@@ -172,11 +178,11 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
         m[h] = top;
         l[h] = __fmul_rn(l[h], old[h]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < KT; ++i) {
           const float a = exp2_approx(__fmul_rn(__fsub_rn(sc[i][2 * h], base), p.scale_log2));
           const float c = exp2_approx(__fmul_rn(__fsub_rn(sc[i][2 * h + 1], base), p.scale_log2));
           l[h] = __fadd_rn(l[h], __fadd_rn(a, c));
-          pr[2 * i + h] = pack2<T>(a, c);         // 16 bits: the product's operand
+          pr[i / 2][i % 2 * 2 + h] = pack2<T>(a, c);   // 16 bits: the product's operand
         }
       }
       if (__any_sync(0xffffffffu, raised)) {
@@ -188,25 +194,28 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
             for (int e = 0; e < 2 * H; ++e) acc[c][j][e] = __fmul_rn(acc[c][j][e], old[e >> 1]);
       }
 #pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        uint32_t x[4][4];
+      for (int u = 0; u < KT / 2; ++u)            // 16 keys at a time
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 2 * t + (i & 1) + 8 * (i >> 1);     // keys 2t, 2t + 1, 2t + 8, 2t + 9; chunk g
-          uint4 v = *reinterpret_cast<const uint4*>(in + kStep / 2 + c * (kFewKeys * 128) + row * 128 + ((g ^ (row & 7)) << 4));
-          if (k0 + row >= end) v = make_uint4(0, 0, 0, 0);    // past a sample's length there may be anything
-          x[i][0] = v.x;
-          x[i][1] = v.y;
-          x[i][2] = v.z;
-          x[i][3] = v.w;
-        }
+        for (int c = 0; c < VC; ++c) {
+          uint32_t x[4][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {             // column 64 c + 8 g + j of this lane's operand
-          const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
-          if (H == 1) acc[c][j][2] = acc[c][j][3] = 0.0f;
-          few_mma<T>(acc[c][j], pr, __byte_perm(x[0][j / 2], x[1][j / 2], pick), __byte_perm(x[2][j / 2], x[3][j / 2], pick));
+          for (int i = 0; i < 4; ++i) {           // keys 2t, 2t + 1, 2t + 8, 2t + 9; chunk g
+            const int row = 16 * u + 2 * t + (i & 1) + 8 * (i >> 1);
+            uint4 v = *reinterpret_cast<const uint4*>(in + kStep / 2 + c * (kKeys * 128) + row * 128 + ((g ^ (row & 7)) << 4));
+            if (k0 + row >= end) v = make_uint4(0, 0, 0, 0);    // past a sample's length there may be anything
+            x[i][0] = v.x;
+            x[i][1] = v.y;
+            x[i][2] = v.z;
+            x[i][3] = v.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {           // column 64 c + 8 g + j of this lane's operand
+            const uint32_t pick = j & 1 ? 0x7632u : 0x5410u;
+            if (H == 1) acc[c][j][2] = acc[c][j][3] = 0.0f;
+            few_mma<T>(acc[c][j], pr[u], __byte_perm(x[0][j / 2], x[1][j / 2], pick),
+                       __byte_perm(x[2][j / 2], x[3][j / 2], pick));
+          }
         }
-      }
       __syncwarp();
       at.step();
       if (lane == 0) {

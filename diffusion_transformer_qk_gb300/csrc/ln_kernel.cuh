@@ -590,6 +590,10 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
   for (int i = 0; i < CPT; ++i) mine[i] = l + i * 32 * W < n_chunks;
   bool ok = true;
   int given_up = 0;
+  // The two buffers alternate from one step to the next, from a unit's last to
+  // the next unit's first too: a group alone in its CTA has no barrier between
+  // units, and a slow warp may still read the sums of the step before.
+  float* buf = red;
   for (long long u = blockIdx.x / p.tiles; u < units; u += unit_step) {
     long long first, last;
     const long long set = rows_of(u, first, last);
@@ -619,7 +623,6 @@ __global__ void __launch_bounds__(kLnBwdThreads, 1) ln_backward_kernel(const __g
     stats(left);
     char* dst = p.dx + (first + grp) * p.dx_stride + (k0 + l) * 16;
     const float2* sums = reinterpret_cast<const float2*>(p.row_sums) + first + grp;   // LONG
-    float* buf = red;
     for (; left > 0; left -= NR, buf = buf == red ? red + kLnRedFloats : red) {
       float2 xh[NR][CPT][4], dy[NR][CPT][4], R[NR];
       float t[2 * NR];

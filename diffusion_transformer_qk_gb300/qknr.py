@@ -312,6 +312,9 @@ def _rows(t: Optional[torch.Tensor], name: str) -> int:
         raise ValueError(f"{name} must be 2-D [tokens, heads*head_dim]")
     if t.stride(1) != 1:
         raise ValueError(f"{name} rows must be contiguous")
+    if t.stride(0) == 0 and t.shape[0] > 1 and t.numel():
+        # to the library 0 is the default stride, and rows that are not there
+        raise ValueError(f"{name} is one row expanded to several: pass its contiguous() copy")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.stride(0)

@@ -289,9 +289,21 @@ Cut cut_dkv(const qknr_attn_args* a) {
                    2 * qknr::kTile, false);
 }
 
+// CTAs of the delta kernel at most: eight on each SM.
+constexpr int kDeltaCtas = 8 * kCtas;
+
+// What fp16's dS takes its powers of two from, behind delta: |do| of each row,
+// a bound on v's rows per CTA of the delta kernel, four bounds per query tile.
+size_t ds_top_bytes(const qknr_attn_args* a) {
+  return static_cast<size_t>(a->batch) * a->n_heads_q * blocks_of(a->seq_q) * 16;
+}
+size_t lift_bytes(const qknr_attn_args* a) {
+  return a->dtype == QKNR_FP16 ? delta_bytes(a) + kDeltaCtas * 4 + ds_top_bytes(a) : 0;
+}
+
 size_t backward_bytes(const qknr_attn_args* a) {
   const size_t q = cut_dq(a).part_bytes, kv = cut_dkv(a).part_bytes;
-  return delta_bytes(a) + (q > kv ? q : kv);      // one after the other in the same place
+  return delta_bytes(a) + lift_bytes(a) + (q > kv ? q : kv);   // the parts one after the other in the same place
 }
 
 void apply(const Cut& c, qknr::AttnParams* kp, void* part) {
@@ -482,7 +494,19 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   kp.sp_dk = msp(dk.span);
   kp.sp_dv = msp(dv.span);
   kp.sp_delta = msp(span_of(kp.delta, 1, 0, static_cast<long long>(delta_bytes(a))));
-  void* part = static_cast<char*>(a->workspace) + delta_bytes(a);
+  void* part = static_cast<char*>(a->workspace) + delta_bytes(a) + lift_bytes(a);
+  if (a->dtype == QKNR_FP16) {
+    kp.v_in = static_cast<const char*>(a->v);
+    kp.v_stride = v.stride * 2;
+    kp.sp_v = msp(v.span);
+    kp.dout_norm = kp.delta + delta_bytes(a) / 4;
+    kp.v_top = kp.dout_norm + delta_bytes(a) / 4;
+    kp.ds_top = kp.v_top + kDeltaCtas;
+    kp.q_tiles = static_cast<int>(blocks_of(a->seq_q));
+    kp.sp_dout_norm = msp(span_of(kp.dout_norm, 1, 0, static_cast<long long>(delta_bytes(a))));
+    kp.sp_v_top = msp(span_of(kp.v_top, 1, 0, 4LL * kDeltaCtas));
+    kp.sp_ds_top = msp(span_of(kp.ds_top, 1, 0, static_cast<long long>(ds_top_bytes(a))));
+  }
 
   int dev = 0;
   qknr_host::DeviceInfo di;
@@ -502,7 +526,13 @@ qknr_status qknr_attn_backward(const qknr_attn_args* a, qknr_stream_t stream) {
   if (a->seq_q > 0) {
     const long long rows = static_cast<long long>(a->batch) * a->seq_q * a->n_heads_q, teams = 256 / (a->head_dim / 8);
     long long grid = (rows + teams - 1) / teams;
+    if (a->dtype == QKNR_FP16) {
+      const long long v_grid = (static_cast<long long>(a->batch) * a->seq_k * a->n_heads_k + teams - 1) / teams;
+      if (v_grid > grid) grid = v_grid;
+    }
     if (grid > 8LL * di.num_sms) grid = 8LL * di.num_sms;
+    if (grid > kDeltaCtas) grid = kDeltaCtas;
+    kp.v_tops = static_cast<int>(grid);
     void* kargs[] = {&kp};
     st = qknr_host::launch_kernel(fn.delta, static_cast<int>(grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), "cudaLaunchKernelExC(attention delta)");

@@ -43,6 +43,14 @@ struct AttnParams {
   char* dv;
   float* lse;
   float* delta;               // [batch][heads_q][seq_q]
+  // fp16 backward: what dS's powers of two come from
+  const char* v_in;
+  long long v_stride;
+  float* dout_norm;           // |do| of each row, like delta
+  float* v_top;               // [delta kernel's CTAs] none of its rows of v is longer
+  int v_tops;
+  float* ds_top;              // [batch][heads_q][q_tiles][4] the largest bound on |ds| among 32 rows
+  int q_tiles;                // 128-row tiles of the queries
   long long o_stride, dout_stride, dq_stride, dk_stride, dv_stride;   // bytes per row
   const int* q_lens;
   const int* k_lens;
@@ -59,7 +67,8 @@ struct AttnParams {
   unsigned flags;
   int* status;
   unsigned long long wait_limit_ns;
-  MemSpan sp_q, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats;
+  MemSpan sp_q, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats,
+      sp_v, sp_dout_norm, sp_v_top, sp_ds_top;
 };
 
 constexpr int kAttnThreads = 384;
@@ -343,16 +352,16 @@ __device__ __forceinline__ void store_cols(char* dst, long long stride, int rows
     if ((lane & ~3) + k < rows) *reinterpret_cast<uint4*>(at + k * stride) = w[k];
 }
 
-// the same values as a partial result: fp32 rows of D values
+// the same values as a partial result: fp32 rows of D values, times f
 template <int D>
-__device__ __forceinline__ void store_part(float* dst, const float (&v)[32], bool some, int lane) {
+__device__ __forceinline__ void store_part(float* dst, const float (&v)[32], float f, bool some, int lane) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint4 w[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float* x = &v[16 * h + 4 * c];
-      w[c] = some ? make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]))
+      w[c] = some ? make_uint4(__float_as_uint(x[0] * f), __float_as_uint(x[1] * f), __float_as_uint(x[2] * f), __float_as_uint(x[3] * f))
                   : make_uint4(0, 0, 0, 0);
     }
     quad_transpose(w, lane);
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         }
         if (!fits) continue;
         if (g.slot >= 0) {
-          store_part<D>(p.part + at * D + 32 * i, o, n > 0, c.lane);
+          store_part<D>(p.part + at * D + 32 * i, o, 1.0f, n > 0, c.lane);
           continue;
         }
         if (i % 2 == 0) {
@@ -805,30 +814,70 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
 // Powers of two that the 16-bit operands carry through their products and
 // the epilogues take out again.  P gets 2^kP, in the exponent: fp16 keeps the
 // small probabilities of long rows out of its subnormals (P <= 1, so 2^14 is
-// in range), bf16 those that ex2.approx would flush to zero.  dS gets 2^kS.
+// in range), bf16 those that ex2.approx would flush to zero.
+//
+// dS gets 2^kS.  bf16 has the exponents of fp32, so a constant does.  fp16 has
+// not: dS = P (dP - delta) is as small as the incoming gradient over the number
+// of keys and as large as |do| |v|, and with no factor gradients of 1e-5 over
+// 4096 keys lose four of five dS to zero.  Its factor comes from the bound
+// |dP - delta| <= b = 2 |do| V, where no row of v is longer than V (o is a mean
+// of v's rows): with 2^e <= b < 2^(e+1), 2^14 P (dP - delta) 2^-e stays below
+// 2^15, and half a subnormal step is 2^-39 b.  In dq a row is a query and has a
+// factor of its own; in dk all queries of a sample's key head go into one sum
+// and share the largest b.  At 4096 x 24 x 128 the bounds cost 20 of 555 us, at
+// 8 x 1 x 4096 x 24 x 128, where v's 200 MB are read once more for them, 34 of
+// 390.
 template <typename T>
 struct GradScale;
 template <>
 struct GradScale<__half> {
-  static constexpr float kP = 14.0f, kS = 0.0f;
+  static constexpr float kP = 14.0f;
+  static constexpr bool kFromData = true;
 };
 template <>
 struct GradScale<__nv_bfloat16> {
-  static constexpr float kP = 24.0f, kS = 24.0f;
+  static constexpr float kP = 24.0f;              // kS too
+  static constexpr bool kFromData = false;
 };
 __device__ __forceinline__ constexpr float grad_scale_down(float k) {   // 2^-k
-  return k == 0.0f ? 1.0f : (k == 14.0f ? 1.0f / 16384.0f : 1.0f / 16777216.0f);
+  return k == 14.0f ? 1.0f / 16384.0f : 1.0f / 16777216.0f;
 }
-// ds = (2^kP p) * (dp * kC - delta * kC)
+// ds = (2^kP p) * (dp * lift - delta * lift), lift = 2^(kS - kP): 2^-e for the
+// bound b, 1 where it says nothing (no gradient, infinities)
 template <typename T>
-constexpr float kGradC = GradScale<T>::kP == GradScale<T>::kS ? 1.0f : 1.0f / 16384.0f;
+__device__ __forceinline__ float grad_lift(float b) {
+  if (!GradScale<T>::kFromData) return 1.0f;
+  const bool use = b >= 0x1p-100f && b < INFINITY;
+  return use ? __uint_as_float((254u << 23) - (__float_as_uint(b) & 0x7f800000u)) : 1.0f;
+}
+// 2^-kS, exact
+template <typename T>
+__device__ __forceinline__ float grad_unlift(float lift) {
+  const float down = grad_scale_down(GradScale<T>::kP);
+  return GradScale<T>::kFromData ? __uint_as_float((254u << 23) - __float_as_uint(lift)) * down : down;
+}
+
+__device__ __forceinline__ float square_sum(const float2 (&v)[4]) {
+  float2 acc = __fmul2_rn(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) acc = __ffma2_rn(v[i], v[i], acc);
+  return __fadd_rn(acc.x, acc.y);
+}
+
+// the largest of a warp's values, in every lane (a NaN does not count)
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
 
 // delta = rowsum(do * o), one team of D/8 lanes per row.  Bound by HBM (50 us
 // for 2 x 8190 x 40 x 128, 6.7 TB/s).  Worked out inside the dq kernel instead,
 // whose tiles load do anyway, each tile waits for its rows of o: the same time
 // there, 150 against 145 us at 3 x 1999 x 16 on 4 heads x 64, causal.
+// fp16: also |do| of each row and a bound on the rows of v (GradScale).
 template <typename T, int D>
-__global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constant__ AttnParams p) {
   constexpr int L = D / 8, TEAMS = 256 / L;
   const int team = threadIdx.x / L, lane = threadIdx.x % L;
   const long long items = static_cast<long long>(p.batch) * p.seq_q * p.heads_q;
@@ -837,7 +886,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
   for (long long first = static_cast<long long>(blockIdx.x) * TEAMS; first < items;
        first += static_cast<long long>(gridDim.x) * TEAMS) {
     const long long it = first + team;
-    float s = 0.0f;
+    float s = 0.0f, n = 0.0f;
     const long long row = it / p.heads_q;
     const int h = static_cast<int>(it - row * p.heads_q);
     if (it < items) {
@@ -851,14 +900,76 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const __grid_constant__
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = __ffma2_rn(x[i], y[i], acc);
         s = __fadd_rn(acc.x, acc.y);
+        if (GradScale<T>::kFromData) n = square_sum(y);
+      }
+    }
+    if (GradScale<T>::kFromData) {
+      // two sums share one tree: the upper lanes take the second
+      const bool upper = lane & (L / 2);
+      s = __fadd_rn(upper ? n : s, __shfl_xor_sync(0xffffffffu, upper ? s : n, L / 2));
+    } else {
+      s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, L / 2));
+    }
+#pragma unroll
+    for (int off = L / 4; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    if (it < items && lane % (L / 2) == 0) {
+      const long long b = row / p.seq_q, at = (b * p.heads_q + h) * p.seq_q + (row - b * p.seq_q);
+      if (lane == 0) {
+        if (in_span(p.delta + at, 4, p.sp_delta, p.status)) p.delta[at] = s;
+      } else if (GradScale<T>::kFromData && in_span(p.dout_norm + at, 4, p.sp_dout_norm, p.status)) {
+        p.dout_norm[at] = __fsqrt_rn(s);
+      }
+    }
+  }
+  if (GradScale<T>::kFromData) {
+    // No row of v that counts is longer than this: a lane keeps the largest sum
+    // of its 8 columns, and a team's rows all stay below the sum over its lanes
+    // (about sqrt(2) times the longest row; no shuffles until the end).
+    constexpr int N = 2;                          // rows in flight
+    const long long rows_v = static_cast<long long>(p.batch) * p.seq_k * p.heads_k, step = static_cast<long long>(gridDim.x) * TEAMS;
+    const int h_step = static_cast<int>(step % p.heads_k), row_step = static_cast<int>(step / p.heads_k);
+    long long it = static_cast<long long>(blockIdx.x) * TEAMS + team;
+    int row = static_cast<int>(it / p.heads_k), h = static_cast<int>(it - static_cast<long long>(row) * p.heads_k);
+    float top = 0.0f;
+    while (it < rows_v) {
+      uint4 x[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (it < rows_v) {
+          const char* src = p.v_in + row * p.v_stride + h * (D * 2) + lane * 16;
+          bool counts = in_span(src, 16, p.sp_v, p.status);
+          if (p.k_lens) {
+            const int b = row / p.seq_k;
+            counts = counts && row - b * p.seq_k < clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
+          }
+          if (counts) x[i] = *reinterpret_cast<const uint4*>(src);
+          it += step;
+          row += row_step;
+          h += h_step;
+          if (h >= p.heads_k) {
+            h -= p.heads_k;
+            ++row;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float2 y[4];
+        Elem<T>::unpack(x[i], y);
+        top = fmaxf(top, square_sum(y));
       }
     }
 #pragma unroll
-    for (int off = L / 2; off >= 1; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    if (it < items && lane == 0) {
-      const long long b = row / p.seq_q;
-      float* out = p.delta + (b * p.heads_q + h) * p.seq_q + (row - b * p.seq_q);
-      if (in_span(out, 4, p.sp_delta, p.status)) *out = s;
+    for (int off = L / 2; off >= 1; off >>= 1) top = __fadd_rn(top, __shfl_xor_sync(0xffffffffu, top, off));
+    __shared__ float tops[8];
+    top = warp_max(top);
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = fmaxf(top, tops[i]);
+      if (in_span(p.v_top + blockIdx.x, 4, p.sp_v_top, p.status)) p.v_top[blockIdx.x] = __fsqrt_rn(top);
     }
   }
   grid_dependents_launch();
@@ -895,6 +1006,7 @@ struct Seg {
   int b, h, q0, slot;
   int q_len, k_len, diag;
   int begin, n;               // key blocks [begin, begin + n)
+  bool opens;                 // the tile's first piece
 };
 }  // namespace dq
 
@@ -928,6 +1040,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.h = at.h;
     g.q0 = at.t * kTile;
     g.slot = w.slot;
+    g.opens = w.u0 == 0;
     g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
     g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
     g.diag = g.k_len - g.q_len;
@@ -1103,17 +1216,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       c.arrive(Q_READY);
       return true;
     };
-    // a tile's row: log-sum and delta
-    auto row_stats = [&](const Seg& g, float& lse, float& delta) {
+    float v_top = 0.0f;                           // no row of v is longer
+    if (GradScale<T>::kFromData) {
+#pragma unroll 4
+      for (int i = c.lane; i < p.v_tops; i += 32)
+        if (in_span(p.v_top + i, 4, p.sp_v_top, p.status)) v_top = fmaxf(v_top, p.v_top[i]);
+      v_top = warp_max(v_top);
+    }
+    // a tile's row: log-sum, delta and the bound on |dP - delta|
+    auto row_stats = [&](const Seg& g, float& lse, float& delta, float& bound) {
       const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + g.q0 + r;
-      lse = delta = 0.0f;
+      lse = delta = bound = 0.0f;
       if (g.q0 + r < p.seq_q && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
         lse = p.lse[at];
         delta = p.delta[at];
+        if (GradScale<T>::kFromData && in_span(p.dout_norm + at, 4, p.sp_dout_norm, p.status))
+          bound = __fmul_rn(2.0f * v_top, p.dout_norm[at]);
       }
     };
     unsigned char* stage = smem + (1 + kK + kV) * kTileBytes<D> + c.warp * kStage<D>;
-    float lse = 0.0f, delta = 0.0f;
+    float lse = 0.0f, delta = 0.0f, bound = 0.0f;
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
     Seg g;
@@ -1121,12 +1243,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       const int row = g.q0 + r;
       int limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
       limit = limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit);
-      if (!ready) row_stats(g, lse, delta);
+      if (!ready) row_stats(g, lse, delta, bound);
+      if (GradScale<T>::kFromData && half == 0 && g.opens) {
+        // for dk, dv: the largest bound of these 32 queries
+        const float top = warp_max(limit > 0 ? bound : 0.0f);
+        float* at = p.ds_top + ((static_cast<long long>(g.b) * p.heads_q + g.h) * p.q_tiles + g.q0 / kTile) * 4 + c.warp;
+        if (c.lane == 0 && in_span(at, 4, p.sp_ds_top, p.status)) *at = top;
+      }
+      const float lift = grad_lift<T>(bound);
       // p = 0 for a row that sees nothing
       const float lse2 = limit == 0 || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
-      const float nl = GradScale<T>::kP - lse2, nd = -delta * kGradC<T>;
+      const float nl = GradScale<T>::kP - lse2, nd = -delta * lift;
       const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
-                   C = make_float2(kGradC<T>, kGradC<T>);
+                   C = make_float2(lift, lift);
       if (g.n > 0) {
         if (!ready) ok = copy_q();
         if (!ok) break;
@@ -1198,7 +1327,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         // and its first products run under this one's epilogue.
         ready = segment(sg + 1, g) && g.n > 0;
         if (ready) {
-          row_stats(g, lse, delta);
+          row_stats(g, lse, delta, bound);
           ok = copy_q();
         }
         if (!ok) break;
@@ -1226,9 +1355,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         }
         if (!fits) continue;
         if (g.slot >= 0)
-          store_part<D>(part + 32 * i, v, some, c.lane);
+          store_part<D>(part + 32 * i, v, grad_unlift<T>(lift), some, c.lane);
         else
-          stage_cols<T, D / 2>(stage, 4 * i, v, p.scale * grad_scale_down(GradScale<T>::kS), some, c.lane);
+          stage_cols<T, D / 2>(stage, 4 * i, v, p.scale * grad_unlift<T>(lift), some, c.lane);
       }
       if (g.slot < 0) {
         fence_async_shared();
@@ -1272,7 +1401,7 @@ __global__ void __launch_bounds__(256) attn_join_grad_kernel(const __grid_consta
     for (int e = 0; e < D / 64; ++e) acc[e] = __fadd2_rn(acc[e], reinterpret_cast<const float2*>(src)[lane + 32 * e]);
   }
   const bool dv = KV && which == 0;
-  const float f = dv ? grad_scale_down(GradScale<T>::kP) : p.scale * grad_scale_down(GradScale<T>::kS);
+  const float f = dv ? 1.0f : p.scale;
   char* base = KV ? (dv ? p.dv : p.dk) : p.dq;
   const long long stride = KV ? (dv ? p.dv_stride : p.dk_stride) : p.dq_stride;
   char* dst = base + (static_cast<long long>(at.b) * seq + row) * stride + at.h * (D * 2);
@@ -1304,7 +1433,7 @@ __device__ __forceinline__ int arrivals(int i) {
   // both chains are done with a tile, with the accumulators
   return (i >= Q_EMPTY && i < O_FULL) || (i >= O_EMPTY && i < S_FULL) || i == DONE ? 2 : 1;
 }
-constexpr int kRowBytes = 2 * 2 * kTile * 4;      // two buffers of (lse, delta) of a tile's queries
+constexpr int kRowBytes = 2 * 2 * kTile * 4 + 16; // two buffers of (lse, delta) of a tile's queries, and their lifts
 template <int D>
 constexpr int kCtl = (2 + kQ + kO) * kTileBytes<D> + kRowBytes;
 template <int D>
@@ -1341,6 +1470,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   grid_dependency_wait();
   grid_dependents_launch();
   float* rows = reinterpret_cast<float*>(smem + (2 + kQ + kO) * kTileBytes<D>);   // [2][2][128]
+  float* lifts = rows + 2 * 2 * kTile;            // [2]
 
   auto segment = [&](int s, Seg& g) {
     AttnWork w;
@@ -1527,7 +1657,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     }
     if (!ok) c.drain_mma(DRAIN + (first_chain ? 0 : 1));
   } else if (c.warp == kAttnRowWarp) {
-    // Warp 11 hands round kP - lse (log2) and -delta kC of the blocks'
+    // Warp 11 hands round kP - lse (log2) and -delta lift of the blocks'
     // queries, up to two blocks ahead.  A query past the length or with no
     // key gets -inf: p = 0.
     int done = 0;
@@ -1535,6 +1665,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       int h = g.h0, t = g.t0;
+      float lift = 1.0f;
+      if (GradScale<T>::kFromData && g.n > 0) {
+        // the largest bound among the queries of this key head
+        const long long each = 4LL * p.q_tiles, n = p.group * each;
+        const float* tops = p.ds_top + (static_cast<long long>(g.b) * p.heads_q + g.h * p.group) * each;
+        float bound = 0.0f;
+#pragma unroll 4
+        for (long long i = c.lane; i < n; i += 32)
+          if (in_span(tops + i, 4, p.sp_ds_top, p.status)) bound = fmaxf(bound, tops[i]);
+        lift = grad_lift<T>(warp_max(bound));
+      }
       for (int i = 0; i < g.n; ++i, ++done) {
         const long long at = (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
         float l[4], d[4];
@@ -1551,8 +1692,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           out[32 * e] = l[e] == -INFINITY ? -INFINITY : __fmaf_rn(l[e], -kLog2e, GradScale<T>::kP);
-          out[kTile + 32 * e] = -d[e] * kGradC<T>;
+          out[kTile + 32 * e] = -d[e] * lift;
         }
+        if (GradScale<T>::kFromData && c.lane == 0) lifts[done & 1] = lift;
         __syncwarp();
         if (c.lane == 0) mbar_arrive(c.bar(ROWS + (done & 1)));
         if (++t == g.end) {
@@ -1567,13 +1709,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
     const uint32_t ts = tmem + half * 64 + lanes, tdp = tmem + kTile + half * 64 + lanes;
-    const float2 SL = make_float2(p.scale_log2, p.scale_log2), C = make_float2(kGradC<T>, kGradC<T>);
+    const float2 SL = make_float2(p.scale_log2, p.scale_log2);
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
     Seg g;
     for (int sg = 0; ok && segment(sg, g); ++sg) {
       const int key = g.k0 + r;
       int t = g.t0;                               // the block's query tile
+      float lift = 1.0f;
       for (int i = 0; i < g.n; ++i, ++done) {
         const float* mine = rows + (done & 1) * 2 * kTile;
         const float4* nl = reinterpret_cast<const float4*>(mine + half * 64);
@@ -1581,6 +1724,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         ok = c.wait(ROWS + (done & 1), done >> 1) && c.wait(S_FULL, done);
         if (!ok) break;
         tc_fence_after();
+        if (GradScale<T>::kFromData) lift = lifts[done & 1];
+        const float2 C = make_float2(lift, lift);
         float s[2][32];
         tmem_load32(ts, s[0]);
         tmem_load32(ts + 32, s[1]);
@@ -1660,7 +1805,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         tc_fence_after();
       }
       const bool some = g.n > 0 && key < g.k_len;
-      const float f = half ? p.scale * grad_scale_down(GradScale<T>::kS) : grad_scale_down(GradScale<T>::kP);
+      const float down = half ? grad_unlift<T>(lift) : grad_scale_down(GradScale<T>::kP), f = half ? p.scale * down : down;
       float* part = p.part + ((static_cast<long long>(g.slot) * 2 + half) * kTile + r) * D;
       char* dst = half ? p.dk + (static_cast<long long>(g.b) * p.seq_k + key) * p.dk_stride + g.h * (D * 2)
                        : p.dv + (static_cast<long long>(g.b) * p.seq_k + key) * p.dv_stride + g.h * (D * 2);
@@ -1678,7 +1823,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         }
         if (!fits) continue;
         if (g.slot >= 0)
-          store_part<D>(part + 32 * i, v, some, c.lane);
+          store_part<D>(part + 32 * i, v, down, some, c.lane);
         else
           store_cols<T>(dst + 64 * i, half ? p.dk_stride : p.dv_stride, there, v, f, some, c.lane);
       }

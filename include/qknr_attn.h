@@ -30,8 +30,10 @@
  * all queries of a key head; longer ones take 256-query tiles.
  *
  * Products run on the tensor cores with fp32 accumulators; p and ds enter
- * their second product rounded to the activation dtype; outputs are rounded
- * once.  No atomics: equal calls give equal bits.
+ * their second product rounded to the activation dtype, times powers of two
+ * that keep them in its range (ds in fp16: taken from |do| and |v|, so that
+ * neither small nor large gradients are lost); outputs are rounded once.  No
+ * atomics: equal calls give equal bits.
  *
  * Ownership and errors follow qknr.h: the caller owns every buffer (the
  * workspace included), the library allocates nothing and never

@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
         l[h] = __fmul_rn(l[h], old[h]);
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
-          const float a = exp2_approx(__fmul_rn(__fsub_rn(sc[i][2 * h], base), p.scale_log2));
-          const float c = exp2_approx(__fmul_rn(__fsub_rn(sc[i][2 * h + 1], base), p.scale_log2));
+          const float a = exp2_approx(__fmaf_rn(__fsub_rn(sc[i][2 * h], base), p.scale_log2, kPLift<T>));
+          const float c = exp2_approx(__fmaf_rn(__fsub_rn(sc[i][2 * h + 1], base), p.scale_log2, kPLift<T>));
           l[h] = __fadd_rn(l[h], __fadd_rn(a, c));
           pr[i / 2][i % 2 * 2 + h] = pack2<T>(a, c);   // 16 bits: the product's operand
         }
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
         if (in_span(dst, 4, p.sp_o, p.status))
           *reinterpret_cast<uint32_t*>(dst) = some ? pack2<T>(__fmul_rn(o.x, inv), __fmul_rn(o.y, inv)) : 0u;
         float* lse = p.lse + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + i;
-        if (c == 0 && in_span(lse, 4, p.sp_lse, p.status)) *lse = some ? __fmaf_rn(top, p.scale, logf(total)) : -INFINITY;
+        if (c == 0 && in_span(lse, 4, p.sp_lse, p.status)) *lse = some ? __fmaf_rn(top, p.scale, log_sum<T>(total)) : -INFINITY;
       }
     }
     // the sums' place is TMA's again; a warp that gave up ends the CTA's work

@@ -372,6 +372,21 @@ __device__ __forceinline__ void store_part(float* dst, const float (&v)[32], flo
 }
 
 // ---------------------------------------------------------------------------
+// The forward kernels' P carries 2^kPLift into its product and into the sum,
+// which takes it out again.  In fp16 a probability below 2^-25 of the row's
+// largest would round to zero: of N keys up to N 2^-25 of the sum, more than
+// half a step of the output from 16384 on.  With 2^7 that is N 2^-32.
+template <typename T>
+constexpr float kPLift = 0.0f;
+template <>
+constexpr float kPLift<__half> = 7.0f;
+// the log of a sum of such values
+template <typename T>
+__device__ __forceinline__ float log_sum(float total) {
+  return logf(kPLift<T> == 0.0f ? total : __fmul_rn(total, 1.0f / 128.0f));
+}
+
+// ---------------------------------------------------------------------------
 // forward: a tile is 256 queries of one head, two halves whose softmaxes
 // alternate with each other's products, so that the tensor cores work on one
 // while the other's row maxima, exponentials and conversions run.  One thread
@@ -393,8 +408,8 @@ constexpr int kCtl = (2 + kK + kV) * kTileBytes<D> + 8 * kStage;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
 // The running maximum is only raised, and the accumulator rescaled, when the
-// new one is more than 2^8 above: p stays below 2^8, which 16-bit floats and
-// the fp32 sums hold as exactly as values below one.
+// new one is more than 2^8 above: p stays below 2^8 (2^15 with kPLift), which
+// 16-bit floats and the fp32 sums hold as exactly as values below one.
 constexpr float kSlack = 8.0f;
 
 struct Seg {
@@ -643,7 +658,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           }
         }
         // a row that has seen nothing yet: exp2(-inf - 0) = 0
-        const float shift = m == -INFINITY ? 0.0f : __fmul_rn(-m, sl);
+        const float shift = m == -INFINITY ? 0.0f : (kPLift<T> == 0.0f ? __fmul_rn(-m, sl) : __fmaf_rn(-m, sl, kPLift<T>));
         const float2 SL = make_float2(sl, sl), SH = make_float2(shift, shift);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -679,7 +694,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       } else {
         const long long l = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
         if (row < p.seq_q && in_span(p.lse + l, 4, p.sp_lse, p.status))
-          p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
+          p.lse[l] = some ? __fmaf_rn(m, p.scale, log_sum<T>(total)) : -INFINITY;
       }
       // checked builds: the rows of a part that this warp writes (a store by TMA stays inside its map)
       const bool fits = __all_sync(0xffffffffu, g.slot < 0 || in_span(p.part + at * D, 4 * D, p.sp_part, p.status));
@@ -799,7 +814,7 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
   const float inv = some ? __frcp_rn(total) : 0.0f;
   const long long l = (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + row;
   if (lane == 0 && in_span(p.lse + l, 4, p.sp_lse, p.status))
-    p.lse[l] = some ? __fmaf_rn(m, p.scale, logf(total)) : -INFINITY;
+    p.lse[l] = some ? __fmaf_rn(m, p.scale, log_sum<T>(total)) : -INFINITY;
   char* dst = p.o + (static_cast<long long>(b) * p.seq_q + row) * p.o_stride + h * (D * 2);
   if (!in_span(dst, D * 2, p.sp_o, p.status)) return;
 #pragma unroll

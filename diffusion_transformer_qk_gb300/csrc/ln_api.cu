@@ -225,6 +225,11 @@ qknr_status qknr_ln_forward(const qknr_ln_args* a, qknr_stream_t stream) {
     return fail(QKNR_ERR_OVERLAP, "y overlaps x without being in place");
   if (hits(so, {kp.sp_weight, kp.sp_bias, kp.sp_mean, kp.sp_rstd}))
     return fail(QKNR_ERR_OVERLAP, "y overlaps a parameter, mean or rstd");
+  const Span mean{static_cast<uintptr_t>(kp.sp_mean.lo), static_cast<uintptr_t>(kp.sp_mean.hi)};
+  const Span rstd{static_cast<uintptr_t>(kp.sp_rstd.lo), static_cast<uintptr_t>(kp.sp_rstd.hi)};
+  for (const Span& s : {mean, rstd})
+    if (hits(s, {kp.sp_x, kp.sp_weight, kp.sp_bias})) return fail(QKNR_ERR_OVERLAP, "mean or rstd overlaps x or a parameter");
+  if (qknr_host::overlaps(mean, rstd)) return fail(QKNR_ERR_OVERLAP, "mean and rstd overlap");
   kp.y = static_cast<char*>(y);
   kp.y_stride = ys * 2;
   kp.sp_y = msp(so);

@@ -76,7 +76,7 @@ void qknr_ln_args_init(qknr_ln_args *a);
 /* Validate and launch the forward pass on `stream` (asynchronous, one
    kernel).  Base addresses and row strides must be 16-byte aligned (mean
    and rstd: 4-byte); `y` must not share an element with an input
-   unless it is x. */
+   unless it is x, mean and rstd none with any other tensor. */
 qknr_status qknr_ln_forward(const qknr_ln_args *args, qknr_stream_t stream);
 
 /* Device bytes qknr_ln_backward needs at `workspace` for these arguments

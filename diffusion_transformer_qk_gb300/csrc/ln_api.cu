@@ -61,6 +61,11 @@ int warps_for(int n_chunks, int cpt, int most) {
 
 qknr::MemSpan msp(Span s) { return qknr::MemSpan{s.lo, s.hi}; }
 
+// Rows that share a parameter row, of those that are there.
+long long sample_rows(const qknr_ln_args* a) {
+  return a->rows_per_batch && a->rows_per_batch < a->tokens ? a->rows_per_batch : a->tokens;
+}
+
 // How the backward pass cuts the rows (nothing here needs a device).
 struct Cut {
   int tiles, group_warps, groups, cpt;
@@ -103,9 +108,9 @@ Cut cut_rows(const qknr_ln_args* a) {
   c.group_warps = warps_for(n_chunks, qknr::kLnBwdCpt, qknr::kLnBwdWarps);
   c.groups = qknr::kLnBwdWarps / c.group_warps;   // groups of several warps: at most 8 named barriers
   c.cpt = (n_chunks + 32 * c.group_warps - 1) / (32 * c.group_warps);
-  c.rows_per_batch = a->rows_per_batch ? a->rows_per_batch : T;
+  c.rows_per_batch = sample_rows(a);
   c.sets = T ? (T + c.rows_per_batch - 1) / c.rows_per_batch : 0;
-  const long long rows = c.rows_per_batch < T ? c.rows_per_batch : T;
+  const long long rows = c.rows_per_batch;
   // One unit per CTA where the samples are few.  Where they are nearly as
   // many as the CTAs, four units per CTA, so that no CTA does twice
   // another's work; where they are more than that, a sample is a unit.
@@ -128,7 +133,7 @@ qknr_status common(const qknr_ln_args* a, qknr::LnParams* kp) {
   const int C = a->hidden, es = 2, pes = a->param_dtype == QKNR_FP32 ? 4 : 2;
   const long long T = a->tokens;
   const long long xs = a->x_stride ? a->x_stride : C, ps = a->param_stride ? a->param_stride : C;
-  const long long rpb = a->rows_per_batch ? a->rows_per_batch : T;
+  const long long rpb = sample_rows(a);
   const long long sets = (T + rpb - 1) / rpb;
   if (!a->x) return fail(QKNR_ERR_NULL, "x is required");
   if (xs < C || ps < C) return fail(QKNR_ERR_SHAPE, "a stride is smaller than hidden");

@@ -23,3 +23,15 @@ LAST = (600 - 1) * 1536 * 2           # bytes to x's last row
 ])
 def test_layer_norm_refuses_statistics_on_other_tensors(lib, change):  # noqa: F811
     refused(lib, "qknr_ln_forward", changed(ln, change), OVERLAP)
+
+
+@pytest.mark.parametrize("T,C", [(600, 1536), (1000, 5120), (7, 64), (100, 9000)])
+@pytest.mark.parametrize("rpb", [1 << 40, (1 << 63) - 600, (1 << 63) - 1])
+def test_a_sample_longer_than_the_call_is_one_sample(lib, T, C, rpb):  # noqa: F811
+    # however long: T + rows_per_batch need not fit in 64 bits
+    sizes = []
+    for value in (0, rpb):
+        n = ctypes.c_size_t(7)
+        assert lib.qknr_ln_workspace_bytes(ctypes.byref(changed(lambda: ln(T, C), dict(rows_per_batch=value))), ctypes.byref(n)) == 0
+        sizes.append(n.value)
+    assert sizes[0] == sizes[1]

@@ -857,6 +857,7 @@ def gn_launch_noalloc(a: QknrGnArgs, stream: Optional[torch.cuda.Stream] = None)
 
 _plans = {}
 _MOST_PLANS = 1024
+_FIXED = (int, float, bool, str, tuple, type(None))
 
 
 class _Plan:
@@ -879,6 +880,8 @@ class _Plan:
 
 
 def _keep(key, plan):
+    if not all(isinstance(x, _FIXED) for x in key):   # a tensor, say: the same object may hold another number
+        return plan
     if len(_plans) >= _MOST_PLANS:
         _plans.clear()
     _plans[key] = plan

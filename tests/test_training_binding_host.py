@@ -38,3 +38,32 @@ def test_an_expanded_row_is_refused(built_lib, call):
 def test_one_row_expanded_to_one_is_a_row():
     with pytest.raises(ValueError, match="CUDA"):
         Q._rows(one_row(1, 64), "x")
+
+
+@pytest.fixture
+def calls(built_lib, monkeypatch):
+    """The argument structs that reach the library, without a device."""
+    seen = []
+    Q.load()
+    monkeypatch.setattr(Q, "_plans", {})
+    monkeypatch.setattr(Q, "_call", lambda fn, a, stream, like: seen.append(a))
+    monkeypatch.setattr(Q, "_empty", lambda shape, dtype, like, stream: torch.empty(shape, dtype=dtype))
+    return seen
+
+
+def test_a_number_in_a_tensor_is_read_at_every_call(calls):
+    # the tensor is the same object, its value is not
+    number = torch.tensor(0.5)
+    for value in (0.5, 2.0, 0.25):
+        number.fill_(value)
+        Q.attention(act(0, 128), act(0, 128), act(0, 128), 1, 1, 128, scale=number, status=False)
+        assert calls[-1].scale == value
+        Q.layer_norm(act(0, 64), eps=number, status=False, mean=None, rstd=None)
+        assert calls[-1].eps == value
+    assert not Q._plans
+
+
+def test_plain_numbers_share_a_plan(calls):
+    for _ in range(3):
+        Q.attention(act(0, 128), act(0, 128), act(0, 128), 1, 1, 128, scale=0.5, causal=True, status=False)
+    assert len(Q._plans) == 1 and all(a.scale == 0.5 and a.causal == 1 for a in calls)

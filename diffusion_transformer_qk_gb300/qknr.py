@@ -902,10 +902,28 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _one_device(like, *tensors) -> None:
+    device = like.get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("all tensors of a call must be on one device")
+
+
 def _call(fn, a, stream, like) -> None:
-    """One library call on ``stream`` (default: the current stream)."""
-    s = torch._C._cuda_getCurrentRawStream(like.get_device()) if stream is None else stream.cuda_stream
-    st = fn(ctypes.byref(a), s)
+    """One library call on ``stream`` (default: the current stream of like's
+    device)."""
+    device = like.get_device()
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device_index == device:
+        s = stream.cuda_stream
+    else:
+        raise ValueError("the stream must be on the tensors' device")
+    if torch._C._cuda_getDevice() == device:      # the library launches on the calling thread's device
+        st = fn(ctypes.byref(a), s)
+    else:
+        with torch.cuda.device(device):
+            st = fn(ctypes.byref(a), s)
     if st != OK:
         raise QknrError(st, load().qknr_last_error().decode())
 
@@ -921,6 +939,7 @@ def _workspace(a, plan, workspace, like, stream):
     else:
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
+        _one_device(like, workspace)
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     return workspace
 
@@ -930,6 +949,7 @@ def _status(a, status, dev_status, like):
     if dev_status is not None:
         if dev_status.dtype != torch.int32 or not dev_status.is_cuda or not dev_status.numel():
             raise ValueError("dev_status must be an int32 CUDA tensor")
+        _one_device(like, dev_status)
         a.dev_status = dev_status.data_ptr()
     elif status:
         word = _status_bufs.get(like.get_device())
@@ -948,10 +968,12 @@ def _match(t, like, name):
     return t
 
 
-def _vector(t, n, name):
-    """A contiguous float32 CUDA tensor of n values."""
+def _vector(t, n, name, like=None):
+    """A contiguous float32 CUDA tensor of n values (on like's device)."""
     if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
         raise ValueError(f"{name} must be a contiguous float32 CUDA tensor of {n} values")
+    if like is not None:
+        _one_device(like, t)
     return t
 
 
@@ -1006,6 +1028,7 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
     key = ("ln", _meta(x), _meta(weight), _meta(bias), _meta(out), rows_per_batch, unit_offset, eps, flags, wait_limit_ns)
     plan = _plans.get(key)
     if plan is None:
+        _one_device(x, weight, bias, out)
         a = ln_args(x, weight, bias, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, flags=flags,
                     wait_limit_ns=wait_limit_ns)
         a.y_stride = x.shape[1] if out is None else _stride(_match(out, x, "out"), "out")
@@ -1013,8 +1036,8 @@ def layer_norm(x, weight=None, bias=None, *, rows_per_batch=None, unit_offset=Fa
     T = x.shape[0]
     if out is None:
         out = _empty(x.shape, x.dtype, x, stream)
-    mean = _empty((T,), torch.float32, x, stream) if mean is None else _vector(mean, T, "mean")
-    rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd")
+    mean = _empty((T,), torch.float32, x, stream) if mean is None else _vector(mean, T, "mean", x)
+    rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd", x)
     a = plan.new()
     a.x, a.y, a.mean, a.rstd = x.data_ptr(), out.data_ptr(), mean.data_ptr(), rstd.data_ptr()
     if weight is not None:
@@ -1037,6 +1060,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
     plan = _plans.get(key)
     T, C = x.shape
     if plan is None:
+        _one_device(x, dy, weight, out)
         a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags,
                     wait_limit_ns=wait_limit_ns)
         a.dy_stride = _stride(_match(dy, x, "dy"), "dy")
@@ -1048,11 +1072,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
     shape, n = plan.info
     if out is None:
         out = _empty(x.shape, x.dtype, x, stream)
-    dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, n, "dweight")
-    dbias = _empty(shape, torch.float32, x, stream) if dbias is None else _vector(dbias, n, "dbias")
+    dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, n, "dweight", x)
+    dbias = _empty(shape, torch.float32, x, stream) if dbias is None else _vector(dbias, n, "dbias", x)
     a = plan.new()
     a.x, a.dy, a.dx = x.data_ptr(), dy.data_ptr(), out.data_ptr()
-    a.mean, a.rstd = _vector(mean, T, "mean").data_ptr(), _vector(rstd, T, "rstd").data_ptr()
+    a.mean, a.rstd = _vector(mean, T, "mean", x).data_ptr(), _vector(rstd, T, "rstd", x).data_ptr()
     a.dweight, a.dbias = dweight.data_ptr(), dbias.data_ptr()
     if weight is not None:
         a.weight = weight.data_ptr()
@@ -1131,6 +1155,7 @@ def qk_norm_rope_packed_backward(dout, qkv, n_heads_q, n_heads_k, n_heads_v, hea
         _match(dout, qkv, "dout")
         if out is not None:
             _match(out, qkv, "out")
+        _one_device(qkv, dout, out, gamma_q, gamma_k, cos, sin)
         _check_table(cos, D, cos_layout, n_heads_q or n_heads_k)
 
         def cols(t, a, b):
@@ -1223,6 +1248,7 @@ def attention(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, c
            _meta(k_lens), _meta(out), flags, wait_limit_ns)
     plan = _plans.get(key)
     if plan is None:
+        _one_device(q, k, v, q_lens, k_lens, out)
         a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
                       k_lens=k_lens, flags=flags, wait_limit_ns=wait_limit_ns)
         a.o_stride = 0 if out is None else _stride(_match(out, q, "out"), "out")
@@ -1230,7 +1256,7 @@ def attention(q, k, v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, c
     shape, n = plan.info
     if out is None:
         out = _empty(q.shape, q.dtype, q, stream)
-    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, n, "lse")
+    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, n, "lse", q)
     a = plan.new()
     a.q, a.k, a.v, a.o, a.lse = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()
     if q_lens is not None:
@@ -1253,6 +1279,7 @@ def attention_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, *, b
            causal, _meta(q_lens), _meta(k_lens), _meta(dq), _meta(dk), _meta(dv), flags, wait_limit_ns)
     plan = _plans.get(key)
     if plan is None:
+        _one_device(q, do, k, v, o, q_lens, k_lens, dq, dk, dv)
         a = attn_args(q, k, v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal, q_lens=q_lens,
                       k_lens=k_lens, flags=flags, wait_limit_ns=wait_limit_ns)
         a.o_stride, a.dout_stride = _stride(_match(o, q, "o"), "o"), _stride(_match(do, q, "do"), "do")
@@ -1268,7 +1295,7 @@ def attention_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, *, b
         dv = _empty(v.shape, v.dtype, v, stream)
     a = plan.new()
     a.q, a.k, a.v, a.o, a.dout = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr()
-    a.lse = _vector(lse, plan.info, "lse").data_ptr()
+    a.lse = _vector(lse, plan.info, "lse", q).data_ptr()
     a.dq, a.dk, a.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
     if q_lens is not None:
         a.q_lens = q_lens.data_ptr()

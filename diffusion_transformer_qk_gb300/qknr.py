@@ -957,9 +957,11 @@ def _status(a, status, dev_status, like):
 
 
 def _stride(t, name):
-    """Row stride of a 2-D view; 0 (the library's default) where it has no
-    elements, whose strides mean nothing."""
-    return _rows(t, name) if t.numel() else 0
+    """Row stride of a 2-D view; 0 (the library's default) where it means
+    nothing: without elements, or with a single row and a stride that would
+    not do for several."""
+    stride = _rows(t, name) if t.numel() else 0
+    return 0 if t.shape[0] == 1 and (stride < t.shape[1] or stride % 8) else stride
 
 
 def _match(t, like, name):

@@ -6,6 +6,7 @@ between its units but the row sums' own barriers, so units of an odd number
 of steps are the ones to look at: the last step of a unit and the first of
 the next must not share a buffer of sums.  Bounds as in test_layernorm_gpu."""
 import pytest
+import torch
 
 from diffusion_transformer_qk_gb300 import qknr as Q
 from tests.test_layernorm_gpu import _lib, both  # noqa: F401  (the fixture)
@@ -28,3 +29,14 @@ def test_samples_of_wide_rows(T, rpb, C):
 @pytest.mark.parametrize("C", [3000, 4096])
 def test_samples_of_two_groups(T, rpb, C):
     both(T, C, "fp16", "fp32", rpb, seed=T + rpb + C)
+
+
+def test_one_row_of_any_stride():
+    s, (y, mean, rstd), grads = both(1, 512, seed=3)
+    wide = torch.zeros(1, 2 * 512 + 3, dtype=torch.bfloat16, device="cuda")
+    x, dy = wide[:, :512], s["dy"].view(512, 1).clone().t()       # row strides of 1027 and of 1
+    x.copy_(s["x"])
+    assert x.stride(0) % 8 and dy.stride(0) == 1
+    got = Q.layer_norm(x, s["weight"], s["bias"])
+    got += Q.layer_norm_backward(dy, x, s["weight"], mean, rstd)
+    assert all(same_bits(a, b) for a, b in zip(got, (y, mean, rstd, *grads)))

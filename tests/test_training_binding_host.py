@@ -175,3 +175,13 @@ def test_a_call_runs_on_its_tensors_device(built_lib, monkeypatch):
     with pytest.raises(ValueError, match="device"):
         Q._call(fn, Q.QknrAttnArgs(), Stream(1), rows(0))
     assert len(seen) == 4
+
+
+@pytest.mark.parametrize("stride", [1, 7, 129, 131])
+def test_the_stride_of_a_single_row_says_nothing(calls, stride):
+    # tensors of one row have whatever row stride they were made with
+    row = Elsewhere(0, like=torch.empty(1000, dtype=torch.bfloat16, device="meta").as_strided((1, 128), (stride, 1)))
+    Q.attention(row, row, row, 1, 1, 128, status=False)
+    assert (calls[-1].q_stride, calls[-1].k_stride, calls[-1].v_stride) == (0, 0, 0)
+    Q.layer_norm(row, None, None, out=row, status=False)
+    assert (calls[-1].x_stride, calls[-1].y_stride) == (0, 0)

@@ -186,7 +186,7 @@ constexpr int kLnMaxStages = 32;                  // all groups' together
 constexpr int kLnOffBars = 0;                     // full[32]
 constexpr int kLnOffAbort = 256;
 constexpr int kLnOffRed = 512;                    // per group two buffers of kLnRedFloats
-constexpr int kLnOffStages = kLnOffRed + kLnWarps * 2 * kLnRedFloats * 4;   // 2560
+constexpr int kLnOffStages = kLnOffRed + kLnWarps * 2 * kLnRedFloats * 4;   // 4608
 static_assert(kLnOffStages % 128 == 0, "shared memory map");
 
 // One group's ring of `stages` stages.  Its rows come in the order in which
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kLnThreads, 1) ln_forward_kernel(const __grid_
       mean[r] = __fmul_rn(t[r], p.inv_c);
       const float2 nm = make_float2(-mean[r], -mean[r]);
       float2 q = make_float2(0.0f, 0.0f);
+      if (r >= n) break;                          // there is no second row
 #pragma unroll
       for (int i = 0; i < CPT; ++i)
 #pragma unroll

@@ -251,9 +251,11 @@ long long blocks_of(int seq) { return (static_cast<long long>(seq) + qknr::kTile
 bool few(const qknr_attn_args* a) { return a->seq_q <= qknr::kFewRows; }
 
 // Their tiles are up to kFewRows rows of a key head.  They go round to the
-// CTAs, the last ones (or all, where they are fewer) cut along the keys.  A
-// share is at least 256 keys, a step of all a CTA's warps; below 1024 keys the
-// second launch costs more than it saves.
+// CTAs, the last ones (or all, where they are fewer) cut along the keys.  Where
+// all are cut, no more CTAs take part than leaves each 256 keys (a step of its
+// warps is 128 to 384); what is left after whole tiles goes to all CTAs, down
+// to a few keys each.  Below 1024 keys the second launch costs more than it
+// saves.
 Cut cut_few(const qknr_attn_args* a) {
   Cut c;
   const long long all = static_cast<long long>(a->seq_q) * (a->n_heads_q / a->n_heads_k);

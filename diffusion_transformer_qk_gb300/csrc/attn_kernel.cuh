@@ -1,9 +1,12 @@
 // Attention forward and backward for sm_103a (formulas: qknr_attn.h).
 //
-// All four kernels' products run on tcgen05 with operands that TMA leaves in
-// shared memory and accumulators in tensor memory; the probabilities (and the
-// score gradients) go back to tensor memory as 16-bit left operands of the
-// second product, in the columns whose scores they replace.  MMAs of
+// The products of the three kernels here that have some (forward, dq, and dk
+// with dv) run on tcgen05 with operands that TMA leaves in shared memory and
+// accumulators in tensor memory; the probabilities (and the score gradients) go
+// back to tensor memory as 16-bit left operands of the second product, in the
+// columns whose scores they replace.  Operands of one product have one type, so
+// that rounding is what 16-bit queries, keys and values cost: h of each
+// probability, where the formula in 32 bits rounds the output alone.  MMAs of
 // one thread run in order, so a product that overwrites an operand of an
 // earlier one needs no wait in between.
 //

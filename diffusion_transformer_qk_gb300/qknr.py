@@ -1055,8 +1055,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
                         dbias=None, workspace=None, stream=None, status=True, dev_status=None, flags=0,
                         wait_limit_ns=0):
     """Gradients of ``layer_norm``: returns (dx, dweight, dbias), the last two
-    float32, of weight's shape ([C] where weight is None).  ``out`` receives
-    dx (default: a new tensor; ``out=dy`` is in place)."""
+    float32: [C], or a row for each sample where ``rows_per_batch`` is given or
+    weight has rows (for its first rows, if x has fewer samples).  ``out``
+    receives dx (default: a new tensor; ``out=dy`` is in place)."""
     key = ("ln_bwd", _meta(dy), _meta(x), _meta(weight), _meta(out), rows_per_batch, unit_offset, flags,
            wait_limit_ns)
     plan = _plans.get(key)

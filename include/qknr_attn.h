@@ -15,7 +15,10 @@
  * whole sequence) and, with causal, j <= i + k_lens[b] - q_lens[b] (the
  * diagonal ends at the last valid query and the last valid key).  A query
  * that sees no key answers o = 0 and lse = -inf.  What lies in rows past the
- * lengths, NaN and infinities included, reaches no output.
+ * lengths, NaN and infinities included, reaches no output.  (Within the
+ * lengths a masked key has p = 0, which does not stop a NaN or an infinity: one
+ * in a key or value may reach the queries of the same tile that the causal mask
+ * hides it from, one in a query or its gradient the gradients of such keys.)
  *
  * The backward pass takes do = dL/do with the forward pass's o and lse and
  * recomputes p:

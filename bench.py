@@ -11,9 +11,10 @@ Prints one JSON line: microseconds per call (whole job), achieved HBM
 bandwidth against the measured copy peak, the CPU oracle's time on a
 bounded sample, an end-to-end number from pinned host buffers (one
 qknr_forward_host call per step), the SM clocks seen during the timed
-region, the launch count, and (with the default workload) every other
-workload and variant timed the same way (``configs``).  ``--impl
-reference`` times the fp64 CPU oracle instead.
+region and the launch count.  With the default workload every other
+workload and variant is timed the same way; those (``configs``, some 20 KB)
+go to stderr, so that the line stays short enough for whoever keeps only the
+end of the output.  ``--impl reference`` times the fp64 CPU oracle instead.
 
 Multi-GPU: one process per GPU (torchrun); every rank runs its own full
 workload (replicas, weak scaling), timing is the max over ranks.
@@ -801,11 +802,12 @@ def run_ours(args, w):
                                           f"fp64 numpy, scaled to a full call of {run.tokens} rows by tokens",
                                 "single_thread": single}
     if world == 1 and args.configs == "all" and w == I.WORKLOADS[DEFAULT_WORKLOAD] and args.tokens is None:
-        line["configs"] = run_config_sweep(dev, status, args.config_steps, 5, peak)
-        line["configs_note"] = ("every workload and variant at its full size, default launch shapes, "
-                                f"{args.config_steps} calls each after 5 warm-up calls; frac = achieved / "
-                                f"{peak_kind} hbm_gbs {peak:.1f} GB/s; kernel sources sha256 "
-                                f"{kernel_source_hash()[:16]}")
+        sweep = {"configs": run_config_sweep(dev, status, args.config_steps, 5, peak),
+                 "configs_note": "every workload and variant at its full size, default launch shapes, "
+                                 f"{args.config_steps} calls each after 5 warm-up calls; frac = achieved / "
+                                 f"{peak_kind} hbm_gbs {peak:.1f} GB/s; kernel sources sha256 "
+                                 f"{kernel_source_hash()[:16]}"}
+        print(json.dumps(sweep), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
     return 0
 
@@ -1062,7 +1064,7 @@ def main(argv=None):
                    help="print the device copy rate at the workloads' sizes (one JSON line each) and exit")
     p.add_argument("--configs", choices=["all", "none"], default="all",
                    help="with the default workload on one GPU: also time every workload and variant "
-                        "(the line's 'configs' object)")
+                        "(one JSON line on stderr, 'configs')")
     p.add_argument("--config-steps", type=int, default=300)
     p.add_argument("--no-e2e", action="store_true")
     p.add_argument("--no-cpu-baseline", action="store_true")

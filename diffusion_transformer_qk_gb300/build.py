@@ -42,6 +42,7 @@ SOURCES = [
     "adaln_inst.cu",
     "gn_api.cu",
     "ln_api.cu",
+    "rms_api.cu",
     "grad_api.cu",
     "attn_api.cu",
 ]

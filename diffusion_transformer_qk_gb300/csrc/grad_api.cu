@@ -250,6 +250,7 @@ qknr_status qknr_backward(const qknr_grad_args* a, qknr_stream_t stream) {
   if (st != QKNR_OK || (!a->dgamma_q && !a->dgamma_k)) return st;
   qknr::PartsParams pp;
   memset(&pp, 0, sizeof(pp));
+  pp.sums = 2;
   pp.parts = kp.parts;
   pp.out[0] = a->n_heads_q ? a->dgamma_q : nullptr;
   pp.out[1] = a->n_heads_k ? a->dgamma_k : nullptr;

@@ -365,6 +365,7 @@ qknr_status qknr_ln_backward(const qknr_ln_args* a, qknr_stream_t stream) {
   if (st != QKNR_OK || !kp.parts || (!kp.dweight && !kp.dbias)) return st;
   qknr::PartsParams pp;
   memset(&pp, 0, sizeof(pp));
+  pp.sums = 2;
   pp.parts = kp.parts;
   pp.out[0] = kp.dweight;
   pp.out[1] = kp.dbias;

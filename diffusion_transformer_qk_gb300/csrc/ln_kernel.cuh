@@ -214,18 +214,20 @@ struct LnRing {
         status(p.status),
         limit(p.wait_limit_ns) {}
 
-  // Row `a` (and `b` behind it) into the next stage, which has been read.
+  // Row `a` (and `b`, and `c`, behind it) into the next stage, which has been read.
   __device__ __forceinline__ void put(const char* a, const MemSpan& sp_a, const char* b, const MemSpan& sp_b,
-                                      unsigned bytes) {
-    if (!in_span(a, bytes, sp_a, status) || (b && !in_span(b, bytes, sp_b, status))) {
+                                      unsigned bytes, const char* c = nullptr, const MemSpan& sp_c = MemSpan{0, 0}) {
+    if (!in_span(a, bytes, sp_a, status) || (b && !in_span(b, bytes, sp_b, status)) ||
+        (c && !in_span(c, bytes, sp_c, status))) {
       *abort_flag = 1;
       return;
     }
     const uint32_t dst = stage0 + put_s * stage_bytes, bar = bars + 8 * put_s;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the group's reads come before the copy
-    mbar_arrive_expect_tx(bar, b ? 2 * bytes : bytes);
+    mbar_arrive_expect_tx(bar, c ? 3 * bytes : b ? 2 * bytes : bytes);
     bulk_load(dst, a, bytes, bar);
     if (b) bulk_load(dst + bytes, b, bytes, bar);
+    if (c) bulk_load(dst + 2 * bytes, c, bytes, bar);
     if (++put_s == stages) put_s = 0;
     ++in_flight;
   }

@@ -7,8 +7,9 @@
 namespace qknr {
 
 struct PartsParams {
-  const float* parts;         // [sets][units][2][cols]
+  const float* parts;         // [sets][units][sums][cols]
   float* out[2];              // [sets][cols] each; null: not wanted
+  int sums;                   // 1 or 2
   int cols;                   // a multiple of 4
   long long units;
   MemSpan sp_parts, sp_out[2];
@@ -26,18 +27,18 @@ static __global__ void __launch_bounds__(32 * kPartsRows) parts_kernel(const __g
   const int col_tiles = (p.cols + kPartsCols - 1) / kPartsCols;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = static_cast<int>(blockIdx.x % col_tiles) * kPartsCols + 4 * tx;
-  const int which = static_cast<int>(blockIdx.x / col_tiles % 2);
-  const long long set = blockIdx.x / col_tiles / 2;
+  const int which = static_cast<int>(blockIdx.x / col_tiles % p.sums);
+  const long long set = blockIdx.x / col_tiles / p.sums;
   auto add = [](float4 a, const float4& b) {
     return make_float4(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y), __fadd_rn(a.z, b.z), __fadd_rn(a.w, b.w));
   };
   grid_dependency_wait();
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < p.cols) {
-    const float* src = p.parts + (set * p.units * 2 + which) * p.cols + c;
+    const float* src = p.parts + (set * p.units * p.sums + which) * p.cols + c;
 #pragma unroll 8
     for (long long u = ty; u < p.units; u += kPartsRows) {
-      const float* at = src + u * 2 * p.cols;
+      const float* at = src + u * p.sums * p.cols;
       if (in_span(at, 16, p.sp_parts, p.status)) s = add(s, __ldcg(reinterpret_cast<const float4*>(at)));
     }
   }
@@ -63,7 +64,7 @@ static __global__ void __launch_bounds__(32 * kPartsRows) parts_kernel(const __g
 }
 
 inline long long parts_grid(const PartsParams& p, long long sets) {
-  return sets * 2 * ((p.cols + kPartsCols - 1) / kPartsCols);
+  return sets * p.sums * ((p.cols + kPartsCols - 1) / kPartsCols);
 }
 
 }  // namespace qknr

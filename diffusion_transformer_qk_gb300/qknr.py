@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import glob
+import math
 import os
 import threading
 from ctypes import c_char, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
@@ -49,12 +50,16 @@ EXPORTS = (
     "qknr_grad_args_init", "qknr_grad_workspace_bytes", "qknr_backward", "qknr_sizeof_grad_args",
     "qknr_attn_args_init", "qknr_attn_workspace_bytes", "qknr_attn_backward_workspace_bytes", "qknr_attn_forward",
     "qknr_attn_backward", "qknr_attn_sizeof_args",
+    "qknr_rms_args_init", "qknr_rms_forward", "qknr_rms_workspace_bytes", "qknr_rms_backward", "qknr_rms_sizeof_args",
 )
 GN_MODE = {"auto": 0, "fused": 1, "two_pass": 2, "cluster": 3}
 GN_FLAG_TEST_NO_RECORDS = 0x2
 GN_NOALLOC_SCRATCH_BYTES = 1 << 20
 HOST_MAX_BUFFERS = 4
 LN_UNIT_OFFSET = 0x10
+RMS_UNIT_OFFSET = 0x10
+RMS_OUT_SAME, RMS_OUT_E4M3 = 0, 1
+RMS_BLOCK = 128
 
 
 class QknrArgs(ctypes.Structure):
@@ -191,6 +196,25 @@ class QknrAttnArgs(ctypes.Structure):
     ]
 
 
+class QknrRmsArgs(ctypes.Structure):
+    """Mirror of ``qknr_rms_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("x", c_void_p), ("residual", c_void_p), ("sum", c_void_p), ("y", c_void_p),
+        ("x_stride", c_int64), ("residual_stride", c_int64), ("sum_stride", c_int64), ("y_stride", c_int64),
+        ("tokens", c_int64), ("hidden", c_int32), ("rows_per_batch", c_int64),
+        ("weight", c_void_p), ("param_dtype", c_int32), ("param_stride", c_int64),
+        ("eps", c_float), ("rstd", c_void_p),
+        ("out", c_int32), ("scale_block", c_int32), ("scales", c_void_p),
+        ("dy", c_void_p), ("dsum", c_void_p), ("dx", c_void_p),
+        ("dy_stride", c_int64), ("dsum_stride", c_int64), ("dx_stride", c_int64),
+        ("dweight", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32), ("wait_limit_ns", c_uint64),
+    ]
+
+
 class QknrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -256,13 +280,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.qknr_forward_host.argtypes = [ctypes.POINTER(QknrArgs), ctypes.POINTER(QknrHostPlan), c_void_p]
         lib.qknr_forward_host.restype = c_int32
         lib.qknr_sizeof_host_plan.restype = c_size_t
-        for name, struct in (("ln", QknrLnArgs), ("grad", QknrGradArgs)):
+        for name, struct in (("ln", QknrLnArgs), ("grad", QknrGradArgs), ("rms", QknrRmsArgs)):
             p_struct = ctypes.POINTER(struct)
             init, space = getattr(lib, f"qknr_{name}_args_init"), getattr(lib, f"qknr_{name}_workspace_bytes")
             init.argtypes, init.restype = [p_struct], None
             space.argtypes, space.restype = [p_struct, ctypes.POINTER(c_size_t)], c_int32
         for fn, struct in ((lib.qknr_ln_forward, QknrLnArgs), (lib.qknr_ln_backward, QknrLnArgs),
-                           (lib.qknr_backward, QknrGradArgs)):
+                           (lib.qknr_backward, QknrGradArgs), (lib.qknr_rms_forward, QknrRmsArgs),
+                           (lib.qknr_rms_backward, QknrRmsArgs)):
             fn.argtypes, fn.restype = [ctypes.POINTER(struct), c_void_p], c_int32
         p_attn = ctypes.POINTER(QknrAttnArgs)
         lib.qknr_attn_args_init.argtypes, lib.qknr_attn_args_init.restype = [p_attn], None
@@ -273,6 +298,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.qknr_attn_sizeof_args.restype = c_size_t
         lib.qknr_ln_sizeof_args.restype = c_size_t
         lib.qknr_sizeof_grad_args.restype = c_size_t
+        lib.qknr_rms_sizeof_args.restype = c_size_t
         if lib.qknr_abi_version() != ABI_VERSION:
             raise RuntimeError("libqknr.so ABI version mismatch")
         if lib.qknr_sizeof_args() != ctypes.sizeof(QknrArgs) or \
@@ -282,6 +308,7 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 lib.qknr_ln_sizeof_args() != ctypes.sizeof(QknrLnArgs) or \
                 lib.qknr_sizeof_grad_args() != ctypes.sizeof(QknrGradArgs) or \
                 lib.qknr_attn_sizeof_args() != ctypes.sizeof(QknrAttnArgs) or \
+                lib.qknr_rms_sizeof_args() != ctypes.sizeof(QknrRmsArgs) or \
                 lib.qknr_sizeof_host_plan() != ctypes.sizeof(QknrHostPlan):
             raise RuntimeError("libqknr.so struct layout differs from the binding")
         if path is None:
@@ -1087,6 +1114,149 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
     workspace = _workspace(a, plan, workspace, x, stream)
     _call((_lib or load()).qknr_ln_backward, a, stream, x)
     return out, dweight, dbias
+
+
+# ---------------------------------------------------------------------------
+# the root-mean-square norm with the residual's addition (include/qknr_rms.h)
+
+def rms_args(x, weight=None, *, rows_per_batch=None, unit_offset=False, eps=1e-6, dev_status=None, flags=0,
+             wait_limit_ns=0) -> QknrRmsArgs:
+    """The arguments both passes share: token rows ``x`` [T, C] and ``weight``
+    [C] or [B, C] (float32 or x's dtype; may be None), row t taking row
+    t // rows_per_batch of it (default: one row)."""
+    a = QknrRmsArgs()
+    load().qknr_rms_args_init(ctypes.byref(a))
+    if x.dtype not in _ACT:
+        raise ValueError("x must be bfloat16 or float16")
+    a.dtype = _ACT[x.dtype]
+    a.x, a.x_stride = x.data_ptr(), _stride(x, "x")
+    a.tokens, a.hidden = x.shape
+    a.rows_per_batch = rows_per_batch or 0
+    sets = -(-x.shape[0] // rows_per_batch) if rows_per_batch else 1
+    if weight is not None:
+        rows = weight.view(1, -1) if weight.dim() == 1 else weight
+        if rows.dim() != 2 or rows.shape[1] != x.shape[1] or rows.shape[0] < sets:
+            raise ValueError(f"weight must be [C] or [{sets}, C]")
+        if weight.dtype not in (torch.float32, x.dtype):
+            raise ValueError("weight must be float32 or of x's dtype")
+        a.weight, a.param_stride = weight.data_ptr(), _stride(rows, "weight")
+        a.param_dtype = FP32 if weight.dtype == torch.float32 else a.dtype
+    a.eps = eps
+    a.dev_status = _ptr(dev_status)
+    a.flags, a.wait_limit_ns = flags | (RMS_UNIT_OFFSET if unit_offset else 0), wait_limit_ns
+    return a
+
+
+def _rms_forward(small, block, x, weight, residual, rows_per_batch, unit_offset, out, scales, sum_out, rstd, eps, stream,
+                 status, dev_status, flags, wait_limit_ns):
+    key = ("rms", small, block, _meta(x), _meta(weight), _meta(residual), _meta(out), _meta(sum_out), rows_per_batch,
+           unit_offset, eps, flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        _one_device(x, weight, residual, out, sum_out)
+        a = rms_args(x, weight, rows_per_batch=rows_per_batch, unit_offset=unit_offset, eps=eps, flags=flags,
+                     wait_limit_ns=wait_limit_ns)
+        if block not in (None, RMS_BLOCK) or (block and x.shape[1] % block):
+            raise ValueError(f"block must be None or {RMS_BLOCK}, with as many columns or a multiple")
+        shape = (x.shape[0], x.shape[1] // block) if block else (x.shape[0],)
+        a.out, a.scale_block = RMS_OUT_E4M3 if small else RMS_OUT_SAME, block or 0
+        if residual is not None:
+            a.residual_stride = _stride(_match(residual, x, "residual"), "residual")
+        elif sum_out is not None:
+            raise ValueError("sum_out is the sum with a residual")
+        if sum_out is not None:
+            a.sum_stride = _stride(_match(sum_out, x, "sum_out"), "sum_out")
+        if out is not None:
+            if out.shape != x.shape or out.dtype != (torch.float8_e4m3fn if small else x.dtype):
+                raise ValueError(f"out must be {tuple(x.shape)} of {torch.float8_e4m3fn if small else x.dtype}")
+            a.y_stride = _stride(out, "out")
+        plan = _keep(key, _Plan(a, None, (shape, math.prod(shape))))
+    T = x.shape[0]
+    if out is None:
+        out = _empty(x.shape, torch.float8_e4m3fn if small else x.dtype, x, stream)
+    rstd = _empty((T,), torch.float32, x, stream) if rstd is None else _vector(rstd, T, "rstd", x)
+    a = plan.new()
+    a.x, a.y, a.rstd = x.data_ptr(), out.data_ptr(), rstd.data_ptr()
+    if weight is not None:
+        a.weight = weight.data_ptr()
+    if small:
+        shape, n = plan.info
+        scales = _empty(shape, torch.float32, x, stream) if scales is None else _vector(scales, n, "scales", x)
+        a.scales = scales.data_ptr()
+    h = x
+    if residual is not None:
+        h = _empty(x.shape, x.dtype, x, stream) if sum_out is None else sum_out
+        a.residual, a.sum = residual.data_ptr(), h.data_ptr()
+    _status(a, status, dev_status, x)
+    _call((_lib or load()).qknr_rms_forward, a, stream, x)
+    return out, scales, rstd, h
+
+
+def rms_norm(x, weight=None, *, residual=None, rows_per_batch=None, unit_offset=False, out=None, sum_out=None, rstd=None,
+             eps=1e-6, stream=None, status=True, dev_status=None, flags=0, wait_limit_ns=0):
+    """Root-mean-square norm of token rows ``x`` [T, C], after the addition of
+    ``residual`` (like x, or None): returns (y, rstd, h) with rstd float32 [T]
+    and h = x + residual in x's dtype, the next residual (x itself without
+    one).  h and rstd are what the backward pass needs.
+
+    ``weight`` is [C], or [B, C] with row t taking row t // rows_per_batch;
+    with ``unit_offset`` the gain is 1 + weight.  Results go to ``out`` (may be
+    x) and ``sum_out`` (may be residual or x), new tensors by default."""
+    out, _, rstd, h = _rms_forward(False, None, x, weight, residual, rows_per_batch, unit_offset, out, None, sum_out, rstd,
+                                   eps, stream, status, dev_status, flags, wait_limit_ns)
+    return out, rstd, h
+
+
+def rms_norm_quantized(x, weight=None, *, residual=None, block=None, rows_per_batch=None, unit_offset=False, out=None,
+                       scales=None, sum_out=None, rstd=None, eps=1e-6, stream=None, status=True, dev_status=None, flags=0,
+                       wait_limit_ns=0):
+    """``rms_norm`` into 8 bits, the input of an 8-bit projection: returns
+    (y, scales, rstd, h) with y torch.float8_e4m3fn [T, C] and scales float32
+    [T], or with ``block=128`` [T, C / 128], so that y * scale is the norm."""
+    return _rms_forward(True, block, x, weight, residual, rows_per_batch, unit_offset, out, scales, sum_out, rstd, eps,
+                        stream, status, dev_status, flags, wait_limit_ns)
+
+
+def rms_norm_backward(dy, x, weight, rstd, *, dsum=None, rows_per_batch=None, unit_offset=False, out=None, dweight=None,
+                      workspace=None, stream=None, status=True, dev_status=None, flags=0, wait_limit_ns=0):
+    """Gradients of ``rms_norm`` for its h as ``x``: returns (dx, dweight).  dx
+    is the gradient of the forward pass's x and of its residual alike; ``dsum``,
+    the gradient that reaches h past the norm, is added to it.  dweight is
+    float32, [C] or a row for each sample (None without a weight).  ``out``
+    receives dx (default: a new tensor; dy or dsum: in place)."""
+    key = ("rms_bwd", _meta(dy), _meta(x), _meta(weight), _meta(dsum), _meta(out), rows_per_batch, unit_offset, flags,
+           wait_limit_ns)
+    plan = _plans.get(key)
+    T, C = x.shape
+    if plan is None:
+        _one_device(x, dy, weight, dsum, out)
+        a = rms_args(x, weight, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags,
+                     wait_limit_ns=wait_limit_ns)
+        a.dy_stride = _stride(_match(dy, x, "dy"), "dy")
+        if dsum is not None:
+            a.dsum_stride = _stride(_match(dsum, x, "dsum"), "dsum")
+        if out is not None:
+            a.dx_stride = _stride(_match(out, x, "out"), "out")
+        sets = -(-T // rows_per_batch) if rows_per_batch else 1
+        shape = (C,) if weight is None or weight.dim() == 1 else (sets, C)
+        plan = _keep(key, _Plan(a, load().qknr_rms_workspace_bytes, (shape, math.prod(shape))))
+    shape, n = plan.info
+    if out is None:
+        out = _empty(x.shape, x.dtype, x, stream)
+    if weight is None:
+        dweight = None
+    else:
+        dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, n, "dweight", x)
+    a = plan.new()
+    a.x, a.dy, a.dx, a.rstd = x.data_ptr(), dy.data_ptr(), out.data_ptr(), _vector(rstd, T, "rstd", x).data_ptr()
+    if weight is not None:
+        a.weight, a.dweight = weight.data_ptr(), dweight.data_ptr()
+    if dsum is not None:
+        a.dsum = dsum.data_ptr()
+    _status(a, status, dev_status, x)
+    workspace = _workspace(a, plan, workspace, x, stream)
+    _call((_lib or load()).qknr_rms_backward, a, stream, x)
+    return out, dweight
 
 
 # ---------------------------------------------------------------------------

@@ -45,6 +45,7 @@ SOURCES = [
     "rms_api.cu",
     "grad_api.cu",
     "attn_api.cu",
+    "attn_seq_api.cu",
 ]
 
 

@@ -56,7 +56,8 @@ __device__ __forceinline__ void few_mma<__half>(float (&c)[4], const uint32_t (&
 
 // H halves of 8 rows.  Lane (g, t) = (lane / 4, lane % 4) owns rows g and, with
 // two halves, g + 8; of their accumulators columns 64 cc + 16 t + 0 .. 15.
-template <typename T, int D, int H>
+// PLANNED: tiles of p.few_rows rows from the plan.
+template <typename T, int D, int H, bool PLANNED = false>
 __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(const __grid_constant__ AttnParams p) {
   constexpr int ROWS = 8 * H, WARPS = few_warps(ROWS), KC = D / 32, VC = D / 64, STAGES = few_stages(ROWS, D);
   constexpr int kKeys = few_keys(D), KT = kKeys / 8;
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   unsigned char* ctl = smem + WARPS * (kRing + ROWS * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * WARPS * STAGES);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3, slot_rows = min(p.group * p.seq_q, kFewRows);
+  const int g = lane >> 2, t = lane & 3, slot_rows = PLANNED ? p.few_rows : min(p.group * p.seq_q, kFewRows);
   const unsigned char* ring = smem + warp * kRing;
   // the warp's barriers
   const AttnCta cta{smem, smem_addr(ring), smem_addr(ctl) + 8 * warp * STAGES, abort_flag, p.status, p.wait_limit_ns, warp, lane};
@@ -83,12 +84,29 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   RingPos<STAGES> at;         // the next step to read
   bool ok = true;
   AttnWork w;
-  for (int s = 0; ok && attn_work(p, s, w); ++s) {
-    // rows row0 + r, r < rows, of key head hk: query (row0 + r) % seq_q of head (row0 + r) / seq_q of its group
-    const int key_head = w.tile / p.tiles, b = key_head / p.heads_k, hk = key_head - b * p.heads_k;
-    const int row0 = (w.tile - key_head * p.tiles) * kFewRows, rows = min(p.group * p.seq_q - row0, kFewRows);
-    const int q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
-    const int k_len = clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
+  AttnPiece piece;
+  for (int s = 0; ok && (PLANNED ? attn_piece(p, s, piece) : attn_work(p, s, w)); ++s) {
+    // rows row0 + r, r < rows, of key head hk: query (row0 + r) % queries of head (row0 + r) / queries of its group
+    int b, hk, row0, rows, q_len, k_len, queries;
+    if (PLANNED) {
+      b = 0;
+      hk = piece.h;
+      row0 = piece.t0;
+      queries = q_len = piece.q_len;
+      k_len = piece.k_len;
+      rows = min(p.group * queries - row0, p.few_rows);
+      w.slot = piece.slot;
+    } else {
+      const int key_head = w.tile / p.tiles;
+      b = key_head / p.heads_k;
+      hk = key_head - b * p.heads_k;
+      row0 = (w.tile - key_head * p.tiles) * kFewRows;
+      queries = p.seq_q;
+      rows = min(p.group * queries - row0, kFewRows);
+      q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
+      k_len = clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
+    }
+    const int q_row = PLANNED ? piece.q_row : 0, k_row = PLANNED ? piece.k_row : 0;
     // keys [0, limit) are seen; the last query sees the most
     const int n = q_len > 0 ? k_len : 0;
     int limit[H];
@@ -96,12 +114,12 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     float m[H], l[H], acc[VC][8][4];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const int r = g + 8 * h, i = (row0 + r) % p.seq_q, head = hk * p.group + (row0 + r) / p.seq_q;
+      const int r = g + 8 * h, i = (row0 + r) % queries, head = hk * p.group + (row0 + r) / queries;
       const bool mine = r < rows && i < q_len;
       m[h] = -INFINITY;
       l[h] = 0.0f;
       limit[h] = mine ? (p.causal ? min(max(i + k_len - q_len + 1, 0), k_len) : k_len) : 0;
-      const char* src = p.q_in + (static_cast<long long>(b) * p.seq_q + i) * p.q_stride + head * (D * 2) + t * 32;
+      const char* src = p.q_in + (static_cast<long long>(b) * p.seq_q + q_row + i) * p.q_stride + head * (D * 2) + t * 32;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         q[h][c] = make_uint4(0, 0, 0, 0);
@@ -116,7 +134,12 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[c][j][e] = 0.0f;
     int begin, end;
-    attn_cut(w, n, begin, end);
+    if (PLANNED) {
+      begin = min(piece.u0 * kTile, n);
+      end = min(piece.u1 * kTile, n);
+    } else {
+      attn_cut(w, n, begin, end);
+    }
     // lane 0: the next step's keys and values into the stage after those in flight
     constexpr int kHop = WARPS * kKeys;
     int ahead = begin + warp * kKeys, in_flight = 0;
@@ -125,8 +148,8 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
       if (ahead >= end || (p.flags & 1u)) return;             // test only: issue nothing
       const uint32_t bar = cta.bar(put), dst = cta.base + put * kStep;
       mbar_arrive_expect_tx(bar, kStep);
-      tma_load_tile(dst, &p.map_k, ahead, hk, b, bar);
-      tma_load_tile(dst + kStep / 2, &p.map_v, ahead, hk, b, bar);
+      tma_load_tile(dst, &p.map_k, k_row + ahead, hk, b, bar);
+      tma_load_tile(dst + kStep / 2, &p.map_v, k_row + ahead, hk, b, bar);
       put = put + 1 == STAGES ? 0 : put + 1;
       ahead += kHop;
       ++in_flight;
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
         total = __fmaf_rn(f, stats[i][r].y, total);
         o = __ffma2_rn(make_float2(f, f), *reinterpret_cast<const float2*>(sums(i, r) + c), o);
       }
-      const int i = (row0 + r) % p.seq_q, h = hk * p.group + (row0 + r) / p.seq_q;
+      const int i = q_row + (row0 + r) % queries, h = hk * p.group + (row0 + r) / queries;
       if (w.slot >= 0) {
         const long long k = static_cast<long long>(w.slot) * slot_rows + r;
         if (in_span(p.part + k * D + c, 8, p.sp_part, p.status)) *reinterpret_cast<float2*>(p.part + k * D + c) = o;

@@ -27,11 +27,26 @@
 // A tile's loads, its first products and the previous tile's epilogue overlap.
 // Every wait is bounded; a role that gives up sets the CTA's abort flag,
 // drains what it started and leaves.
+//
+// PLANNED instances take their tiles from a list that the device has worked
+// out (attn_plan.cuh): sequences whose lengths the host does not know, their
+// rows one after the other in q and k.  PREFIX instances (forward) read the
+// blocks of a prefix, the same for every sample, before a sample's own.
 #pragma once
 
 #include "tc.cuh"
 
 namespace qknr {
+
+// A plan in the caller's workspace (attn_plan.cuh).
+struct AttnPlan {
+  int* head;                  // items of a head, first row of k that belongs to a sequence, the row after the last
+  int2* spans;                // [CTAs + 1] where each CTA's share begins: head * items + item, unit
+  int4* items;                // [items][2] q row, q_len, k row, k_len; first row in its sequence, blocks, units, query tiles before
+  long long* prefix;          // [items] units before
+  int* seq_items;             // [batch] first item of each sequence, or null
+  MemSpan sp;
+};
 
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
@@ -72,6 +87,14 @@ struct AttnParams {
   unsigned long long wait_limit_ns;
   MemSpan sp_q, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats,
       sp_v, sp_dout_norm, sp_v_top, sp_ds_top;
+  // PLANNED (batch is 1, seq_q and seq_k are all rows)
+  AttnPlan plan;
+  int few_rows;               // rows of a tile of a few queries
+  int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
+  int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
+  // PREFIX
+  CUtensorMap map_prefix_k, map_prefix_v;
+  int prefix, prefix_blocks;  // keys, blocks of 128
 };
 
 constexpr int kAttnThreads = 384;
@@ -267,6 +290,34 @@ __device__ __forceinline__ bool attn_work(const AttnParams& p, int s, AttnWork& 
   return true;
 }
 
+// PLANNED: piece s of a CTA's share.
+struct AttnPiece {
+  int h, e, u0, u1, slot;     // head line, item; units [u0, u1) of its contraction
+  int q_row, q_len, k_row, k_len, t0, blocks, tiles0;
+};
+__device__ __forceinline__ bool attn_piece(const AttnParams& p, int s, AttnPiece& w) {
+  const int c = static_cast<int>(blockIdx.x), n = p.plan.head[0];
+  if (!in_span(p.plan.spans + c, 16, p.plan.sp, p.status)) return false;
+  const int2 from = p.plan.spans[c], to = p.plan.spans[c + 1];
+  const int tile = from.x + s;
+  if (tile > to.x || (tile == to.x && to.y == 0)) return false;
+  w.h = tile / n;
+  w.e = tile - w.h * n;
+  if (!in_span(p.plan.items + 2LL * w.e, 32, p.plan.sp, p.status)) return false;
+  const int4 q = p.plan.items[2LL * w.e], x = p.plan.items[2LL * w.e + 1];
+  w.q_row = q.x;
+  w.q_len = q.y;
+  w.k_row = q.z;
+  w.k_len = q.w;
+  w.t0 = x.x;
+  w.blocks = x.y;
+  w.tiles0 = x.w;
+  w.u0 = s == 0 ? from.y : 0;
+  w.u1 = tile == to.x ? to.y : x.z;
+  w.slot = w.u0 > 0 ? 2 * c : w.u1 < x.z ? 2 * c + 1 : p.keep ? 2 * static_cast<int>(gridDim.x) + tile : -1;
+  return w.u0 < w.u1;
+}
+
 // The tile's place.  Without a causal mask the tiles of a head follow each
 // other; with one, tiles of the same cost do (`heavy_last`: the later rows
 // cost more), the costly ones first.
@@ -417,6 +468,7 @@ constexpr float kSlack = 8.0f;
 
 struct Seg {
   int b, h, q0, slot;
+  int q_row, k_row;           // PLANNED: the sequence's first rows
   int q_len, k_len, diag;     // causal: query i sees keys up to i + diag
   int begin;                  // first key block
   int nb[2];                  // key blocks of each half
@@ -424,7 +476,7 @@ struct Seg {
 };
 }  // namespace fwd
 
-template <typename T, int D>
+template <typename T, int D, bool PLANNED = false, bool PREFIX = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __grid_constant__ AttnParams p) {
   using namespace fwd;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -448,14 +500,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
 
   auto segment = [&](int s, Seg& g) {
     AttnWork w;
-    if (!attn_work(p, s, w)) return false;
-    const AttnPlace at = attn_place(p, w.tile, p.heads_q, true);
-    g.b = at.b;
-    g.h = at.h;
-    g.q0 = at.t * kRows;
-    g.slot = w.slot;
-    g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
-    g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    AttnPiece piece;
+    if (PLANNED) {
+      if (!attn_piece(p, s, piece)) return false;
+      g.b = 0;
+      g.h = piece.h;
+      g.q0 = piece.t0;
+      g.slot = piece.slot;
+      g.q_row = piece.q_row;
+      g.k_row = piece.k_row;
+      g.q_len = piece.q_len;
+      g.k_len = piece.k_len;
+    } else {
+      if (!attn_work(p, s, w)) return false;
+      const AttnPlace at = attn_place(p, w.tile, p.heads_q, true);
+      g.b = at.b;
+      g.h = at.h;
+      g.q0 = at.t * kRows;
+      g.slot = w.slot;
+      g.q_row = g.k_row = 0;
+      g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
+      g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    }
     g.diag = g.k_len - g.q_len;
     int nb[2];
 #pragma unroll
@@ -464,9 +530,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       int keys = first >= g.q_len ? 0 : (p.causal ? last + g.diag : g.k_len);
       keys = keys < 0 ? 0 : (keys > g.k_len ? g.k_len : keys);
       nb[t] = (keys + kTile - 1) / kTile;
+      if (PREFIX && first < g.q_len) nb[t] += p.prefix_blocks;
     }
     int end;
-    attn_cut(w, nb[0] > nb[1] ? nb[0] : nb[1], g.begin, end);
+    if (PLANNED) {
+      g.begin = piece.u0 < piece.blocks ? piece.u0 : piece.blocks;
+      end = piece.u1 < piece.blocks ? piece.u1 : piece.blocks;
+    } else {
+      attn_cut(w, nb[0] > nb[1] ? nb[0] : nb[1], g.begin, end);
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int last = nb[t] < end ? nb[t] : end;
@@ -491,27 +563,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           Seg next;
           if (segment(s + 1, next))
             for (int t = 0; t < 2; ++t)
-              if (next.nb[t]) tma_prefetch_tile(&p.map_q, next.q0 + t * kTile, next.h, next.b);
+              if (next.nb[t]) tma_prefetch_tile(&p.map_q, next.q_row + next.q0 + t * kTile, next.h, next.b);
         }
         for (int t = 0; t < 2 && ok; ++t) {
           if (g.nb[t] == 0) continue;
           ok = c.wait1(Q_EMPTY + t, uses[t] + 1);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(Q_FULL + t), kTileBytes<D>);
-          tma_load_tile(c.base + t * kTileBytes<D>, &p.map_q, g.q0 + t * kTile, g.h, g.b, c.bar(Q_FULL + t));
+          tma_load_tile(c.base + t * kTileBytes<D>, &p.map_q, g.q_row + g.q0 + t * kTile, g.h, g.b, c.bar(Q_FULL + t));
           ++uses[t];
         }
         const int hk = g.h / p.group;
         for (int j = 0; ok && j < g.blocks; ++j, k.step(), v.step()) {
+          const bool shared = PREFIX && g.begin + j < p.prefix_blocks;
+          const int row = g.k_row + (g.begin + j - (PREFIX && !shared ? p.prefix_blocks : 0)) * kTile, kb = shared ? 0 : g.b;
           ok = c.wait1(K_EMPTY + k.s, k.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
-          tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
+          tma_load_tile(sk + k.s * kTileBytes<D>, shared ? &p.map_prefix_k : &p.map_k, row, hk, kb, c.bar(K_FULL + k.s));
           ++ik;
           ok = c.wait1(V_EMPTY + v.s, v.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
-          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
+          tma_load_tile(sv + v.s * kTileBytes<D>, shared ? &p.map_prefix_v : &p.map_v, row, hk, kb, c.bar(V_FULL + v.s));
           ++iv;
         }
       }
@@ -533,8 +607,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.blocks == 0) continue;
       const int n0 = g.nb[0], n1 = g.nb[1], blocks = g.blocks;
-      // the block whose V has rows past the sample's keys
-      const int ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : blocks;
+      // the block whose V has rows past the sample's keys (past a prefix's TMA reads zeros)
+      const int ragged = (PLANNED || g.k_len < p.seq_k ? g.k_len / kTile - g.begin : blocks) + (PREFIX ? p.prefix_blocks : 0);
       ok = (n0 == 0 || c.wait(Q_FULL, uses[0])) && (n1 == 0 || c.wait(Q_FULL + 1, uses[1])) && c.wait(K_FULL + k.s, k.phase);
       if (!ok) break;
       tc_fence_after();
@@ -562,7 +636,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           if (t == 0) {
             ok = c.wait(bv, pv, bk, pk, bp, pp);
             if (!ok) break;
-            if (j >= ragged) zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j) * kTile, c.lane);
+            if (j >= ragged) zero_rows<D>(smem + (2 + kK + v.s) * kTileBytes<D>, g.k_len - (g.begin + j - (PREFIX ? p.prefix_blocks : 0)) * kTile, c.lane);
           } else if (j < n) {
             ok = c.wait(bp, pp);
             if (!ok) break;
@@ -608,11 +682,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     Seg g;
     for (int sg = 0; ok && segment(sg, g); ++sg) {
       const int n = t ? g.nb[1] : g.nb[0];
-      int limit;                                  // keys from the first block on that this query sees
+      int limit, shared = 0;                      // keys from the first block on that this query sees; PREFIX: of the prefix
       {
         const int row = g.q0 + t * kTile + r;
         limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
         limit = (limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit)) - g.begin * kTile;
+        if (PREFIX) {
+          limit += p.prefix_blocks * kTile;
+          shared = (row < g.q_len ? p.prefix : 0) - g.begin * kTile;
+        }
       }
       float m = -INFINITY;
       float2 sum = make_float2(0.0f, 0.0f);
@@ -626,7 +704,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         tmem_wait_load(s[0]);
 #pragma unroll
         for (int i = 1; i < 4; ++i) tmem_loaded(s[i]);
-        const int seen = limit - j * kTile;
+        const int seen = (PREFIX && g.begin + j < p.prefix_blocks ? shared : limit) - j * kTile;
         if (__any_sync(0xffffffffu, seen < kTile)) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -689,18 +767,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       const float inv = some ? __frcp_rn(total) : 0.0f;
       segment(sg, g);                             // again: the loop above has no registers to keep it in
       const int row = g.q0 + t * kTile + r;
-      const long long at = static_cast<long long>(g.slot) * kRows + t * kTile + r;   // a part's row
+      const long long at = static_cast<long long>(g.slot) * (PLANNED ? p.slot_rows : kRows) + t * kTile + r;   // a part's row
       if (g.slot >= 0) {
         // a part of the keys: unnormalised, with its maximum and sum
-        if (in_span(p.stats + 2 * at, 8, p.sp_stats, p.status))
+        if ((!PLANNED || row < g.q_len) && in_span(p.stats + 2 * at, 8, p.sp_stats, p.status))
           *reinterpret_cast<float2*>(p.stats + 2 * at) = make_float2(m, total);
       } else {
-        const long long l = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + row;
-        if (row < p.seq_q && in_span(p.lse + l, 4, p.sp_lse, p.status))
+        const long long l = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + g.q_row + row;
+        if (row < (PLANNED ? g.q_len : p.seq_q) && in_span(p.lse + l, 4, p.sp_lse, p.status))
           p.lse[l] = some ? __fmaf_rn(m, p.scale, log_sum<T>(total)) : -INFINITY;
       }
+      // PLANNED: rows behind a sequence's last one belong to the next, so that a warp's rows go one by one where some do
+      const int there = g.q_len - (row - c.lane);
+      const bool rows_end = PLANNED && g.slot < 0 && there < kOutRows;
       // checked builds: the rows of a part that this warp writes (a store by TMA stays inside its map)
-      const bool fits = __all_sync(0xffffffffu, g.slot < 0 || in_span(p.part + at * D, 4 * D, p.sp_part, p.status));
+      const bool fits = (!PLANNED || there > 0) &&
+                        __all_sync(0xffffffffu, g.slot < 0 || in_span(p.part + at * D, 4 * D, p.sp_part, p.status));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float o[32];
@@ -714,6 +796,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           store_part<D>(p.part + at * D + 32 * i, o, 1.0f, n > 0, c.lane);
           continue;
         }
+        if (rows_end) {
+          char* dst = p.o + static_cast<long long>(g.q_row + row) * p.o_stride + g.h * (D * 2) + 64 * i;
+          if (__all_sync(0xffffffffu, c.lane >= there || in_span(dst, 64, p.sp_o, p.status)))
+            store_cols<T>(dst, p.o_stride, there, o, inv, some, c.lane);
+          continue;
+        }
         if (i % 2 == 0) {
           // the store before has read the stage
           if (c.lane == 0) tma_store_wait_read();
@@ -723,7 +811,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
         if (i % 2 == 1) {
           fence_async_shared();
           __syncwarp();
-          if (c.lane == 0 && row < p.seq_q) tma_store_box(&p.map_out, smem_addr(stage), 0, row, i / 2, g.h, g.b);
+          if (c.lane == 0 && (PLANNED || row < p.seq_q)) tma_store_box(&p.map_out, smem_addr(stage), 0, g.q_row + row, i / 2, g.h, g.b);
         }
       }
     }
@@ -894,7 +982,7 @@ __device__ __forceinline__ float warp_max(float v) {
 // whose tiles load do anyway, each tile waits for its rows of o: the same time
 // there, 150 against 145 us at 3 x 1999 x 16 on 4 heads x 64, causal.
 // fp16: also |do| of each row and a bound on the rows of v (GradScale).
-template <typename T, int D>
+template <typename T, int D, bool PLANNED = false>
 __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constant__ AttnParams p) {
   constexpr int L = D / 8, TEAMS = 256 / L;
   const int team = threadIdx.x / L, lane = threadIdx.x % L;
@@ -957,6 +1045,7 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
         if (it < rows_v) {
           const char* src = p.v_in + row * p.v_stride + h * (D * 2) + lane * 16;
           bool counts = in_span(src, 16, p.sp_v, p.status);
+          if (PLANNED) counts = counts && row >= p.plan.head[1] && row < p.plan.head[2];
           if (p.k_lens) {
             const int b = row / p.seq_k;
             counts = counts && row - b * p.seq_k < clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
@@ -1022,13 +1111,15 @@ constexpr int kSmem = kCtl<D> + 256;
 
 struct Seg {
   int b, h, q0, slot;
+  int q_row, k_row;           // PLANNED: the sequence's first rows
   int q_len, k_len, diag;
+  int top;                    // the tile's place in ds_top
   int begin, n;               // key blocks [begin, begin + n)
   bool opens;                 // the tile's first piece
 };
 }  // namespace dq
 
-template <typename T, int D>
+template <typename T, int D, bool PLANNED = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_constant__ AttnParams p) {
   using namespace dq;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -1051,6 +1142,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   grid_dependents_launch();
 
   auto segment = [&](int s, Seg& g) {
+    if (PLANNED) {
+      AttnPiece piece;
+      if (!attn_piece(p, s, piece)) return false;
+      g.b = 0;
+      g.h = piece.h;
+      g.q0 = piece.t0;
+      g.slot = piece.slot;
+      g.opens = piece.u0 == 0;
+      g.q_row = piece.q_row;
+      g.k_row = piece.k_row;
+      g.q_len = piece.q_len;
+      g.k_len = piece.k_len;
+      g.diag = g.k_len - g.q_len;
+      g.top = piece.e;
+      g.begin = piece.u0 < piece.blocks ? piece.u0 : piece.blocks;
+      g.n = (piece.u1 < piece.blocks ? piece.u1 : piece.blocks) - g.begin;
+      return true;
+    }
     AttnWork w;
     if (!attn_work(p, s, w)) return false;
     const AttnPlace at = attn_place(p, w.tile, p.heads_q, true);
@@ -1059,6 +1168,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.q0 = at.t * kTile;
     g.slot = w.slot;
     g.opens = w.u0 == 0;
+    g.q_row = g.k_row = 0;
+    g.top = at.t;
     g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
     g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
     g.diag = g.k_len - g.q_len;
@@ -1085,8 +1196,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
           // the next tile's queries come from HBM: on their way while this one's keys come from L2
           Seg next;
           if (segment(s + 1, next) && next.n > 0) {
-            tma_prefetch_tile(&p.map_q, next.q0, next.h, next.b);
-            tma_prefetch_tile(&p.map_do, next.q0, next.h, next.b);
+            tma_prefetch_tile(&p.map_q, next.q_row + next.q0, next.h, next.b);
+            tma_prefetch_tile(&p.map_do, next.q_row + next.q0, next.h, next.b);
           }
         }
         if (g.n == 0) continue;
@@ -1097,9 +1208,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(K_FULL + k.s), kTileBytes<D>);
           if (j < 0)
-            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_q, g.q0, g.h, g.b, c.bar(K_FULL + k.s));
+            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_q, g.q_row + g.q0, g.h, g.b, c.bar(K_FULL + k.s));
           else
-            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
+            tma_load_tile(sk + k.s * kTileBytes<D>, &p.map_k, g.k_row + (g.begin + j) * kTile, hk, g.b, c.bar(K_FULL + k.s));
           ++ik;
           k.step();
           if (j < 0) continue;
@@ -1107,13 +1218,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
             ok = c.wait1(O_EMPTY, io + 1);
             if (!ok) break;
             mbar_arrive_expect_tx(c.bar(O_FULL), kTileBytes<D>);
-            tma_load_tile(sdo, &p.map_do, g.q0, g.h, g.b, c.bar(O_FULL));
+            tma_load_tile(sdo, &p.map_do, g.q_row + g.q0, g.h, g.b, c.bar(O_FULL));
             ++io;
           }
           ok = c.wait1(V_EMPTY + v.s, v.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(V_FULL + v.s), kTileBytes<D>);
-          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
+          tma_load_tile(sv + v.s * kTileBytes<D>, &p.map_v, g.k_row + (g.begin + j) * kTile, hk, g.b, c.bar(V_FULL + v.s));
           ++iv;
           v.step();
         }
@@ -1133,7 +1244,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
-      const int n = g.n, ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
+      const int n = g.n, ragged = PLANNED || g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
       // block j's S: its K has landed, with nothing past the sample's keys
       auto scores = [&](int j) {
         if (!c.wait(K_FULL + ks.s, ks.phase)) return false;
@@ -1182,7 +1293,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     Seg g;
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
-      const int n = g.n, ragged = g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
+      const int n = g.n, ragged = PLANNED || g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
       ok = c.wait(O_FULL, live);
       for (int j = 0; ok && j < n; ++j, ++done) {
         ok = c.wait(V_FULL + v.s, v.phase);
@@ -1243,9 +1354,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     }
     // a tile's row: log-sum, delta and the bound on |dP - delta|
     auto row_stats = [&](const Seg& g, float& lse, float& delta, float& bound) {
-      const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + g.q0 + r;
+      const long long at = (static_cast<long long>(g.b) * p.heads_q + g.h) * p.seq_q + g.q_row + g.q0 + r;
       lse = delta = bound = 0.0f;
-      if (g.q0 + r < p.seq_q && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
+      if (g.q0 + r < (PLANNED ? g.q_len : p.seq_q) && in_span(p.lse + at, 4, p.sp_lse, p.status) && in_span(p.delta + at, 4, p.sp_delta, p.status)) {
         lse = p.lse[at];
         delta = p.delta[at];
         if (GradScale<T>::kFromData && in_span(p.dout_norm + at, 4, p.sp_dout_norm, p.status))
@@ -1265,7 +1376,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       if (GradScale<T>::kFromData && half == 0 && g.opens) {
         // for dk, dv: the largest bound of these 32 queries
         const float top = warp_max(limit > 0 ? bound : 0.0f);
-        float* at = p.ds_top + ((static_cast<long long>(g.b) * p.heads_q + g.h) * p.q_tiles + g.q0 / kTile) * 4 + c.warp;
+        float* at = p.ds_top + ((static_cast<long long>(g.b) * p.heads_q + g.h) * p.q_tiles + g.top) * 4 + c.warp;
         if (c.lane == 0 && in_span(at, 4, p.sp_ds_top, p.status)) *at = top;
       }
       const float lift = grad_lift<T>(bound);
@@ -1358,6 +1469,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       float* part = p.part + (static_cast<long long>(g.slot) * kTile + r) * D + half * (D / 2);
       // checked builds: the rows of a part that this warp writes (a store by TMA stays inside its map)
       const bool fits = __all_sync(0xffffffffu, g.slot < 0 || in_span(part, 2 * D, p.sp_part, p.status));
+      // PLANNED: rows behind a sequence's last one belong to the next, so that a warp's rows go one by one where some do
+      const int there = g.q_len - (row - c.lane);
+      const bool rows_end = PLANNED && g.slot < 0 && there < kOutRows;
       if (g.slot < 0) {
         // the store before has read the stage
         if (c.lane == 0) tma_store_wait_read();
@@ -1372,17 +1486,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
           if (i == D / 64 - 1) c.arrive(ACC_FREE);
         }
         if (!fits) continue;
-        if (g.slot >= 0)
+        if (g.slot >= 0) {
           store_part<D>(part + 32 * i, v, grad_unlift<T>(lift), some, c.lane);
-        else
+        } else if (rows_end) {
+          char* dst = p.dq + static_cast<long long>(g.q_row + row) * p.dq_stride + g.h * (D * 2) + half * D + 64 * i;
+          if (__all_sync(0xffffffffu, c.lane >= there || in_span(dst, 64, p.sp_dq, p.status)))
+            store_cols<T>(dst, p.dq_stride, there, v, p.scale * grad_unlift<T>(lift), some, c.lane);
+        } else
           stage_cols<T, D / 2>(stage, 4 * i, v, p.scale * grad_unlift<T>(lift), some, c.lane);
       }
-      if (g.slot < 0) {
+      if (g.slot < 0 && !rows_end) {
         fence_async_shared();
         __syncwarp();
         // half of the columns: the second 64 of 128, or 32 of 64
-        if (c.lane == 0 && row < p.seq_q)
-          tma_store_box(&p.map_out, smem_addr(stage), D == 128 ? 0 : half * 32, row, D == 128 ? half : 0, g.h, g.b);
+        if (c.lane == 0 && (PLANNED || row < p.seq_q))
+          tma_store_box(&p.map_out, smem_addr(stage), D == 128 ? 0 : half * 32, g.q_row + row, D == 128 ? half : 0, g.h, g.b);
       }
     }
     if (c.lane == 0) tma_store_wait();
@@ -1459,14 +1577,16 @@ constexpr int kSmem = kCtl<D> + 256;
 
 struct Seg {
   int b, h, k0, slot;         // h: key head
+  int q_row, k_row;           // PLANNED: the sequence's first rows
   int q_len, k_len, diag;
+  int top, q_tiles;           // the sample's first place in ds_top of a head, its count
   int first, end;             // query tiles [first, end) see one of these keys
   int n;                      // blocks
   int h0, t0;                 // head and query tile of the first
 };
 }  // namespace dkv
 
-template <typename T, int D>
+template <typename T, int D, bool PLANNED = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p) {
   using namespace dkv;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -1492,14 +1612,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
 
   auto segment = [&](int s, Seg& g) {
     AttnWork w;
-    if (!attn_work(p, s, w)) return false;
-    const AttnPlace at = attn_place(p, w.tile, p.heads_k, false);
-    g.b = at.b;
-    g.h = at.h;
-    g.k0 = at.t * kTile;
-    g.slot = w.slot;
-    g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
-    g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+    AttnPiece piece;
+    if (PLANNED) {
+      if (!attn_piece(p, s, piece)) return false;
+      g.b = 0;
+      g.h = piece.h;
+      g.k0 = piece.t0;
+      g.slot = piece.slot;
+      g.q_row = piece.q_row;
+      g.k_row = piece.k_row;
+      g.q_len = piece.q_len;
+      g.k_len = piece.k_len;
+      g.top = piece.tiles0;
+      g.q_tiles = (g.q_len + kTile - 1) / kTile;
+    } else {
+      if (!attn_work(p, s, w)) return false;
+      const AttnPlace at = attn_place(p, w.tile, p.heads_k, false);
+      g.b = at.b;
+      g.h = at.h;
+      g.k0 = at.t * kTile;
+      g.slot = w.slot;
+      g.q_row = g.k_row = 0;
+      g.q_len = clamp_len(p.q_lens, at.b, p.seq_q, p.sp_q_lens, p.status);
+      g.k_len = clamp_len(p.k_lens, at.b, p.seq_k, p.sp_k_lens, p.status);
+      g.top = 0;
+      g.q_tiles = p.q_tiles;
+    }
     g.diag = g.k_len - g.q_len;
     g.first = 0;
     g.end = (g.q_len + kTile - 1) / kTile;
@@ -1507,7 +1645,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     if (g.k0 >= g.k_len || g.first > g.end) g.first = g.end;
     const int per_head = g.end - g.first;
     int begin, end;
-    attn_cut(w, per_head * p.group, begin, end);
+    if (PLANNED) {
+      begin = piece.u0 < piece.blocks ? piece.u0 : piece.blocks;
+      end = piece.u1 < piece.blocks ? piece.u1 : piece.blocks;
+    } else {
+      attn_cut(w, per_head * p.group, begin, end);
+    }
     g.n = end - begin;
     g.h0 = g.h * p.group + (per_head ? begin / per_head : 0);
     g.t0 = g.first + (per_head ? begin % per_head : 0);
@@ -1528,34 +1671,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         {
           Seg next;
           if (segment(s + 1, next) && next.n > 0) {
-            tma_prefetch_tile(&p.map_k, next.k0, next.h, next.b);
-            tma_prefetch_tile(&p.map_v, next.k0, next.h, next.b);
+            tma_prefetch_tile(&p.map_k, next.k_row + next.k0, next.h, next.b);
+            tma_prefetch_tile(&p.map_v, next.k_row + next.k0, next.h, next.b);
           }
         }
         if (g.n == 0) continue;
         ok = c.wait1(K_EMPTY, uses + 1);
         if (!ok) break;
         mbar_arrive_expect_tx(c.bar(K_FULL), kTileBytes<D>);
-        tma_load_tile(sk, &p.map_k, g.k0, g.h, g.b, c.bar(K_FULL));
+        tma_load_tile(sk, &p.map_k, g.k_row + g.k0, g.h, g.b, c.bar(K_FULL));
         ++uses;
         int h = g.h0, t = g.t0;
         for (int i = 0; i < g.n; ++i, q.step(), o.step()) {
           ok = c.wait1(Q_EMPTY + q.s, q.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(Q_FULL + q.s), kTileBytes<D>);
-          tma_load_tile(sq + q.s * kTileBytes<D>, &p.map_q, t * kTile, h, g.b, c.bar(Q_FULL + q.s));
+          tma_load_tile(sq + q.s * kTileBytes<D>, &p.map_q, g.q_row + t * kTile, h, g.b, c.bar(Q_FULL + q.s));
           ++iq;
           if (i == 0) {
             ok = c.wait1(V_EMPTY, uses);
             if (!ok) break;
             mbar_arrive_expect_tx(c.bar(V_FULL), kTileBytes<D>);
-            tma_load_tile(sv, &p.map_v, g.k0, g.h, g.b, c.bar(V_FULL));
+            tma_load_tile(sv, &p.map_v, g.k_row + g.k0, g.h, g.b, c.bar(V_FULL));
             ++vuses;
           }
           ok = c.wait1(O_EMPTY + o.s, o.phase ^ 1u);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(O_FULL + o.s), kTileBytes<D>);
-          tma_load_tile(sdo + o.s * kTileBytes<D>, &p.map_do, t * kTile, h, g.b, c.bar(O_FULL + o.s));
+          tma_load_tile(sdo + o.s * kTileBytes<D>, &p.map_do, g.q_row + t * kTile, h, g.b, c.bar(O_FULL + o.s));
           ++io;
           if (++t == g.end) {
             t = g.first;
@@ -1584,7 +1727,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     for (int s = 0; ok && segment(s, g); ++s) {
       if (g.n == 0) continue;
       const int n = g.n;
-      const bool ragged = g.q_len < p.seq_q;
+      const bool ragged = PLANNED || g.q_len < p.seq_q;
       int t = g.t0;                               // the block's query tile
       // A tile that has landed: nothing past the sample's queries.  (Both
       // chains write the zeros: the same ones, before either gives the tile
@@ -1686,16 +1829,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       float lift = 1.0f;
       if (GradScale<T>::kFromData && g.n > 0) {
         // the largest bound among the queries of this key head
-        const long long each = 4LL * p.q_tiles, n = p.group * each;
-        const float* tops = p.ds_top + (static_cast<long long>(g.b) * p.heads_q + g.h * p.group) * each;
+        const long long each = 4LL * p.q_tiles, n = PLANNED ? 4LL * g.q_tiles : p.group * each;
+        const float* tops = p.ds_top + (static_cast<long long>(g.b) * p.heads_q + g.h * p.group) * each + 4LL * g.top;
         float bound = 0.0f;
+        for (int h = 0; h < (PLANNED ? p.group : 1); ++h, tops += each)
 #pragma unroll 4
-        for (long long i = c.lane; i < n; i += 32)
-          if (in_span(tops + i, 4, p.sp_ds_top, p.status)) bound = fmaxf(bound, tops[i]);
+          for (long long i = c.lane; i < n; i += 32)
+            if (in_span(tops + i, 4, p.sp_ds_top, p.status)) bound = fmaxf(bound, tops[i]);
         lift = grad_lift<T>(warp_max(bound));
       }
       for (int i = 0; i < g.n; ++i, ++done) {
-        const long long at = (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + t * kTile + c.lane;
+        const long long at = (static_cast<long long>(g.b) * p.heads_q + h) * p.seq_q + g.q_row + t * kTile + c.lane;
         float l[4], d[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -1825,12 +1969,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       const bool some = g.n > 0 && key < g.k_len;
       const float down = half ? grad_unlift<T>(lift) : grad_scale_down(GradScale<T>::kP), f = half ? p.scale * down : down;
       float* part = p.part + ((static_cast<long long>(g.slot) * 2 + half) * kTile + r) * D;
-      char* dst = half ? p.dk + (static_cast<long long>(g.b) * p.seq_k + key) * p.dk_stride + g.h * (D * 2)
-                       : p.dv + (static_cast<long long>(g.b) * p.seq_k + key) * p.dv_stride + g.h * (D * 2);
-      const int there = p.seq_k - (key - c.lane);   // rows from the warp's first on
+      const int rows_k = PLANNED ? g.k_len : p.seq_k;
+      char* dst = half ? p.dk + (static_cast<long long>(g.b) * p.seq_k + g.k_row + key) * p.dk_stride + g.h * (D * 2)
+                       : p.dv + (static_cast<long long>(g.b) * p.seq_k + g.k_row + key) * p.dv_stride + g.h * (D * 2);
+      const int there = rows_k - (key - c.lane);    // rows from the warp's first on
       const bool fits =
           __all_sync(0xffffffffu, g.slot >= 0 ? in_span(part, 4 * D, p.sp_part, p.status)
-                                              : key >= p.seq_k || in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status));
+                                              : key >= rows_k || in_span(dst, D * 2, half ? p.sp_dk : p.sp_dv, p.status));
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         float v[32];

@@ -51,6 +51,9 @@ EXPORTS = (
     "qknr_attn_args_init", "qknr_attn_workspace_bytes", "qknr_attn_backward_workspace_bytes", "qknr_attn_forward",
     "qknr_attn_backward", "qknr_attn_sizeof_args",
     "qknr_rms_args_init", "qknr_rms_forward", "qknr_rms_workspace_bytes", "qknr_rms_backward", "qknr_rms_sizeof_args",
+    "qknr_pack_args_init", "qknr_pack_workspace_bytes", "qknr_pack_backward_workspace_bytes", "qknr_pack_forward",
+    "qknr_pack_backward", "qknr_pack_sizeof_args",
+    "qknr_prefix_args_init", "qknr_prefix_workspace_bytes", "qknr_prefix_forward", "qknr_prefix_sizeof_args",
 )
 GN_MODE = {"auto": 0, "fused": 1, "two_pass": 2, "cluster": 3}
 GN_FLAG_TEST_NO_RECORDS = 0x2
@@ -215,6 +218,40 @@ class QknrRmsArgs(ctypes.Structure):
     ]
 
 
+class QknrPackArgs(ctypes.Structure):
+    """Mirror of ``qknr_pack_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("o", c_void_p), ("lse", c_void_p),
+        ("q_stride", c_int64), ("k_stride", c_int64), ("v_stride", c_int64), ("o_stride", c_int64),
+        ("batch", c_int32), ("rows_q", c_int32), ("rows_k", c_int32),
+        ("n_heads_q", c_int32), ("n_heads_k", c_int32), ("head_dim", c_int32),
+        ("q_starts", c_void_p), ("k_starts", c_void_p), ("scale", c_float), ("causal", c_int32),
+        ("dout", c_void_p), ("dq", c_void_p), ("dk", c_void_p), ("dv", c_void_p),
+        ("dout_stride", c_int64), ("dq_stride", c_int64), ("dk_stride", c_int64), ("dv_stride", c_int64),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32), ("wait_limit_ns", c_uint64),
+    ]
+
+
+class QknrPrefixArgs(ctypes.Structure):
+    """Mirror of ``qknr_prefix_args``."""
+
+    _fields_ = [
+        ("abi_version", c_uint32), ("dtype", c_int32),
+        ("q", c_void_p), ("k", c_void_p), ("v", c_void_p), ("prefix_k", c_void_p), ("prefix_v", c_void_p),
+        ("o", c_void_p), ("lse", c_void_p),
+        ("q_stride", c_int64), ("k_stride", c_int64), ("v_stride", c_int64),
+        ("prefix_k_stride", c_int64), ("prefix_v_stride", c_int64), ("o_stride", c_int64),
+        ("batch", c_int32), ("seq_q", c_int32), ("seq_k", c_int32), ("prefix", c_int32),
+        ("n_heads_q", c_int32), ("n_heads_k", c_int32), ("head_dim", c_int32),
+        ("q_lens", c_void_p), ("k_lens", c_void_p), ("scale", c_float), ("causal", c_int32),
+        ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+        ("dev_status", c_void_p), ("flags", c_uint32), ("wait_limit_ns", c_uint64),
+    ]
+
+
 class QknrError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS.get(status, status)}: {message}")
@@ -299,6 +336,16 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.qknr_ln_sizeof_args.restype = c_size_t
         lib.qknr_sizeof_grad_args.restype = c_size_t
         lib.qknr_rms_sizeof_args.restype = c_size_t
+        for name, struct, fns in (("pack", QknrPackArgs, ("forward", "backward")), ("prefix", QknrPrefixArgs, ("forward",))):
+            p_struct = ctypes.POINTER(struct)
+            init = getattr(lib, f"qknr_{name}_args_init")
+            init.argtypes, init.restype = [p_struct], None
+            getattr(lib, f"qknr_{name}_sizeof_args").restype = c_size_t
+            for way in fns:
+                fn = getattr(lib, f"qknr_{name}_{way}")
+                fn.argtypes, fn.restype = [p_struct, c_void_p], c_int32
+                space = getattr(lib, f"qknr_{name}_" + ("backward_" if way == "backward" else "") + "workspace_bytes")
+                space.argtypes, space.restype = [p_struct, ctypes.POINTER(c_size_t)], c_int32
         if lib.qknr_abi_version() != ABI_VERSION:
             raise RuntimeError("libqknr.so ABI version mismatch")
         if lib.qknr_sizeof_args() != ctypes.sizeof(QknrArgs) or \
@@ -309,6 +356,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                 lib.qknr_sizeof_grad_args() != ctypes.sizeof(QknrGradArgs) or \
                 lib.qknr_attn_sizeof_args() != ctypes.sizeof(QknrAttnArgs) or \
                 lib.qknr_rms_sizeof_args() != ctypes.sizeof(QknrRmsArgs) or \
+                lib.qknr_pack_sizeof_args() != ctypes.sizeof(QknrPackArgs) or \
+                lib.qknr_prefix_sizeof_args() != ctypes.sizeof(QknrPrefixArgs) or \
                 lib.qknr_sizeof_host_plan() != ctypes.sizeof(QknrHostPlan):
             raise RuntimeError("libqknr.so struct layout differs from the binding")
         if path is None:
@@ -1478,3 +1527,188 @@ def attention_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, *, b
     workspace = _workspace(a, plan, workspace, q, stream)
     _call((_lib or load()).qknr_attn_backward, a, stream, q)
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# attention over packed sequences and its backward pass (include/qknr_pack.h)
+
+def _int32s(t, n, name):
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} values")
+    return t.data_ptr()
+
+
+def _heads_of(a, tensors, n_heads_q, n_heads_k, head_dim):
+    """The types, widths and strides of q, k, v and tensors like them into a."""
+    first = next(t for _, t in tensors)
+    if first.dtype not in _ACT or any(t.dtype != first.dtype for _, t in tensors):
+        raise ValueError(", ".join(name for name, _ in tensors) + " must share one dtype: bfloat16 or float16")
+    a.dtype = _ACT[first.dtype]
+    a.n_heads_q, a.n_heads_k, a.head_dim = n_heads_q, n_heads_k, head_dim
+    for name, t in tensors:
+        heads = n_heads_q if name == "q" else n_heads_k
+        setattr(a, name + "_stride", _stride(t, name))
+        if t.shape[1] != heads * head_dim:
+            raise ValueError(f"{name} must be [rows, {heads * head_dim}]")
+        setattr(a, name, t.data_ptr())
+
+
+def _scale_of(a, scale):
+    if scale is not None:
+        a.scale = scale
+        if not 0 < a.scale < float("inf"):                  # as fp32
+            raise ValueError("scale must be positive and finite")
+
+
+def pack_args(q, k, v, n_heads_q, n_heads_k, head_dim, q_starts, k_starts=None, *, scale=None, causal=False, dev_status=None,
+              flags=0, wait_limit_ns=0) -> QknrPackArgs:
+    """The arguments both passes share: token rows q [rows_q, Hq * D], k and v
+    [rows_k, Hk * D] (views with any row stride) and where the sequences begin
+    in them (int32 [batch + 1] on the device; ``k_starts`` None: q_starts)."""
+    a = QknrPackArgs()
+    load().qknr_pack_args_init(ctypes.byref(a))
+    _heads_of(a, (("q", q), ("k", k), ("v", v)), n_heads_q, n_heads_k, head_dim)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v need the same number of rows")
+    if max(q.shape[0], k.shape[0]) >= 1 << 31:
+        raise ValueError("2^31 rows or more")
+    a.rows_q, a.rows_k, a.batch = q.shape[0], k.shape[0], max(q_starts.numel() - 1, 0)
+    a.q_starts = _int32s(q_starts, a.batch + 1, "q_starts")
+    if k_starts is not None:
+        a.k_starts = _int32s(k_starts, a.batch + 1, "k_starts")
+    _scale_of(a, scale)
+    a.causal = int(bool(causal))
+    a.dev_status = _ptr(dev_status)
+    a.flags, a.wait_limit_ns = flags, wait_limit_ns
+    return a
+
+
+def attention_packed(q, k, v, n_heads_q, n_heads_k, head_dim, q_starts, k_starts=None, *, scale=None, causal=False, out=None,
+                     lse=None, workspace=None, stream=None, status=True, dev_status=None, flags=0, wait_limit_ns=0):
+    """Attention over sequences packed one after the other: sequence b is the
+    rows q_starts[b] .. q_starts[b + 1] - 1 of q [rows_q, Hq * D] and
+    k_starts[b] .. of k and v [rows_k, Hk * D] (int32 [batch + 1] on the device;
+    ``k_starts`` None: q_starts).  Returns (o [rows_q, Hq * D], lse float32
+    [Hq, rows_q]); ``causal`` and what a query without keys answers are
+    ``attention``'s.  Rows that belong to no sequence keep what ``out`` and
+    ``lse`` held there (new tensors by default, uninitialised)."""
+    key = ("pack", _meta(q), _meta(k), _meta(v), n_heads_q, n_heads_k, head_dim, _meta(q_starts), _meta(k_starts), scale,
+           causal, _meta(out), flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        _one_device(q, k, v, q_starts, k_starts, out)
+        a = pack_args(q, k, v, n_heads_q, n_heads_k, head_dim, q_starts, k_starts, scale=scale, causal=causal, flags=flags,
+                      wait_limit_ns=wait_limit_ns)
+        a.o_stride = 0 if out is None else _stride(_match(out, q, "out"), "out")
+        plan = _keep(key, _Plan(a, load().qknr_pack_workspace_bytes))
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    n = q.shape[0] * n_heads_q
+    lse = _empty((n_heads_q, q.shape[0]), torch.float32, q, stream) if lse is None else _vector(lse, n, "lse", q)
+    a = plan.new()
+    a.q, a.k, a.v, a.o, a.lse = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()
+    a.q_starts = q_starts.data_ptr()
+    if k_starts is not None:
+        a.k_starts = k_starts.data_ptr()
+    _status(a, status, dev_status, q)
+    workspace = _workspace(a, plan, workspace, q, stream)
+    _call((_lib or load()).qknr_pack_forward, a, stream, q)
+    return out, lse
+
+
+def attention_packed_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_dim, q_starts, k_starts=None, *, scale=None,
+                              causal=False, dq=None, dk=None, dv=None, workspace=None, stream=None, status=True,
+                              dev_status=None, flags=0, wait_limit_ns=0):
+    """Gradients of ``attention_packed`` from do, its inputs and its outputs o
+    and lse: returns (dq, dk, dv), new tensors unless given (column views of
+    one packed buffer are fine).  Rows that belong to no sequence keep what
+    they held."""
+    key = ("pack_bwd", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), n_heads_q, n_heads_k, head_dim, _meta(q_starts),
+           _meta(k_starts), scale, causal, _meta(dq), _meta(dk), _meta(dv), flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        _one_device(q, do, k, v, o, q_starts, k_starts, dq, dk, dv)
+        a = pack_args(q, k, v, n_heads_q, n_heads_k, head_dim, q_starts, k_starts, scale=scale, causal=causal, flags=flags,
+                      wait_limit_ns=wait_limit_ns)
+        a.o_stride, a.dout_stride = _stride(_match(o, q, "o"), "o"), _stride(_match(do, q, "do"), "do")
+        for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            if t is not None:
+                setattr(a, name + "_stride", _stride(_match(t, like, name), name))
+        plan = _keep(key, _Plan(a, load().qknr_pack_backward_workspace_bytes))
+    if dq is None:
+        dq = _empty(q.shape, q.dtype, q, stream)
+    if dk is None:
+        dk = _empty(k.shape, k.dtype, k, stream)
+    if dv is None:
+        dv = _empty(v.shape, v.dtype, v, stream)
+    a = plan.new()
+    a.q, a.k, a.v, a.o, a.dout = q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr()
+    a.lse = _vector(lse, q.shape[0] * n_heads_q, "lse", q).data_ptr()
+    a.dq, a.dk, a.dv = dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
+    a.q_starts = q_starts.data_ptr()
+    if k_starts is not None:
+        a.k_starts = k_starts.data_ptr()
+    _status(a, status, dev_status, q)
+    workspace = _workspace(a, plan, workspace, q, stream)
+    _call((_lib or load()).qknr_pack_backward, a, stream, q)
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# attention beside a shared prefix (include/qknr_prefix.h)
+
+def prefix_args(q, k, v, prefix_k, prefix_v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False,
+                q_lens=None, k_lens=None, dev_status=None, flags=0, wait_limit_ns=0) -> QknrPrefixArgs:
+    """The arguments of ``attention_prefix`` without its outputs."""
+    a = QknrPrefixArgs()
+    load().qknr_prefix_args_init(ctypes.byref(a))
+    _heads_of(a, (("q", q), ("k", k), ("v", v), ("prefix_k", prefix_k), ("prefix_v", prefix_v)), n_heads_q, n_heads_k, head_dim)
+    if batch < 1 or q.shape[0] % batch or k.shape[0] % batch:
+        raise ValueError("q, k and v must be [batch * seq, ...]")
+    if k.shape[0] != v.shape[0] or prefix_k.shape[0] != prefix_v.shape[0]:
+        raise ValueError("k and v, prefix_k and prefix_v need the same number of rows")
+    if max(q.shape[0], k.shape[0], prefix_k.shape[0]) >= 1 << 31:
+        raise ValueError("2^31 rows or more")
+    a.batch, a.seq_q, a.seq_k, a.prefix = batch, q.shape[0] // batch, k.shape[0] // batch, prefix_k.shape[0]
+    for name, t in (("q_lens", q_lens), ("k_lens", k_lens)):
+        if t is not None:
+            setattr(a, name, _int32s(t, batch, name))
+    _scale_of(a, scale)
+    a.causal = int(bool(causal))
+    a.dev_status = _ptr(dev_status)
+    a.flags, a.wait_limit_ns = flags, wait_limit_ns
+    return a
+
+
+def attention_prefix(q, k, v, prefix_k, prefix_v, n_heads_q, n_heads_k, head_dim, *, batch=1, scale=None, causal=False,
+                     q_lens=None, k_lens=None, out=None, lse=None, workspace=None, stream=None, status=True, dev_status=None,
+                     flags=0, wait_limit_ns=0):
+    """``attention`` for samples whose keys all begin with the same rows
+    ``prefix_k`` and ``prefix_v`` [prefix, Hk * D], held once: query rows q
+    [batch * seq_q, Hq * D] see all of the prefix and, as in ``attention``,
+    their sample's own k and v [batch * seq_k, Hk * D] (seq_k may be 0).
+    Returns (o, lse float32 [batch, Hq, seq_q]) over both."""
+    key = ("prefix", _meta(q), _meta(k), _meta(v), _meta(prefix_k), _meta(prefix_v), n_heads_q, n_heads_k, head_dim, batch,
+           scale, causal, _meta(q_lens), _meta(k_lens), _meta(out), flags, wait_limit_ns)
+    plan = _plans.get(key)
+    if plan is None:
+        _one_device(q, k, v, prefix_k, prefix_v, q_lens, k_lens, out)
+        a = prefix_args(q, k, v, prefix_k, prefix_v, n_heads_q, n_heads_k, head_dim, batch=batch, scale=scale, causal=causal,
+                        q_lens=q_lens, k_lens=k_lens, flags=flags, wait_limit_ns=wait_limit_ns)
+        a.o_stride = 0 if out is None else _stride(_match(out, q, "out"), "out")
+        plan = _keep(key, _Plan(a, load().qknr_prefix_workspace_bytes, ((batch, n_heads_q, a.seq_q), q.shape[0] * n_heads_q)))
+    shape, n = plan.info
+    if out is None:
+        out = _empty(q.shape, q.dtype, q, stream)
+    lse = _empty(shape, torch.float32, q, stream) if lse is None else _vector(lse, n, "lse", q)
+    a = plan.new()
+    a.q, a.k, a.v, a.o, a.lse = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()
+    a.prefix_k, a.prefix_v = prefix_k.data_ptr(), prefix_v.data_ptr()
+    if q_lens is not None:
+        a.q_lens = q_lens.data_ptr()
+    if k_lens is not None:
+        a.k_lens = k_lens.data_ptr()
+    _status(a, status, dev_status, q)
+    workspace = _workspace(a, plan, workspace, q, stream)
+    _call((_lib or load()).qknr_prefix_forward, a, stream, q)
+    return out, lse

@@ -37,6 +37,10 @@ __host__ __device__ constexpr int few_smem(int rows, int d) {
   return few_warps(rows) * (few_ring_bytes(rows, d) + rows * 8 + few_stages(rows, d) * 8) + 16;
 }
 
+// PLANNED: the table of sequences behind that
+__host__ __device__ constexpr int few_table(int rows, int d) { return (few_smem(rows, d) + 15) / 16 * 16; }
+__host__ __device__ constexpr int few_planned_smem(int rows, int d) { return few_table(rows, d) + static_cast<int>(sizeof(AttnTable)); }
+
 template <typename T>
 __device__ __forceinline__ void few_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -81,11 +85,16 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
+  AttnTable& table = *reinterpret_cast<AttnTable*>(smem + few_table(ROWS, D));
+  if (PLANNED && p.table) {
+    if (warp == 0) plan_table(p.seqs, table, lane, p.status);
+    __syncthreads();
+  }
   RingPos<STAGES> at;         // the next step to read
   bool ok = true;
   AttnWork w;
   AttnPiece piece;
-  for (int s = 0; ok && (PLANNED ? attn_piece(p, s, piece) : attn_work(p, s, w)); ++s) {
+  for (int s = 0; ok && (PLANNED ? attn_piece(p, table, s, piece) : attn_work(p, s, w)); ++s) {
     // rows row0 + r, r < rows, of key head hk: query (row0 + r) % queries of head (row0 + r) / queries of its group
     int b, hk, row0, rows, q_len, k_len, queries;
     if (PLANNED) {

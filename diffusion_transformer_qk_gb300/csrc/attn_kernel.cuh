@@ -38,15 +38,41 @@
 
 namespace qknr {
 
-// A plan in the caller's workspace (attn_plan.cuh).
+// Sequences, and what their tiles are (attn_plan.cuh).
+enum { kPlanQueries, kPlanKeys, kPlanFew };       // a tile's rows: a head's queries, a key head's keys, or its group * q_len queries
+struct AttnSeqs {
+  int kind;
+  int rows;                   // rows of a tile
+  int heads, group, causal;   // heads: lines of tiles
+  int batch, seq_q, seq_k;    // sequence b: rows b * seq .. of lens[b] (null: seq) rows,
+  const int* q_lens;
+  const int* k_lens;
+  const int* q_starts;        // or, where these are given, rows starts[b] .. starts[b + 1] of seq rows in all
+  const int* k_starts;
+  MemSpan sp_q_lens, sp_k_lens, sp_q_starts, sp_k_starts;
+};
+
+// A plan in the caller's workspace.
 struct AttnPlan {
-  int* head;                  // items of a head, first row of k that belongs to a sequence, the row after the last
-  int2* spans;                // [CTAs + 1] where each CTA's share begins: head * items + item, unit
+  int4* head;                 // items of a head; first row of k that belongs to a sequence, the row after the last; waves
+  int2* spans;                // [CTAs + 1] where each CTA's share behind the waves begins: head * items + item, unit
   int4* items;                // [items][2] q row, q_len, k row, k_len; first row in its sequence, blocks, units, query tiles before
-  long long* prefix;          // [items] units before
+  long long* prefix;          // [items + 1] units before
   int* seq_items;             // [batch] first item of each sequence, or null
   MemSpan sp;
 };
+
+// The same for up to 32 sequences whose tiles all go out whole, worked out by
+// each CTA in its shared memory: no plan, no kernel that makes it.
+constexpr int kTableSeqs = 32;
+struct AttnTable {
+  int4 seqs[kTableSeqs];      // q row, q_len, k row, k_len
+  int first[kTableSeqs + 1];  // items before
+  int q_tiles[kTableSeqs];    // query tiles before
+};
+
+// its place behind a CTA's barriers, abort flag and tensor memory address
+constexpr int attn_table_at(int bars) { return (8 * bars + 8 + 15) / 16 * 16; }
 
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
@@ -89,6 +115,8 @@ struct AttnParams {
       sp_v, sp_dout_norm, sp_v_top, sp_ds_top;
   // PLANNED (batch is 1, seq_q and seq_k are all rows)
   AttnPlan plan;
+  AttnSeqs seqs;
+  int table;                  // no plan: AttnTable
   int few_rows;               // rows of a tile of a few queries
   int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
   int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
@@ -290,19 +318,104 @@ __device__ __forceinline__ bool attn_work(const AttnParams& p, int s, AttnWork& 
   return true;
 }
 
+// The blocks of item t of a sequence.
+__device__ __forceinline__ int plan_blocks(const AttnSeqs& j, int t, int q_len, int k_len) {
+  const int diag = k_len - q_len;
+  if (j.kind == kPlanFew) return (k_len + kTile - 1) / kTile;
+  if (j.kind == kPlanQueries) {
+    const int last = min(t * j.rows + j.rows, q_len);
+    const int keys = j.causal ? min(max(last + diag, 0), k_len) : k_len;
+    return (keys + kTile - 1) / kTile;
+  }
+  const int k0 = t * j.rows, end = (q_len + kTile - 1) / kTile;
+  const int first = j.causal && k0 - diag > 0 ? min((k0 - diag) / kTile, end) : 0;
+  return (end - first) * j.group;
+}
+
+// Starts are clamped to the rows there are.
+__device__ __forceinline__ int plan_start(const int* starts, const MemSpan& sp, int b, int rows, int* status) {
+  return in_span(starts + b, 4, sp, status) ? min(max(starts[b], 0), rows) : 0;
+}
+__device__ __forceinline__ int plan_rows(const AttnSeqs& j, int q_len, int k_len) {
+  return j.kind == kPlanKeys ? k_len : j.kind == kPlanFew ? q_len * j.group : q_len;
+}
+
+// One warp.  A start that falls counts as the largest before it: whatever they
+// say, no row belongs to two sequences.
+__device__ __forceinline__ void plan_table(const AttnSeqs& j, AttnTable& out, int lane, int* status) {
+  auto ends = [&](const int* starts, const MemSpan& sp, int rows, int& lo) {
+    int v = lane < j.batch ? plan_start(starts, sp, lane + 1, rows, status) : 0;
+    const int first = plan_start(starts, sp, 0, rows, status);
+    v = max(v, first);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, off));   // lanes below `off`: their own
+    lo = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) lo = first;
+    return v;
+  };
+  int4 s;
+  s.y = ends(j.q_starts, j.sp_q_starts, j.seq_q, s.x) - s.x;
+  s.w = ends(j.k_starts, j.sp_k_starts, j.seq_k, s.z) - s.z;
+  int n = lane < j.batch ? (plan_rows(j, s.y, s.w) + j.rows - 1) / j.rows : 0, q = lane < j.batch ? (s.y + kTile - 1) / kTile : 0;
+  const int mine_n = n, mine_q = q;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, n, off), b = __shfl_up_sync(0xffffffffu, q, off);
+    if (lane >= off) {
+      n += a;
+      q += b;
+    }
+  }
+  out.seqs[lane] = s;
+  out.first[lane] = n - mine_n;
+  out.q_tiles[lane] = q - mine_q;
+  if (lane == 31) out.first[32] = n;
+}
+
 // PLANNED: piece s of a CTA's share.
 struct AttnPiece {
   int h, e, u0, u1, slot;     // head line, item; units [u0, u1) of its contraction
   int q_row, q_len, k_row, k_len, t0, blocks, tiles0;
 };
-__device__ __forceinline__ bool attn_piece(const AttnParams& p, int s, AttnPiece& w) {
-  const int c = static_cast<int>(blockIdx.x), n = p.plan.head[0];
+__device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable& table, int s, AttnPiece& w) {
+  const int c = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+  int tile = s * ctas + (s & 1 ? ctas - 1 - c : c);
+  w.u0 = 0;
+  w.slot = -1;
+  if (p.table) {
+    const int n = table.first[kTableSeqs];
+    if (s * ctas >= n * p.seqs.heads) return false;
+    if (tile >= n * p.seqs.heads) tile = 0, w.u0 = 1;           // nothing for this CTA in the last wave
+    w.h = tile / n;
+    w.e = tile - w.h * n;
+    int b = 0;
+#pragma unroll
+    for (int step = kTableSeqs / 2; step >= 1; step >>= 1)
+      if (table.first[b + step] <= w.e) b += step;
+    const int4 q = table.seqs[b];
+    w.q_row = q.x;
+    w.q_len = q.y;
+    w.k_row = q.z;
+    w.k_len = q.w;
+    const int t = w.e - table.first[b];
+    w.t0 = t * p.seqs.rows;
+    w.blocks = plan_blocks(p.seqs, t, q.y, q.w);
+    w.tiles0 = table.q_tiles[b];
+    w.u1 = w.blocks + 1;
+    return w.u0 == 0;
+  }
   if (!in_span(p.plan.spans + c, 16, p.plan.sp, p.status)) return false;
-  const int2 from = p.plan.spans[c], to = p.plan.spans[c + 1];
-  const int tile = from.x + s;
-  if (tile > to.x || (tile == to.x && to.y == 0)) return false;
-  w.h = tile / n;
-  w.e = tile - w.h * n;
+  const int4 head = *p.plan.head;
+  int u1 = 0;                 // 0: to the end
+  if (s >= head.w) {
+    const int2 from = p.plan.spans[c], to = p.plan.spans[c + 1];
+    tile = from.x + s - head.w;
+    if (tile > to.x || (tile == to.x && to.y == 0)) return false;
+    if (s == head.w) w.u0 = from.y;
+    if (tile == to.x) u1 = to.y;
+  }
+  w.h = tile / head.x;
+  w.e = tile - w.h * head.x;
   if (!in_span(p.plan.items + 2LL * w.e, 32, p.plan.sp, p.status)) return false;
   const int4 q = p.plan.items[2LL * w.e], x = p.plan.items[2LL * w.e + 1];
   w.q_row = q.x;
@@ -312,9 +425,8 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, int s, AttnPiece
   w.t0 = x.x;
   w.blocks = x.y;
   w.tiles0 = x.w;
-  w.u0 = s == 0 ? from.y : 0;
-  w.u1 = tile == to.x ? to.y : x.z;
-  w.slot = w.u0 > 0 ? 2 * c : w.u1 < x.z ? 2 * c + 1 : p.keep ? 2 * static_cast<int>(gridDim.x) + tile : -1;
+  w.u1 = u1 ? u1 : x.z;
+  w.slot = w.u0 > 0 ? 2 * c : w.u1 < x.z ? 2 * c + 1 : p.keep ? 2 * ctas + tile : -1;
   return w.u0 < w.u1;
 }
 
@@ -453,14 +565,18 @@ constexpr int kRows = 2 * kTile;
 constexpr int kK = 2, kV = 2;                     // K and V tiles in flight
 enum { Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
        S_FULL = V_EMPTY + kV, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, O_FREE = O_DONE + 2, DRAIN = O_FREE + 2, BARS };
-__device__ __forceinline__ int arrivals(int i) {
-  return (i >= P_FULL && i < O_DONE) || (i >= O_FREE && i < DRAIN) ? 4 : 1;
+__device__ __forceinline__ int arrivals(int i, bool grouped) {
+  return (i >= P_FULL && i < O_DONE) || (i >= O_FREE && i < DRAIN) || (grouped && i < Q_EMPTY) ? 4 : 1;
 }
 constexpr int kStage = kOutRows * 128;            // a warp's staged rows: 64 columns
 template <int D>
 constexpr int kCtl = (2 + kK + kV) * kTileBytes<D> + 8 * kStage;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
+constexpr int kTableAt = attn_table_at(BARS);
+template <int D>
+constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
+static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
 // The running maximum is only raised, and the accumulator rescaled, when the
 // new one is more than 2^8 above: p stays below 2^8 (2^15 with kPLift), which
 // 16-bit floats and the fp32 sums hold as exactly as values below one.
@@ -476,7 +592,10 @@ struct Seg {
 };
 }  // namespace fwd
 
-template <typename T, int D, bool PLANNED = false, bool PREFIX = false>
+// GROUPED: a tile is 256 rows of a key head's group * q_len, query x % q_len of
+// head x / q_len of its group, which the threads that own them fetch; all
+// results go to slots, and there is no causal mask.
+template <typename T, int D, bool PLANNED = false, bool PREFIX = false, bool GROUPED = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __grid_constant__ AttnParams p) {
   using namespace fwd;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -486,7 +605,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   const AttnCta c{smem, smem_addr(smem), smem_addr(ctl), abort_flag, p.status, p.wait_limit_ns,
                   __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), static_cast<int>(threadIdx.x & 31)};
   if (threadIdx.x == 0) {
-    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), arrivals(i));
+    for (int i = 0; i < BARS; ++i) mbar_init(c.bar(i), arrivals(i, GROUPED));
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -497,19 +616,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
   grid_dependents_launch();
+  AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
+  if (PLANNED && p.table) {
+    if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
+    __syncthreads();
+  }
 
   auto segment = [&](int s, Seg& g) {
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece(p, s, piece)) return false;
+      if (!attn_piece(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
       g.slot = piece.slot;
       g.q_row = piece.q_row;
       g.k_row = piece.k_row;
-      g.q_len = piece.q_len;
+      g.q_len = GROUPED ? piece.q_len * p.group : piece.q_len;
       g.k_len = piece.k_len;
     } else {
       if (!attn_work(p, s, w)) return false;
@@ -527,7 +651,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int first = g.q0 + t * kTile, last = first + kTile < g.q_len ? first + kTile : g.q_len;
-      int keys = first >= g.q_len ? 0 : (p.causal ? last + g.diag : g.k_len);
+      int keys = first >= g.q_len ? 0 : (!GROUPED && p.causal ? last + g.diag : g.k_len);
       keys = keys < 0 ? 0 : (keys > g.k_len ? g.k_len : keys);
       nb[t] = (keys + kTile - 1) / kTile;
       if (PREFIX && first < g.q_len) nb[t] += p.prefix_blocks;
@@ -558,7 +682,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       bool ok = true;
       Seg g;
       for (int s = 0; ok && segment(s, g); ++s) {
-        {
+        if (!GROUPED) {
           // the next tile's queries come from HBM: on their way while this one's keys come from L2
           Seg next;
           if (segment(s + 1, next))
@@ -566,14 +690,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
               if (next.nb[t]) tma_prefetch_tile(&p.map_q, next.q_row + next.q0 + t * kTile, next.h, next.b);
         }
         for (int t = 0; t < 2 && ok; ++t) {
-          if (g.nb[t] == 0) continue;
+          if (GROUPED || g.nb[t] == 0) continue;
           ok = c.wait1(Q_EMPTY + t, uses[t] + 1);
           if (!ok) break;
           mbar_arrive_expect_tx(c.bar(Q_FULL + t), kTileBytes<D>);
           tma_load_tile(c.base + t * kTileBytes<D>, &p.map_q, g.q_row + g.q0 + t * kTile, g.h, g.b, c.bar(Q_FULL + t));
           ++uses[t];
         }
-        const int hk = g.h / p.group;
+        const int hk = GROUPED ? g.h : g.h / p.group;
         for (int j = 0; ok && j < g.blocks; ++j, k.step(), v.step()) {
           const bool shared = PREFIX && g.begin + j < p.prefix_blocks;
           const int row = g.k_row + (g.begin + j - (PREFIX && !shared ? p.prefix_blocks : 0)) * kTile, kb = shared ? 0 : g.b;
@@ -677,15 +801,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     const uint32_t ts = tmem + t * kTile + lanes, to = tmem + 2 * kTile + t * kTile + lanes;
     unsigned char* stage = smem + (2 + kK + kV) * kTileBytes<D> + c.warp * kStage;
     const float sl = p.scale_log2, slack = kSlack / sl;
-    int done = 0;                                 // blocks so far
+    int done = 0, fetched = 0;                    // blocks, tiles' queries so far
     bool ok = true;
     Seg g;
     for (int sg = 0; ok && segment(sg, g); ++sg) {
       const int n = t ? g.nb[1] : g.nb[0];
+      if (GROUPED && n > 0) {
+        ok = c.wait(Q_EMPTY + t, ++fetched);
+        if (!ok) break;
+        const int x = g.q0 + t * kTile + r, q_len = g.q_len / p.group;
+        const char* src = p.q_in + static_cast<long long>(g.q_row + x % q_len) * p.q_stride + (g.h * p.group + x / q_len) * (D * 2);
+        unsigned char* dst = smem + t * kTileBytes<D> + r * 128;
+        const bool there = x < g.q_len && in_span(src, D * 2, p.sp_q, p.status);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {         // where the swizzle puts 16-byte chunk i of the row
+          const uint4 w = there ? *reinterpret_cast<const uint4*>(src + 16 * i) : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * (kTile * 128) + (((i & 7) ^ (r & 7)) << 4)) = w;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (c.lane == 0) mbar_arrive(c.bar(Q_FULL + t));
+      }
       int limit, shared = 0;                      // keys from the first block on that this query sees; PREFIX: of the prefix
       {
         const int row = g.q0 + t * kTile + r;
-        limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
+        limit = row < g.q_len ? (!GROUPED && p.causal ? row + g.diag + 1 : g.k_len) : 0;
         limit = (limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit)) - g.begin * kTile;
         if (PREFIX) {
           limit += p.prefix_blocks * kTile;
@@ -1032,6 +1172,21 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
     // of its 8 columns, and a team's rows all stay below the sum over its lanes
     // (about sqrt(2) times the longest row; no shuffles until the end).
     constexpr int N = 2;                          // rows in flight
+    __shared__ int range[2];                      // PLANNED: the rows of v that belong to a sequence
+    if (PLANNED) {
+      if (threadIdx.x < 32 && p.table) {
+        const int v = static_cast<int>(threadIdx.x) < p.seqs.batch
+                          ? plan_start(p.seqs.k_starts, p.seqs.sp_k_starts, threadIdx.x + 1, p.seqs.seq_k, p.status)
+                          : 0;
+        const int first = plan_start(p.seqs.k_starts, p.seqs.sp_k_starts, 0, p.seqs.seq_k, p.status);
+        const int end = __reduce_max_sync(0xffffffffu, max(v, first));
+        if (threadIdx.x == 0) range[0] = first, range[1] = end;
+      } else if (threadIdx.x == 0) {
+        range[0] = p.plan.head->y;
+        range[1] = p.plan.head->z;
+      }
+      __syncthreads();
+    }
     const long long rows_v = static_cast<long long>(p.batch) * p.seq_k * p.heads_k, step = static_cast<long long>(gridDim.x) * TEAMS;
     const int h_step = static_cast<int>(step % p.heads_k), row_step = static_cast<int>(step / p.heads_k);
     long long it = static_cast<long long>(blockIdx.x) * TEAMS + team;
@@ -1045,7 +1200,7 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
         if (it < rows_v) {
           const char* src = p.v_in + row * p.v_stride + h * (D * 2) + lane * 16;
           bool counts = in_span(src, 16, p.sp_v, p.status);
-          if (PLANNED) counts = counts && row >= p.plan.head[1] && row < p.plan.head[2];
+          if (PLANNED) counts = counts && row >= range[0] && row < range[1];
           if (p.k_lens) {
             const int b = row / p.seq_k;
             counts = counts && row - b * p.seq_k < clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
@@ -1108,6 +1263,10 @@ template <int D>
 constexpr int kCtl = (1 + kK + kV) * kTileBytes<D> + 8 * kStage<D>;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
+constexpr int kTableAt = attn_table_at(BARS);
+template <int D>
+constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
+static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
 
 struct Seg {
   int b, h, q0, slot;
@@ -1140,11 +1299,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
   grid_dependents_launch();
+  AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
+  if (PLANNED && p.table) {
+    if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
+    __syncthreads();
+  }
 
   auto segment = [&](int s, Seg& g) {
     if (PLANNED) {
       AttnPiece piece;
-      if (!attn_piece(p, s, piece)) return false;
+      if (!attn_piece(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
@@ -1574,6 +1738,10 @@ template <int D>
 constexpr int kCtl = (2 + kQ + kO) * kTileBytes<D> + kRowBytes;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
+constexpr int kTableAt = attn_table_at(BARS);
+template <int D>
+constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
+static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
 
 struct Seg {
   int b, h, k0, slot;         // h: key head
@@ -1607,6 +1775,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   const uint32_t tmem = *tmem_word;
   grid_dependency_wait();
   grid_dependents_launch();
+  AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
+  if (PLANNED && p.table) {
+    if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
+    __syncthreads();
+  }
   float* rows = reinterpret_cast<float*>(smem + (2 + kQ + kO) * kTileBytes<D>);   // [2][2][128]
   float* lifts = rows + 2 * 2 * kTile;            // [2]
 
@@ -1614,7 +1787,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece(p, s, piece)) return false;
+      if (!attn_piece(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.k0 = piece.t0;

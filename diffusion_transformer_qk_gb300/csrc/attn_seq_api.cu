@@ -32,19 +32,15 @@ qknr::AttnPlan take_plan(Space* ws, long long items, long long batch, bool seq_i
   qknr::AttnPlan p;
   const size_t from = ws->used;
   char* const lo = ws->base + from;
-  p.head = ws->take<int>(4);
+  p.head = ws->take<int4>(1);
   p.spans = ws->take<int2>(kCtas + 1);
   p.items = ws->take<int4>(2 * items);
-  p.prefix = ws->take<long long>(items);
+  p.prefix = ws->take<long long>(items + 1);
   p.seq_items = seq_items ? ws->take<int>(batch) : nullptr;
   p.sp = msp(span_of(lo, 1, 0, static_cast<long long>(ws->used - from)));
   return p;
 }
 
-// What a cut costs: partial results and the kernel that joins them, about six
-// blocks' time at head_dim 128 and twelve at 64, so that tiles of twice as
-// many go out whole (a share is then off by one tile at most).
-int whole_units(int head_dim) { return head_dim == 128 ? 12 : 24; }
 constexpr int kLeastUnits = 3;                    // of a share
 constexpr int kLeastFew = 2;
 
@@ -56,13 +52,21 @@ struct Job {
   int slot_rows;              // fp32 rows of a partial result
   bool cuts;                  // some tile may be cut
   bool keep = false;
+  bool table = false;         // no plan: every CTA works its tiles out
   long long slots() const { return keep ? 2 * kCtas + heads * items : cuts ? 2 * kCtas : 0; }
 };
+
+bool is_few(const Job& j) { return j.kind == qknr::kPlanFew && j.rows <= qknr::kFewRows; }
+
+// What a cut costs: partial results and the kernel that joins them, about six
+// blocks' time at head_dim 128 and twelve at 64, so that tiles of twice as
+// many go out whole (a share is then off by one tile at most).
+int whole_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 3 : a->head_dim == 128 ? 12 : 24; }
 
 Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_rows, long long batch, long long units,
            int slot_rows) {
   Job j{kind, rows, heads, max_items(of_rows, batch, rows), units, slot_rows, false};
-  j.cuts = units > (kind == qknr::kPlanFew ? 3 : whole_units(a->head_dim));
+  j.cuts = units > whole_units(a, j);
   return j;
 }
 
@@ -81,8 +85,8 @@ Job forward_job(const qknr_attn_args* a, long long rows, long long batch, int ke
 }
 
 struct Kernels {
-  const void *fwd, *few[2], *joint, *delta, *dq, *dkv, *join_fwd, *join_few, *join_dq, *join_dkv, *join_prefix, *join_halves;
-  int fwd_smem, dq_smem, dkv_smem;
+  const void *fwd, *few[2], *grouped, *joint, *delta, *dq, *dkv, *join_fwd, *join_few, *join_dq, *join_dkv, *join_prefix, *join_halves;
+  int planned_smem, joint_smem, dq_smem, dkv_smem;
 };
 
 template <typename T, int D>
@@ -90,6 +94,7 @@ Kernels kernels() {
   return Kernels{reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D, true>),
                  {reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 1, true>),
                   reinterpret_cast<const void*>(qknr::attn_few_kernel<T, D, 2, true>)},
+                 reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D, true, false, true>),
                  reinterpret_cast<const void*>(qknr::attn_forward_kernel<T, D, false, true>),
                  reinterpret_cast<const void*>(qknr::attn_delta_kernel<T, D, true>),
                  reinterpret_cast<const void*>(qknr::attn_dq_kernel<T, D, true>),
@@ -100,7 +105,8 @@ Kernels kernels() {
                  reinterpret_cast<const void*>(qknr::plan_join_grad_kernel<T, D, true>),
                  reinterpret_cast<const void*>(qknr::prefix_join_kernel<T, D>),
                  reinterpret_cast<const void*>(qknr::attn_join_forward_kernel<T, D, false>),
-                 qknr::fwd::kSmem<D>, qknr::dq::kSmem<D>, qknr::dkv::kSmem<D>};
+                 qknr::fwd::kPlannedSmem<D>, qknr::fwd::kSmem<D>, qknr::dq::kPlannedSmem<D>,
+                 qknr::dkv::kPlannedSmem<D>};
 }
 
 Kernels kernels_for(const qknr_attn_args* a) {
@@ -117,14 +123,14 @@ qknr_status launch_plan(const qknr::AttnPlanParams& pp, int jobs, const qknr_att
 }
 
 void fill_job(const qknr_attn_args* a, const Job& j, const qknr::AttnPlan& plan, qknr::AttnPlanJob* out) {
-  out->kind = j.kind;
-  out->rows = j.rows;
-  out->heads = j.heads;
-  out->group = a->n_heads_q / a->n_heads_k;
-  out->causal = a->causal != 0;
+  out->seqs.kind = j.kind;
+  out->seqs.rows = j.rows;
+  out->seqs.heads = j.heads;
+  out->seqs.group = a->n_heads_q / a->n_heads_k;
+  out->seqs.causal = a->causal != 0;
   out->ctas = kCtas;
-  out->whole = j.kind == qknr::kPlanFew ? 3 : whole_units(a->head_dim);
-  out->least = j.kind == qknr::kPlanFew ? kLeastFew : kLeastUnits;
+  out->whole = whole_units(a, j);
+  out->least = is_few(j) ? kLeastFew : kLeastUnits;
   out->max_items = static_cast<int>(j.items);
   out->plan = plan;
 }
@@ -141,10 +147,10 @@ void take_parts(Space* ws, const qknr_attn_args* a, const Job& j, bool stats, qk
 // The pass over q rows by k rows whose tiles are `j`'s.
 qknr_status launch_forward(const qknr_attn_args* a, const Job& j, const Kernels& fn, qknr::AttnParams* kp, int dev,
                            const qknr_host::DeviceInfo& di, qknr_stream_t stream) {
-  if (j.kind == qknr::kPlanFew)
-    return launch(fn.few[j.rows / 16], kCtas, 32 * qknr::few_warps(j.rows), qknr::few_smem(j.rows, a->head_dim), a, kp, dev, di,
-                  stream, "cudaLaunchKernelExC(attention, few queries)");
-  return launch(fn.fwd, kCtas, qknr::kAttnThreads, fn.fwd_smem, a, kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
+  if (is_few(j))
+    return launch(fn.few[j.rows / 16], kCtas, 32 * qknr::few_warps(j.rows), qknr::few_planned_smem(j.rows, a->head_dim), a, kp, dev,
+                  di, stream, "cudaLaunchKernelExC(attention, few queries)");
+  return launch(j.kind == qknr::kPlanFew ? fn.grouped : fn.fwd, kCtas, qknr::kAttnThreads, fn.planned_smem, a, kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
 }
 
 qknr_status launch_join(const void* fn, const Job& j, const qknr_attn_args* a, qknr::AttnParams* kp, qknr_stream_t stream,
@@ -152,7 +158,7 @@ qknr_status launch_join(const void* fn, const Job& j, const qknr_attn_args* a, q
   if (!j.cuts) return QKNR_OK;
   int ctas = kCtas;
   void* kargs[] = {kp, &ctas};
-  return qknr_host::launch_kernel(fn, (kCtas - 1) * qknr::kPlanJoinCtas, 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
+  return qknr_host::launch_kernel(fn, (kCtas - 1) * qknr::plan_join_ctas(is_few(j)), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,
                                   !(a->flags & QKNR_FLAG_NO_OVERLAP), what);
 }
 
@@ -194,7 +200,7 @@ qknr_status check_pack(const qknr_pack_args* p, qknr_attn_args* a) {
   if (p->batch < 0) return fail(QKNR_ERR_SHAPE, "negative batch");
   // items of the smallest tiles (8 rows of a key head), for every head
   const long long rows = p->rows_q > p->rows_k ? p->rows_q : p->rows_k;
-  if ((rows / 8 + p->batch + 1) * p->n_heads_q > 0x7fffffffLL)
+  if ((rows / 8 + p->batch + 1) * p->n_heads_q > 0x7fffffffLL || rows * (p->n_heads_q / p->n_heads_k) > 0x7fffff00LL)
     return fail(QKNR_ERR_UNSUPPORTED, "more than 2^31 tiles");
   return QKNR_OK;
 }
@@ -206,7 +212,7 @@ qknr_status check_starts(const qknr_pack_args* p) {
   return QKNR_OK;
 }
 
-void pack_sequences(const qknr_pack_args* p, qknr::AttnPlanJob* j) {
+void pack_sequences(const qknr_pack_args* p, qknr::AttnSeqs* j) {
   j->batch = p->batch;
   j->seq_q = p->rows_q;
   j->seq_k = p->rows_k;
@@ -219,7 +225,7 @@ void pack_sequences(const qknr_pack_args* p, qknr::AttnPlanJob* j) {
 // What both passes put where.
 struct PackSpace {
   Job job[2];
-  qknr::AttnPlan plan[2];
+  qknr::AttnPlan plan[2] = {};
   float *delta, *dout_norm, *v_top, *ds_top;
   size_t delta_n, ds_top_n;
 };
@@ -228,7 +234,8 @@ constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k);
-  s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
+  s->job[0].table = !s->job[0].cuts && p->batch <= qknr::kTableSeqs;
+  if (!s->job[0].table) s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
 }
 
@@ -237,7 +244,11 @@ void pack_backward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space
   s->job[0] = job_of(a, qknr::kPlanQueries, qknr::kTile, a->n_heads_q, p->rows_q, p->batch, blocks_of(p->rows_k) + 1, qknr::kTile);
   s->job[1] = job_of(a, qknr::kPlanKeys, qknr::kTile, a->n_heads_k, p->rows_k, p->batch, blocks_of(p->rows_q) * group + 1,
                      2 * qknr::kTile);
-  for (int i = 0; i < 2; ++i) s->plan[i] = take_plan(ws, s->job[i].items, p->batch, false);
+  const bool table = !s->job[0].cuts && !s->job[1].cuts && p->batch <= qknr::kTableSeqs;
+  for (int i = 0; i < 2; ++i) {
+    s->job[i].table = table;
+    if (!table) s->plan[i] = take_plan(ws, s->job[i].items, p->batch, false);
+  }
   s->delta_n = static_cast<size_t>(a->n_heads_q) * p->rows_q;
   s->delta = ws->take<float>(s->delta_n);
   // what fp16's dS takes its powers of two from
@@ -293,7 +304,8 @@ qknr_status check_prefix(const qknr_prefix_args* p, qknr_attn_args* a) {
   const qknr_status st = check_shape(a);
   if (st != QKNR_OK) return st;
   if (p->prefix < 0) return fail(QKNR_ERR_SHAPE, "negative prefix");
-  if ((static_cast<long long>(p->batch) * p->seq_q / 8 + p->batch + 1) * p->n_heads_q > 0x7fffffffLL ||
+  const long long rows = static_cast<long long>(p->batch) * p->seq_q;
+  if ((rows / 8 + p->batch + 1) * p->n_heads_q > 0x7fffffffLL || rows * (p->n_heads_q / p->n_heads_k) > 0x7fffff00LL ||
       static_cast<long long>(p->prefix) + p->seq_k > 0x7fffff00LL)
     return fail(QKNR_ERR_UNSUPPORTED, "more than 2^31 rows or tiles");
   return QKNR_OK;
@@ -313,15 +325,18 @@ bool together(const qknr_attn_args* a, int prefix) {
   double both = 8.0 + rows * heads * D * 16.0 * byte;
   const double few_prefix = group * rows / 16.0 + 1.0, few_own = group * a->seq_q / 16.0 + 1.0, key = 4.0 * D * a->n_heads_k * byte;
   both += few(a->batch * static_cast<long long>(a->seq_q), 1) ? prefix * key * few_prefix
-                                                              : static_cast<double>(blocks_of(static_cast<int>(rows))) * heads * np * block;
+                                                              : std::fmin(std::ceil(rows / 128.0) * heads, std::ceil(group * rows / 128.0) * a->n_heads_k) * np * block;
   both += few(a->seq_q, 1) ? B * a->seq_k * key * few_own : own;
   return both < apart;
 }
 
+// Tiles of 128 rows.
+long long halves(long long rows) { return (rows + qknr::kTile - 1) / qknr::kTile; }
+
 struct PrefixSpace {
   bool split;                 // prefix and own keys in passes of their own
   Job job[2];                 // of the prefix, of the samples' keys
-  qknr::AttnPlan plan[2];
+  qknr::AttnPlan plan[2] = {};
   Cut cut;                    // otherwise
 };
 
@@ -338,11 +353,15 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
   }
   const long long rows = static_cast<long long>(a->batch) * a->seq_q;
   s->job[0] = forward_job(a, rows, 1, p->prefix);
+  // the heads of a group in one tile where that leaves fewer rows of a tile empty
+  const long long group = a->n_heads_q / a->n_heads_k;
+  if (s->job[0].kind == qknr::kPlanQueries && halves(group * rows) < group * halves(rows))
+    s->job[0] = job_of(a, qknr::kPlanFew, qknr::fwd::kRows, a->n_heads_k, group * rows, 1, blocks_of(p->prefix) + 1, qknr::fwd::kRows);
   s->job[1] = forward_job(a, rows, a->batch, a->seq_k);
   for (int i = 0; i < 2; ++i) {
     Job& j = s->job[i];
     j.keep = true;
-    if (j.kind == qknr::kPlanQueries && (i ? a->seq_q : rows) <= qknr::kTile) j.slot_rows = qknr::kTile;
+    if (!is_few(j) && (i ? a->seq_q : j.kind == qknr::kPlanFew ? group * rows : rows) <= qknr::kTile) j.slot_rows = qknr::kTile;
     if ((i ? a->seq_k : p->prefix) == 0) j.keep = j.cuts = false;   // the pass is not made
     s->plan[i] = take_plan(ws, j.items, a->batch, i == 1);
     take_parts(ws, a, j, true, &kp[i]);
@@ -419,7 +438,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   memset(&pp, 0, sizeof(pp));
   pp.status = p->dev_status;
   fill_job(&a, s.job[0], s.plan[0], &pp.job[0]);
-  pack_sequences(p, &pp.job[0]);
+  pack_sequences(p, &pp.job[0].seqs);
   const Span space = span_of(p->workspace, 1, 0, static_cast<long long>(ws.used));
   const Span lse{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)};
   st = check_overlap(&a, {&o}, {&q, &k, &v}, {lse, space},
@@ -427,6 +446,8 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   if (st != QKNR_OK) return st;
   if (qknr_host::overlaps(lse, space)) return fail(QKNR_ERR_OVERLAP, "lse and the workspace overlap");
   kp.plan = s.plan[0];
+  kp.seqs = pp.job[0].seqs;
+  kp.table = s.job[0].table;
   kp.few_rows = s.job[0].rows;
   kp.slot_rows = s.job[0].slot_rows;
   kp.q_in = static_cast<const char*>(p->q);
@@ -439,8 +460,8 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   int dev = 0;
   qknr_host::DeviceInfo di;
   if ((st = device(&dev, &di)) != QKNR_OK) return st;
-  const bool is_few = s.job[0].kind == qknr::kPlanFew;
-  const int box = is_few ? qknr::few_keys(a.head_dim) : qknr::kTile;
+  const bool a_few = is_few(s.job[0]);
+  const int box = a_few ? qknr::few_keys(a.head_dim) : qknr::kTile;
   if ((st = make_map(&kp.map_q, &a, p->q, q.stride, p->rows_q, p->n_heads_q)) != QKNR_OK) return st;
   if ((st = make_map(&kp.map_out, &a, p->o, o.stride, p->rows_q, p->n_heads_q, qknr::kOutRows, 64)) != QKNR_OK) return st;
   if (p->rows_k > 0) {   // without keys the kernels load nothing
@@ -448,9 +469,9 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, &a, p->v, v.stride, p->rows_k, p->n_heads_k, box)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(&a);
-  if ((st = launch_plan(pp, 1, &a, stream)) != QKNR_OK) return st;
+  if (!kp.table && (st = launch_plan(pp, 1, &a, stream)) != QKNR_OK) return st;
   if ((st = launch_forward(&a, s.job[0], fn, &kp, dev, di, stream)) != QKNR_OK) return st;
-  return launch_join(is_few ? fn.join_few : fn.join_fwd, s.job[0], &a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
+  return launch_join(a_few ? fn.join_few : fn.join_fwd, s.job[0], &a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
 }
 
 qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
@@ -479,7 +500,7 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
   pp.status = p->dev_status;
   for (int i = 0; i < 2; ++i) {
     fill_job(&a, s.job[i], s.plan[i], &pp.job[i]);
-    pack_sequences(p, &pp.job[i]);
+    pack_sequences(p, &pp.job[i].seqs);
   }
   const Span space = span_of(p->workspace, 1, 0, static_cast<long long>(ws.used));
   const Span lse{static_cast<uintptr_t>(kp.sp_lse.lo), static_cast<uintptr_t>(kp.sp_lse.hi)};
@@ -531,9 +552,11 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, &a, p->v, v.stride, p->rows_k, p->n_heads_k)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(&a);
-  if ((st = launch_plan(pp, 2, &a, stream)) != QKNR_OK) return st;
+  kp.table = s.job[0].table;
+  if (!kp.table && (st = launch_plan(pp, 2, &a, stream)) != QKNR_OK) return st;
   auto use = [&](int i) {
     kp.plan = s.plan[i];
+    kp.seqs = pp.job[i].seqs;
     kp.part = parts[i].part;
     kp.sp_part = parts[i].sp_part;
   };
@@ -642,7 +665,7 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
       if ((st = make_map(&kp.map_prefix_k, &shared, p->prefix_k, pk.stride, p->prefix, p->n_heads_k)) != QKNR_OK) return st;
       if ((st = make_map(&kp.map_prefix_v, &shared, p->prefix_v, pv.stride, p->prefix, p->n_heads_k)) != QKNR_OK) return st;
     }
-    st = launch(fn.joint, s.cut.ctas, qknr::kAttnThreads, fn.fwd_smem, &a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
+    st = launch(fn.joint, s.cut.ctas, qknr::kAttnThreads, fn.joint_smem, &a, &kp, dev, di, stream, "cudaLaunchKernelExC(attention)");
     if (st != QKNR_OK) return st;
     return join(fn.join_halves, s.cut, qknr::fwd::kRows, &a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
   }
@@ -658,7 +681,7 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     const Job& j = s.job[i];
     const qknr_attn_args& side = sides[i];
     fill_job(&a, j, s.plan[i], &pp.job[i]);
-    qknr::AttnPlanJob& pj = pp.job[i];
+    qknr::AttnSeqs& pj = pp.job[i].seqs;
     pj.batch = i ? p->batch : 1;
     pj.seq_q = i ? p->seq_q : side.seq_q;
     pj.seq_k = i ? p->seq_k : p->prefix;
@@ -678,6 +701,7 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     w.seq_q = side.seq_q;
     w.seq_k = side.seq_k;
     w.plan = s.plan[i];
+    w.seqs = pj;
     w.few_rows = j.rows;
     w.slot_rows = j.slot_rows;
     w.keep = 1;
@@ -685,8 +709,7 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     w.stats = parts[i].stats;
     w.sp_part = parts[i].sp_part;
     w.sp_stats = parts[i].sp_stats;
-    const bool is_few = j.kind == qknr::kPlanFew;
-    const int box = is_few ? qknr::few_keys(a.head_dim) : qknr::kTile;
+    const int box = is_few(j) ? qknr::few_keys(a.head_dim) : qknr::kTile;
     if ((st = make_map(&w.map_q, &side, p->q, q.stride, side.seq_q, p->n_heads_q)) != QKNR_OK) return st;
     if (side.seq_k > 0) {
       const Rows &rk = i ? k : pk, &rv = i ? v : pv;
@@ -697,8 +720,8 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     js.plan = s.plan[i];
     js.part = w.part;
     js.stats = w.stats;
-    js.few = is_few;
-    js.few_rows = j.rows;
+    js.few = j.kind == qknr::kPlanFew;
+    js.rows = j.rows;
     js.slot_rows = j.slot_rows;
     js.ctas = kCtas;
     js.there = side.seq_k > 0;

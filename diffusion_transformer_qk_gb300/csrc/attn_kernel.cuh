@@ -55,9 +55,11 @@ struct AttnSeqs {
 // A plan in the caller's workspace.
 struct AttnPlan {
   int4* head;                 // items of a head; first row of k that belongs to a sequence, the row after the last; waves
-  int2* spans;                // [CTAs + 1] where each CTA's share behind the waves begins: head * items + item, unit
+  int2* spans;                // [CTAs + 1] where each CTA's share behind the waves begins: tile of the line, unit
   int4* items;                // [items][2] q row, q_len, k row, k_len; first row in its sequence, blocks, units, query tiles before
-  long long* prefix;          // [items + 1] units before
+  int2* runs;                 // [items] first and count of the items of its cost
+  int* ranks;                 // [items] the place of each in the line, in the sequences' order, or null
+  long long* prefix;          // [items + 1] units before, of many items
   int* seq_items;             // [batch] first item of each sequence, or null
   MemSpan sp;
 };
@@ -71,8 +73,19 @@ struct AttnTable {
   int q_tiles[kTableSeqs];    // query tiles before
 };
 
+// The pieces of a CTA's share as the forward and dq kernels' planning warp
+// hands them round: the other roles read a piece from shared memory, a few
+// tiles behind, instead of working it out from global memory where a tile
+// begins and ends (3 x 1999 x 16 on 4 heads x 64, causal: 72 us, 717 at 2 x
+// 4608 x 48 x 128).
+constexpr int kPieces = 4;
+struct AttnPieces {
+  int4 at[kPieces][3];
+};
+
 // its place behind a CTA's barriers, abort flag and tensor memory address
 constexpr int attn_table_at(int bars) { return (8 * bars + 8 + 15) / 16 * 16; }
+constexpr int attn_pieces_at(int bars) { return attn_table_at(bars) + (static_cast<int>(sizeof(AttnTable)) + 15) / 16 * 16; }
 
 struct AttnParams {
   CUtensorMap map_q, map_k, map_v, map_do;
@@ -250,6 +263,39 @@ struct AttnCta {
   __device__ __forceinline__ bool wait(int i, uint32_t phase) const {
     return __all_sync(0xffffffffu, wait1(i, phase));
   }
+  // PLANNED, forward and dq: the consumers' side of the pieces.  One thread or
+  // (whole) a warp; false at the end, and where the wait ran out (`lost`).
+  __device__ __forceinline__ bool piece(int full, const AttnPieces& pieces, int s, bool whole, int4 (&v)[3], bool& lost) const {
+    const int i = s % kPieces;
+    const uint32_t phase = static_cast<uint32_t>(s / kPieces);
+    if (!(whole ? wait(full + i, phase) : wait1(full + i, phase))) {
+      lost = true;
+      return false;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = pieces.at[i][k];
+    return v[2].w != 0;
+  }
+  // one thread, or (whole) a warp that has read what it needs of piece s
+  __device__ __forceinline__ void release(int empty, int s, bool whole) const {
+    if (whole) __syncwarp();
+    if (!whole || lane == 0) mbar_arrive(bar(empty + s % kPieces));
+  }
+  // The planning warp: piece s (valid or the end) to the others.
+  __device__ __forceinline__ bool hand_round(int full, int empty, AttnPieces& pieces, int s, int4 a, int4 b, int4 d) const {
+    const int i = s % kPieces;
+    AttnCta patient = *this;
+    patient.limit = limit << 10;                  // a tile may take long; who waits for its parts sets the abort flag
+    if (!patient.wait(empty + i, static_cast<uint32_t>(s / kPieces) ^ 1u)) return false;
+    if (lane == 0) {
+      pieces.at[i][0] = a;
+      pieces.at[i][1] = b;
+      pieces.at[i][2] = d;
+      mbar_arrive(bar(full + i));
+    }
+    __syncwarp();
+    return true;
+  }
   // Whole warp, three barriers that are likely to be complete: lane 0 looks at
   // the first, lane 1 at the second, the others at the third.  Shared memory
   // answers slowly while the tensor cores read it: one look after the other
@@ -372,6 +418,13 @@ __device__ __forceinline__ void plan_table(const AttnSeqs& j, AttnTable& out, in
   if (lane == 31) out.first[32] = n;
 }
 
+// (head, item) of a tile of the line: items of one cost go head by head.
+__device__ __forceinline__ int2 plan_tile(const AttnPlan& plan, int heads, int tile) {
+  const int2 run = plan.runs[tile / heads];
+  const int x = tile - run.x * heads, h = x / run.y;
+  return make_int2(h, run.x + x - h * run.y);
+}
+
 // PLANNED: piece s of a CTA's share.
 struct AttnPiece {
   int h, e, u0, u1, slot;     // head line, item; units [u0, u1) of its contraction
@@ -414,8 +467,10 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     if (s == head.w) w.u0 = from.y;
     if (tile == to.x) u1 = to.y;
   }
-  w.h = tile / head.x;
-  w.e = tile - w.h * head.x;
+  if (tile >= head.x * p.seqs.heads || !in_span(p.plan.runs + tile / p.seqs.heads, 8, p.plan.sp, p.status)) return false;
+  const int2 at = plan_tile(p.plan, p.seqs.heads, tile);
+  w.h = at.x;
+  w.e = at.y;
   if (!in_span(p.plan.items + 2LL * w.e, 32, p.plan.sp, p.status)) return false;
   const int4 q = p.plan.items[2LL * w.e], x = p.plan.items[2LL * w.e + 1];
   w.q_row = q.x;
@@ -564,8 +619,10 @@ namespace fwd {
 constexpr int kRows = 2 * kTile;
 constexpr int kK = 2, kV = 2;                     // K and V tiles in flight
 enum { Q_FULL = 0, Q_EMPTY = 2, K_FULL = 4, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
-       S_FULL = V_EMPTY + kV, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, O_FREE = O_DONE + 2, DRAIN = O_FREE + 2, BARS };
+       S_FULL = V_EMPTY + kV, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2, O_FREE = O_DONE + 2, DRAIN = O_FREE + 2,
+       PIECE_FULL, PIECE_EMPTY = PIECE_FULL + kPieces, BARS = PIECE_EMPTY + kPieces };
 __device__ __forceinline__ int arrivals(int i, bool grouped) {
+  if (i >= PIECE_EMPTY) return 10;                // the loading and the issuing warp, eight of the softmax
   return (i >= P_FULL && i < O_DONE) || (i >= O_FREE && i < DRAIN) || (grouped && i < Q_EMPTY) ? 4 : 1;
 }
 constexpr int kStage = kOutRows * 128;            // a warp's staged rows: 64 columns
@@ -574,8 +631,9 @@ constexpr int kCtl = (2 + kK + kV) * kTileBytes<D> + 8 * kStage;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
 constexpr int kTableAt = attn_table_at(BARS);
+constexpr int kPiecesAt = attn_pieces_at(BARS);
 template <int D>
-constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
+constexpr int kPlannedSmem = kCtl<D> + kPiecesAt + static_cast<int>(sizeof(AttnPieces));
 static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
 // The running maximum is only raised, and the accumulator rescaled, when the
 // new one is more than 2^8 above: p stays below 2^8 (2^15 with kPLift), which
@@ -622,7 +680,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     __syncthreads();
   }
 
-  auto segment = [&](int s, Seg& g) {
+  auto work_out = [&](int s, Seg& g) {
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
@@ -671,6 +729,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     g.blocks = g.nb[0] > g.nb[1] ? g.nb[0] : g.nb[1];
     return true;
   };
+  AttnPieces& pieces = *reinterpret_cast<AttnPieces*>(ctl + kPiecesAt);
+  // piece s; `whole`: the warp asks together
+  bool lost = false;
+  auto segment = [&](int s, Seg& g, bool whole) {
+    if (!PLANNED) return work_out(s, g);
+    int4 v[3];
+    if (!c.piece(PIECE_FULL, pieces, s, whole, v, lost)) return false;
+    g.b = 0;
+    g.h = v[0].x;
+    g.q0 = v[0].y;
+    g.slot = v[0].z;
+    g.begin = v[0].w;
+    g.q_row = v[1].x;
+    g.q_len = v[1].y;
+    g.k_row = v[1].z;
+    g.k_len = v[1].w;
+    g.nb[0] = v[2].x;
+    g.nb[1] = v[2].y;
+    g.diag = g.k_len - g.q_len;
+    g.blocks = g.nb[0] > g.nb[1] ? g.nb[0] : g.nb[1];
+    return true;
+  };
   const uint32_t sk = c.base + 2 * kTileBytes<D>, sv = c.base + (2 + kK) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
@@ -681,11 +761,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       int uses[2] = {0, 0}, ik = 0, iv = 0;
       bool ok = true;
       Seg g;
-      for (int s = 0; ok && segment(s, g); ++s) {
+      for (int s = 0; ok && segment(s, g, false); ++s) {
         if (!GROUPED) {
           // the next tile's queries come from HBM: on their way while this one's keys come from L2
           Seg next;
-          if (segment(s + 1, next))
+          if (segment(s + 1, next, false))
             for (int t = 0; t < 2; ++t)
               if (next.nb[t]) tma_prefetch_tile(&p.map_q, next.q_row + next.q0 + t * kTile, next.h, next.b);
         }
@@ -712,6 +792,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           tma_load_tile(sv + v.s * kTileBytes<D>, shared ? &p.map_prefix_v : &p.map_v, row, hk, kb, c.bar(V_FULL + v.s));
           ++iv;
         }
+        if (PLANNED) c.release(PIECE_EMPTY, s, false);
       }
       if (!ok || *abort_flag) {
         c.drain(K_FULL, kK, ik);
@@ -728,7 +809,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     int uses[2] = {0, 0}, done[2] = {0, 0};       // tiles, blocks of each half so far
     bool ok = true;
     Seg g;
-    for (int s = 0; ok && segment(s, g); ++s) {
+    for (int s = 0; ok && segment(s, g, true); ++s) {
+      if (PLANNED) c.release(PIECE_EMPTY, s, true);
       if (g.blocks == 0) continue;
       const int n0 = g.nb[0], n1 = g.nb[1], blocks = g.blocks;
       // the block whose V has rows past the sample's keys (past a prefix's TMA reads zeros)
@@ -792,7 +874,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       uses[0] += n0 > 0;
       uses[1] += n1 > 0;
     }
-    if (!ok) c.drain_mma(DRAIN);
+    if (!ok || lost) c.drain_mma(DRAIN);
+  } else if (PLANNED && c.warp == kAttnMma2Warp) {
+    Seg g;
+    for (int s = 0;; ++s) {
+      const bool more = work_out(s, g);
+      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, pieces, s, make_int4(g.h, g.q0, g.slot, g.begin),
+                        make_int4(g.q_row, g.q_len, g.k_row, g.k_len), make_int4(g.nb[0], g.nb[1], 0, more)) || !more)
+        break;
+    }
   } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // softmax: a thread per query
@@ -804,7 +894,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     int done = 0, fetched = 0;                    // blocks, tiles' queries so far
     bool ok = true;
     Seg g;
-    for (int sg = 0; ok && segment(sg, g); ++sg) {
+    for (int sg = 0; ok && segment(sg, g, true); ++sg) {
       const int n = t ? g.nb[1] : g.nb[0];
       if (GROUPED && n > 0) {
         ok = c.wait(Q_EMPTY + t, ++fetched);
@@ -905,7 +995,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
       const float total = __fadd_rn(sum.x, sum.y);
       const bool some = total != 0.0f;
       const float inv = some ? __frcp_rn(total) : 0.0f;
-      segment(sg, g);                             // again: the loop above has no registers to keep it in
+      segment(sg, g, true);                       // again: the loop above has no registers to keep it in
       const int row = g.q0 + t * kTile + r;
       const long long at = static_cast<long long>(g.slot) * (PLANNED ? p.slot_rows : kRows) + t * kTile + r;   // a part's row
       if (g.slot >= 0) {
@@ -954,6 +1044,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           if (c.lane == 0 && (PLANNED || row < p.seq_q)) tma_store_box(&p.map_out, smem_addr(stage), 0, g.q_row + row, i / 2, g.h, g.b);
         }
       }
+      if (PLANNED) c.release(PIECE_EMPTY, sg, true);
     }
     if (c.lane == 0) tma_store_wait();
     tc_fence_before();
@@ -1253,8 +1344,9 @@ constexpr int kK = 3, kV = 2;                     // K (and Q) and V tiles in fl
 constexpr int kColS = 0, kColDp = kTile, kColDq = 2 * kTile, kColDs = 3 * kTile, kColQ = 3 * kTile + 64;
 enum { O_FULL = 0, O_EMPTY, K_FULL, K_EMPTY = K_FULL + kK, V_FULL = K_EMPTY + kK, V_EMPTY = V_FULL + kV,
        Q_READY = V_EMPTY + kV, S_FULL, S_FREE, DP_FULL, DP_FREE, DS_FULL, DS_FREE, DONE, ACC_FREE, DRAIN,
-       BARS = DRAIN + 2 };
+       PIECE_FULL = DRAIN + 2, PIECE_EMPTY = PIECE_FULL + kPieces, BARS = PIECE_EMPTY + kPieces };
 __device__ __forceinline__ int arrivals(int i) {
+  if (i >= PIECE_EMPTY) return 11;                // the loading warp, two issuing ones, eight workers
   return i == Q_READY || i == S_FREE || i == DP_FREE || i == DS_FULL || i == ACC_FREE ? 8 : 1;
 }
 template <int D>
@@ -1264,8 +1356,9 @@ constexpr int kCtl = (1 + kK + kV) * kTileBytes<D> + 8 * kStage<D>;
 template <int D>
 constexpr int kSmem = kCtl<D> + 256;
 constexpr int kTableAt = attn_table_at(BARS);
+constexpr int kPiecesAt = attn_pieces_at(BARS);
 template <int D>
-constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
+constexpr int kPlannedSmem = kCtl<D> + kPiecesAt + static_cast<int>(sizeof(AttnPieces));
 static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
 
 struct Seg {
@@ -1305,7 +1398,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     __syncthreads();
   }
 
-  auto segment = [&](int s, Seg& g) {
+  auto work_out = [&](int s, Seg& g) {
     if (PLANNED) {
       AttnPiece piece;
       if (!attn_piece(p, table, s, piece)) return false;
@@ -1319,7 +1412,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       g.q_len = piece.q_len;
       g.k_len = piece.k_len;
       g.diag = g.k_len - g.q_len;
-      g.top = piece.e;
+      g.top = piece.tiles0 + piece.t0 / kTile;
       g.begin = piece.u0 < piece.blocks ? piece.u0 : piece.blocks;
       g.n = (piece.u1 < piece.blocks ? piece.u1 : piece.blocks) - g.begin;
       return true;
@@ -1345,6 +1438,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.n = end - g.begin;
     return true;
   };
+  AttnPieces& pieces = *reinterpret_cast<AttnPieces*>(ctl + kPiecesAt);
+  // piece s; `whole`: the warp asks together
+  bool lost = false;
+  auto segment = [&](int s, Seg& g, bool whole) {
+    if (!PLANNED) return work_out(s, g);
+    int4 v[3];
+    if (!c.piece(PIECE_FULL, pieces, s, whole, v, lost)) return false;
+    g.b = 0;
+    g.h = v[0].x;
+    g.q0 = v[0].y;
+    g.slot = v[0].z;
+    g.begin = v[0].w;
+    g.q_row = v[1].x;
+    g.q_len = v[1].y;
+    g.k_row = v[1].z;
+    g.k_len = v[1].w;
+    g.n = v[2].x;
+    g.top = v[2].y;
+    g.opens = v[2].z;
+    g.diag = g.k_len - g.q_len;
+    return true;
+  };
   const uint32_t sdo = c.base, sk = c.base + kTileBytes<D>, sv = c.base + (1 + kK) * kTileBytes<D>;
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
@@ -1355,15 +1470,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       int ik = 0, iv = 0, io = 0;
       bool ok = true;
       Seg g;
-      for (int s = 0; ok && segment(s, g); ++s) {
+      for (int s = 0; ok && segment(s, g, false); ++s) {
         {
           // the next tile's queries come from HBM: on their way while this one's keys come from L2
           Seg next;
-          if (segment(s + 1, next) && next.n > 0) {
+          if (segment(s + 1, next, false) && next.n > 0) {
             tma_prefetch_tile(&p.map_q, next.q_row + next.q0, next.h, next.b);
             tma_prefetch_tile(&p.map_do, next.q_row + next.q0, next.h, next.b);
           }
         }
+        if (PLANNED) c.release(PIECE_EMPTY, s, false);
         if (g.n == 0) continue;
         const int hk = g.h / p.group;
         for (int j = -1; j < g.n; ++j) {
@@ -1406,7 +1522,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     int done = 0, live = 0;                       // blocks of the tiles before, tiles
     bool ok = true;
     Seg g;
-    for (int s = 0; ok && segment(s, g); ++s) {
+    for (int s = 0; ok && segment(s, g, true); ++s) {
+      if (PLANNED) c.release(PIECE_EMPTY, s, true);
       if (g.n == 0) continue;
       const int n = g.n, ragged = PLANNED || g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
       // block j's S: its K has landed, with nothing past the sample's keys
@@ -1448,14 +1565,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       done += n;
       ++live;
     }
-    if (!ok) c.drain_mma(DRAIN);
+    if (!ok || lost) c.drain_mma(DRAIN);
   } else if (c.warp == kAttnMma2Warp) {
     // dP of each block, when the block's before has been read
     RingPos<kV> v;
     int done = 0, live = 0;
     bool ok = true;
     Seg g;
-    for (int s = 0; ok && segment(s, g); ++s) {
+    for (int s = 0; ok && segment(s, g, true); ++s) {
+      if (PLANNED) c.release(PIECE_EMPTY, s, true);
       if (g.n == 0) continue;
       const int n = g.n, ragged = PLANNED || g.k_len < p.seq_k ? g.k_len / kTile - g.begin : n;
       ok = c.wait(O_FULL, live);
@@ -1476,7 +1594,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       }
       ++live;
     }
-    if (!ok) c.drain_mma(DRAIN + 1);
+    if (!ok || lost) c.drain_mma(DRAIN + 1);
+  } else if (PLANNED && c.warp == kAttnRowWarp) {
+    Seg g;
+    for (int s = 0;; ++s) {
+      const bool more = work_out(s, g);
+      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, pieces, s, make_int4(g.h, g.q0, g.slot, g.begin),
+                        make_int4(g.q_row, g.q_len, g.k_row, g.k_len), make_int4(g.n, g.top, g.opens, more)) || !more)
+        break;
+    }
   } else if (c.warp < kAttnMmaWarp) {
     more_registers<kAttnWorkRegs>();
     // a thread per query and half of the block's keys
@@ -1532,7 +1658,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
     Seg g;
-    for (int sg = 0; ok && segment(sg, g); ++sg) {
+    for (int sg = 0; ok && segment(sg, g, true); ++sg) {
       const int row = g.q0 + r;
       int limit = row < g.q_len ? (p.causal ? row + g.diag + 1 : g.k_len) : 0;
       limit = limit < 0 ? 0 : (limit > g.k_len ? g.k_len : limit);
@@ -1618,13 +1744,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       if (g.n > 0) {
         // Every S of this tile is done: the next one's Q can take Q's place,
         // and its first products run under this one's epilogue.
-        ready = segment(sg + 1, g) && g.n > 0;
+        ready = segment(sg + 1, g, true) && g.n > 0;
         if (ready) {
           row_stats(g, lse, delta, bound);
           ok = copy_q();
         }
         if (!ok) break;
-        segment(sg, g);
+        segment(sg, g, true);
         ok = c.wait(DONE, live++);
         if (!ok) break;
         tc_fence_after();
@@ -1666,6 +1792,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (c.lane == 0 && (PLANNED || row < p.seq_q))
           tma_store_box(&p.map_out, smem_addr(stage), D == 128 ? 0 : half * 32, g.q_row + row, D == 128 ? half : 0, g.h, g.b);
       }
+      if (PLANNED) c.release(PIECE_EMPTY, sg, true);
     }
     if (c.lane == 0) tma_store_wait();
     tc_fence_before();

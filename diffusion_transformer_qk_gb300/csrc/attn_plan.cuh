@@ -1,17 +1,18 @@
 // Work lists of attention over sequences whose lengths only the device knows
 // (packed sequences; samples with lengths beside a shared prefix), for sm_103a.
 //
-// A head's tiles, of all sequences one after the other, form a line of items;
-// a call's work is that line once per head.  An item's cost is its blocks (the
-// iterations of its contraction) and one unit for its epilogue.  CTAs take the
-// line's tiles in waves, neighbours next to each other, so that the keys of a
-// few heads at a time are read from L2 (2 x 4608 x 48 x 128, whose keys and
-// values are 226 MB: 3 GB from HBM and 785 us where each CTA walks a stretch of
-// the line of its own instead).  The waves end where the CTA that they gave most
-// has its share of the whole; what is left of the line is dealt out so that
-// all shares are equal, cut inside a tile where that is worth it, and parts of
-// a tile are joined in a fixed order by a second kernel.  So a batch of one
-// long and many short sequences keeps all SMs busy to the end.
+// A head's tiles, of all sequences, are its items; an item's cost is its blocks
+// (the iterations of its contraction) and one unit for its epilogue.  The
+// call's tiles form a line: the costliest items first, those of one cost
+// together, head by head.  CTAs take the line's tiles in waves, every other wave
+// the other way round, so that neighbours read the same keys at the same time
+// (2 x 4608 x 48 x 128, whose keys and values are 226 MB: 3 GB from HBM and 785
+// us where each CTA walks a stretch of the line of its own, 678 in waves) and
+// all get their part of the costly ones.  The waves end where a CTA would get
+// more than its share of the whole; what is left of the line, its cheapest
+// tiles, is dealt out so that all shares are equal, cut inside a tile where that
+// is worth it, and a second kernel joins the parts of a tile in a fixed order.
+// Where no tile is worth a cut, everything goes in waves.
 //
 // attn_plan_kernel works the items and the shares out, in one CTA.
 #pragma once
@@ -34,8 +35,8 @@ struct AttnPlanParams {
   int* status;
 };
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanNear = 2048;                   // items whose sums stay in shared memory
+constexpr int kPlanThreads = 256;
+constexpr int kPlanNear = 1024;                   // items that are sorted, of up to kPlanThreads sequences
 
 // Inclusive scan over the CTA's threads; `all`: over everybody.
 template <typename V, typename OP>
@@ -62,50 +63,77 @@ __device__ __forceinline__ V plan_scan(V v, OP op, V* warps, V& all) {
   return warp == 0 ? v : op(before, v);
 }
 
-// One CTA per job.
-static __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnPlanParams p) {
+// One CTA per job.  V: int for up to kPlanThreads sequences of up to kPlanNear
+// items, all of whose units fit into it.  Others keep the sequences' order.
+template <typename V>
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnPlanParams p) {
+  constexpr bool kNear = sizeof(V) == 4;
   __shared__ long long warps[32];
   __shared__ int4 seqs[kPlanThreads];             // q row, q_len, k row, k_len
-  __shared__ int firsts[kPlanThreads + 1], tiles0[kPlanThreads];
-  __shared__ long long near[kPlanNear + 1];       // units before each item
+  __shared__ int firsts[kPlanThreads + 1], tiles0[kPlanThreads], ends[kPlanThreads];
+  __shared__ __align__(16) int costs[kNear ? kPlanNear : 1];   // units of each item, in the sequences' order
+  __shared__ int line[kNear ? kPlanNear + 1 : 1]; // in the line's order: units, then units before
+  __shared__ int2 runs[kNear ? kPlanNear : 1];    // first and count of the items of the same cost
   const AttnPlanJob& job = p.job[blockIdx.x];
   const AttnSeqs& j = job.seqs;
   const AttnPlan& out = job.plan;
   int* iwarps = reinterpret_cast<int*>(warps);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  V* vwarps = reinterpret_cast<V*>(warps);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ctas = job.ctas, H = j.heads;
   const auto add = [](auto a, auto b) { return a + b; };
   const auto most = [](int a, int b) { return a > b ? a : b; };
   grid_dependency_wait();
   grid_dependents_launch();
   // A start that falls counts as the largest before it: whatever they say, no
   // row belongs to two sequences.
+  const bool same = j.q_starts && j.q_starts == j.k_starts && j.seq_q == j.seq_k;
   int items = 0, q_tiles = 0, q_at = 0, k_at = 0;
   if (j.q_starts) q_at = plan_start(j.q_starts, j.sp_q_starts, 0, j.seq_q, p.status);
   if (j.k_starts) k_at = plan_start(j.k_starts, j.sp_k_starts, 0, j.seq_k, p.status);
   const int k_first = k_at;
-  auto range = [&](const int* starts, const MemSpan& sp, int b, bool there, int rows, int& at, int& lo, int& len) {
-    const int v = there ? plan_start(starts, sp, b + 1, rows, p.status) : 0;
+  auto range = [&](int v, bool there, int& at, int& lo, int& len) {
     int all;
     const int end = max(plan_scan<int>(v, most, iwarps, all), at);
+    ends[tid] = end;                              // the scan before has been read: there was a barrier since
     __syncthreads();
-    firsts[tid] = end;
-    __syncthreads();
-    lo = tid ? firsts[tid - 1] : at;
+    lo = tid ? ends[tid - 1] : at;
     len = there ? end - lo : 0;
     at = max(at, all);
   };
+  auto record = [&](int i, int q, int t, int4 seq, int blocks, int2 run) {
+    int4* at = out.items + 2LL * i;
+    if (i >= job.max_items || !in_span(at, 32, out.sp, p.status) || !in_span(out.runs + i, 8, out.sp, p.status)) return;
+    at[0] = seq;
+    at[1] = make_int4(t * j.rows, blocks, blocks + 1, tiles0[q]);
+    out.runs[i] = run;
+  };
+  // the last sequence of the chunk that begins at or before item i
+  auto sequence = [&](int i) {
+    int q = 0;
+#pragma unroll
+    for (int step = kPlanThreads / 2; step >= 1; step >>= 1)
+      if (firsts[q + step] <= i) q += step;
+    return q;
+  };
+  int costliest = 0;
   for (int base = 0; base < j.batch; base += kPlanThreads) {
     const int b = base + tid;
     const bool there = b < j.batch;
     int4 s = make_int4(0, 0, 0, 0);
+    const int vq = j.q_starts && there ? plan_start(j.q_starts, j.sp_q_starts, b + 1, j.seq_q, p.status) : 0;
+    const int vk = j.k_starts && there && !same ? plan_start(j.k_starts, j.sp_k_starts, b + 1, j.seq_k, p.status) : 0;
     if (j.q_starts) {
-      range(j.q_starts, j.sp_q_starts, b, there, j.seq_q, q_at, s.x, s.y);
+      range(vq, there, q_at, s.x, s.y);
     } else if (there) {
       s.x = b * j.seq_q;
       s.y = clamp_len(j.q_lens, b, j.seq_q, j.sp_q_lens, p.status);
     }
-    if (j.k_starts) {
-      range(j.k_starts, j.sp_k_starts, b, there, j.seq_k, k_at, s.z, s.w);
+    if (same) {
+      s.z = s.x;
+      s.w = s.y;
+      k_at = q_at;
+    } else if (j.k_starts) {
+      range(vk, there, k_at, s.z, s.w);
     } else if (there) {
       s.z = b * j.seq_k;
       s.w = clamp_len(j.k_lens, b, j.seq_k, j.sp_k_lens, p.status);
@@ -120,102 +148,119 @@ static __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __
     tiles0[tid] = q_tiles + static_cast<int>(upto >> 32) - static_cast<int>(nq);
     if (tid == kPlanThreads - 1) firsts[kPlanThreads] = items + static_cast<int>(all);
     if (there && out.seq_items && in_span(out.seq_items + b, 4, out.sp, p.status)) out.seq_items[b] = first;
+    const int from_item = items;
     items += static_cast<int>(all);
     q_tiles += static_cast<int>(all >> 32);
     __syncthreads();
-    // a warp per sequence
-    for (int i = warp; i < kPlanThreads && base + i < j.batch; i += kPlanThreads / 32) {
-      const int4 q = seqs[i];
-      const int from = firsts[i], count = firsts[i + 1] - from;
-      for (int t = lane; t < count; t += 32) {
-        int4* at = out.items + 2LL * (from + t);
-        const int blocks = plan_blocks(j, t, q.y, q.w);
-        if (from + t >= job.max_items || !in_span(at, 32, out.sp, p.status)) continue;
-        at[0] = q;
-        at[1] = make_int4(t * j.rows, blocks, blocks + 1, tiles0[i]);
-        if (from + t < kPlanNear) near[from + t] = blocks + 1;
+    for (int i = from_item + tid; i < items; i += kPlanThreads) {
+      const int q = sequence(i), t = i - firsts[q], blocks = plan_blocks(j, t, seqs[q].y, seqs[q].w);
+      costliest = max(costliest, blocks + 1);
+      if (kNear) {
+        if (i < kPlanNear) costs[i] = blocks + 1;
+      } else {
+        // without a causal mask a sequence's items cost the same
+        record(i, q, t, seqs[q], blocks, j.causal ? make_int2(i, 1) : make_int2(firsts[q], firsts[q + 1] - firsts[q]));
+        if (out.ranks && in_span(out.ranks + i, 4, out.sp, p.status)) out.ranks[i] = i;
       }
+    }
+    if (!kNear) __syncthreads();
+  }
+  if (kNear) {
+    // an item's place: how many cost more, or as much and come before it
+    if (items > kPlanNear) items = kPlanNear;     // the host has counted
+    if (tid < 4 && items + tid < kPlanNear) costs[items + tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < items; i += kPlanThreads) {
+      const int mine = costs[i];
+      int more = 0, equal = 0, before = 0;
+      for (int k = 0; k < items; k += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(costs + k);
+        more += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        const int e0 = o.x == mine, e1 = o.y == mine, e2 = o.z == mine, e3 = o.w == mine;
+        equal += e0 + e1 + e2 + e3;
+        before += (e0 & (k < i)) + (e1 & (k + 1 < i)) + (e2 & (k + 2 < i)) + (e3 & (k + 3 < i));
+      }
+      const int at = more + before, q = sequence(i);
+      line[at] = mine;
+      runs[at] = make_int2(more, equal);
+      record(at, q, i - firsts[q], seqs[q], mine - 1, make_int2(more, equal));
+      if (out.ranks && in_span(out.ranks + i, 4, out.sp, p.status)) out.ranks[i] = at;
     }
     __syncthreads();
   }
-  // where each item's units begin, and the costliest
-  auto unit_of = [&](int i) -> int { return in_span(out.items + 2LL * i, 32, out.sp, p.status) ? out.items[2LL * i + 1].z : 0; };
-  long long units = 0;
-  int costliest = 0;
+  // where each item's units begin
+  V units = 0;
   for (int base = 0; base < items; base += kPlanThreads) {
     const int i = base + tid;
-    const int u = i >= items ? 0 : i < kPlanNear ? static_cast<int>(near[i]) : unit_of(i);
-    long long all;
-    const long long upto = units + plan_scan<long long>(u, add, warps, all);   // everybody has read their `near`
+    V u = 0, all;
+    if (i < items) {
+      if (kNear) u = line[i];
+      else if (in_span(out.items + 2LL * i, 32, out.sp, p.status)) u = out.items[2LL * i + 1].z;
+    }
+    const V upto = units + plan_scan<V>(u, add, vwarps, all);   // everybody has read their `line`
     units += all;
-    costliest = max(costliest, u);
-    if (i < items && i < kPlanNear) near[i] = upto - u;
-    if (i < items && items > kPlanNear && in_span(out.prefix + i, 8, out.sp, p.status)) out.prefix[i] = upto - u;
+    if (i < items) {
+      if (kNear) line[i] = upto - u;
+      else if (in_span(out.prefix + i, 8, out.sp, p.status)) out.prefix[i] = upto - u;
+    }
   }
   if (tid == 0) {
-    if (items <= kPlanNear) near[items] = units;
+    if (kNear) line[items] = units;
     else if (in_span(out.prefix + items, 8, out.sp, p.status)) out.prefix[items] = units;
   }
-  int top;
-  plan_scan<int>(costliest, most, iwarps, top);
+  costliest = __reduce_max_sync(0xffffffffu, costliest);
   __syncthreads();
-  auto before = [&](int i) -> long long { return items <= kPlanNear ? near[i] : out.prefix[i]; };
-  // The waves: CTA c takes tile s * ctas + c, every other wave the other way
-  // round, as long as nobody has more than an equal share of the whole.
-  const long long work = units * j.heads, tiles = static_cast<long long>(items) * j.heads;
-  long long active = work / job.least;
-  if (active > job.ctas) active = job.ctas;
+  if (lane == 0) iwarps[warp] = costliest;
+  __syncthreads();
+  costliest = __reduce_max_sync(0xffffffffu, lane < kPlanThreads / 32 ? iwarps[lane] : 0);
+  auto before = [&](int i) -> V { return kNear ? line[kNear ? i : 0] : static_cast<V>(out.prefix[i]); };
+  auto run_of = [&](int i) { return kNear ? runs[kNear ? i : 0] : out.runs[i]; };
+  const V work = units * H, tiles = static_cast<V>(items) * H;
+  V active = work / job.least;
+  if (active > ctas) active = ctas;
   if (active < 1) active = 1;
   const int c = tid;
-  long long mine = 0, share = 0;                  // what the waves give CTA c; its share of the whole
+  V mine = 0, share = 0;                          // what the waves give CTA c; its share of the whole
+  const V each = work / active, over = work % active;
+  if (c < active) share = each + (over * (c + 1) / active - over * c / active);
   int waves = 0;
-  if (c < active) share = work / active * (c + 1) + work % active * (c + 1) / active - (work / active * c + work % active * c / active);
-  if (active == job.ctas && c < job.ctas) {
-    for (waves = 0; (waves + 1LL) * job.ctas <= tiles; ++waves) {
-      const long long tile = static_cast<long long>(waves) * job.ctas + (waves & 1 ? job.ctas - 1 - c : c);
-      const int e = static_cast<int>(tile % items);
-      mine += before(e + 1) - before(e);
-      if (mine > share) break;
+  const bool whole = costliest <= job.whole;
+  if (whole) {
+    waves = static_cast<int>((tiles + ctas - 1) / ctas);
+  } else if (active == ctas) {
+    for (; (waves + 1LL) * ctas <= tiles; ++waves) {
+      const V tile = static_cast<V>(waves) * ctas + (waves & 1 ? ctas - 1 - c : c);
+      const int i = static_cast<int>(tile / H);
+      const V next = c < ctas ? mine + before(i + 1) - before(i) : 0;
+      if (__syncthreads_or(next > share)) break;
+      mine = next;
     }
-  } else {
-    waves = active == job.ctas ? 0x7fffffff : 0;  // no CTA: no say
   }
-  {
-    int least;
-    plan_scan<int>(waves, [](int a, int b) { return a < b ? a : b; }, iwarps, least);
-    waves = least;
-  }
-  mine = 0;
-  if (c < job.ctas)
-    for (int s = 0; s < waves; ++s) {
-      const int e = static_cast<int>((static_cast<long long>(s) * job.ctas + (s & 1 ? job.ctas - 1 - c : c)) % items);
-      mine += before(e + 1) - before(e);
-    }
   // Behind them: CTA c's share begins where those before it end.
-  long long all;
-  const long long rest = c < active ? share - mine : 0, upto = plan_scan<long long>(rest, add, warps, all);
-  if (c <= job.ctas) {
-    int2 at = make_int2(j.heads * items, 0);
-    if (c < active && units > 0) {
-      const long long tile0 = static_cast<long long>(waves) * job.ctas, h0 = tile0 / items;
-      const long long x = h0 * units + before(static_cast<int>(tile0 - h0 * items)) + upto - rest;
-      const int h = static_cast<int>(x / units);
-      const long long off = x - h * units;
-      if (h < j.heads) {
-        int lo = 0, hi = items - 1;               // the last item that begins at or before `off`
+  V all;
+  const V rest = c < active ? share - mine : 0, upto = plan_scan<V>(rest, add, vwarps, all);
+  if (c <= ctas) {
+    int2 at = make_int2(static_cast<int>(tiles), 0);
+    const V tile0 = static_cast<V>(waves) * ctas;
+    if (c < active && !whole && tile0 < tiles) {
+      const int i0 = static_cast<int>(tile0 / H), first0 = run_of(i0).x;
+      const V x = before(first0) * H + (tile0 - static_cast<V>(first0) * H) * (before(i0 + 1) - before(i0)) + upto - rest;
+      if (x < work) {
+        int lo = 0, hi = items - 1;               // the last item whose run's units are at or before x
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (before(mid) <= off) lo = mid;
+          if (before(mid) * H <= x) lo = mid;
           else hi = mid - 1;
         }
-        int o = static_cast<int>(off - before(lo));
-        const int u = static_cast<int>(before(lo + 1) - before(lo));
-        // no cut where it saves little: within two blocks of an end, or at all
-        if (top <= job.whole || o < 2 || u - o < 3) {
-          lo += 2 * o >= u;
+        const int first = run_of(lo).x, u = static_cast<int>(before(lo + 1) - before(lo));
+        const V off = x - before(first) * H;
+        int tile = first * H + static_cast<int>(off / u), o = static_cast<int>(off % u);
+        // no cut where it saves little: within two blocks of an end
+        if (o < 2 || u - o < 3) {
+          tile += 2 * o >= u;
           o = 0;
         }
-        at = make_int2(h * items + lo, o);
+        at = make_int2(tile, o);
       }
     }
     if (in_span(out.spans + c, 8, out.sp, p.status)) out.spans[c] = at;
@@ -232,10 +277,13 @@ struct PlanParts {
   __device__ __forceinline__ int slot(int i) const { return i == 0 ? 2 * c + 1 : 2 * (c + i); }
 };
 
-// A whole warp: how the shares cut tile `tile`.
+// A whole warp: how the shares cut tile `tile`.  (MOST: CTAs at most.)
+constexpr int kPlanMostCtas = 159;
 __device__ __forceinline__ PlanParts plan_parts(const AttnPlan& plan, int ctas, int tile, int lane, int* status) {
   int before = 0, cuts = 0;
-  for (int c = lane; c - lane <= ctas; c += 32) {
+#pragma unroll
+  for (int i = 0; i <= kPlanMostCtas / 32; ++i) {
+    const int c = 32 * i + lane;
     int2 at = make_int2(0x7fffffff, 0);
     if (c <= ctas && in_span(plan.spans + c, 8, plan.sp, status)) at = plan.spans[c];
     before += __popc(__ballot_sync(0xffffffffu, at.x < tile || (at.x == tile && at.y == 0)));
@@ -251,11 +299,19 @@ __device__ __forceinline__ int plan_cut_tile(const AttnPlan& plan, int c, int* s
   return at.y > 0 && (prev.x != at.x || prev.y == 0) ? at.x : -1;
 }
 
+// Partial results: rows of D sums and their (maximum, sum).
+struct PartsView {
+  const float* part;
+  const float* stats;
+  MemSpan sp_part, sp_stats;
+};
+
 // CTAs that share a cut tile's rows.
 __host__ __device__ constexpr int plan_join_ctas(bool few) { return few ? 1 : 8; }
 
 // o = sum_i w_i o_i / sum_i w_i l_i over the parts of one row, w_i =
-// exp2((m_i - max m) scale): first all maxima, then the sums.
+// exp2((m_i - max m) scale), a warp per row.  32 parts' maxima and sums come at
+// a time, a lane's each; `place(i, side)` is part i's row among `side`'s slots.
 template <int D>
 struct RowJoin {
   float m = -INFINITY, total = 0.0f;
@@ -264,20 +320,39 @@ struct RowJoin {
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) acc[e] = make_float2(0.0f, 0.0f);
   }
-  template <typename P>
-  __device__ __forceinline__ void top(const P& p, long long k) {
-    if (in_span(p.stats + 2 * k, 8, p.sp_stats, p.status)) m = fmaxf(m, p.stats[2 * k]);
-  }
-  template <typename P>
-  __device__ __forceinline__ void add(const P& p, long long k, int lane) {
-    if (!in_span(p.stats + 2 * k, 8, p.sp_stats, p.status) || !in_span(p.part + k * D, 4 * D, p.sp_part, p.status)) return;
-    const float2 st = *reinterpret_cast<const float2*>(p.stats + 2 * k);
-    // a part that saw no key has sum 0, maximum -inf and zeros
-    const float w = st.x == m ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(st.x, m), p.scale_log2));
-    total = __fmaf_rn(w, st.y, total);
-    const float2* src = reinterpret_cast<const float2*>(p.part + k * D) + lane;
+  template <typename F>
+  __device__ __forceinline__ void add(int n, int lane, float scale_log2, int* status, F place) {
+    for (int base = 0; base < n; base += 32) {
+      const PartsView* side = nullptr;
+      long long k = 0;
+      float2 st = make_float2(-INFINITY, 0.0f);
+      if (base + lane < n) {
+        k = place(base + lane, side);
+        if (in_span(side->stats + 2 * k, 8, side->sp_stats, status)) st = *reinterpret_cast<const float2*>(side->stats + 2 * k);
+      }
+      const float top = fmaxf(m, warp_max(st.x));
+      // a part that saw no key has sum 0, maximum -inf and zeros
+      const float w = st.x == top ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(st.x, top), scale_log2));
+      const float old = m == top ? 1.0f : exp2_approx(__fmul_rn(__fsub_rn(m, top), scale_log2));
+      m = top;
+      float l = __fmul_rn(w, st.y);
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) acc[e] = __ffma2_rn(make_float2(w, w), src[32 * e], acc[e]);
+      for (int off = 16; off >= 1; off >>= 1) l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, off));
+      total = __fmaf_rn(total, old, l);
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) acc[e] = __fmul2_rn(acc[e], make_float2(old, old));
+      const int count = n - base < 32 ? n - base : 32;
+#pragma unroll 8
+      for (int i = 0; i < count; ++i) {
+        const PartsView* from = nullptr;
+        const long long at = place(base + i, from);
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        if (!in_span(from->part + at * D, 4 * D, from->sp_part, status)) continue;
+        const float2* src = reinterpret_cast<const float2*>(from->part + at * D) + lane;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) acc[e] = __ffma2_rn(make_float2(f, f), src[32 * e], acc[e]);
+      }
+    }
   }
   // a warp's row of o and its lse
   template <typename T, typename P>
@@ -303,18 +378,20 @@ __global__ void __launch_bounds__(256) plan_join_forward_kernel(const __grid_con
   const int tile = plan_cut_tile(p.plan, c, p.status);
   if (tile < 0) return;
   const PlanParts parts = plan_parts(p.plan, ctas, tile, lane, p.status);
-  const int n = p.plan.head->x, head = tile / n;
-  const int4 s = p.plan.items[2LL * (tile - head * n)], w = p.plan.items[2LL * (tile - head * n) + 1];
+  const int2 at = plan_tile(p.plan, p.seqs.heads, tile);
+  const int head = at.x;
+  const PartsView view{p.part, p.stats, p.sp_part, p.sp_stats};
+  const int4 s = p.plan.items[2LL * at.y], w = p.plan.items[2LL * at.y + 1];
   for (int r = (static_cast<int>(blockIdx.x) % N) * 8 + warp; r < rows; r += 8 * N) {
     const int x = w.x + r;
     if (x >= (FEW ? s.y * p.group : s.y)) return;
     const int h = FEW ? head * p.group + x / s.y : head;
     const long long row = s.x + (FEW ? x % s.y : x);
     RowJoin<D> j;
-#pragma unroll 4
-    for (int i = 0; i <= parts.cuts; ++i) j.top(p, static_cast<long long>(parts.slot(i)) * rows + r);
-#pragma unroll 4
-    for (int i = 0; i <= parts.cuts; ++i) j.add(p, static_cast<long long>(parts.slot(i)) * rows + r, lane);
+    j.add(parts.cuts + 1, lane, p.scale_log2, p.status, [&](int i, const PartsView*& side) {
+      side = &view;
+      return static_cast<long long>(parts.slot(i)) * rows + r;
+    });
     j.template write<T>(p, p.o + row * p.o_stride + h * (D * 2), p.lse + static_cast<long long>(h) * p.seq_q + row, lane);
   }
 }
@@ -329,8 +406,9 @@ __global__ void __launch_bounds__(256) plan_join_grad_kernel(const __grid_consta
   const int tile = plan_cut_tile(p.plan, c, p.status);
   if (tile < 0) return;
   const PlanParts parts = plan_parts(p.plan, ctas, tile, lane, p.status);
-  const int n = p.plan.head->x, h = tile / n;
-  const int4 s = p.plan.items[2LL * (tile - h * n)], w = p.plan.items[2LL * (tile - h * n) + 1];
+  const int2 at = plan_tile(p.plan, p.seqs.heads, tile);
+  const int h = at.x;
+  const int4 s = p.plan.items[2LL * at.y], w = p.plan.items[2LL * at.y + 1];
   for (int r = (static_cast<int>(blockIdx.x) % N) * 8 + warp; r < kRows; r += 8 * N) {
     const int x = w.x + r % kTile;
     if (x >= (KV ? s.w : s.y)) continue;
@@ -359,15 +437,11 @@ __global__ void __launch_bounds__(256) plan_join_grad_kernel(const __grid_consta
 // Attention beside a shared prefix: the results of one pass, all in slots.
 struct PrefixSide {
   AttnPlan plan;
-  const float* part;
-  const float* stats;
+  PartsView parts;
   int few;                    // tiles of a key head's group * q_len rows, else of one head's queries
   int rows, slot_rows;        // of a tile, of a slot
-  int ctas;
+  int ctas, heads;            // lines of tiles
   int there;                  // the pass was made
-  float scale_log2;
-  int* status;
-  MemSpan sp_part, sp_stats;
 };
 
 struct PrefixJoinParams {
@@ -377,7 +451,7 @@ struct PrefixJoinParams {
   long long o_stride;
   const int* q_lens;
   int batch, seq_q, heads_q, group;
-  float scale;
+  float scale, scale_log2;
   int* status;
   MemSpan sp_o, sp_lse, sp_q_lens;
 };
@@ -395,8 +469,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   const int q_len = clamp_len(p.q_lens, b, p.seq_q, p.sp_q_lens, p.status);
   RowJoin<D> j;
   if (i < q_len) {
-    int r[2], tile[2];
-    PlanParts parts[2];
+    int r[2] = {0, 0}, tile[2] = {0, 0}, n[2] = {0, 0};
+    PlanParts parts[2] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const PrefixSide& s = p.side[k];
@@ -405,25 +479,23 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
       const int at = k == 0 ? row : i, rows = k == 0 ? p.batch * p.seq_q : q_len;
       int first = 0;
       if (k == 1 && in_span(s.plan.seq_items + b, 4, s.plan.sp, p.status)) first = s.plan.seq_items[b];
-      const int x = s.few ? hh * rows + at : at, of = s.rows;
-      tile[k] = (s.few ? hk : h) * s.plan.head->x + first + x / of;
-      r[k] = x % of;
+      const int x = s.few ? hh * rows + at : at, e = first + x / s.rows;
+      // the tile's place in the line
+      const int i = in_span(s.plan.ranks + e, 4, s.plan.sp, p.status) ? s.plan.ranks[e] : 0;
+      const int2 run = in_span(s.plan.runs + i, 8, s.plan.sp, p.status) ? s.plan.runs[i] : make_int2(i, 1);
+      tile[k] = run.x * s.heads + (s.few ? hk : h) * run.y + i - run.x;
+      r[k] = x % s.rows;
       parts[k] = plan_parts(s.plan, s.ctas, tile[k], lane, p.status);
+      n[k] = parts[k].cuts + 1;
     }
-    auto each = [&](auto f) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const PrefixSide& s = p.side[k];
-        if (!s.there) continue;
-#pragma unroll 4
-        for (int c = 0; c <= parts[k].cuts; ++c) {
-          const int slot = parts[k].cuts ? parts[k].slot(c) : 2 * s.ctas + tile[k];
-          f(s, static_cast<long long>(slot) * s.slot_rows + r[k]);
-        }
-      }
-    };
-    each([&](const PrefixSide& s, long long k) { j.top(s, k); });
-    each([&](const PrefixSide& s, long long k) { j.add(s, k, lane); });
+    j.add(n[0] + n[1], lane, p.scale_log2, p.status, [&](int c, const PartsView*& side) {
+      const int k = c >= n[0];
+      const int cut = k ? c - n[0] : c;
+      side = &p.side[k].parts;
+      const PlanParts& of = parts[k];
+      const int slot = of.cuts ? of.slot(cut) : 2 * p.side[k].ctas + tile[k];
+      return static_cast<long long>(slot) * p.side[k].slot_rows + r[k];
+    });
   }
   j.template write<T>(p, p.o + static_cast<long long>(row) * p.o_stride + h * (D * 2),
                       p.lse + (static_cast<long long>(b) * p.heads_q + h) * p.seq_q + i, lane);

@@ -35,6 +35,8 @@ qknr::AttnPlan take_plan(Space* ws, long long items, long long batch, bool seq_i
   p.head = ws->take<int4>(1);
   p.spans = ws->take<int2>(kCtas + 1);
   p.items = ws->take<int4>(2 * items);
+  p.runs = ws->take<int2>(items);
+  p.ranks = seq_items ? ws->take<int>(items) : nullptr;
   p.prefix = ws->take<long long>(items + 1);
   p.seq_items = seq_items ? ws->take<int>(batch) : nullptr;
   p.sp = msp(span_of(lo, 1, 0, static_cast<long long>(ws->used - from)));
@@ -114,10 +116,17 @@ Kernels kernels_for(const qknr_attn_args* a) {
   return a->head_dim == 64 ? kernels<__half, 64>() : kernels<__half, 128>();
 }
 
-qknr_status launch_plan(const qknr::AttnPlanParams& pp, int jobs, const qknr_attn_args* a, qknr_stream_t stream) {
+qknr_status launch_plan(const qknr::AttnPlanParams& pp, const Job* of, int jobs, const qknr_attn_args* a, qknr_stream_t stream) {
+  static_assert(kCtas <= qknr::kPlanMostCtas && kCtas < qknr::kPlanThreads, "a thread per share");
   qknr::AttnPlanParams copy = pp;
   void* kargs[] = {&copy};
-  return qknr_host::launch_kernel(reinterpret_cast<const void*>(qknr::attn_plan_kernel), jobs, qknr::kPlanThreads, 0,
+  bool narrow = true;
+  for (int i = 0; i < jobs; ++i)
+    narrow = narrow && pp.job[i].max_items <= qknr::kPlanNear && pp.job[i].seqs.batch <= qknr::kPlanThreads &&
+             static_cast<double>(pp.job[i].max_items) * static_cast<double>(of[i].units) * pp.job[i].seqs.heads < 2e9;
+  const void* fn = narrow ? reinterpret_cast<const void*>(qknr::attn_plan_kernel<int>)
+                          : reinterpret_cast<const void*>(qknr::attn_plan_kernel<long long>);
+  return qknr_host::launch_kernel(fn, jobs, qknr::kPlanThreads, 0,
                                   reinterpret_cast<cudaStream_t>(stream), kargs, !(a->flags & QKNR_FLAG_NO_OVERLAP),
                                   "cudaLaunchKernelExC(attention plan)");
 }
@@ -222,6 +231,13 @@ void pack_sequences(const qknr_pack_args* p, qknr::AttnSeqs* j) {
   j->sp_k_starts = msp(span_of(j->k_starts, p->batch + 1LL, 4, 4));
 }
 
+// Whether every CTA can work its tiles out: few sequences, whose tiles go out
+// whole and are too few to be worth an order (5 x 77 tokens of 16 heads: 8 us
+// against 18 with a plan).
+bool table_does(const Job& j, long long batch) {
+  return !j.cuts && batch <= qknr::kTableSeqs && j.heads * j.items <= 2 * kCtas;
+}
+
 // What both passes put where.
 struct PackSpace {
   Job job[2];
@@ -234,7 +250,7 @@ constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k);
-  s->job[0].table = !s->job[0].cuts && p->batch <= qknr::kTableSeqs;
+  s->job[0].table = table_does(s->job[0], p->batch);
   if (!s->job[0].table) s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
 }
@@ -244,7 +260,7 @@ void pack_backward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space
   s->job[0] = job_of(a, qknr::kPlanQueries, qknr::kTile, a->n_heads_q, p->rows_q, p->batch, blocks_of(p->rows_k) + 1, qknr::kTile);
   s->job[1] = job_of(a, qknr::kPlanKeys, qknr::kTile, a->n_heads_k, p->rows_k, p->batch, blocks_of(p->rows_q) * group + 1,
                      2 * qknr::kTile);
-  const bool table = !s->job[0].cuts && !s->job[1].cuts && p->batch <= qknr::kTableSeqs;
+  const bool table = table_does(s->job[0], p->batch) && table_does(s->job[1], p->batch);
   for (int i = 0; i < 2; ++i) {
     s->job[i].table = table;
     if (!table) s->plan[i] = take_plan(ws, s->job[i].items, p->batch, false);
@@ -363,7 +379,7 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
     j.keep = true;
     if (!is_few(j) && (i ? a->seq_q : j.kind == qknr::kPlanFew ? group * rows : rows) <= qknr::kTile) j.slot_rows = qknr::kTile;
     if ((i ? a->seq_k : p->prefix) == 0) j.keep = j.cuts = false;   // the pass is not made
-    s->plan[i] = take_plan(ws, j.items, a->batch, i == 1);
+    s->plan[i] = take_plan(ws, j.items, a->batch, true);
     take_parts(ws, a, j, true, &kp[i]);
   }
 }
@@ -469,7 +485,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, &a, p->v, v.stride, p->rows_k, p->n_heads_k, box)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(&a);
-  if (!kp.table && (st = launch_plan(pp, 1, &a, stream)) != QKNR_OK) return st;
+  if (!kp.table && (st = launch_plan(pp, s.job, 1, &a, stream)) != QKNR_OK) return st;
   if ((st = launch_forward(&a, s.job[0], fn, &kp, dev, di, stream)) != QKNR_OK) return st;
   return launch_join(a_few ? fn.join_few : fn.join_fwd, s.job[0], &a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
 }
@@ -553,7 +569,7 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
   }
   const Kernels fn = kernels_for(&a);
   kp.table = s.job[0].table;
-  if (!kp.table && (st = launch_plan(pp, 2, &a, stream)) != QKNR_OK) return st;
+  if (!kp.table && (st = launch_plan(pp, s.job, 2, &a, stream)) != QKNR_OK) return st;
   auto use = [&](int i) {
     kp.plan = s.plan[i];
     kp.seqs = pp.job[i].seqs;
@@ -718,17 +734,13 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     }
     qknr::PrefixSide& js = jp.side[i];
     js.plan = s.plan[i];
-    js.part = w.part;
-    js.stats = w.stats;
+    js.parts = qknr::PartsView{w.part, w.stats, w.sp_part, w.sp_stats};
     js.few = j.kind == qknr::kPlanFew;
     js.rows = j.rows;
     js.slot_rows = j.slot_rows;
     js.ctas = kCtas;
+    js.heads = j.heads;
     js.there = side.seq_k > 0;
-    js.scale_log2 = kp.scale_log2;
-    js.status = p->dev_status;
-    js.sp_part = w.sp_part;
-    js.sp_stats = w.sp_stats;
   }
   jp.o = kp.o;
   jp.lse = kp.lse;
@@ -739,11 +751,12 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
   jp.heads_q = p->n_heads_q;
   jp.group = kp.group;
   jp.scale = kp.scale;
+  jp.scale_log2 = kp.scale_log2;
   jp.status = p->dev_status;
   jp.sp_o = kp.sp_o;
   jp.sp_lse = kp.sp_lse;
   jp.sp_q_lens = kp.sp_q_lens;
-  if ((st = launch_plan(pp, 2, &a, stream)) != QKNR_OK) return st;
+  if ((st = launch_plan(pp, s.job, 2, &a, stream)) != QKNR_OK) return st;
   for (int i = 0; i < 2; ++i)
     if (sides[i].seq_k > 0 && (st = launch_forward(&a, s.job[i], fn, &pass[i], dev, di, stream)) != QKNR_OK) return st;
   const long long items = static_cast<long long>(p->batch) * p->seq_q * p->n_heads_q;

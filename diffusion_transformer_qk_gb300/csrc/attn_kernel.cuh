@@ -43,6 +43,7 @@ enum { kPlanQueries, kPlanKeys, kPlanFew };       // a tile's rows: a head's que
 struct AttnSeqs {
   int kind;
   int rows;                   // rows of a tile
+  int over;                   // units of a tile beside its blocks, one each
   int heads, group, causal;   // heads: lines of tiles
   int batch, seq_q, seq_k;    // sequence b: rows b * seq .. of lens[b] (null: seq) rows,
   const int* q_lens;
@@ -454,7 +455,7 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     w.t0 = t * p.seqs.rows;
     w.blocks = plan_blocks(p.seqs, t, q.y, q.w);
     w.tiles0 = table.q_tiles[b];
-    w.u1 = w.blocks + 1;
+    w.u1 = w.blocks + p.seqs.over;
     return w.u0 == 0;
   }
   if (!in_span(p.plan.spans + c, 16, p.plan.sp, p.status)) return false;
@@ -482,7 +483,7 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
   w.tiles0 = x.w;
   w.u1 = u1 ? u1 : x.z;
   w.slot = w.u0 > 0 ? 2 * c : w.u1 < x.z ? 2 * c + 1 : p.keep ? 2 * ctas + tile : -1;
-  return w.u0 < w.u1;
+  return w.u0 <= w.u1;        // a share of nothing inside a tile: an empty part, which the join counts too
 }
 
 // The tile's place.  Without a causal mask the tiles of a head follow each

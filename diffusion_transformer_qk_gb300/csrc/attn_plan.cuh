@@ -2,7 +2,7 @@
 // (packed sequences; samples with lengths beside a shared prefix), for sm_103a.
 //
 // A head's tiles, of all sequences, are its items; an item's cost is its blocks
-// (the iterations of its contraction) and one unit for its epilogue.  The
+// (the iterations of its contraction) and some units for its beginning and end.  The
 // call's tiles form a line: the costliest items first, those of one cost
 // together, head by head.  CTAs take the line's tiles in waves, every other wave
 // the other way round, so that neighbours read the same keys at the same time
@@ -25,6 +25,7 @@ struct AttnPlanJob {
   AttnSeqs seqs;
   int ctas;
   int whole;                  // tiles are not cut if none costs more than this
+  int cut;                    // units that cutting some costs
   int least;                  // units of a share at least
   int max_items;
   AttnPlan plan;
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     int4* at = out.items + 2LL * i;
     if (i >= job.max_items || !in_span(at, 32, out.sp, p.status) || !in_span(out.runs + i, 8, out.sp, p.status)) return;
     at[0] = seq;
-    at[1] = make_int4(t * j.rows, blocks, blocks + 1, tiles0[q]);
+    at[1] = make_int4(t * j.rows, blocks, blocks + j.over, tiles0[q]);
     out.runs[i] = run;
   };
   // the last sequence of the chunk that begins at or before item i
@@ -154,9 +155,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     __syncthreads();
     for (int i = from_item + tid; i < items; i += kPlanThreads) {
       const int q = sequence(i), t = i - firsts[q], blocks = plan_blocks(j, t, seqs[q].y, seqs[q].w);
-      costliest = max(costliest, blocks + 1);
+      costliest = max(costliest, blocks + j.over);
       if (kNear) {
-        if (i < kPlanNear) costs[i] = blocks + 1;
+        if (i < kPlanNear) costs[i] = blocks + j.over;
       } else {
         // without a causal mask a sequence's items cost the same
         record(i, q, t, seqs[q], blocks, j.causal ? make_int2(i, 1) : make_int2(firsts[q], firsts[q + 1] - firsts[q]));
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       const int at = more + before, q = sequence(i);
       line[at] = mine;
       runs[at] = make_int2(more, equal);
-      record(at, q, i - firsts[q], seqs[q], mine - 1, make_int2(more, equal));
+      record(at, q, i - firsts[q], seqs[q], mine - j.over, make_int2(more, equal));
       if (out.ranks && in_span(out.ranks + i, 4, out.sp, p.status)) out.ranks[i] = at;
     }
     __syncthreads();
@@ -223,17 +224,35 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   V mine = 0, share = 0;                          // what the waves give CTA c; its share of the whole
   const V each = work / active, over = work % active;
   if (c < active) share = each + (over * (c + 1) / active - over * c / active);
-  int waves = 0;
-  const bool whole = costliest <= job.whole;
-  if (whole) {
-    waves = static_cast<int>((tiles + ctas - 1) / ctas);
-  } else if (active == ctas) {
-    for (; (waves + 1LL) * ctas <= tiles; ++waves) {
-      const V tile = static_cast<V>(waves) * ctas + (waves & 1 ? ctas - 1 - c : c);
-      const int i = static_cast<int>(tile / H);
-      const V next = c < ctas ? mine + before(i + 1) - before(i) : 0;
-      if (__syncthreads_or(next > share)) break;
-      mine = next;
+  // all in waves where that makes nobody later than the cuts would
+  const int last = static_cast<int>((tiles + ctas - 1) / ctas);
+  auto cost = [&](V tile) -> V { return before(static_cast<int>(tile / H) + 1) - before(static_cast<int>(tile / H)); };
+  bool whole = costliest <= job.whole;
+  int waves = whole ? last : 0;
+  if (!whole && active == ctas) {
+    V total = 0, last_but_one = 0;
+    bool even = true;                             // nobody has more than its share
+    int s = 0;
+    for (; s < last; ++s) {
+      const V tile = static_cast<V>(s) * ctas + (s & 1 ? ctas - 1 - c : c);
+      if (c < ctas && tile < tiles) total += cost(tile);
+      if (__syncthreads_or(c < ctas && total > share + job.cut)) break;
+      even = !__syncthreads_or(c < ctas && total > share) && even && (s + 1LL) * ctas <= tiles;
+      if (even) {
+        last_but_one = mine;
+        mine = total;
+        waves = s + 1;
+      }
+    }
+    whole = s == last;
+    if (whole) waves = last;
+    // what is left: no tile in more than three or so parts
+    V left;
+    plan_scan<V>(c < ctas ? share - mine : 0, add, vwarps, left);
+    const V tile0 = static_cast<V>(waves) * ctas;
+    if (!whole && waves > 0 && tile0 < tiles && left * 3 < cost(tile0) * ctas) {
+      mine = last_but_one;
+      --waves;
     }
   }
   // Behind them: CTA c's share begins where those before it end.
@@ -256,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         const V off = x - before(first) * H;
         int tile = first * H + static_cast<int>(off / u), o = static_cast<int>(off % u);
         // no cut where it saves little: within two blocks of an end
-        if (o < 2 || u - o < 3) {
+        if (o < 2 || u - o < j.over + 2) {
           tile += 2 * o >= u;
           o = 0;
         }

@@ -43,14 +43,14 @@ qknr::AttnPlan take_plan(Space* ws, long long items, long long batch, bool seq_i
   return p;
 }
 
-constexpr int kLeastUnits = 3;                    // of a share
-constexpr int kLeastFew = 2;
+constexpr int kLeastUnits = 6;                    // of a share
+constexpr int kLeastFew = 4;
 
 // One kind of tile of a call.
 struct Job {
   int kind, rows, heads;
   long long items;            // at most
-  long long units;            // of the costliest item, at most
+  long long units;            // of the costliest item, at most (job_of: its blocks)
   int slot_rows;              // fp32 rows of a partial result
   bool cuts;                  // some tile may be cut
   bool keep = false;
@@ -63,12 +63,16 @@ bool is_few(const Job& j) { return j.kind == qknr::kPlanFew && j.rows <= qknr::k
 // What a cut costs: partial results and the kernel that joins them, about six
 // blocks' time at head_dim 128 and twelve at 64, so that tiles of twice as
 // many go out whole (a share is then off by one tile at most).
-int whole_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 3 : a->head_dim == 128 ? 12 : 24; }
+int whole_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 5 : a->head_dim == 128 ? 12 : 24; }
+
+// What a tile costs beside its blocks, in blocks: its queries' way, the epilogue.
+int over_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 3 : a->head_dim == 128 ? 2 : 3; }
 
 Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_rows, long long batch, long long units,
            int slot_rows) {
   Job j{kind, rows, heads, max_items(of_rows, batch, rows), units, slot_rows, false};
-  j.cuts = units > whole_units(a, j);
+  j.units += over_units(a, j);
+  j.cuts = j.units > whole_units(a, j);
   return j;
 }
 
@@ -81,9 +85,9 @@ Job forward_job(const qknr_attn_args* a, long long rows, long long batch, int ke
   if (may_few && few(rows, batch)) {
     const long long group = a->n_heads_q / a->n_heads_k;
     const int tile = group * rows <= 8 * batch ? 8 : 16;
-    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys) + 1, tile);
+    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys), tile);
   }
-  return job_of(a, qknr::kPlanQueries, qknr::fwd::kRows, a->n_heads_q, rows, batch, blocks_of(keys) + 1, qknr::fwd::kRows);
+  return job_of(a, qknr::kPlanQueries, qknr::fwd::kRows, a->n_heads_q, rows, batch, blocks_of(keys), qknr::fwd::kRows);
 }
 
 struct Kernels {
@@ -138,7 +142,9 @@ void fill_job(const qknr_attn_args* a, const Job& j, const qknr::AttnPlan& plan,
   out->seqs.group = a->n_heads_q / a->n_heads_k;
   out->seqs.causal = a->causal != 0;
   out->ctas = kCtas;
+  out->seqs.over = over_units(a, j);
   out->whole = whole_units(a, j);
+  out->cut = whole_units(a, j) / 2;
   out->least = is_few(j) ? kLeastFew : kLeastUnits;
   out->max_items = static_cast<int>(j.items);
   out->plan = plan;
@@ -257,8 +263,8 @@ void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space*
 
 void pack_backward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams kp[2]) {
   const int group = a->n_heads_q / a->n_heads_k;
-  s->job[0] = job_of(a, qknr::kPlanQueries, qknr::kTile, a->n_heads_q, p->rows_q, p->batch, blocks_of(p->rows_k) + 1, qknr::kTile);
-  s->job[1] = job_of(a, qknr::kPlanKeys, qknr::kTile, a->n_heads_k, p->rows_k, p->batch, blocks_of(p->rows_q) * group + 1,
+  s->job[0] = job_of(a, qknr::kPlanQueries, qknr::kTile, a->n_heads_q, p->rows_q, p->batch, blocks_of(p->rows_k), qknr::kTile);
+  s->job[1] = job_of(a, qknr::kPlanKeys, qknr::kTile, a->n_heads_k, p->rows_k, p->batch, blocks_of(p->rows_q) * group,
                      2 * qknr::kTile);
   const bool table = table_does(s->job[0], p->batch) && table_does(s->job[1], p->batch);
   for (int i = 0; i < 2; ++i) {
@@ -372,7 +378,7 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
   // the heads of a group in one tile where that leaves fewer rows of a tile empty
   const long long group = a->n_heads_q / a->n_heads_k;
   if (s->job[0].kind == qknr::kPlanQueries && halves(group * rows) < group * halves(rows))
-    s->job[0] = job_of(a, qknr::kPlanFew, qknr::fwd::kRows, a->n_heads_k, group * rows, 1, blocks_of(p->prefix) + 1, qknr::fwd::kRows);
+    s->job[0] = job_of(a, qknr::kPlanFew, qknr::fwd::kRows, a->n_heads_k, group * rows, 1, blocks_of(p->prefix), qknr::fwd::kRows);
   s->job[1] = forward_job(a, rows, a->batch, a->seq_k);
   for (int i = 0; i < 2; ++i) {
     Job& j = s->job[i];

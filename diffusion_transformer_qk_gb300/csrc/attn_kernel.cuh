@@ -266,15 +266,20 @@ struct AttnCta {
   }
   // PLANNED, forward and dq: the consumers' side of the pieces.  One thread or
   // (whole) a warp; false at the end, and where the wait ran out (`lost`).
-  __device__ __forceinline__ bool piece(int full, const AttnPieces& pieces, int s, bool whole, int4 (&v)[3], bool& lost) const {
+  __device__ __forceinline__ bool piece(int full, int pieces_at, int s, bool whole, int4 (&v)[3], bool& lost) const {
     const int i = s % kPieces;
     const uint32_t phase = static_cast<uint32_t>(s / kPieces);
     if (!(whole ? wait(full + i, phase) : wait1(full + i, phase))) {
       lost = true;
       return false;
     }
+    const uint32_t at = bars + pieces_at + i * 48;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] = pieces.at[i][k];
+    for (int k = 0; k < 3; ++k)
+      asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[k].x), "=r"(v[k].y), "=r"(v[k].z), "=r"(v[k].w)
+                   : "r"(at + 16 * k)
+                   : "memory");
     return v[2].w != 0;
   }
   // one thread, or (whole) a warp that has read what it needs of piece s
@@ -283,15 +288,16 @@ struct AttnCta {
     if (!whole || lane == 0) mbar_arrive(bar(empty + s % kPieces));
   }
   // The planning warp: piece s (valid or the end) to the others.
-  __device__ __forceinline__ bool hand_round(int full, int empty, AttnPieces& pieces, int s, int4 a, int4 b, int4 d) const {
+  __device__ __forceinline__ bool hand_round(int full, int empty, int pieces_at, int s, int4 a, int4 b, int4 d) const {
     const int i = s % kPieces;
     AttnCta patient = *this;
     patient.limit = limit << 10;                  // a tile may take long; who waits for its parts sets the abort flag
     if (!patient.wait(empty + i, static_cast<uint32_t>(s / kPieces) ^ 1u)) return false;
     if (lane == 0) {
-      pieces.at[i][0] = a;
-      pieces.at[i][1] = b;
-      pieces.at[i][2] = d;
+      const uint32_t at = bars + pieces_at + i * 48;
+      asm volatile("st.shared.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w) : "memory");
+      asm volatile("st.shared.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(at + 16), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
+      asm volatile("st.shared.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(at + 32), "r"(d.x), "r"(d.y), "r"(d.z), "r"(d.w) : "memory");
       mbar_arrive(bar(full + i));
     }
     __syncwarp();
@@ -730,13 +736,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     g.blocks = g.nb[0] > g.nb[1] ? g.nb[0] : g.nb[1];
     return true;
   };
-  AttnPieces& pieces = *reinterpret_cast<AttnPieces*>(ctl + kPiecesAt);
   // piece s; `whole`: the warp asks together
   bool lost = false;
   auto segment = [&](int s, Seg& g, bool whole) {
     if (!PLANNED) return work_out(s, g);
     int4 v[3];
-    if (!c.piece(PIECE_FULL, pieces, s, whole, v, lost)) return false;
+    if (!c.piece(PIECE_FULL, kPiecesAt, s, whole, v, lost)) return false;
     g.b = 0;
     g.h = v[0].x;
     g.q0 = v[0].y;
@@ -880,7 +885,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     Seg g;
     for (int s = 0;; ++s) {
       const bool more = work_out(s, g);
-      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, pieces, s, make_int4(g.h, g.q0, g.slot, g.begin),
+      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, kPiecesAt, s, make_int4(g.h, g.q0, g.slot, g.begin),
                         make_int4(g.q_row, g.q_len, g.k_row, g.k_len), make_int4(g.nb[0], g.nb[1], 0, more)) || !more)
         break;
     }
@@ -960,7 +965,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
           ok = c.wait(O_DONE + t, done - 1);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
+          // (unrolled, it spills registers of the loop around it where a piece's numbers take some)
+#pragma unroll (PLANNED ? 1 : D / 16)
           for (int i = 0; i < D / 16; ++i) {
             uint32_t o[16];
             tmem_fetch16(to + 16 * i, o);
@@ -1439,13 +1445,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.n = end - g.begin;
     return true;
   };
-  AttnPieces& pieces = *reinterpret_cast<AttnPieces*>(ctl + kPiecesAt);
   // piece s; `whole`: the warp asks together
   bool lost = false;
   auto segment = [&](int s, Seg& g, bool whole) {
     if (!PLANNED) return work_out(s, g);
     int4 v[3];
-    if (!c.piece(PIECE_FULL, pieces, s, whole, v, lost)) return false;
+    if (!c.piece(PIECE_FULL, kPiecesAt, s, whole, v, lost)) return false;
     g.b = 0;
     g.h = v[0].x;
     g.q0 = v[0].y;
@@ -1600,7 +1605,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     Seg g;
     for (int s = 0;; ++s) {
       const bool more = work_out(s, g);
-      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, pieces, s, make_int4(g.h, g.q0, g.slot, g.begin),
+      if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, kPiecesAt, s, make_int4(g.h, g.q0, g.slot, g.begin),
                         make_int4(g.q_row, g.q_len, g.k_row, g.k_len), make_int4(g.n, g.top, g.opens, more)) || !more)
         break;
     }

@@ -60,7 +60,10 @@ __device__ __forceinline__ void few_mma<__half>(float (&c)[4], const uint32_t (&
 
 // H halves of 8 rows.  Lane (g, t) = (lane / 4, lane % 4) owns rows g and, with
 // two halves, g + 8; of their accumulators columns 64 cc + 16 t + 0 .. 15.
-// PLANNED: tiles of p.few_rows rows from the plan.
+// PLANNED: tiles of p.few_rows rows from the plan.  The warps form groups of
+// p.few_group, each on a tile of its own: over a few hundred keys a tile's
+// beginning and end take longer than its steps (64 samples of up to 512 keys of 8
+// heads x 128: FEW_GROUPS).
 template <typename T, int D, int H, bool PLANNED = false>
 __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(const __grid_constant__ AttnParams p) {
   constexpr int ROWS = 8 * H, WARPS = few_warps(ROWS), KC = D / 32, VC = D / 64, STAGES = few_stages(ROWS, D);
@@ -90,11 +93,13 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     if (warp == 0) plan_table(p.seqs, table, lane, p.status);
     __syncthreads();
   }
+  const int group = PLANNED ? p.few_group : WARPS, grp = PLANNED ? warp / group : 0, gw = warp - grp * group;
+  const int groups = PLANNED ? WARPS / group : 1;
   RingPos<STAGES> at;         // the next step to read
   bool ok = true;
   AttnWork w;
   AttnPiece piece;
-  for (int s = 0; ok && (PLANNED ? attn_piece(p, table, s, piece) : attn_work(p, s, w)); ++s) {
+  for (int s = grp; ok && (PLANNED ? attn_piece(p, table, s, piece) : attn_work(p, s, w)); s += groups) {
     // rows row0 + r, r < rows, of key head hk: query (row0 + r) % queries of head (row0 + r) / queries of its group
     int b, hk, row0, rows, q_len, k_len, queries;
     if (PLANNED) {
@@ -150,8 +155,8 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
       attn_cut(w, n, begin, end);
     }
     // lane 0: the next step's keys and values into the stage after those in flight
-    constexpr int kHop = WARPS * kKeys;
-    int ahead = begin + warp * kKeys, in_flight = 0;
+    const int kHop = group * kKeys;
+    int ahead = begin + gw * kKeys, in_flight = 0;
     int put = at.s;
     auto fetch = [&]() {
       if (ahead >= end || (p.flags & 1u)) return;             // test only: issue nothing
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     if (lane == 0)
       for (int i = 0; i < STAGES; ++i) fetch();
 #pragma unroll 1
-    for (int k0 = begin + warp * kKeys; k0 < end; k0 += kHop) {
+    for (int k0 = begin + gw * kKeys; k0 < end; k0 += kHop) {
       ok = cta.wait(at.s, at.phase);
       if (!ok) break;
       const unsigned char* in = ring + at.s * kStep;
@@ -276,18 +281,20 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
             *reinterpret_cast<float4*>(sums(warp, r) + 64 * c + 16 * t + 8 * e + j) =
                 make_float4(acc[c][j][2 * h + e], acc[c][j + 1][2 * h + e], acc[c][j + 2][2 * h + e], acc[c][j + 3][2 * h + e]);
     }
-    __syncthreads();
-    // the CTA's warps: a thread per two columns of a row
-    for (int x = threadIdx.x; x < rows * (D / 2); x += blockDim.x) {
+    if (PLANNED) named_barrier_sync(1 + grp, 32 * group);
+    else __syncthreads();
+    // the group's warps: a thread per two columns of a row
+    const int first = grp * group, behind = first + group;
+    for (int x = threadIdx.x - 32 * first; x < rows * (D / 2); x += 32 * group) {
       const int r = x / (D / 2), c = x % (D / 2) * 2;
       float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) top = fmaxf(top, stats[i][r].x);
+#pragma unroll (PLANNED ? 4 : WARPS)
+      for (int i = first; i < behind; ++i) top = fmaxf(top, stats[i][r].x);
       const float base = top == -INFINITY ? 0.0f : top;
       float total = 0.0f;
       float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < WARPS; ++i) {
+#pragma unroll (PLANNED ? 4 : WARPS)
+      for (int i = first; i < behind; ++i) {
         const float f = exp2_approx(__fmul_rn(__fsub_rn(stats[i][r].x, base), p.scale_log2));
         total = __fmaf_rn(f, stats[i][r].y, total);
         o = __ffma2_rn(make_float2(f, f), *reinterpret_cast<const float2*>(sums(i, r) + c), o);
@@ -308,9 +315,9 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
         if (c == 0 && in_span(lse, 4, p.sp_lse, p.status)) *lse = some ? __fmaf_rn(top, p.scale, log_sum<T>(total)) : -INFINITY;
       }
     }
-    // the sums' place is TMA's again; a warp that gave up ends the CTA's work
+    // the sums' place is TMA's again; a warp that gave up ends its group's work
     fence_async_shared();
-    ok = !__syncthreads_or(!ok);
+    ok = PLANNED ? named_barrier_and(1 + grp, 32 * group, ok) : !__syncthreads_or(!ok);
   }
 }
 

@@ -131,7 +131,7 @@ struct AttnParams {
   AttnPlan plan;
   AttnSeqs seqs;
   int table;                  // no plan: AttnTable
-  int few_rows;               // rows of a tile of a few queries
+  int few_rows, few_group;    // a few queries: rows of a tile, warps on a tile
   int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
   int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
   // PREFIX

@@ -55,6 +55,7 @@ struct Job {
   bool cuts;                  // some tile may be cut
   bool keep = false;
   bool table = false;         // no plan: every CTA works its tiles out
+  int few_group = 0;          // a few queries: warps on a tile
   long long slots() const { return keep ? 2 * kCtas + heads * items : cuts ? 2 * kCtas : 0; }
 };
 
@@ -63,14 +64,18 @@ bool is_few(const Job& j) { return j.kind == qknr::kPlanFew && j.rows <= qknr::k
 // What a cut costs: partial results and the kernel that joins them, about six
 // blocks' time at head_dim 128 and twelve at 64, so that tiles of twice as
 // many go out whole (a share is then off by one tile at most).
-int whole_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 5 : a->head_dim == 128 ? 12 : 24; }
+int whole_units(const qknr_attn_args* a, const Job& j) {
+  if (is_few(j)) return j.few_group < qknr::few_warps(j.rows) ? 12 : 5;
+  return a->head_dim == 128 ? 12 : 24;
+}
 
 // What a tile costs beside its blocks, in blocks: its queries' way, the epilogue.
 int over_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 3 : a->head_dim == 128 ? 2 : 3; }
 
 Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_rows, long long batch, long long units,
-           int slot_rows) {
+           int slot_rows, int few_group = 0) {
   Job j{kind, rows, heads, max_items(of_rows, batch, rows), units, slot_rows, false};
+  j.few_group = few_group;
   j.units += over_units(a, j);
   j.cuts = j.units > whole_units(a, j);
   return j;
@@ -80,12 +85,16 @@ Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_
 // (attn_api.cu).  The host knows their mean only, and any mix comes out right.
 bool few(long long rows, long long batch) { return rows <= qknr::kFewRows * batch; }
 
-// The forward pass's tiles of `rows` query rows in `batch` sequences over up to `keys` keys.
-Job forward_job(const qknr_attn_args* a, long long rows, long long batch, int keys, bool may_few = true) {
-  if (may_few && few(rows, batch)) {
+// The forward pass's tiles of `rows` query rows in `batch` sequences over up to
+// `keys` keys, `mean_keys` on average.
+constexpr long long kFewGroupKeys = 768;
+Job forward_job(const qknr_attn_args* a, long long rows, long long batch, int keys, long long mean_keys) {
+  if (few(rows, batch)) {
     const long long group = a->n_heads_q / a->n_heads_k;
     const int tile = group * rows <= 8 * batch ? 8 : 16;
-    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys), tile);
+    // all warps of a CTA on one tile's keys, or three (four) where they are few
+    const int warps = mean_keys > kFewGroupKeys ? qknr::few_warps(tile) : tile == 8 ? 3 : 4;
+    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys), tile, warps);
   }
   return job_of(a, qknr::kPlanQueries, qknr::fwd::kRows, a->n_heads_q, rows, batch, blocks_of(keys), qknr::fwd::kRows);
 }
@@ -255,7 +264,7 @@ struct PackSpace {
 constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at most
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
-  s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k);
+  s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k, p->batch ? p->rows_k / p->batch : 0);
   s->job[0].table = table_does(s->job[0], p->batch);
   if (!s->job[0].table) s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
@@ -374,12 +383,12 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
     return;
   }
   const long long rows = static_cast<long long>(a->batch) * a->seq_q;
-  s->job[0] = forward_job(a, rows, 1, p->prefix);
+  s->job[0] = forward_job(a, rows, 1, p->prefix, p->prefix);
   // the heads of a group in one tile where that leaves fewer rows of a tile empty
   const long long group = a->n_heads_q / a->n_heads_k;
   if (s->job[0].kind == qknr::kPlanQueries && halves(group * rows) < group * halves(rows))
     s->job[0] = job_of(a, qknr::kPlanFew, qknr::fwd::kRows, a->n_heads_k, group * rows, 1, blocks_of(p->prefix), qknr::fwd::kRows);
-  s->job[1] = forward_job(a, rows, a->batch, a->seq_k);
+  s->job[1] = forward_job(a, rows, a->batch, a->seq_k, a->seq_k);
   for (int i = 0; i < 2; ++i) {
     Job& j = s->job[i];
     j.keep = true;
@@ -471,6 +480,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   kp.seqs = pp.job[0].seqs;
   kp.table = s.job[0].table;
   kp.few_rows = s.job[0].rows;
+  kp.few_group = s.job[0].few_group;
   kp.slot_rows = s.job[0].slot_rows;
   kp.q_in = static_cast<const char*>(p->q);
   kp.q_stride = q.stride * 2;
@@ -725,6 +735,7 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     w.plan = s.plan[i];
     w.seqs = pj;
     w.few_rows = j.rows;
+    w.few_group = j.few_group;
     w.slot_rows = j.slot_rows;
     w.keep = 1;
     w.part = parts[i].part;

@@ -291,7 +291,7 @@ struct AttnCta {
   __device__ __forceinline__ bool hand_round(int full, int empty, int pieces_at, int s, int4 a, int4 b, int4 d) const {
     const int i = s % kPieces;
     AttnCta patient = *this;
-    patient.limit = limit << 10;                  // a tile may take long; who waits for its parts sets the abort flag
+    patient.limit = limit >> 53 ? ~0ull : limit << 10;   // a tile may take long; who waits for its parts sets the abort flag
     if (!patient.wait(empty + i, static_cast<uint32_t>(s / kPieces) ^ 1u)) return false;
     if (lane == 0) {
       const uint32_t at = bars + pieces_at + i * 48;

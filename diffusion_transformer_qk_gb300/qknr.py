@@ -931,6 +931,7 @@ def gn_launch_noalloc(a: QknrGnArgs, stream: Optional[torch.cuda.Stream] = None)
 # and kept; a call then copies the struct and puts its pointers in.  Nothing
 # is kept of the tensors themselves.
 
+_byref = ctypes.byref
 _plans = {}
 _MOST_PLANS = 1024
 _FIXED = (int, float, bool, str, tuple, type(None))
@@ -973,6 +974,8 @@ def _empty(shape, dtype, like, stream):
     """A new tensor on like's device that belongs to the stream the call runs
     on, so that its memory is not handed out again while that stream uses it."""
     if stream is None:
+        if dtype is like.dtype and shape == like.shape and like.is_contiguous():
+            return torch.empty_like(like)         # half a microsecond less
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -996,10 +999,10 @@ def _call(fn, a, stream, like) -> None:
     else:
         raise ValueError("the stream must be on the tensors' device")
     if torch._C._cuda_getDevice() == device:      # the library launches on the calling thread's device
-        st = fn(ctypes.byref(a), s)
+        st = fn(_byref(a), s)
     else:
         with torch.cuda.device(device):
-            st = fn(ctypes.byref(a), s)
+            st = fn(_byref(a), s)
     if st != OK:
         raise QknrError(st, load().qknr_last_error().decode())
 

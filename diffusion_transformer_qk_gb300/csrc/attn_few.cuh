@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(smem + few_table(ROWS, D));
-  if (PLANNED && p.table) {
+  if (PLANNED && p.from == kFromTable) {
     if (warp == 0) plan_table(p.seqs, table, lane, p.status);
     __syncthreads();
   }
@@ -99,16 +99,17 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   bool ok = true;
   AttnWork w;
   AttnPiece piece;
-  for (int s = grp; ok && (PLANNED ? attn_piece(p, table, s, piece) : attn_work(p, s, w)); s += groups) {
+  for (int s = grp; ok && (PLANNED ? attn_piece<true>(p, table, s, piece) : attn_work(p, s, w)); s += groups) {
     // rows row0 + r, r < rows, of key head hk: query (row0 + r) % queries of head (row0 + r) / queries of its group
     int b, hk, row0, rows, q_len, k_len, queries;
     if (PLANNED) {
       b = 0;
       hk = piece.h;
       row0 = piece.t0;
-      queries = q_len = piece.q_len;
+      q_len = piece.q_len;
+      queries = q_len > 0 ? q_len : 1;
       k_len = piece.k_len;
-      rows = min(p.group * queries - row0, p.few_rows);
+      rows = min(p.group * q_len - row0, p.few_rows);
       w.slot = piece.slot;
     } else {
       const int key_head = w.tile / p.tiles;

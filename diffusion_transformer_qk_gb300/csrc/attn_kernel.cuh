@@ -74,6 +74,17 @@ struct AttnTable {
   int q_tiles[kTableSeqs];    // query tiles before
 };
 
+// Where no plan is needed either: one sequence whose tiles all cost the same
+// (kFromUniform), or samples of a fixed number of rows whose tiles all go out
+// whole, each working out its own lengths (kFromSamples; a few queries).
+enum { kFromPlan, kFromTable, kFromUniform, kFromSamples };
+struct AttnUniform {
+  int tiles, units;           // of the line; of each tile
+  int active;                 // CTAs that get a share (0: tiles go out whole)
+  int items;                  // tiles of a head (kFromSamples: of all samples, per_sample each)
+  int per_sample;
+};
+
 // The pieces of a CTA's share as the forward and dq kernels' planning warp
 // hands them round: the other roles read a piece from shared memory, a few
 // tiles behind, instead of working it out from global memory where a tile
@@ -130,7 +141,8 @@ struct AttnParams {
   // PLANNED (batch is 1, seq_q and seq_k are all rows)
   AttnPlan plan;
   AttnSeqs seqs;
-  int table;                  // no plan: AttnTable
+  int from;                   // kFrom...: where tiles come from
+  AttnUniform uniform;
   int few_rows, few_group;    // a few queries: rows of a tile, warps on a tile
   int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
   int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
@@ -425,6 +437,19 @@ __device__ __forceinline__ void plan_table(const AttnSeqs& j, AttnTable& out, in
   if (lane == 31) out.first[32] = n;
 }
 
+// Where CTA c's share of a uniform line begins: (tile, unit).
+__device__ __forceinline__ int2 uniform_span(const AttnUniform& u, int over, int c) {
+  const long long work = static_cast<long long>(u.tiles) * u.units;
+  if (c >= u.active) return make_int2(u.tiles, 0);
+  const long long x = work / u.active * c + work % u.active * c / u.active;
+  int tile = static_cast<int>(x / u.units), o = static_cast<int>(x - static_cast<long long>(tile) * u.units);
+  if (o < 2 || u.units - o < over + 2) {          // as attn_plan_kernel
+    tile += 2 * o >= u.units;
+    o = 0;
+  }
+  return make_int2(tile, o);
+}
+
 // (head, item) of a tile of the line: items of one cost go head by head.
 __device__ __forceinline__ int2 plan_tile(const AttnPlan& plan, int heads, int tile) {
   const int2 run = plan.runs[tile / heads];
@@ -437,12 +462,13 @@ struct AttnPiece {
   int h, e, u0, u1, slot;     // head line, item; units [u0, u1) of its contraction
   int q_row, q_len, k_row, k_len, t0, blocks, tiles0;
 };
+template <bool FORWARD>
 __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable& table, int s, AttnPiece& w) {
   const int c = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
   int tile = s * ctas + (s & 1 ? ctas - 1 - c : c);
   w.u0 = 0;
   w.slot = -1;
-  if (p.table) {
+  if (p.from == kFromTable) {
     const int n = table.first[kTableSeqs];
     if (s * ctas >= n * p.seqs.heads) return false;
     if (tile >= n * p.seqs.heads) tile = 0, w.u0 = 1;           // nothing for this CTA in the last wave
@@ -463,6 +489,37 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     w.tiles0 = table.q_tiles[b];
     w.u1 = w.blocks + p.seqs.over;
     return w.u0 == 0;
+  }
+  if (FORWARD && p.from >= kFromUniform) {
+    const AttnUniform& u = p.uniform;
+    int end = 0;              // 0: the tile's
+    tile = s * ctas + c;
+    if (u.active) {
+      const int2 from = uniform_span(u, p.seqs.over, c), to = uniform_span(u, p.seqs.over, c + 1);
+      tile = from.x + s;
+      if (tile > to.x || (tile == to.x && to.y == 0)) return false;
+      if (s == 0) w.u0 = from.y;
+      if (tile == to.x) end = to.y;
+    }
+    if (tile >= u.tiles) return false;
+    w.h = tile / u.items;
+    w.e = tile - w.h * u.items;
+    int b = 0, t = w.e;
+    if (p.from == kFromSamples) {
+      b = w.e / u.per_sample;
+      t = w.e - b * u.per_sample;
+    }
+    w.q_row = b * p.seqs.seq_q;
+    w.k_row = b * p.seqs.seq_k;
+    w.q_len = clamp_len(p.seqs.q_lens, b, p.seqs.seq_q, p.seqs.sp_q_lens, p.status);
+    w.k_len = clamp_len(p.seqs.k_lens, b, p.seqs.seq_k, p.seqs.sp_k_lens, p.status);
+    w.t0 = t * p.seqs.rows;
+    if (w.t0 >= plan_rows(p.seqs, w.q_len, w.k_len)) w.k_len = 0;   // a sample with fewer rows: nothing in this tile
+    w.blocks = plan_blocks(p.seqs, t, w.q_len, w.k_len);
+    w.tiles0 = 0;
+    w.u1 = end ? end : w.blocks + p.seqs.over;
+    w.slot = w.u0 > 0 ? 2 * c : end ? 2 * c + 1 : p.keep ? 2 * ctas + tile : -1;
+    return w.u0 <= w.u1;
   }
   if (!in_span(p.plan.spans + c, 16, p.plan.sp, p.status)) return false;
   const int4 head = *p.plan.head;
@@ -682,7 +739,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
-  if (PLANNED && p.table) {
+  if (PLANNED && p.from == kFromTable) {
     if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
     __syncthreads();
   }
@@ -691,7 +748,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece(p, table, s, piece)) return false;
+      if (!attn_piece<true>(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
@@ -1272,7 +1329,7 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
     constexpr int N = 2;                          // rows in flight
     __shared__ int range[2];                      // PLANNED: the rows of v that belong to a sequence
     if (PLANNED) {
-      if (threadIdx.x < 32 && p.table) {
+      if (threadIdx.x < 32 && p.from == kFromTable) {
         const int v = static_cast<int>(threadIdx.x) < p.seqs.batch
                           ? plan_start(p.seqs.k_starts, p.seqs.sp_k_starts, threadIdx.x + 1, p.seqs.seq_k, p.status)
                           : 0;
@@ -1400,7 +1457,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
-  if (PLANNED && p.table) {
+  if (PLANNED && p.from == kFromTable) {
     if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
     __syncthreads();
   }
@@ -1408,7 +1465,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   auto work_out = [&](int s, Seg& g) {
     if (PLANNED) {
       AttnPiece piece;
-      if (!attn_piece(p, table, s, piece)) return false;
+      if (!attn_piece<false>(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
@@ -1909,7 +1966,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
-  if (PLANNED && p.table) {
+  if (PLANNED && p.from == kFromTable) {
     if (c.warp == 0) plan_table(p.seqs, table, c.lane, p.status);
     __syncthreads();
   }
@@ -1920,7 +1977,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece(p, table, s, piece)) return false;
+      if (!attn_piece<false>(p, table, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.k0 = piece.t0;

@@ -298,17 +298,24 @@ struct PlanParts {
 
 // A whole warp: how the shares cut tile `tile`.  (MOST: CTAs at most.)
 constexpr int kPlanMostCtas = 159;
-__device__ __forceinline__ PlanParts plan_parts(const AttnPlan& plan, int ctas, int tile, int lane, int* status) {
+template <typename F>
+__device__ __forceinline__ PlanParts plan_parts(int ctas, int tile, int lane, F span) {
   int before = 0, cuts = 0;
 #pragma unroll
   for (int i = 0; i <= kPlanMostCtas / 32; ++i) {
     const int c = 32 * i + lane;
     int2 at = make_int2(0x7fffffff, 0);
-    if (c <= ctas && in_span(plan.spans + c, 8, plan.sp, status)) at = plan.spans[c];
+    if (c <= ctas) at = span(c);
     before += __popc(__ballot_sync(0xffffffffu, at.x < tile || (at.x == tile && at.y == 0)));
     cuts += __popc(__ballot_sync(0xffffffffu, at.x == tile && at.y > 0));
   }
   return PlanParts{before - 1, cuts};
+}
+
+__device__ __forceinline__ PlanParts plan_parts(const AttnPlan& plan, int ctas, int tile, int lane, int* status) {
+  return plan_parts(ctas, tile, lane, [&](int c) {
+    return in_span(plan.spans + c, 8, plan.sp, status) ? plan.spans[c] : make_int2(0x7fffffff, 0);
+  });
 }
 
 // The tile that boundary c of the shares is the first to cut, or -1.
@@ -461,6 +468,8 @@ struct PrefixSide {
   int rows, slot_rows;        // of a tile, of a slot
   int ctas, heads;            // lines of tiles
   int there;                  // the pass was made
+  int from, over;             // kFrom...
+  AttnUniform uniform;
 };
 
 struct PrefixJoinParams {
@@ -496,24 +505,37 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
       if (!s.there) continue;
       // the row's place among its sequence's
       const int at = k == 0 ? row : i, rows = k == 0 ? p.batch * p.seq_q : q_len;
+      const int x = s.few ? hh * rows + at : at;
+      r[k] = x % s.rows;
+      n[k] = 1;
+      if (s.from >= kFromUniform) {
+        const AttnUniform& u = s.uniform;
+        tile[k] = (s.few ? hk : h) * u.items + (s.from == kFromSamples ? b * u.per_sample : 0) + x / s.rows;
+        if (u.active) parts[k] = plan_parts(s.ctas, tile[k], lane, [&](int c) { return uniform_span(u, s.over, c); });
+        n[k] += parts[k].cuts;
+        continue;
+      }
       int first = 0;
       if (k == 1 && in_span(s.plan.seq_items + b, 4, s.plan.sp, p.status)) first = s.plan.seq_items[b];
-      const int x = s.few ? hh * rows + at : at, e = first + x / s.rows;
+      const int e = first + x / s.rows;
       // the tile's place in the line
       const int i = in_span(s.plan.ranks + e, 4, s.plan.sp, p.status) ? s.plan.ranks[e] : 0;
       const int2 run = in_span(s.plan.runs + i, 8, s.plan.sp, p.status) ? s.plan.runs[i] : make_int2(i, 1);
       tile[k] = run.x * s.heads + (s.few ? hk : h) * run.y + i - run.x;
-      r[k] = x % s.rows;
       parts[k] = plan_parts(s.plan, s.ctas, tile[k], lane, p.status);
-      n[k] = parts[k].cuts + 1;
+      n[k] += parts[k].cuts;
     }
+    // slot of part c of the first side, of the second
+    const int slot0 = parts[0].cuts ? 2 * parts[0].c : 2 * p.side[0].ctas + tile[0];
+    const int slot1 = parts[1].cuts ? 2 * parts[1].c : 2 * p.side[1].ctas + tile[1];
+    const bool cut0 = parts[0].cuts > 0, cut1 = parts[1].cuts > 0;
+    const int n0 = n[0], r0 = r[0], r1 = r[1];
     j.add(n[0] + n[1], lane, p.scale_log2, p.status, [&](int c, const PartsView*& side) {
-      const int k = c >= n[0];
-      const int cut = k ? c - n[0] : c;
-      side = &p.side[k].parts;
-      const PlanParts& of = parts[k];
-      const int slot = of.cuts ? of.slot(cut) : 2 * p.side[k].ctas + tile[k];
-      return static_cast<long long>(slot) * p.side[k].slot_rows + r[k];
+      const bool second = c >= n0;
+      const int i = second ? c - n0 : c;
+      const int slot = (second ? slot1 : slot0) + ((second ? cut1 : cut0) ? (i == 0 ? 1 : 2 * i) : 0);
+      side = second ? &p.side[1].parts : &p.side[0].parts;
+      return static_cast<long long>(slot) * (second ? p.side[1].slot_rows : p.side[0].slot_rows) + (second ? r1 : r0);
     });
   }
   j.template write<T>(p, p.o + static_cast<long long>(row) * p.o_stride + h * (D * 2),

@@ -54,7 +54,8 @@ struct Job {
   int slot_rows;              // fp32 rows of a partial result
   bool cuts;                  // some tile may be cut
   bool keep = false;
-  bool table = false;         // no plan: every CTA works its tiles out
+  int from = qknr::kFromPlan; // where the CTAs have their tiles from
+  qknr::AttnUniform uniform{};
   int few_group = 0;          // a few queries: warps on a tile
   long long slots() const { return keep ? 2 * kCtas + heads * items : cuts ? 2 * kCtas : 0; }
 };
@@ -265,8 +266,8 @@ constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k, p->batch ? p->rows_k / p->batch : 0);
-  s->job[0].table = table_does(s->job[0], p->batch);
-  if (!s->job[0].table) s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
+  if (table_does(s->job[0], p->batch)) s->job[0].from = qknr::kFromTable;
+  else s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
 }
 
@@ -277,8 +278,8 @@ void pack_backward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space
                      2 * qknr::kTile);
   const bool table = table_does(s->job[0], p->batch) && table_does(s->job[1], p->batch);
   for (int i = 0; i < 2; ++i) {
-    s->job[i].table = table;
-    if (!table) s->plan[i] = take_plan(ws, s->job[i].items, p->batch, false);
+    if (table) s->job[i].from = qknr::kFromTable;
+    else s->plan[i] = take_plan(ws, s->job[i].items, p->batch, false);
   }
   s->delta_n = static_cast<size_t>(a->n_heads_q) * p->rows_q;
   s->delta = ws->take<float>(s->delta_n);
@@ -394,7 +395,20 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
     j.keep = true;
     if (!is_few(j) && (i ? a->seq_q : j.kind == qknr::kPlanFew ? group * rows : rows) <= qknr::kTile) j.slot_rows = qknr::kTile;
     if ((i ? a->seq_k : p->prefix) == 0) j.keep = j.cuts = false;   // the pass is not made
-    s->plan[i] = take_plan(ws, j.items, a->batch, true);
+    if (i == 0) {
+      j.from = qknr::kFromUniform;
+      j.items = ((j.kind == qknr::kPlanFew ? group * rows : rows) + j.rows - 1) / j.rows;
+      const long long tiles = j.heads * j.items, most = tiles * j.units / (is_few(j) ? kLeastFew : kLeastUnits);
+      const int active = j.cuts ? static_cast<int>(most < 1 ? 1 : most < kCtas ? most : kCtas) : 0;
+      j.uniform = qknr::AttnUniform{static_cast<int>(tiles), static_cast<int>(j.units), active, static_cast<int>(j.items), 0};
+    } else if (is_few(j) && !j.cuts) {
+      j.from = qknr::kFromSamples;
+      const int each = static_cast<int>((group * a->seq_q + j.rows - 1) / j.rows);
+      j.items = static_cast<long long>(each) * a->batch;
+      j.uniform = qknr::AttnUniform{static_cast<int>(j.heads * j.items), 0, 0, static_cast<int>(j.items), each};
+    } else {
+      s->plan[i] = take_plan(ws, j.items, a->batch, true);
+    }
     take_parts(ws, a, j, true, &kp[i]);
   }
 }
@@ -478,7 +492,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   if (qknr_host::overlaps(lse, space)) return fail(QKNR_ERR_OVERLAP, "lse and the workspace overlap");
   kp.plan = s.plan[0];
   kp.seqs = pp.job[0].seqs;
-  kp.table = s.job[0].table;
+  kp.from = s.job[0].from;
   kp.few_rows = s.job[0].rows;
   kp.few_group = s.job[0].few_group;
   kp.slot_rows = s.job[0].slot_rows;
@@ -501,7 +515,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, &a, p->v, v.stride, p->rows_k, p->n_heads_k, box)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(&a);
-  if (!kp.table && (st = launch_plan(pp, s.job, 1, &a, stream)) != QKNR_OK) return st;
+  if (kp.from == qknr::kFromPlan && (st = launch_plan(pp, s.job, 1, &a, stream)) != QKNR_OK) return st;
   if ((st = launch_forward(&a, s.job[0], fn, &kp, dev, di, stream)) != QKNR_OK) return st;
   return launch_join(a_few ? fn.join_few : fn.join_fwd, s.job[0], &a, &kp, stream, "cudaLaunchKernelExC(attention, joining)");
 }
@@ -584,8 +598,8 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
     if ((st = make_map(&kp.map_v, &a, p->v, v.stride, p->rows_k, p->n_heads_k)) != QKNR_OK) return st;
   }
   const Kernels fn = kernels_for(&a);
-  kp.table = s.job[0].table;
-  if (!kp.table && (st = launch_plan(pp, s.job, 2, &a, stream)) != QKNR_OK) return st;
+  kp.from = s.job[0].from;
+  if (kp.from == qknr::kFromPlan && (st = launch_plan(pp, s.job, 2, &a, stream)) != QKNR_OK) return st;
   auto use = [&](int i) {
     kp.plan = s.plan[i];
     kp.seqs = pp.job[i].seqs;
@@ -734,6 +748,8 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     w.seq_k = side.seq_k;
     w.plan = s.plan[i];
     w.seqs = pj;
+    w.from = j.from;
+    w.uniform = j.uniform;
     w.few_rows = j.rows;
     w.few_group = j.few_group;
     w.slot_rows = j.slot_rows;
@@ -757,6 +773,9 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     js.slot_rows = j.slot_rows;
     js.ctas = kCtas;
     js.heads = j.heads;
+    js.from = j.from;
+    js.over = pj.over;
+    js.uniform = j.uniform;
     js.there = side.seq_k > 0;
   }
   jp.o = kp.o;
@@ -773,7 +792,9 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
   jp.sp_o = kp.sp_o;
   jp.sp_lse = kp.sp_lse;
   jp.sp_q_lens = kp.sp_q_lens;
-  if ((st = launch_plan(pp, s.job, 2, &a, stream)) != QKNR_OK) return st;
+  // only the samples' own keys may take a plan
+  pp.job[0] = pp.job[1];
+  if (s.job[1].from == qknr::kFromPlan && (st = launch_plan(pp, s.job + 1, 1, &a, stream)) != QKNR_OK) return st;
   for (int i = 0; i < 2; ++i)
     if (sides[i].seq_k > 0 && (st = launch_forward(&a, s.job[i], fn, &pass[i], dev, di, stream)) != QKNR_OK) return st;
   const long long items = static_cast<long long>(p->batch) * p->seq_q * p->n_heads_q;

@@ -297,3 +297,51 @@ def test_waits_are_bounded():
         f()
         assert int(word.item()) == Q.ERR_TIMEOUT
     both([300, 40], None, 2, 1, 64, seed=18)
+
+
+@pytest.mark.parametrize("lens,Hq,Hk,D", [([2800, 591, 619], 12, 12, 128), ([686, 560, 1844], 8, 8, 128), ([3000, 200, 90], 6, 2, 64)])
+@pytest.mark.parametrize("few", [False, True])
+def test_a_workspace_full_of_nan(lens, Hq, Hk, D, few):
+    # whatever a workspace held, every part that a join adds up has been written: also those of CTAs whose share of the
+    # work left over is nothing, which the first two shapes have inside a tile
+    s = make([3] * len(lens) if few else lens, lens if few else None, Hq, Hk, D, seed=20)
+    ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")
+    o, lse = call(s, workspace=ws)
+    o2, lse2 = call(s)
+    assert same_bits(o, o2) and same_bits(lse, lse2)
+    ws.fill_(255)
+    grads = call_backward(s, s["do"], o, lse, workspace=ws)
+    assert all(same_bits(a, b) for a, b in zip(grads, call_backward(s, s["do"], o, lse)))
+    one, rows, keys = list(each(s))[1]
+    TA.check_forward(one, s["dtype"], o[rows], lse[:, rows])
+    TA.check_backward(one, s["dtype"], s["do"][rows], o[rows], lse[:, rows], grads[0][rows], grads[1][keys], grads[2][keys])
+
+
+def test_lengths_at_random():
+    # the plan's every turn: some sequences or many, tiles that go out whole and tiles that are cut
+    for seed in range(24):
+        gen = np.random.Generator(np.random.PCG64(100 + seed))
+        B = int(gen.integers(1, 40 if seed % 2 else 6))
+        most = int(gen.integers(1, 200 if B > 6 else 2500))
+        lens = gen.integers(0, most + 1, size=B).tolist()
+        Hk, group, D = int(gen.integers(1, 5)), int(gen.choice([1, 2, 3])), int(gen.choice([64, 128]))
+        lens_k = None if seed % 3 else gen.integers(0, most + 1, size=B).tolist()
+        s = make(lens, lens_k, Hk * group, Hk, D, causal=bool(seed & 4), dtype="fp16" if seed & 8 else "bf16", seed=seed)
+        o, lse = call(s)
+        grads = call_backward(s, s["do"], o, lse)
+        kw = dict(causal=s["causal"], scale=s["scale"])
+        for one, rows, keys in each(s):
+            a, b = rows.stop - rows.start, keys.stop - keys.start
+            if a == 0 or b == 0:
+                continue
+            # the same sequence through attention() as a sample of its own: a rounding of o or of a gradient apart, and
+            # p's and ds's own roundings (h each of the terms' sum, which random signs keep below 1 here)
+            o1, l1 = Q.attention(one["q"], one["k"], one["v"], s["Hq"], s["Hk"], D, **kw)
+            tol = 4 * 2.0 ** (-11 if s["dtype"] == "fp16" else -8)
+            fin = torch.isfinite(l1[0])
+            assert torch.equal(fin, torch.isfinite(lse[:, rows])) and (l1[0] - lse[:, rows])[fin].abs().max() < 1e-4
+            assert (o1.float() - o[rows].float()).abs().max() <= tol * max(1.0, float(o1.float().abs().max()))
+            ref = Q.attention_backward(s["do"][rows], one["q"], one["k"], one["v"], o[rows], lse[:, rows].contiguous()[None],
+                                       s["Hq"], s["Hk"], D, **kw)
+            for x, y in zip((grads[0][rows], grads[1][keys], grads[2][keys]), ref):
+                assert (x.float() - y.float()).abs().max() <= tol * max(1.0, float(y.float().abs().max())), (seed, a, b)

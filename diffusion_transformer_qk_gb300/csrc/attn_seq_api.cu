@@ -71,7 +71,7 @@ int whole_units(const qknr_attn_args* a, const Job& j) {
 }
 
 // What a tile costs beside its blocks, in blocks: its queries' way, the epilogue.
-int over_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 3 : a->head_dim == 128 ? 2 : 3; }
+int over_units(const qknr_attn_args* a, const Job& j) { return is_few(j) ? 4 : a->head_dim == 128 ? 2 : 3; }
 
 Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_rows, long long batch, long long units,
            int slot_rows, int few_group = 0) {
@@ -86,16 +86,22 @@ Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_
 // (attn_api.cu).  The host knows their mean only, and any mix comes out right.
 bool few(long long rows, long long batch) { return rows <= qknr::kFewRows * batch; }
 
+// Warps that share a tile of a few queries: all of a CTA's where there is much
+// to read.  Over a few hundred keys a tile's beginning and end take longer than
+// its steps: then three (of eight: four), so that more tiles are in work at a
+// time (64 samples of up to 512 keys of 8 heads x 128 beside their prefix: 69 us
+// with twelve, 62 with three; 16 x 1 query over up to 4096 keys of 24 heads: 73
+// against 82).
+constexpr long long kFewGroupKeys = 768;
+int few_group(int rows, long long mean_keys) { return mean_keys > kFewGroupKeys ? qknr::few_warps(rows) : rows == 8 ? 3 : 4; }
+
 // The forward pass's tiles of `rows` query rows in `batch` sequences over up to
 // `keys` keys, `mean_keys` on average.
-constexpr long long kFewGroupKeys = 768;
 Job forward_job(const qknr_attn_args* a, long long rows, long long batch, int keys, long long mean_keys) {
   if (few(rows, batch)) {
     const long long group = a->n_heads_q / a->n_heads_k;
     const int tile = group * rows <= 8 * batch ? 8 : 16;
-    // all warps of a CTA on one tile's keys, or three (four) where they are few
-    const int warps = mean_keys > kFewGroupKeys ? qknr::few_warps(tile) : tile == 8 ? 3 : 4;
-    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys), tile, warps);
+    return job_of(a, qknr::kPlanFew, tile, a->n_heads_k, group * rows, batch, blocks_of(keys), tile, few_group(tile, mean_keys));
   }
   return job_of(a, qknr::kPlanQueries, qknr::fwd::kRows, a->n_heads_q, rows, batch, blocks_of(keys), qknr::fwd::kRows);
 }
@@ -343,27 +349,40 @@ qknr_status check_prefix(const qknr_prefix_args* p, qknr_attn_args* a) {
   return QKNR_OK;
 }
 
-// Whether the queries of the whole batch go through the prefix together, as
-// one sequence, and then through their own keys.  Otherwise each sample's
-// tiles of 128 rows go through both.  Costs in microseconds: a block of 128
-// rows by 128 keys takes an SM 0.8 (head_dim 64: 0.5), a part of a row some
-// 16 bytes for each value to write and read, the three more launches 8.
-bool together(const qknr_attn_args* a, int prefix) {
-  const double D = a->head_dim, block = (D == 128 ? 0.8 : 0.5) / kCtas, byte = 1.0 / 6.5e6;
-  const double B = a->batch, heads = a->n_heads_q, rows = B * a->seq_q, group = heads / a->n_heads_k;
-  const double np = static_cast<double>(blocks_of(prefix)), nk = static_cast<double>(blocks_of(a->seq_k));
-  const double own = B * static_cast<double>(blocks_of(a->seq_q)) * heads * nk * block;
-  const double apart = B * static_cast<double>(blocks_of(a->seq_q)) * heads * np * block + own;
-  double both = 8.0 + rows * heads * D * 16.0 * byte;
-  const double few_prefix = group * rows / 16.0 + 1.0, few_own = group * a->seq_q / 16.0 + 1.0, key = 4.0 * D * a->n_heads_k * byte;
-  both += few(a->batch * static_cast<long long>(a->seq_q), 1) ? prefix * key * few_prefix
-                                                              : std::fmin(std::ceil(rows / 128.0) * heads, std::ceil(group * rows / 128.0) * a->n_heads_k) * np * block;
-  both += few(a->seq_q, 1) ? B * a->seq_k * key * few_own : own;
-  return both < apart;
-}
-
 // Tiles of 128 rows.
 long long halves(long long rows) { return (rows + qknr::kTile - 1) / qknr::kTile; }
+
+// What the batch's `rows` queries cost on their way through the prefix
+// together, in microseconds: as a few queries, 16 rows of a key head at a time
+// with the keys read for each, or in tiles, 128 rows by 128 keys in 0.8 on an SM
+// (head_dim 64: 0.5).  (16 samples of 32 heads on 8 beside 32768 keys x 128: 98 us
+// with four passes of a few queries, 68 in tiles.)
+double few_prefix(const qknr_attn_args* a, long long rows, int prefix) {
+  if (!few(rows, 1)) return 1e30;
+  const double passes = std::ceil(static_cast<double>(a->n_heads_q / a->n_heads_k * rows) / 16.0);
+  return passes * prefix * 4.0 * a->head_dim * a->n_heads_k / 6.2e6;
+}
+double block_us(const qknr_attn_args* a) { return (a->head_dim == 128 ? 0.8 : 0.5) / kCtas; }
+double tile_prefix(const qknr_attn_args* a, long long rows, int prefix) {
+  const long long group = a->n_heads_q / a->n_heads_k;
+  const double by_head = static_cast<double>(halves(rows)) * a->n_heads_q, by_group = static_cast<double>(halves(group * rows)) * a->n_heads_k;
+  return 8.0 + (by_head < by_group ? by_head : by_group) * static_cast<double>(blocks_of(prefix)) * block_us(a);
+}
+
+// Whether the queries of the whole batch go through the prefix together, as
+// one sequence, and then through their own keys.  Otherwise each sample's
+// tiles of 128 rows go through both.  A part of a row costs some 16 bytes for
+// each value to write and read, the two more launches 8 us.
+bool together(const qknr_attn_args* a, int prefix) {
+  const double D = a->head_dim, B = a->batch, heads = a->n_heads_q, byte = 1.0 / 6.2e6;
+  const long long rows = static_cast<long long>(a->batch) * a->seq_q;
+  const double halved = B * static_cast<double>(halves(a->seq_q)) * heads * block_us(a);
+  const double own = halved * static_cast<double>(blocks_of(a->seq_k)), apart = halved * static_cast<double>(blocks_of(prefix)) + own;
+  const double passes = std::ceil(heads / a->n_heads_k * a->seq_q / 16.0);
+  const double few_p = few_prefix(a, rows, prefix), tile_p = tile_prefix(a, rows, prefix);
+  const double few_own = few(a->seq_q, 1) ? passes * B * a->seq_k * 4.0 * D * a->n_heads_k * byte : own;
+  return 8.0 + static_cast<double>(rows) * heads * D * 16.0 * byte + (few_p < tile_p ? few_p : tile_p) + few_own < apart;
+}
 
 struct PrefixSpace {
   bool split;                 // prefix and own keys in passes of their own
@@ -384,9 +403,12 @@ void prefix_space(const qknr_prefix_args* p, const qknr_attn_args* a, Space* ws,
     return;
   }
   const long long rows = static_cast<long long>(a->batch) * a->seq_q;
-  s->job[0] = forward_job(a, rows, 1, p->prefix, p->prefix);
-  // the heads of a group in one tile where that leaves fewer rows of a tile empty
   const long long group = a->n_heads_q / a->n_heads_k;
+  if (few_prefix(a, rows, p->prefix) <= tile_prefix(a, rows, p->prefix))
+    s->job[0] = forward_job(a, rows, 1, p->prefix, p->prefix);
+  else
+    s->job[0] = job_of(a, qknr::kPlanQueries, qknr::fwd::kRows, a->n_heads_q, rows, 1, blocks_of(p->prefix), qknr::fwd::kRows);
+  // the heads of a group in one tile where that leaves fewer rows of a tile empty
   if (s->job[0].kind == qknr::kPlanQueries && halves(group * rows) < group * halves(rows))
     s->job[0] = job_of(a, qknr::kPlanFew, qknr::fwd::kRows, a->n_heads_k, group * rows, 1, blocks_of(p->prefix), qknr::fwd::kRows);
   s->job[1] = forward_job(a, rows, a->batch, a->seq_k, a->seq_k);

@@ -123,18 +123,6 @@ __device__ __forceinline__ void named_barrier_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// The same, and whether every thread's `v` was true.
-__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool v) {
-  uint32_t all;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.and.aligned.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(all)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
-      : "memory");
-  return all != 0;
-}
-
 // 1-D bulk copy global -> this CTA's shared memory, completion counted in
 // bytes on `bar`.  Both addresses 16-byte aligned, bytes a multiple of 16.
 // The source is marked evict-first in L2: every byte is streamed once.

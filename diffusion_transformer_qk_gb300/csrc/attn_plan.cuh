@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       const V tile = static_cast<V>(s) * ctas + (s & 1 ? ctas - 1 - c : c);
       if (c < ctas && tile < tiles) total += cost(tile);
       if (__syncthreads_or(c < ctas && total > share + job.cut)) break;
-      even = !__syncthreads_or(c < ctas && total > share) && even && (s + 1LL) * ctas <= tiles;
+      if (even) even = !__syncthreads_or(c < ctas && total > share) && (s + 1LL) * ctas <= tiles;
       if (even) {
         last_but_one = mine;
         mine = total;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     V left;
     plan_scan<V>(c < ctas ? share - mine : 0, add, vwarps, left);
     const V tile0 = static_cast<V>(waves) * ctas;
-    if (!whole && waves > 0 && tile0 < tiles && left * 3 < cost(tile0) * ctas) {
+    if (!whole && waves > 0 && tile0 < tiles && 3LL * left < static_cast<long long>(cost(tile0)) * ctas) {
       mine = last_but_one;
       --waves;
     }

@@ -1253,7 +1253,8 @@ def rms_norm(x, weight=None, *, residual=None, rows_per_batch=None, unit_offset=
 
     ``weight`` is [C], or [B, C] with row t taking row t // rows_per_batch;
     with ``unit_offset`` the gain is 1 + weight.  Results go to ``out`` (may be
-    x) and ``sum_out`` (may be residual or x), new tensors by default."""
+    x, whose values are then gone where there is no residual) and ``sum_out``
+    (may be residual or x), new tensors by default."""
     out, _, rstd, h = _rms_forward(False, None, x, weight, residual, rows_per_batch, unit_offset, out, None, sum_out, rstd,
                                    eps, stream, status, dev_status, flags, wait_limit_ns)
     return out, rstd, h
@@ -1296,7 +1297,8 @@ def rms_norm_backward(dy, x, weight, rstd, *, dsum=None, rows_per_batch=None, un
     if out is None:
         out = _empty(x.shape, x.dtype, x, stream)
     if weight is None:
-        dweight = None
+        if dweight is not None:
+            raise ValueError("dweight is the gradient of a weight")
     else:
         dweight = _empty(shape, torch.float32, x, stream) if dweight is None else _vector(dweight, n, "dweight", x)
     a = plan.new()

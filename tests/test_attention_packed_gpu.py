@@ -345,3 +345,31 @@ def test_lengths_at_random():
                                        s["Hq"], s["Hk"], D, **kw)
             for x, y in zip((grads[0][rows], grads[1][keys], grads[2][keys]), ref):
                 assert (x.float() - y.float()).abs().max() <= tol * max(1.0, float(y.float().abs().max())), (seed, a, b)
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([1, 1], [0, 0]), ([3, 0, 9], [0, 0, 0]), ([0, 0], [0, 0]), ([1] * 40, [0] * 39 + [3])])
+@pytest.mark.parametrize("causal", [False, True])
+def test_a_few_queries_without_keys(lens_q, lens_k, causal):
+    both(lens_q, lens_k, 4, 2, 64, causal=causal, seed=21, behind=4)
+
+
+def test_more_items_than_the_plan_sorts():
+    # 1100 tiles of a head and 300 sequences: the plan keeps the sequences' order.  Checked against attention() where
+    # lengths repeat, so that one batch of it does them all
+    lens = [40, 700, 900] * 100
+    s = make(lens, None, 2, 1, 64, causal=True, seed=22)
+    o, lse = call(s)
+    grads = call_backward(s, s["do"], o, lse)
+    for n in set(lens):
+        at = [a for a, m in zip(s["sq"], lens) if m == n]
+        pick = torch.cat([torch.arange(a, a + n, device="cuda") for a in at])
+        q, k, v, do = (s[x][pick].contiguous() for x in ("q", "k", "v", "do"))
+        kw = dict(batch=len(at), causal=True, scale=s["scale"])
+        o1, l1 = Q.attention(q, k, v, 2, 1, 64, **kw)
+        mine = lse[:, pick].view(2, len(at), n).transpose(0, 1).contiguous()
+        # a rounding of o apart, and p's own roundings
+        assert (o1.float() - o[pick].float()).abs().max() <= 4 * 2.0 ** -8 * float(o1.float().abs().max())
+        assert (l1 - mine).abs().max() < 1e-4
+        ref = Q.attention_backward(do, q, k, v, o[pick].contiguous(), mine, 2, 1, 64, **kw)
+        for a, b in zip(grads, ref):
+            assert (a[pick].float() - b.float()).abs().max() <= 4 * 2.0 ** -8 * max(1.0, float(b.float().abs().max()))

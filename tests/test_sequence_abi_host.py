@@ -214,6 +214,7 @@ F8 = torch.float8_e4m3fn
     lambda: Q.rms_norm_quantized(act(0, 128), block=64),
     lambda: Q.rms_norm_backward(act(0, 64), act(0, 128), None, act(0)),
     lambda: Q.rms_norm_backward(act(0, 64), act(0, 64), None, act(0, dtype=torch.float32), dsum=act(0, 32)),
+    lambda: Q.rms_norm_backward(act(0, 64), act(0, 64), None, act(0, dtype=torch.float32), dweight=act(64, dtype=torch.float32)),
     lambda: Q.attention_packed(act(4, 128), act(4, 128), act(4, 128), 1, 1, 128, i32(2)),         # not on a GPU
     lambda: Q.attention_packed(act(0, 128), act(0, 64), act(0, 128), 1, 1, 128, i32(2)),
     lambda: Q.attention_packed(act(0, 128), act(0, 128), act(0, 128), 1, 1, 128, i32(2)),         # starts on the CPU

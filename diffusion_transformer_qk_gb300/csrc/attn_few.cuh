@@ -37,9 +37,10 @@ __host__ __device__ constexpr int few_smem(int rows, int d) {
   return few_warps(rows) * (few_ring_bytes(rows, d) + rows * 8 + few_stages(rows, d) * 8) + 16;
 }
 
-// PLANNED: the table of sequences behind that
+// PLANNED: the table of sequences, and where the CTA's share of them begins and
+// ends, behind that
 __host__ __device__ constexpr int few_table(int rows, int d) { return (few_smem(rows, d) + 15) / 16 * 16; }
-__host__ __device__ constexpr int few_planned_smem(int rows, int d) { return few_table(rows, d) + static_cast<int>(sizeof(AttnTable)); }
+__host__ __device__ constexpr int few_planned_smem(int rows, int d) { return few_table(rows, d) + static_cast<int>(sizeof(AttnTable)) + 16; }
 
 template <typename T>
 __device__ __forceinline__ void few_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -90,9 +91,20 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(smem + few_table(ROWS, D));
-  if (PLANNED && p.from == kFromTable) {
+  int2* share = reinterpret_cast<int2*>(smem + few_table(ROWS, D) + sizeof(AttnTable));
+  if (PLANNED && (p.from == kFromTable || p.from == kFromShares)) {
     if (warp == 0) plan_table(p.seqs, table, lane, p.status);
     __syncthreads();
+    if (p.from == kFromShares) {
+      if (threadIdx.x < 2) {
+        const int c = static_cast<int>(blockIdx.x + threadIdx.x), ctas = static_cast<int>(gridDim.x);
+        share[threadIdx.x] = table_span(table, p.seqs, p.least, ctas, c);
+        // for the join: where the share begins (the last CTA: and ends)
+        if ((threadIdx.x == 0 || c == ctas) && in_span(p.plan.spans + c, 8, p.plan.sp, p.status))
+          p.plan.spans[c] = share[threadIdx.x];
+      }
+      __syncthreads();
+    }
   }
   const int group = PLANNED ? p.few_group : WARPS, grp = PLANNED ? warp / group : 0, gw = warp - grp * group;
   const int groups = PLANNED ? WARPS / group : 1;
@@ -100,7 +112,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
   bool ok = true;
   AttnWork w;
   AttnPiece piece;
-  for (int s = grp; ok && (PLANNED ? attn_piece<true>(p, table, s, piece) : attn_work(p, s, w)); s += groups) {
+  for (int s = grp; ok && (PLANNED ? attn_piece<true>(p, table, share, s, piece) : attn_work(p, s, w)); s += groups) {
     // rows row0 + r, r < rows, of key head hk: query (row0 + r) % queries of head (row0 + r) / queries of its group
     int b, hk, row0, rows, q_len, k_len, queries;
     if (PLANNED) {
@@ -112,6 +124,14 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
       k_len = piece.k_len;
       rows = min(p.group * q_len - row0, p.few_rows);
       w.slot = piece.slot;
+      if (p.from == kFromShares && gw == 0 && lane == 0 && w.slot == 2 * static_cast<int>(blockIdx.x) + 1) {
+        // for the join: a tile that others end
+        int4* at = p.plan.items + 2LL * blockIdx.x;
+        if (in_span(at, 32, p.plan.sp, p.status)) {
+          at[0] = make_int4(piece.q_row, piece.q_len, piece.k_row, piece.k_len);
+          at[1] = make_int4(piece.t0, piece.h, 0, 0);
+        }
+      }
     } else {
       const int key_head = w.tile / p.tiles;
       b = key_head / p.heads_k;

@@ -71,13 +71,15 @@ constexpr int kTableSeqs = 32;
 struct AttnTable {
   int4 seqs[kTableSeqs];      // q row, q_len, k row, k_len
   int first[kTableSeqs + 1];  // items before
-  int q_tiles[kTableSeqs];    // query tiles before
+  int before[kTableSeqs + 1]; // query tiles before; a few queries: units of a head's items before
 };
 
 // Where no plan is needed either: one sequence whose tiles all cost the same
 // (kFromUniform), or samples of a fixed number of rows whose tiles all go out
 // whole, each working out its own lengths (kFromSamples; a few queries).
-enum { kFromPlan, kFromTable, kFromUniform, kFromSamples };
+// kFromShares: the table's sequences in equal shares, cut inside a tile (a few
+// queries): 16 x 1 query over up to 4096 keys of 24 heads x 128 68 us, 73 with a plan.
+enum { kFromPlan, kFromTable, kFromShares, kFromUniform, kFromSamples };
 struct AttnUniform {
   int tiles, units;           // of the line; of each tile
   int active;                 // CTAs that get a share (0: tiles go out whole)
@@ -143,6 +145,7 @@ struct AttnParams {
   int from;                   // kFrom...: where tiles come from
   AttnUniform uniform;
   int few_rows, few_group;    // a few queries: rows of a tile, warps on a tile
+  int least;                  // kFromShares: units of a share at least
   int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
   int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
   // PREFIX
@@ -432,8 +435,51 @@ __device__ __forceinline__ void plan_table(const AttnSeqs& j, AttnTable& out, in
   }
   out.seqs[lane] = s;
   out.first[lane] = n - mine_n;
-  out.q_tiles[lane] = q - mine_q;
   if (lane == 31) out.first[32] = n;
+  if (j.kind != kPlanFew) {
+    out.before[lane] = q - mine_q;
+    return;
+  }
+  const int mine_u = mine_n * (plan_blocks(j, 0, s.y, s.w) + j.over);
+  int u = mine_u;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, u, off);
+    if (lane >= off) u += a;
+  }
+  out.before[lane] = u - mine_u;
+  if (lane == 31) out.before[32] = u;
+}
+
+// The last sequence of the table that begins at or before `at` (of first or before).
+__device__ __forceinline__ int table_find(const int (&from)[kTableSeqs + 1], int at) {
+  int b = 0;
+#pragma unroll
+  for (int step = kTableSeqs / 2; step >= 1; step >>= 1)
+    if (from[b + step] <= at) b += step;
+  return b;
+}
+
+// kFromShares: where CTA c's share begins, (tile, unit).  Shares are equal
+// stretches of the line that has a head's items in the sequences' order: keys
+// of a few queries are read once, so that neighbours have nothing to share.
+__device__ __forceinline__ int2 table_span(const AttnTable& table, const AttnSeqs& j, int least, int ctas, int c) {
+  const int items = table.first[kTableSeqs], units = table.before[kTableSeqs];
+  const long long work = static_cast<long long>(units) * j.heads;
+  const int tiles = items * j.heads;
+  long long active = work / least;
+  if (active > ctas) active = ctas;
+  if (active < 1) active = 1;
+  const long long x = c < active ? work / active * c + work % active * c / active : work;
+  if (x >= work) return make_int2(tiles, 0);
+  const int h = static_cast<int>(x / units), off = static_cast<int>(x - static_cast<long long>(h) * units);
+  const int b = table_find(table.before, off), u = plan_blocks(j, 0, table.seqs[b].y, table.seqs[b].w) + j.over;
+  int tile = h * items + table.first[b] + (off - table.before[b]) / u, o = (off - table.before[b]) % u;
+  if (o < 2 || u - o < j.over + 2) {              // as attn_plan_kernel
+    tile += 2 * o >= u;
+    o = 0;
+  }
+  return make_int2(tile, o);
 }
 
 // Where CTA c's share of a uniform line begins: (tile, unit).
@@ -461,8 +507,9 @@ struct AttnPiece {
   int h, e, u0, u1, slot;     // head line, item; units [u0, u1) of its contraction
   int q_row, q_len, k_row, k_len, t0, blocks, tiles0;
 };
+// `share` (kFromShares): where it begins and ends.
 template <bool FORWARD>
-__device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable& table, int s, AttnPiece& w) {
+__device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable& table, const int2* share, int s, AttnPiece& w) {
   const int c = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
   int tile = s * ctas + (s & 1 ? ctas - 1 - c : c);
   w.u0 = 0;
@@ -473,10 +520,7 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     if (tile >= n * p.seqs.heads) tile = 0, w.u0 = 1;           // nothing for this CTA in the last wave
     w.h = tile / n;
     w.e = tile - w.h * n;
-    int b = 0;
-#pragma unroll
-    for (int step = kTableSeqs / 2; step >= 1; step >>= 1)
-      if (table.first[b + step] <= w.e) b += step;
+    const int b = table_find(table.first, w.e);
     const int4 q = table.seqs[b];
     w.q_row = q.x;
     w.q_len = q.y;
@@ -485,9 +529,30 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     const int t = w.e - table.first[b];
     w.t0 = t * p.seqs.rows;
     w.blocks = plan_blocks(p.seqs, t, q.y, q.w);
-    w.tiles0 = table.q_tiles[b];
+    w.tiles0 = table.before[b];
     w.u1 = w.blocks + p.seqs.over;
     return w.u0 == 0;
+  }
+  if (FORWARD && share != nullptr && p.from == kFromShares) {
+    const int2 from = share[0], to = share[1];
+    tile = from.x + s;
+    if (tile > to.x || (tile == to.x && to.y == 0)) return false;
+    const int n = table.first[kTableSeqs];
+    w.h = tile / n;
+    w.e = tile - w.h * n;
+    const int b = table_find(table.first, w.e);
+    const int4 q = table.seqs[b];
+    w.q_row = q.x;
+    w.q_len = q.y;
+    w.k_row = q.z;
+    w.k_len = q.w;
+    w.t0 = (w.e - table.first[b]) * p.seqs.rows;
+    w.blocks = plan_blocks(p.seqs, 0, q.y, q.w);
+    w.tiles0 = 0;
+    if (s == 0) w.u0 = from.y;
+    w.u1 = tile == to.x ? to.y : w.blocks + p.seqs.over;
+    w.slot = w.u0 > 0 ? 2 * c : tile == to.x ? 2 * c + 1 : -1;
+    return w.u0 <= w.u1;
   }
   if (FORWARD && p.from >= kFromUniform) {
     const AttnUniform& u = p.uniform;
@@ -747,7 +812,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece<true>(p, table, s, piece)) return false;
+      if (!attn_piece<true>(p, table, nullptr, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
@@ -1464,7 +1529,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
   auto work_out = [&](int s, Seg& g) {
     if (PLANNED) {
       AttnPiece piece;
-      if (!attn_piece<false>(p, table, s, piece)) return false;
+      if (!attn_piece<false>(p, table, nullptr, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.q0 = piece.t0;
@@ -1976,7 +2041,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     AttnWork w;
     AttnPiece piece;
     if (PLANNED) {
-      if (!attn_piece<false>(p, table, s, piece)) return false;
+      if (!attn_piece<false>(p, table, nullptr, s, piece)) return false;
       g.b = 0;
       g.h = piece.h;
       g.k0 = piece.t0;

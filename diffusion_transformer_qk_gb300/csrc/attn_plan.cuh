@@ -404,10 +404,17 @@ __global__ void __launch_bounds__(256) plan_join_forward_kernel(const __grid_con
   const int tile = plan_cut_tile(p.plan, c, p.status);
   if (tile < 0) return;
   const PlanParts parts = plan_parts(p.plan, ctas, tile, lane, p.status);
-  const int2 at = plan_tile(p.plan, p.seqs.heads, tile);
-  const int head = at.x;
+  int head, item;
+  if (FEW && p.from == kFromShares) {             // the CTA that began the tile has written it down
+    item = parts.c;
+    head = p.plan.items[2LL * item + 1].y;
+  } else {
+    const int2 at = plan_tile(p.plan, p.seqs.heads, tile);
+    head = at.x;
+    item = at.y;
+  }
   const PartsView view{p.part, p.stats, p.sp_part, p.sp_stats};
-  const int4 s = p.plan.items[2LL * at.y], w = p.plan.items[2LL * at.y + 1];
+  const int4 s = p.plan.items[2LL * item], w = p.plan.items[2LL * item + 1];
   for (int r = (static_cast<int>(blockIdx.x) % N) * 8 + warp; r < rows; r += 8 * N) {
     const int x = w.x + r;
     if (x >= (FEW ? s.y * p.group : s.y)) return;

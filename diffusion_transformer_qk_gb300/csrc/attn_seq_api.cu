@@ -272,8 +272,11 @@ constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k, p->batch ? p->rows_k / p->batch : 0);
-  if (table_does(s->job[0], p->batch)) s->job[0].from = qknr::kFromTable;
-  else s->plan[0] = take_plan(ws, s->job[0].items, p->batch, false);
+  Job& j = s->job[0];
+  if (table_does(j, p->batch)) j.from = qknr::kFromTable;
+  else if (is_few(j) && p->batch <= qknr::kTableSeqs && static_cast<double>(j.items) * static_cast<double>(j.units) < 2e9)
+    j.from = qknr::kFromShares;                   // its spans and cut tiles' records take a plan's place
+  if (j.from != qknr::kFromTable) s->plan[0] = take_plan(ws, j.items > kCtas ? j.items : kCtas, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
 }
 
@@ -517,6 +520,7 @@ qknr_status qknr_pack_forward(const qknr_pack_args* p, qknr_stream_t stream) {
   kp.from = s.job[0].from;
   kp.few_rows = s.job[0].rows;
   kp.few_group = s.job[0].few_group;
+  kp.least = kLeastFew;
   kp.slot_rows = s.job[0].slot_rows;
   kp.q_in = static_cast<const char*>(p->q);
   kp.q_stride = q.stride * 2;

@@ -373,3 +373,30 @@ def test_more_items_than_the_plan_sorts():
         ref = Q.attention_backward(do, q, k, v, o[pick].contiguous(), mine, 2, 1, 64, **kw)
         for a, b in zip(grads, ref):
             assert (a[pick].float() - b.float()).abs().max() <= 4 * 2.0 ** -8 * max(1.0, float(b.float().abs().max()))
+
+
+def test_outputs_beside_inputs():
+    s = make([129, 64, 300], None, 2, 1, 64, causal=True, seed=24)
+    o, lse = call(s)
+    wide = torch.full((493, 2 * 128 + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, :128] = s["q"]
+    o2, lse2 = call(dict(s, q=wide[:, :128]), out=wide[:, 128:256])
+    assert same_bits(o, o2) and same_bits(lse, lse2)
+    assert same_bits(wide[:, :128], s["q"]) and (wide[:, 256:] == 7.0).all()
+
+
+def test_two_streams_at_once():
+    # two calls in flight, each with its own workspace from the binding
+    a, b = make([900, 30, 2000], None, 4, 2, 64, causal=True, seed=25), make([1] * 20, [700] * 20, 8, 2, 128, seed=26)
+    ref = [call(s) for s in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(call(s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert same_bits(o, ref[i][0]) and same_bits(lse, ref[i][1])

@@ -149,3 +149,37 @@ def test_waits_are_bounded():
         assert int(word.item()) == Q.ERR_TIMEOUT
         o, lse = call(s)
         check(s, o, lse)
+
+
+@pytest.mark.parametrize("B,Sq,Sk,P,Hq,Hk,D", [
+    (1, 4000, 4000, 130, 4, 4, 128),      # causal tiles as two halves, the prefix a small part
+    (3, 1, 5000, 3000, 6, 2, 64),         # own keys long enough to be cut
+    (3, 3, 5000, 200, 16, 1, 128),
+    (24, 130, 64, 20000, 2, 2, 64),       # tiles of 256 rows in both passes
+    (5, 16, 700, 9000, 3, 3, 128),
+])
+@pytest.mark.parametrize("causal", [False, True])
+def test_each_way_through(B, Sq, Sk, P, Hq, Hk, D, causal):
+    run(B, Sq, Sk, P, Hq, Hk, D, causal=causal, k_lens=None if B == 1 else [Sk - 7 * i for i in range(B)][:B] if Sk > 7 * B else None, seed=8)
+
+
+def test_a_workspace_full_of_nan():
+    # whatever a workspace held, every part that a join adds up has been written
+    for shape, heads in (((64, 1, 100, 3000), (8, 2, 128)), ((3, 1, 5000, 3000), (6, 2, 64)), ((16, 40, 64, 4000), (6, 2, 128)),
+                         ((2, 300, 300, 4000), (6, 6, 64))):
+        s = make(*shape, *heads, k_lens=[(i * 37) % (shape[2] + 1) for i in range(shape[0])], seed=9)
+        ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")
+        o, lse = call(s, workspace=ws)
+        o2, lse2 = call(s)
+        assert same_bits(o, o2) and same_bits(lse, lse2)
+        check(s, o, lse)
+
+
+def test_outputs_beside_inputs():
+    # q and o as columns of one buffer, keys of prefix and samples as columns of another
+    s, o, lse = run(40, 2, 64, 3000, 4, 2, 64, seed=10)
+    wide = torch.full((80, 2 * 256 + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    wide[:, :256] = s["q"]
+    far = dict(s, q=wide[:, :256])
+    o2, _ = call(far, out=wide[:, 256:512])
+    assert same_bits(o, o2) and same_bits(wide[:, :256], s["q"]) and (wide[:, 512:] == 7.0).all()

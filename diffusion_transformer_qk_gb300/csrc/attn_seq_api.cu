@@ -355,36 +355,46 @@ qknr_status check_prefix(const qknr_prefix_args* p, qknr_attn_args* a) {
 // Tiles of 128 rows.
 long long halves(long long rows) { return (rows + qknr::kTile - 1) / qknr::kTile; }
 
-// What the batch's `rows` queries cost on their way through the prefix
-// together, in microseconds: as a few queries, 16 rows of a key head at a time
-// with the keys read for each, or in tiles, 128 rows by 128 keys in 0.8 on an SM
-// (head_dim 64: 0.5).  (16 samples of 32 heads on 8 beside 32768 keys x 128: 98 us
-// with four passes of a few queries, 68 in tiles.)
+// Estimated times in microseconds, from measurements of both forms at some
+// forty shapes (1 to 60 samples of 1 to 600 queries beside 100 to 16000 keys).
+//
+// Of a block of 128 keys for `rows` queries of a head, on all SMs: 256 of them
+// at a time in 1.7 (head_dim 64: 1.0); 128 or fewer, whose scores, exponentials
+// and products follow each other, in 1.8 (1.5).
+double block_us(const qknr_attn_args* a, long long rows) {
+  const double both = a->head_dim == 128 ? 1.7 : 1.0, one = a->head_dim == 128 ? 1.8 : 1.5;
+  const long long rest = rows % qknr::fwd::kRows;
+  return (static_cast<double>(rows / qknr::fwd::kRows) * both + (rest == 0 ? 0.0 : rest <= qknr::kTile ? one : both)) / kCtas;
+}
+// Of the batch's `rows` queries through the prefix together: as a few queries,
+// 16 rows of a key head at a time with the keys read for each, or in tiles.  (16
+// samples of 32 heads on 8 beside 32768 keys x 128: 98 us with four passes of a few
+// queries, 68 in tiles.)
 double few_prefix(const qknr_attn_args* a, long long rows, int prefix) {
   if (!few(rows, 1)) return 1e30;
   const double passes = std::ceil(static_cast<double>(a->n_heads_q / a->n_heads_k * rows) / 16.0);
   return passes * prefix * 4.0 * a->head_dim * a->n_heads_k / 6.2e6;
 }
-double block_us(const qknr_attn_args* a) { return (a->head_dim == 128 ? 0.8 : 0.5) / kCtas; }
 double tile_prefix(const qknr_attn_args* a, long long rows, int prefix) {
   const long long group = a->n_heads_q / a->n_heads_k;
-  const double by_head = static_cast<double>(halves(rows)) * a->n_heads_q, by_group = static_cast<double>(halves(group * rows)) * a->n_heads_k;
-  return 8.0 + (by_head < by_group ? by_head : by_group) * static_cast<double>(blocks_of(prefix)) * block_us(a);
+  const double by_head = block_us(a, rows) * a->n_heads_q, by_group = block_us(a, group * rows) * a->n_heads_k;
+  return 8.0 + (by_head < by_group ? by_head : by_group) * static_cast<double>(blocks_of(prefix));
 }
 
 // Whether the queries of the whole batch go through the prefix together, as
 // one sequence, and then through their own keys.  Otherwise each sample's
-// tiles of 128 rows go through both.  A part of a row costs some 16 bytes for
-// each value to write and read, the two more launches 8 us.
+// tiles go through both, cut and joined where they are few and long.
 bool together(const qknr_attn_args* a, int prefix) {
   const double D = a->head_dim, B = a->batch, heads = a->n_heads_q, byte = 1.0 / 6.2e6;
   const long long rows = static_cast<long long>(a->batch) * a->seq_q;
-  const double halved = B * static_cast<double>(halves(a->seq_q)) * heads * block_us(a);
-  const double own = halved * static_cast<double>(blocks_of(a->seq_k)), apart = halved * static_cast<double>(blocks_of(prefix)) + own;
+  const long long np = blocks_of(prefix), nk = blocks_of(a->seq_k);
+  const double block = B * heads * block_us(a, a->seq_q);
+  const double apart = (np + nk > 12 ? 15.0 : 8.0) + block * static_cast<double>(np + nk);
   const double passes = std::ceil(heads / a->n_heads_k * a->seq_q / 16.0);
+  const double own = few(a->seq_q, 1) ? passes * B * a->seq_k * 4.0 * D * a->n_heads_k * byte : 8.0 + block * static_cast<double>(nk);
   const double few_p = few_prefix(a, rows, prefix), tile_p = tile_prefix(a, rows, prefix);
-  const double few_own = few(a->seq_q, 1) ? passes * B * a->seq_k * 4.0 * D * a->n_heads_k * byte : own;
-  return 8.0 + static_cast<double>(rows) * heads * D * 16.0 * byte + (few_p < tile_p ? few_p : tile_p) + few_own < apart;
+  // a part of a row costs some 16 bytes for each value to write and read
+  return 11.0 + static_cast<double>(rows) * heads * D * 16.0 * byte + (few_p < tile_p ? few_p : tile_p) + own < apart;
 }
 
 struct PrefixSpace {

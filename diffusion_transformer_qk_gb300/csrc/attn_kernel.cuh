@@ -1797,8 +1797,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (c.lane == 0 && in_span(at, 4, p.sp_ds_top, p.status)) *at = top;
       }
       const float lift = grad_lift<T>(bound);
-      // p = 0 for a row that sees nothing
-      const float lse2 = limit == 0 || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
+      // p = 0 for a row that sees nothing.  PLANNED: for one that sees a single key too, whose probability is 1
+      // whatever its score: dq is 0, not what rounding leaves of dp - delta.
+      const float lse2 = limit <= (PLANNED ? 1 : 0) || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
       const float nl = GradScale<T>::kP - lse2, nd = -delta * lift;
       const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
                    C = make_float2(lift, lift);
@@ -2365,6 +2366,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
           for (int a = 0; a < 2; ++a)
 #pragma unroll
             for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
+        }
+        if (PLANNED) {
+          // queries up to here see this key alone: no gradient for their scores (dq's rows of a single key)
+          const int alone = key > 0 ? 0 : g.k_len == 1 ? 64 : p.causal ? from + 1 : 0;
+          if (__any_sync(0xffffffffu, alone > 0)) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[a][e] = 32 * a + e >= alone ? s[a][e] : 0.0f;
+          }
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {

@@ -9,7 +9,9 @@
  * .. k_starts[b + 1] - 1; the starts are device arrays of batch + 1 values.
  * Formulas, scale, rounding and what a query that sees no key answers are
  * qknr_attn.h's, with q_len = q_starts[b + 1] - q_starts[b] and k_len likewise:
- * with causal, query i of a sequence sees its keys j <= i + k_len - q_len.
+ * with causal, query i of a sequence sees its keys j <= i + k_len - q_len.  A
+ * query that sees one key adds exactly nothing to dq and dk: its probability
+ * is 1 whatever its score.
  *
  * Starts are clamped to 0 .. rows, and one below an earlier one counts as the
  * largest of them, so that no row belongs to two sequences whatever they say.

@@ -400,3 +400,24 @@ def test_two_streams_at_once():
     for i in range(2):
         for o, lse in got[i]:
             assert same_bits(o, ref[i][0]) and same_bits(lse, ref[i][1])
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("fp16", 128)])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens_q,lens_k", [([2, 1, 2, 4], [1, 1, 1, 1]), ([300, 130, 1], [1, 2, 300]), ([200, 1, 70, 129], None),
+                                           ([129, 400], [65, 300])])
+def test_a_single_key_has_no_gradient_of_its_score(lens_q, lens_k, causal, dtype, D):
+    # its probability is 1 whatever the score: exact zeros, not what dp - delta leaves of rounding
+    s, o, lse, (dq, dk, dv) = both(lens_q, lens_k, 4, 2, D, dtype=dtype, causal=causal, seed=31)
+    alone = 0
+    for (a, b), (c, d) in S.sequences(s["sq"], s["sk"], s["q"].shape[0], s["k"].shape[0]):
+        if d - c == 1:
+            assert not dq[a:b].float().any() and not dk[c:d].float().any()
+            alone += 1
+        elif causal and 0 <= (b - a) - (d - c) < b - a:
+            # the first query that sees a key sees one
+            assert not dq[b - (d - c)].float().any()
+            alone += 1
+    assert alone or lens_k == [65, 300] and not causal
+    # and the others' gradients are there
+    assert dv.float().any()

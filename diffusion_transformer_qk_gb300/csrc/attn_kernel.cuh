@@ -1977,26 +1977,29 @@ __global__ void __launch_bounds__(256) attn_join_grad_kernel(const __grid_consta
 // which both kernels work out): a block's exponentials, products and
 // conversions on eight warps take about as long as its four products, and the
 // accumulators leave tensor memory no room for a second block's scores.
+// At head_dim 64 they do (kTurns 2): products take turns on three buffers.  S of
+// block j + 1 goes where dS of j - 1 was, and dP of j + 1 where P of j was, so
+// that one warp issues dV and dP, the other dK and S two blocks ahead, and the
+// eight warps find each product done when they come for it.
 
 namespace dkv {
-constexpr int kQ = 3, kO = 2;                     // Q and dO tiles in flight
-enum { K_FULL = 0, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ,
-       O_EMPTY = O_FULL + kO, S_FULL = O_EMPTY + kO, P_FULL, DP_FULL, DS_FULL, ROWS, ROWS_FREE = ROWS + 2,
-       DONE = ROWS_FREE + 2, ACC_FREE, DRAIN, BARS = DRAIN + 2 };
-__device__ __forceinline__ int arrivals(int i) {
-  if (i == P_FULL || i == DS_FULL || i == ACC_FREE || (i >= ROWS_FREE && i < DONE)) return 8;
-  // both chains are done with a tile, with the accumulators
-  return (i >= Q_EMPTY && i < O_FULL) || (i >= O_EMPTY && i < S_FULL) || i == DONE ? 2 : 1;
-}
+template <int D>
+constexpr int kTurns = D == 64 ? 2 : 1;           // blocks whose scores, or dP, may be there at once
+template <int D>
+constexpr int kQ = D == 64 ? 4 : 3;               // Q tiles in flight
+template <int D>
+constexpr int kO = D == 64 ? 3 : 2;               // dO tiles in flight
+template <int D>
+constexpr int kBars = 4 + 2 * kQ<D> + 2 * kO<D> + 4 * kTurns<D> + 8;
 constexpr int kRowBytes = 2 * 2 * kTile * 4 + 16; // two buffers of (lse, delta) of a tile's queries, and their lifts
 template <int D>
-constexpr int kCtl = (2 + kQ + kO) * kTileBytes<D> + kRowBytes;
+constexpr int kCtl = (2 + kQ<D> + kO<D>) * kTileBytes<D> + kRowBytes;
 template <int D>
-constexpr int kSmem = kCtl<D> + 256;
-constexpr int kTableAt = attn_table_at(BARS);
+constexpr int kTableAt = attn_table_at(kBars<D>);
 template <int D>
-constexpr int kPlannedSmem = kCtl<D> + kTableAt + static_cast<int>(sizeof(AttnTable));
-static_assert(8 * BARS + 8 <= 256, "shared memory behind the tiles");
+constexpr int kSmem = kCtl<D> + kTableAt<D>;
+template <int D>
+constexpr int kPlannedSmem = kSmem<D> + static_cast<int>(sizeof(AttnTable));
 
 struct Seg {
   int b, h, k0, slot;         // h: key head
@@ -2012,6 +2015,21 @@ struct Seg {
 template <typename T, int D, bool PLANNED = false>
 __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_constant__ AttnParams p) {
   using namespace dkv;
+  constexpr int kQ = dkv::kQ<D>, kO = dkv::kO<D>, kTurns = dkv::kTurns<D>, kTableAt = dkv::kTableAt<D>;
+  enum { K_FULL = 0, K_EMPTY, V_FULL, V_EMPTY, Q_FULL, Q_EMPTY = Q_FULL + kQ, O_FULL = Q_EMPTY + kQ,
+         O_EMPTY = O_FULL + kO, S_FULL = O_EMPTY + kO, P_FULL = S_FULL + kTurns, DP_FULL = P_FULL + kTurns,
+         DS_FULL = DP_FULL + kTurns, ROWS = DS_FULL + kTurns, ROWS_FREE = ROWS + 2, DONE = ROWS_FREE + 2, ACC_FREE,
+         DRAIN, BARS = DRAIN + 2 };
+  static_assert(BARS == kBars<D>, "barriers");
+  auto arrivals = [](int i) {
+    if ((i >= P_FULL && i < DP_FULL) || (i >= DS_FULL && i < ROWS) || i == ACC_FREE || (i >= ROWS_FREE && i < DONE)) return 8;
+    // both chains are done with a tile (of one turn), with the accumulators
+    const bool tile = (i >= Q_EMPTY && i < O_FULL) || (i >= O_EMPTY && i < S_FULL);
+    return (kTurns == 1 && tile) || i == DONE ? 2 : 1;
+  };
+  // a block's barrier of kTurns, and its phase
+  auto turn = [](int first, int block) { return kTurns == 1 ? first : first + (block & 1); };
+  auto lap = [](int block) { return static_cast<uint32_t>(kTurns == 1 ? block : block >> 1); };
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* ctl = smem + kCtl<D>;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(ctl + 8 * BARS);
@@ -2086,6 +2104,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
   };
   const uint32_t sk = c.base, sv = c.base + kTileBytes<D>, sq = c.base + 2 * kTileBytes<D>,
                  sdo = c.base + (2 + kQ) * kTileBytes<D>;
+  // dV's and dK's place
+  const uint32_t acc_v = tmem + (kTurns == 1 ? 2 : 3) * kTile, acc_k = acc_v + (kTurns == 1 ? kTile : D);
 
   if (c.warp >= kAttnMmaWarp) fewer_registers<kAttnIssueRegs>();
   if (c.warp == kAttnLoadWarp) {
@@ -2142,7 +2162,83 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       }
     }
     __syncwarp();
-  } else if (c.warp == kAttnMmaWarp || c.warp == kAttnMma2Warp) {
+  } else if (kTurns == 2 && (c.warp == kAttnMmaWarp || c.warp == kAttnMma2Warp)) {
+    // Two chains: dP(0), then per block dV += P^T dO, dP(next) in P's place;
+    // S(0), S(1), then per block dK += dS^T Q, S(the one after next) in dS's
+    // place.  A chain's products run in the order of their issue, so that each
+    // finds its place free.  (`ahead`: the tile of the chain's next S or dP,
+    // `at`: of its next sum.)
+    const bool v_chain = c.warp == kAttnMmaWarp;
+    const int ring = v_chain ? kO : kQ, full = v_chain ? O_FULL : Q_FULL, empty = v_chain ? O_EMPTY : Q_EMPTY;
+    const uint32_t left = v_chain ? sv : sk, tiles = v_chain ? sdo : sq, acc = v_chain ? acc_v : acc_k;
+    const int score_full = v_chain ? DP_FULL : S_FULL, sum_full = v_chain ? P_FULL : DS_FULL;
+    const int left_full = v_chain ? V_FULL : K_FULL, left_empty = v_chain ? V_EMPTY : K_EMPTY;
+    const int lead = v_chain ? 1 : 2;             // blocks from a sum to the scores that take its place
+    int ahead = 0, at = 0;
+    uint32_t ahead_phase = 0;
+    int done = 0, scores = 0, live = 0;           // blocks, scores issued and tiles so far
+    // Block j's P^T and dS^T lie in buffers 2 j and 2 j + 1 (mod 3), and the
+    // chain's scores of block j + lead after them.
+    int place = v_chain ? 0 : 1;                  // of the next sum
+    int score_place = v_chain ? 1 : 0;            // of the next scores
+    bool ok = true;
+    Seg g;
+    for (int s = 0; ok && segment(s, g); ++s) {
+      if (g.n == 0) continue;
+      const int n = g.n;
+      const bool ragged = PLANNED || g.q_len < p.seq_q;
+      int t = g.t0, issued = 0;                   // the query tile of the next scores; scores of this tile so far
+      // the next scores' tile has landed: nothing past the sample's queries
+      auto arrived = [&]() {
+        if (!c.wait(full + ahead, ahead_phase)) return false;
+        if (ragged && (t + 1) * kTile > g.q_len) zero_rows<D>(smem + (tiles - c.base) + ahead * kTileBytes<D>, g.q_len - t * kTile, c.lane);
+        return true;
+      };
+      auto issue = [&]() {                        // one thread
+        mma_rows<T, D>(tmem + score_place * kTile, left, tiles + ahead * kTileBytes<D>);
+        mma_commit(c.bar(turn(score_full, scores)));
+        if (issued + 1 == n) mma_commit(c.bar(left_empty));
+      };
+      auto step = [&]() {
+        ++scores;
+        ++issued;
+        score_place = score_place == 0 ? 2 : score_place - 1;   // + 2 mod 3
+        if (++ahead == ring) {
+          ahead = 0;
+          ahead_phase ^= 1u;
+        }
+        if (++t == g.end) t = g.first;
+      };
+      ok = c.wait(left_full, live);
+      while (ok && issued < lead && issued < n) {
+        ok = arrived();
+        if (!ok) break;
+        if (elect_one()) issue();
+        __syncwarp();
+        step();
+      }
+      for (int i = 0; ok && i < n; ++i, ++done) {
+        const bool more = issued < n;
+        // the accumulators have been read for the tile before
+        ok = (!more || arrived()) && (i > 0 || live == 0 || c.wait(ACC_FREE, live - 1)) &&
+             c.wait(turn(sum_full, done), lap(done));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          mma_cols<T, D, true>(acc, tmem + place * kTile, tiles + at * kTileBytes<D>, i > 0);
+          mma_commit(c.bar(empty + at));
+          if (i + 1 == n) mma_commit(c.bar(DONE));
+          if (more) issue();
+        }
+        __syncwarp();
+        place = place == 0 ? 2 : place - 1;
+        if (++at == ring) at = 0;
+        if (more) step();
+      }
+      ++live;
+    }
+    if (!ok) c.drain_mma(DRAIN + (v_chain ? 0 : 1));
+  } else if (kTurns == 1 && (c.warp == kAttnMmaWarp || c.warp == kAttnMma2Warp)) {
     // Two chains of the same form: S(0), then per block dV += P^T dO, S(next);
     // dP(0), then per block dK += dS^T Q, dP(next).  (`a`: the tile of the
     // chain's first product, `b`: of its second.)
@@ -2298,7 +2394,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
     // a thread per key and half of the block's queries
     const int half = c.warp >> 2, r = (c.warp & 3) * 32 + c.lane;
     const uint32_t lanes = static_cast<uint32_t>(c.warp & 3) << 21;
-    const uint32_t ts = tmem + half * 64 + lanes, tdp = tmem + kTile + half * 64 + lanes;
+    int s_at = 0, dp_at = 1;                      // the block's buffers
     const float2 SL = make_float2(p.scale_log2, p.scale_log2);
     int done = 0, live = 0;                       // blocks and tiles so far
     bool ok = true;
@@ -2311,7 +2407,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
         const float* mine = rows + (done & 1) * 2 * kTile;
         const float4* nl = reinterpret_cast<const float4*>(mine + half * 64);
         const float4* nd = reinterpret_cast<const float4*>(mine + kTile + half * 64);
-        ok = c.wait(ROWS + (done & 1), done >> 1) && c.wait(S_FULL, done);
+        const uint32_t ts = tmem + s_at * kTile + half * 64 + lanes, tdp = tmem + dp_at * kTile + half * 64 + lanes;
+        ok = c.wait(ROWS + (done & 1), done >> 1) && c.wait(turn(S_FULL, done), lap(done));
         if (!ok) break;
         tc_fence_after();
         if (GradScale<T>::kFromData) lift = lifts[done & 1];
@@ -2352,8 +2449,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
           tmem_store16(ts + 16 * a, w);
         }
         tmem_wait_store();
-        c.arrive(P_FULL);
-        ok = c.wait(DP_FULL, done);
+        c.arrive(turn(P_FULL, done));
+        ok = c.wait(turn(DP_FULL, done), lap(done));
         if (!ok) break;
         tc_fence_after();
         float d[2][32];
@@ -2394,8 +2491,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
           tmem_store16(tdp + 16 * a, w);
         }
         tmem_wait_store();
-        c.arrive(DS_FULL);
+        c.arrive(turn(DS_FULL, done));
         if (c.lane == 0) mbar_arrive(c.bar(ROWS_FREE + (done & 1)));
+        if (kTurns == 2) {
+          const int next = 3 - s_at - dp_at;
+          dp_at = s_at;
+          s_at = next;
+        }
       }
       if (!ok) break;
       // the first group writes dv, the second dk
@@ -2418,7 +2520,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
       for (int i = 0; i < D / 32; ++i) {
         float v[32];
         if (g.n > 0) {
-          tmem_load32(tmem + (2 + half) * kTile + 32 * i + lanes, v);
+          tmem_load32((half ? acc_k : acc_v) + 32 * i + lanes, v);
           tmem_wait_load(v);
           if (i == D / 32 - 1) c.arrive(ACC_FREE);
         }

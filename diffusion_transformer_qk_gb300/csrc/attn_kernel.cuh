@@ -1346,7 +1346,11 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
   constexpr int L = D / 8, TEAMS = 256 / L;
   const int team = threadIdx.x / L, lane = threadIdx.x % L;
   const long long items = static_cast<long long>(p.batch) * p.seq_q * p.heads_q;
-  grid_dependency_wait();
+  // A plan lets this pass begin once all before it has ended, and runs beside
+  // it: only the rows of v that count wait for the plan (gradients of 9215
+  // tokens x 16 on 4 x 64: 171 us without, 166 so).
+  const bool beside_plan = PLANNED && p.from == kFromPlan;
+  if (!beside_plan) grid_dependency_wait();
   // (row, head) with the heads of a row next to each other
   for (long long first = static_cast<long long>(blockIdx.x) * TEAMS; first < items;
        first += static_cast<long long>(gridDim.x) * TEAMS) {
@@ -1386,6 +1390,7 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
       }
     }
   }
+  if (beside_plan) grid_dependency_wait();        // and who waits for this pass has waited for the plan
   if (GradScale<T>::kFromData) {
     // No row of v that counts is longer than this: a lane keeps the largest sum
     // of its 8 columns, and a team's rows all stay below the sum over its lanes

@@ -205,7 +205,7 @@ inline Cut cut_tiles(const qknr_attn_args* a, int seq, int heads, int rows, long
   // A causal mask's tiles cost 1 to `blocks` iterations, so that equal shares
   // of the cheap ones left over gain nothing.  They go out whole, the costly
   // ones first, every other wave the other way round (backward of 3 x 1999 x 16
-  // on 4 heads x 64: 147 us, 189 with the rest shared out); or all as two
+  // on 4 heads x 64: 133 us, 169 with the rest shared out); or all as two
   // halves, where a costly one alone takes longer than an even spread would:
   // by more than the 32 iterations that partial results of all tiles cost
   // (backward of 8192 x 24 on 3 heads x 128: 189 more, 980 against 1136 us;

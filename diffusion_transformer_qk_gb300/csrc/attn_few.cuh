@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     fence_barrier_init();
   }
   __syncthreads();
-  grid_dependency_wait();
+  const bool beside = PLANNED && p.beside;
+  if (!beside) grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(smem + few_table(ROWS, D));
   int2* share = reinterpret_cast<int2*>(smem + few_table(ROWS, D) + sizeof(AttnTable));
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(cons
     fence_async_shared();
     ok = PLANNED ? named_barrier_and(1 + grp, 32 * group, ok) : !__syncthreads_or(!ok);
   }
+  if (beside) grid_dependency_wait();
 }
 
 }  // namespace qknr

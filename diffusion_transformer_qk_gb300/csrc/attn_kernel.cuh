@@ -146,6 +146,8 @@ struct AttnParams {
   AttnUniform uniform;
   int few_rows, few_group;    // a few queries: rows of a tile, warps on a tile
   int least;                  // kFromShares: units of a share at least
+  int beside;                 // forward: the launch before this one waited for all before it, and writes nothing this one
+                              // reads: no wait at the start, and one at the end for those who wait for this launch
   int keep;                   // every tile's result goes to a slot: those that are not cut to 2 * CTAs + tile
   int slot_rows;              // forward: rows of a slot, 128 where no sequence has more queries, else 256
   // PREFIX
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
-  grid_dependency_wait();
+  if (!(PLANNED && p.beside)) grid_dependency_wait();
   grid_dependents_launch();
   AttnTable& table = *reinterpret_cast<AttnTable*>(ctl + kTableAt);
   if (PLANNED && p.from == kFromTable) {
@@ -1182,6 +1184,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_forward_kernel(const __g
     tc_fence_after();
     tmem_free(tmem, 512);
   }
+  if (PLANNED && p.beside) grid_dependency_wait();
 }
 
 // The parts of the r-th tile that was cut, `tile`: count of them; where it was

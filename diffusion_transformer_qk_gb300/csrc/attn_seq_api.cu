@@ -790,6 +790,11 @@ qknr_status qknr_prefix_forward(const qknr_prefix_args* p, qknr_stream_t stream)
     w.few_group = j.few_group;
     w.slot_rows = j.slot_rows;
     w.keep = 1;
+    // Neither pass needs the other's results: the second's CTAs begin where
+    // the first's have ended (4 samples' query beside 1000 keys and 100 of their
+    // own, 24 x 128: 14.1 us on the device, 19.5 where they wait; 256 beside 4096
+    // and 128, 32 on 8: 75 against 84; 64 x 32 queries beside 8192: 292 against 289).
+    w.beside = i == 1 && sides[0].seq_k > 0;
     w.part = parts[i].part;
     w.stats = parts[i].stats;
     w.sp_part = parts[i].sp_part;

@@ -355,8 +355,8 @@ qknr_status check_prefix(const qknr_prefix_args* p, qknr_attn_args* a) {
 // Tiles of 128 rows.
 long long halves(long long rows) { return (rows + qknr::kTile - 1) / qknr::kTile; }
 
-// Estimated times in microseconds, from measurements of both forms at some
-// forty shapes (1 to 60 samples of 1 to 600 queries beside 100 to 16000 keys).
+// Estimated times in microseconds, from measurements of both forms at 120
+// shapes (1 to 64 samples of 1 to 600 queries beside 100 to 16000 keys).
 //
 // Of a block of 128 keys for `rows` queries of a head, on all SMs: 256 of them
 // at a time in 1.7 (head_dim 64: 1.0); 128 or fewer, whose scores, exponentials
@@ -391,10 +391,15 @@ bool together(const qknr_attn_args* a, int prefix) {
   const double block = B * heads * block_us(a, a->seq_q);
   const double apart = (np + nk > 12 ? 15.0 : 8.0) + block * static_cast<double>(np + nk);
   const double passes = std::ceil(heads / a->n_heads_k * a->seq_q / 16.0);
-  const double own = few(a->seq_q, 1) ? passes * B * a->seq_k * 4.0 * D * a->n_heads_k * byte : 8.0 + block * static_cast<double>(nk);
+  const double own = few(a->seq_q, 1) ? passes * B * a->seq_k * 4.0 * D * a->n_heads_k * byte
+                                     : 20.0 + block * static_cast<double>(nk);   // a plan, then tiles
   const double few_p = few_prefix(a, rows, prefix), tile_p = tile_prefix(a, rows, prefix);
   // a part of a row costs some 16 bytes for each value to write and read
-  return 11.0 + static_cast<double>(rows) * heads * D * 16.0 * byte + (few_p < tile_p ? few_p : tile_p) + own < apart;
+  const double both = 6.0 + static_cast<double>(rows) * heads * D * 16.0 * byte + (few_p < tile_p ? few_p : tile_p) + own;
+  // A call outside a graph takes as long as the host needs for three launches,
+  // or for one: both times count.  (33 x 1 query beside 485 keys and 18, 4 heads x
+  // 64: 30 against 21 us called one by one, much the same in a graph.)
+  return both + std::fmax(both, 28.0) < apart + std::fmax(apart, 20.0);
 }
 
 struct PrefixSpace {

@@ -421,3 +421,39 @@ def test_a_single_key_has_no_gradient_of_its_score(lens_q, lens_k, causal, dtype
     assert alone or lens_k == [65, 300] and not causal
     # and the others' gradients are there
     assert dv.float().any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_calls_on_one_workspace_in_a_row(D):
+    # passes of one call run beside each other, calls do not: with one workspace for all of them, nothing waited for
+    a = make([2800, 591, 619], None, 12, 12, D, dtype="fp16", seed=41, garbage=False)
+    b = make([1100, 900, 40, 1500], None, 8, 2, D, dtype="fp16", causal=True, seed=42, garbage=False)
+    gen = np.random.Generator(np.random.PCG64(43))
+    q, k, v, pk, pv = (normal(gen, (n, H * D), torch.float16, 1.0)
+                       for n, H in ((48, 8), (48 * 64, 2), (48 * 64, 2), (3000, 2), (3000, 2)))
+
+    at = [ints(s["sq"]) for s in (a, b)]
+
+    def calls(**kw):
+        got = []
+        for s, sq in zip((a, b), at):
+            args = (s["Hq"], s["Hk"], s["D"], sq)
+            kw.update(scale=s["scale"], causal=s["causal"])
+            o, lse = Q.attention_packed(s["q"], s["k"], s["v"], *args, **kw)
+            got += [o, lse, *Q.attention_packed_backward(s["do"], s["q"], s["k"], s["v"], o, lse, *args, **kw)]
+            got += Q.attention_prefix(q, k, v, pk, pv, 8, 2, D, batch=48, **kw)
+        return got
+
+    apart = calls()
+    torch.cuda.synchronize()
+    ws = torch.full((1 << 28,), 255, dtype=torch.uint8, device="cuda")
+    rounds = [calls(workspace=ws) for _ in range(4)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        captured = calls(workspace=ws)
+    for _ in range(4):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in (*rounds, captured):
+        assert all(same_bits(x, y) for x, y in zip(got, apart))

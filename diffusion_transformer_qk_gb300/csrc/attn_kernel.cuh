@@ -34,6 +34,7 @@
 // blocks of a prefix, the same for every sample, before a sample's own.
 #pragma once
 
+#include "attn_share.cuh"
 #include "tc.cuh"
 
 namespace qknr {
@@ -476,12 +477,8 @@ __device__ __forceinline__ int2 table_span(const AttnTable& table, const AttnSeq
   if (x >= work) return make_int2(tiles, 0);
   const int h = static_cast<int>(x / units), off = static_cast<int>(x - static_cast<long long>(h) * units);
   const int b = table_find(table.before, off), u = plan_blocks(j, 0, table.seqs[b].y, table.seqs[b].w) + j.over;
-  int tile = h * items + table.first[b] + (off - table.before[b]) / u, o = (off - table.before[b]) % u;
-  if (o < 2 || u - o < j.over + 2) {              // as attn_plan_kernel
-    tile += 2 * o >= u;
-    o = 0;
-  }
-  return make_int2(tile, o);
+  const int tile = h * items + table.first[b] + (off - table.before[b]) / u, o = share_cut((off - table.before[b]) % u, u, j.over);
+  return o == u ? make_int2(tile + 1, 0) : make_int2(tile, o);
 }
 
 // Where CTA c's share of a uniform line begins: (tile, unit).
@@ -489,12 +486,8 @@ __device__ __forceinline__ int2 uniform_span(const AttnUniform& u, int over, int
   const long long work = static_cast<long long>(u.tiles) * u.units;
   if (c >= u.active) return make_int2(u.tiles, 0);
   const long long x = work / u.active * c + work % u.active * c / u.active;
-  int tile = static_cast<int>(x / u.units), o = static_cast<int>(x - static_cast<long long>(tile) * u.units);
-  if (o < 2 || u.units - o < over + 2) {          // as attn_plan_kernel
-    tile += 2 * o >= u.units;
-    o = 0;
-  }
-  return make_int2(tile, o);
+  const int tile = static_cast<int>(x / u.units), o = share_cut(static_cast<int>(x - static_cast<long long>(tile) * u.units), u.units, over);
+  return o == u.units ? make_int2(tile + 1, 0) : make_int2(tile, o);
 }
 
 // (head, item) of a tile of the line: items of one cost go head by head.

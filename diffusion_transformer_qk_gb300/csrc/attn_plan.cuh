@@ -273,13 +273,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
         }
         const int first = run_of(lo).x, u = static_cast<int>(before(lo + 1) - before(lo));
         const V off = x - before(first) * H;
-        int tile = first * H + static_cast<int>(off / u), o = static_cast<int>(off % u);
-        // no cut where it saves little: within two blocks of an end
-        if (o < 2 || u - o < j.over + 2) {
-          tile += 2 * o >= u;
-          o = 0;
-        }
-        at = make_int2(tile, o);
+        const int tile = first * H + static_cast<int>(off / u), o = share_cut(static_cast<int>(off % u), u, j.over);
+        at = o == u ? make_int2(tile + 1, 0) : make_int2(tile, o);
       }
     }
     if (in_span(out.spans + c, 8, out.sp, p.status)) out.spans[c] = at;

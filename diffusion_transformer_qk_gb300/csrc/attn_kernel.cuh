@@ -1285,7 +1285,8 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
 // of v's rows): with 2^e <= b < 2^(e+1), 2^14 P (dP - delta) 2^-e stays below
 // 2^15, and half a subnormal step is 2^-39 b.  In dq a row is a query and has a
 // factor of its own; in dk all queries of a sample's key head go into one sum
-// and share the largest b.  At 4096 x 24 x 128 the bounds cost 20 us (4 %), at
+// and share the largest b.  Packed sequences take |do| V + |delta|, which is no
+// more and holds for an o over other keys too.  At 4096 x 24 x 128 the bounds cost 20 us (4 %), at
 // 8 x 1 x 4096 x 24 x 128, where v's 200 MB are read once more for them, 34 of
 // 390.
 template <typename T>
@@ -1316,6 +1317,18 @@ template <typename T>
 __device__ __forceinline__ float grad_unlift(float lift) {
   const float down = grad_scale_down(GradScale<T>::kP);
   return GradScale<T>::kFromData ? __uint_as_float((254u << 23) - __float_as_uint(lift)) * down : down;
+}
+
+// Whether the probability of the one key that a query sees (2^kP times it: `p`)
+// is 1 as far as fp32 can tell: the gradient of that score is then 0, and not
+// what rounding leaves of dP - delta.  `nl` is kP - lse (log2).  Score and
+// log-sum are good to 2^-20 of the log-sum, or 2^-13 where the score's terms
+// cancel; a lse over other calls' keys too that leaves them less than 2^-13 of
+// the probability leaves this key's gradient below the rounding of o in delta
+// (half a step of fp16: 2^-11).
+template <typename T>
+__device__ __forceinline__ bool only_key(float p, float nl) {
+  return fabsf(__fmaf_rn(p, grad_scale_down(GradScale<T>::kP), -1.0f)) <= __fmaf_rn(fabsf(nl), 0x1p-20f, 0x1p-13f);
 }
 
 __device__ __forceinline__ float square_sum(const float2 (&v)[4]) {
@@ -1778,7 +1791,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         lse = p.lse[at];
         delta = p.delta[at];
         if (GradScale<T>::kFromData && in_span(p.dout_norm + at, 4, p.sp_dout_norm, p.status))
-          bound = __fmul_rn(2.0f * v_top, p.dout_norm[at]);
+          bound = PLANNED ? __fmaf_rn(v_top, p.dout_norm[at], fabsf(delta)) : __fmul_rn(2.0f * v_top, p.dout_norm[at]);
       }
     };
     unsigned char* stage = smem + (1 + kK + kV) * kTileBytes<D> + c.warp * kStage<D>;
@@ -1798,9 +1811,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         if (c.lane == 0 && in_span(at, 4, p.sp_ds_top, p.status)) *at = top;
       }
       const float lift = grad_lift<T>(bound);
-      // p = 0 for a row that sees nothing.  PLANNED: for one that sees a single key too, whose probability is 1
-      // whatever its score: dq is 0, not what rounding leaves of dp - delta.
-      const float lse2 = limit <= (PLANNED ? 1 : 0) || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
+      // p = 0 for a row that sees nothing
+      const float lse2 = limit == 0 || lse == -INFINITY ? INFINITY : __fmul_rn(lse, kLog2e);
       const float nl = GradScale<T>::kP - lse2, nd = -delta * lift;
       const float2 SL = make_float2(p.scale_log2, p.scale_log2), NL = make_float2(nl, nl), ND = make_float2(nd, nd),
                    C = make_float2(lift, lift);
@@ -1849,6 +1861,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
               d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
             }
         }
+        if (PLANNED && limit == 1 && seen == 1 && only_key<T>(s[0][0], nl)) s[0][0] = 0.0f;
         if (done > 0) {
           // dQ has read the dS of the block before
           ok = c.wait(DS_FREE, done - 1);
@@ -2467,13 +2480,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
             for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
         }
         if (PLANNED) {
-          // queries up to here see this key alone: no gradient for their scores (dq's rows of a single key)
+          // queries up to here see this key alone
           const int alone = key > 0 ? 0 : g.k_len == 1 ? 64 : p.causal ? from + 1 : 0;
           if (__any_sync(0xffffffffu, alone > 0)) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[a][e] = 32 * a + e >= alone ? s[a][e] : 0.0f;
+              for (int e = 0; e < 32; ++e)
+                if (32 * a + e < alone && only_key<T>(s[a][e], mine[half * 64 + 32 * a + e])) s[a][e] = 0.0f;
           }
         }
 #pragma unroll

@@ -1626,8 +1626,9 @@ def attention_packed_backward(do, q, k, v, o, lse, n_heads_q, n_heads_k, head_di
                               dev_status=None, flags=0, wait_limit_ns=0):
     """Gradients of ``attention_packed`` from do, its inputs and its outputs o
     and lse: returns (dq, dk, dv), new tensors unless given (column views of
-    one packed buffer are fine).  Rows that belong to no sequence keep what
-    they held."""
+    one packed buffer are fine).  With o and lse over more keys than the call
+    has (keys split over calls) they are its keys' part.  Rows that belong to
+    no sequence keep what they held."""
     key = ("pack_bwd", _meta(do), _meta(q), _meta(k), _meta(v), _meta(o), n_heads_q, n_heads_k, head_dim, _meta(q_starts),
            _meta(k_starts), scale, causal, _meta(dq), _meta(dk), _meta(dv), flags, wait_limit_ns)
     plan = _plans.get(key)

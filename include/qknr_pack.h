@@ -9,9 +9,13 @@
  * .. k_starts[b + 1] - 1; the starts are device arrays of batch + 1 values.
  * Formulas, scale, rounding and what a query that sees no key answers are
  * qknr_attn.h's, with q_len = q_starts[b + 1] - q_starts[b] and k_len likewise:
- * with causal, query i of a sequence sees its keys j <= i + k_len - q_len.  A
- * query that sees one key adds exactly nothing to dq and dk: its probability
- * is 1 whatever its score.
+ * with causal, query i of a sequence sees its keys j <= i + k_len - q_len.
+ *
+ * The backward pass's o and lse may run over more keys than the call has (keys
+ * split over calls, own keys beside a prefix): dq, dk and dv are then what its
+ * keys add to the gradients.  A query that sees one key and whose lse is that
+ * key's score adds exactly nothing to dq and dk: its probability is 1 whatever
+ * the score.
  *
  * Starts are clamped to 0 .. rows, and one below an earlier one counts as the
  * largest of them, so that no row belongs to two sequences whatever they say.
@@ -41,7 +45,7 @@ typedef struct qknr_pack_args {
   uint32_t abi_version;       /* QKNR_ABI_VERSION */
   int32_t dtype;              /* activations and gradients: QKNR_BF16 or QKNR_FP16 */
   const void *q, *k, *v;      /* device token rows */
-  void *o;                    /* forward: written; backward: the forward pass's */
+  void *o;                    /* forward: written; backward: the forward pass's, or a joint one */
   float *lse;                 /* device [n_heads_q, rows_q]; likewise */
   int64_t q_stride, k_stride, v_stride, o_stride;   /* elements per row; 0 = heads * D */
   int32_t batch;              /* sequences; 0: nothing is done */

@@ -1321,14 +1321,13 @@ __device__ __forceinline__ float grad_unlift(float lift) {
 
 // Whether the probability of the one key that a query sees (2^kP times it: `p`)
 // is 1 as far as fp32 can tell: the gradient of that score is then 0, and not
-// what rounding leaves of dP - delta.  `nl` is kP - lse (log2).  Score and
-// log-sum are good to 2^-20 of the log-sum, or 2^-13 where the score's terms
-// cancel; a lse over other calls' keys too that leaves them less than 2^-13 of
-// the probability leaves this key's gradient below the rounding of o in delta
-// (half a step of fp16: 2^-11).
+// what rounding leaves of dP - delta.  Score and log-sum are good to less than
+// 2^-12 up to about 1000; a lse over other calls' keys too that leaves them less
+// than that of the probability leaves this key's gradient below the rounding of
+// o in delta (half a step of fp16: 2^-11).
 template <typename T>
-__device__ __forceinline__ bool only_key(float p, float nl) {
-  return fabsf(__fmaf_rn(p, grad_scale_down(GradScale<T>::kP), -1.0f)) <= __fmaf_rn(fabsf(nl), 0x1p-20f, 0x1p-13f);
+__device__ __forceinline__ bool only_key(float p) {
+  return fabsf(__fmaf_rn(p, grad_scale_down(GradScale<T>::kP), -1.0f)) <= 0x1p-12f;
 }
 
 __device__ __forceinline__ float square_sum(const float2 (&v)[4]) {
@@ -1850,8 +1849,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         tmem_wait_load(d[0]);
         tmem_loaded(d[1]);
         c.arrive(DP_FREE);
-        const int seen = limit - (g.begin + j) * kTile - half * 64;
+        int seen = limit - (g.begin + j) * kTile - half * 64;
         if (__any_sync(0xffffffffu, seen < 64)) {
+          if (PLANNED && limit == 1 && seen == 1 && only_key<T>(s[0][0])) seen = 0;
           // p = 0 and a finite dp - delta where the row does not see the key
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -1861,7 +1861,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
               d[i][e] = 32 * i + e < seen ? d[i][e] : 0.0f;
             }
         }
-        if (PLANNED && limit == 1 && seen == 1 && only_key<T>(s[0][0], nl)) s[0][0] = 0.0f;
         if (done > 0) {
           // dQ has read the dS of the block before
           ok = c.wait(DS_FREE, done - 1);
@@ -2479,16 +2478,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dkv_kernel(const __grid_
 #pragma unroll
             for (int e = 0; e < 32; ++e) d[a][e] = 32 * a + e >= from ? d[a][e] : 0.0f;
         }
-        if (PLANNED) {
-          // queries up to here see this key alone
-          const int alone = key > 0 ? 0 : g.k_len == 1 ? 64 : p.causal ? from + 1 : 0;
-          if (__any_sync(0xffffffffu, alone > 0)) {
+        // A sequence of one key: dk is 0 too.  (Of several, what rounding leaves of the ds of a query that sees the first
+        // alone, 2^-20 of dP, goes into a sum with other queries'.)
+        if (PLANNED && g.k_len == 1) {
 #pragma unroll
-            for (int a = 0; a < 2; ++a)
+          for (int a = 0; a < 2; ++a)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (32 * a + e < alone && only_key<T>(s[a][e], mine[half * 64 + 32 * a + e])) s[a][e] = 0.0f;
-          }
+            for (int e = 0; e < 32; ++e)
+              if (only_key<T>(s[a][e])) s[a][e] = 0.0f;
         }
 #pragma unroll
         for (int a = 0; a < 2; ++a) {

@@ -14,8 +14,8 @@
  * The backward pass's o and lse may run over more keys than the call has (keys
  * split over calls, own keys beside a prefix): dq, dk and dv are then what its
  * keys add to the gradients.  A query that sees one key and whose lse is that
- * key's score adds exactly nothing to dq and dk: its probability is 1 whatever
- * the score.
+ * key's score gets exact zeros in dq, as a sequence's only key does in dk: the
+ * probability is 1 whatever the score.
  *
  * Starts are clamped to 0 .. rows, and one below an earlier one counts as the
  * largest of them, so that no row belongs to two sequences whatever they say.

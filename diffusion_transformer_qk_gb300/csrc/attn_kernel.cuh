@@ -56,7 +56,7 @@ struct AttnSeqs {
 
 // A plan in the caller's workspace.
 struct AttnPlan {
-  int4* head;                 // items of a head; first row of k that belongs to a sequence, the row after the last; waves
+  int2* head;                 // items of a head, waves
   int2* spans;                // [CTAs + 1] where each CTA's share behind the waves begins: tile of the line, unit
   int4* items;                // [items][2] q row, q_len, k row, k_len; first row in its sequence, blocks, units, query tiles before
   int2* runs;                 // [items] first and count of the items of its cost
@@ -120,6 +120,7 @@ struct AttnParams {
   float* dout_norm;           // |do| of each row, like delta
   float* v_top;               // [delta kernel's CTAs] none of its rows of v is longer
   int v_tops;
+  float* v_norm;              // PLANNED: [heads_k][seq_k] |v| of each row, and behind them [heads_k][blocks] the longest of 32 rows
   float* ds_top;              // [batch][heads_q][q_tiles][4] the largest bound on |ds| among 32 rows
   int q_tiles;                // 128-row tiles of the queries
   long long o_stride, dout_stride, dq_stride, dk_stride, dv_stride;   // bytes per row
@@ -139,7 +140,7 @@ struct AttnParams {
   int* status;
   unsigned long long wait_limit_ns;
   MemSpan sp_q, sp_o, sp_dout, sp_dq, sp_dk, sp_dv, sp_lse, sp_delta, sp_q_lens, sp_k_lens, sp_part, sp_stats,
-      sp_v, sp_dout_norm, sp_v_top, sp_ds_top;
+      sp_v, sp_dout_norm, sp_v_top, sp_v_norm, sp_ds_top;
   // PLANNED (batch is 1, seq_q and seq_k are all rows)
   AttnPlan plan;
   AttnSeqs seqs;
@@ -581,13 +582,13 @@ __device__ __forceinline__ bool attn_piece(const AttnParams& p, const AttnTable&
     return w.u0 <= w.u1;
   }
   if (!in_span(p.plan.spans + c, 16, p.plan.sp, p.status)) return false;
-  const int4 head = *p.plan.head;
+  const int2 head = *p.plan.head;
   int u1 = 0;                 // 0: to the end
-  if (s >= head.w) {
+  if (s >= head.y) {
     const int2 from = p.plan.spans[c], to = p.plan.spans[c + 1];
-    tile = from.x + s - head.w;
+    tile = from.x + s - head.y;
     if (tile > to.x || (tile == to.x && to.y == 0)) return false;
-    if (s == head.w) w.u0 = from.y;
+    if (s == head.y) w.u0 = from.y;
     if (tile == to.x) u1 = to.y;
   }
   if (tile >= head.x * p.seqs.heads || !in_span(p.plan.runs + tile / p.seqs.heads, 8, p.plan.sp, p.status)) return false;
@@ -1285,8 +1286,9 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const __grid_con
 // of v's rows): with 2^e <= b < 2^(e+1), 2^14 P (dP - delta) 2^-e stays below
 // 2^15, and half a subnormal step is 2^-39 b.  In dq a row is a query and has a
 // factor of its own; in dk all queries of a sample's key head go into one sum
-// and share the largest b.  Packed sequences take |do| V + |delta|, which is no
-// more and holds for an o over other keys too.  At 4096 x 24 x 128 the bounds cost 20 us (4 %), at
+// and share the largest b.  Packed sequences, which may be other people's, each
+// have a V of their own, and take |do| V + |delta|, which is no more than b and
+// holds for an o over other keys too.  At 4096 x 24 x 128 the bounds cost 20 us (4 %), at
 // 8 x 1 x 4096 x 24 x 128, where v's 200 MB are read once more for them, 34 of
 // 390.
 template <typename T>
@@ -1344,19 +1346,39 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+constexpr int kVBlock = 32;
+__host__ __device__ constexpr int v_blocks(int rows) { return rows / kVBlock + (rows % kVBlock != 0); }
+
+// A warp: the longest of rows [first, end) of v in a key head (PLANNED).
+__device__ __forceinline__ float longest_v(const AttnParams& p, int h, int first, int end, int lane) {
+  const float* rows = p.v_norm + h * static_cast<long long>(p.seq_k);
+  const float* blocks = p.v_norm + p.heads_k * static_cast<long long>(p.seq_k) + h * static_cast<long long>(v_blocks(p.seq_k));
+  const int b0 = v_blocks(first), b1 = end / kVBlock;            // whole blocks
+  auto at = [&](const float* from, int i, int to) { return i < to && in_span(from + i, 4, p.sp_v_norm, p.status) ? from[i] : 0.0f; };
+  // the rows before and behind them, and up to 4096 rows' blocks, on their way together
+  const float head = at(rows, first + lane, b0 < b1 ? b0 * kVBlock : end), tail = at(rows, (b0 < b1 ? b1 * kVBlock : first + 32) + lane, end);
+  float v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = at(blocks, b0 + 32 * k + lane, b1);
+  float top = fmaxf(fmaxf(fmaxf(head, tail), fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+#pragma unroll 4
+  for (int i = b0 + 128 + lane; i < b1; i += 32) top = fmaxf(top, at(blocks, i, b1));
+  return warp_max(top);
+}
+
 // delta = rowsum(do * o), one team of D/8 lanes per row.  Bound by HBM (50 us
 // for 2 x 8190 x 40 x 128, 6.7 TB/s).  Worked out inside the dq kernel instead,
 // whose tiles load do anyway, each tile waits for its rows of o: the same time
 // there, 150 against 145 us at 3 x 1999 x 16 on 4 heads x 64, causal.
-// fp16: also |do| of each row and a bound on the rows of v (GradScale).
+// fp16: also |do| of each row and a bound on the rows of v (GradScale); PLANNED:
+// |v| of each row, of which the dq kernel takes a sequence's.
 template <typename T, int D, bool PLANNED = false>
 __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constant__ AttnParams p) {
   constexpr int L = D / 8, TEAMS = 256 / L;
   const int team = threadIdx.x / L, lane = threadIdx.x % L;
   const long long items = static_cast<long long>(p.batch) * p.seq_q * p.heads_q;
   // A plan lets this pass begin once all before it has ended, and runs beside
-  // it: only the rows of v that count wait for the plan (gradients of 9215
-  // tokens x 16 on 4 x 64: 171 us without, 166 so).
+  // it (gradients of 9215 tokens x 16 on 4 x 64: 171 us without, 166 so).
   const bool beside_plan = PLANNED && p.from == kFromPlan;
   if (!beside_plan) grid_dependency_wait();
   // (row, head) with the heads of a row next to each other
@@ -1398,27 +1420,42 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
       }
     }
   }
-  if (beside_plan) grid_dependency_wait();        // and who waits for this pass has waited for the plan
-  if (GradScale<T>::kFromData) {
+  if (PLANNED && GradScale<T>::kFromData) {
+    // a warp per 32 rows of a key head
+    constexpr int ROWS = 32 / L;                  // of a load
+    const int blocks = v_blocks(p.seq_k), wl = threadIdx.x & 31;
+    for (long long u = blockIdx.x * 8LL + (threadIdx.x >> 5); u < static_cast<long long>(blocks) * p.heads_k; u += gridDim.x * 8LL) {
+      const int block = static_cast<int>(u / p.heads_k), h = static_cast<int>(u - static_cast<long long>(block) * p.heads_k);
+      const int row0 = block * kVBlock, there = p.seq_k - row0;
+      const char* src = p.v_in + (row0 + wl / L) * p.v_stride + h * (D * 2) + lane * 16;
+      float mine = 0.0f;                          // of row row0 + wl
+#pragma unroll 1
+      for (int i = 0; i < L; ++i) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (i * ROWS + wl / L < there && in_span(src, 16, p.sp_v, p.status)) x = *reinterpret_cast<const uint4*>(src);
+        src += ROWS * p.v_stride;
+        float2 y[4];
+        Elem<T>::unpack(x, y);
+        float n = square_sum(y);
+#pragma unroll
+        for (int off = L / 2; off >= 1; off >>= 1) n = __fadd_rn(n, __shfl_xor_sync(0xffffffffu, n, off));
+        n = __shfl_sync(0xffffffffu, n, wl % ROWS * L);
+        if (wl / ROWS == i) mine = n;
+      }
+      mine = wl < there ? __fsqrt_rn(mine) : 0.0f;
+      float* at = p.v_norm + h * static_cast<long long>(p.seq_k) + row0 + wl;
+      if (wl < there && in_span(at, 4, p.sp_v_norm, p.status)) *at = mine;
+      mine = warp_max(mine);
+      at = p.v_norm + p.heads_k * static_cast<long long>(p.seq_k) + h * static_cast<long long>(blocks) + block;
+      if (wl == 0 && in_span(at, 4, p.sp_v_norm, p.status)) *at = mine;
+    }
+  }
+  if (beside_plan) grid_dependency_wait();        // who waits for this pass has waited for the plan
+  if (!PLANNED && GradScale<T>::kFromData) {
     // No row of v that counts is longer than this: a lane keeps the largest sum
     // of its 8 columns, and a team's rows all stay below the sum over its lanes
     // (about sqrt(2) times the longest row; no shuffles until the end).
     constexpr int N = 2;                          // rows in flight
-    __shared__ int range[2];                      // PLANNED: the rows of v that belong to a sequence
-    if (PLANNED) {
-      if (threadIdx.x < 32 && p.from == kFromTable) {
-        const int v = static_cast<int>(threadIdx.x) < p.seqs.batch
-                          ? plan_start(p.seqs.k_starts, p.seqs.sp_k_starts, threadIdx.x + 1, p.seqs.seq_k, p.status)
-                          : 0;
-        const int first = plan_start(p.seqs.k_starts, p.seqs.sp_k_starts, 0, p.seqs.seq_k, p.status);
-        const int end = __reduce_max_sync(0xffffffffu, max(v, first));
-        if (threadIdx.x == 0) range[0] = first, range[1] = end;
-      } else if (threadIdx.x == 0) {
-        range[0] = p.plan.head->y;
-        range[1] = p.plan.head->z;
-      }
-      __syncthreads();
-    }
     const long long rows_v = static_cast<long long>(p.batch) * p.seq_k * p.heads_k, step = static_cast<long long>(gridDim.x) * TEAMS;
     const int h_step = static_cast<int>(step % p.heads_k), row_step = static_cast<int>(step / p.heads_k);
     long long it = static_cast<long long>(blockIdx.x) * TEAMS + team;
@@ -1432,7 +1469,6 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
         if (it < rows_v) {
           const char* src = p.v_in + row * p.v_stride + h * (D * 2) + lane * 16;
           bool counts = in_span(src, 16, p.sp_v, p.status);
-          if (PLANNED) counts = counts && row >= range[0] && row < range[1];
           if (p.k_lens) {
             const int b = row / p.seq_k;
             counts = counts && row - b * p.seq_k < clamp_len(p.k_lens, b, p.seq_k, p.sp_k_lens, p.status);
@@ -1507,6 +1543,7 @@ struct Seg {
   int q_row, k_row;           // PLANNED: the sequence's first rows
   int q_len, k_len, diag;
   int top;                    // the tile's place in ds_top
+  float v_top;                // PLANNED, fp16: no row of the sequence's v is longer
   int begin, n;               // key blocks [begin, begin + n)
   bool opens;                 // the tile's first piece
 };
@@ -1596,7 +1633,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     g.k_len = v[1].w;
     g.n = v[2].x;
     g.top = v[2].y;
-    g.opens = v[2].z;
+    g.v_top = __int_as_float(v[2].z);
+    g.opens = v[2].w & 2;
     g.diag = g.k_len - g.q_len;
     return true;
   };
@@ -1614,7 +1652,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         {
           // the next tile's queries come from HBM: on their way while this one's keys come from L2
           Seg next;
-          if (segment(s + 1, next, false) && next.n > 0) {
+          // (not before the first one's loads, which would wait for a second piece)
+          if ((!PLANNED || s > 0) && segment(s + 1, next, false) && next.n > 0) {
             tma_prefetch_tile(&p.map_q, next.q_row + next.q0, next.h, next.b);
             tma_prefetch_tile(&p.map_do, next.q_row + next.q0, next.h, next.b);
           }
@@ -1739,8 +1778,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     Seg g;
     for (int s = 0;; ++s) {
       const bool more = work_out(s, g);
+      // (A barrier of its own for the bound, which only the workers want, is no faster.  Gradients of 9215 tokens x 16 on 4
+      // x 64: 168 us, 167 with one bound for all sequences.)
+      float v_top = 0.0f;
+      if (GradScale<T>::kFromData && more && g.n > 0)
+        v_top = longest_v(p, g.h / p.group, g.k_row, g.k_row + g.k_len, c.lane);
       if (!c.hand_round(PIECE_FULL, PIECE_EMPTY, kPiecesAt, s, make_int4(g.h, g.q0, g.slot, g.begin),
-                        make_int4(g.q_row, g.q_len, g.k_row, g.k_len), make_int4(g.n, g.top, g.opens, more)) || !more)
+                        make_int4(g.q_row, g.q_len, g.k_row, g.k_len),
+                        make_int4(g.n, g.top, __float_as_int(v_top), more ? (g.opens ? 3 : 1) : 0)) || !more)
         break;
     }
   } else if (c.warp < kAttnMmaWarp) {
@@ -1776,7 +1821,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
       return true;
     };
     float v_top = 0.0f;                           // no row of v is longer
-    if (GradScale<T>::kFromData) {
+    if (!PLANNED && GradScale<T>::kFromData) {
 #pragma unroll 4
       for (int i = c.lane; i < p.v_tops; i += 32)
         if (in_span(p.v_top + i, 4, p.sp_v_top, p.status)) v_top = fmaxf(v_top, p.v_top[i]);
@@ -1790,7 +1835,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
         lse = p.lse[at];
         delta = p.delta[at];
         if (GradScale<T>::kFromData && in_span(p.dout_norm + at, 4, p.sp_dout_norm, p.status))
-          bound = PLANNED ? __fmaf_rn(v_top, p.dout_norm[at], fabsf(delta)) : __fmul_rn(2.0f * v_top, p.dout_norm[at]);
+          bound = PLANNED ? __fmaf_rn(g.v_top, p.dout_norm[at], fabsf(delta)) : __fmul_rn(2.0f * v_top, p.dout_norm[at]);
       }
     };
     unsigned char* stage = smem + (1 + kK + kV) * kTileBytes<D> + c.warp * kStage<D>;

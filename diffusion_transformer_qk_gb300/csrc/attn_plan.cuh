@@ -91,7 +91,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   int items = 0, q_tiles = 0, q_at = 0, k_at = 0;
   if (j.q_starts) q_at = plan_start(j.q_starts, j.sp_q_starts, 0, j.seq_q, p.status);
   if (j.k_starts) k_at = plan_start(j.k_starts, j.sp_k_starts, 0, j.seq_k, p.status);
-  const int k_first = k_at;
   auto range = [&](int v, bool there, int& at, int& lo, int& len) {
     int all;
     const int end = max(plan_scan<int>(v, most, iwarps, all), at);
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     }
     if (in_span(out.spans + c, 8, out.sp, p.status)) out.spans[c] = at;
   }
-  if (tid == 0 && in_span(out.head, 16, out.sp, p.status)) *out.head = make_int4(items, k_first, k_at, waves);
+  if (tid == 0 && in_span(out.head, 8, out.sp, p.status)) *out.head = make_int2(items, waves);
 }
 
 // ---------------------------------------------------------------------------

@@ -32,7 +32,7 @@ qknr::AttnPlan take_plan(Space* ws, long long items, long long batch, bool seq_i
   qknr::AttnPlan p;
   const size_t from = ws->used;
   char* const lo = ws->base + from;
-  p.head = ws->take<int4>(1);
+  p.head = ws->take<int2>(1);
   p.spans = ws->take<int2>(kCtas + 1);
   p.items = ws->take<int4>(2 * items);
   p.runs = ws->take<int2>(items);
@@ -264,11 +264,9 @@ bool table_does(const Job& j, long long batch) {
 struct PackSpace {
   Job job[2];
   qknr::AttnPlan plan[2] = {};
-  float *delta, *dout_norm, *v_top, *ds_top;
-  size_t delta_n, ds_top_n;
+  float *delta, *dout_norm, *v_norm, *ds_top;
+  size_t delta_n, v_norm_n, ds_top_n;
 };
-
-constexpr int kDeltaCtas = 8 * kCtas;             // CTAs of the delta kernel at most
 
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k, p->batch ? p->rows_k / p->batch : 0);
@@ -296,7 +294,8 @@ void pack_backward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space
   const bool lifts = a->dtype == QKNR_FP16;
   s->ds_top_n = lifts ? static_cast<size_t>(a->n_heads_q) * s->job[0].items * 4 : 0;
   s->dout_norm = ws->take<float>(lifts ? s->delta_n : 0);
-  s->v_top = ws->take<float>(lifts ? kDeltaCtas : 0);
+  s->v_norm_n = lifts ? a->n_heads_k * (static_cast<size_t>(p->rows_k) + qknr::v_blocks(p->rows_k)) : 0;
+  s->v_norm = ws->take<float>(s->v_norm_n);
   s->ds_top = ws->take<float>(s->ds_top_n);
   // the parts one after the other in the same place
   Space here = *ws, end = *ws;
@@ -616,11 +615,11 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
     kp.v_stride = v.stride * 2;
     kp.sp_v = msp(v.span);
     kp.dout_norm = s.dout_norm;
-    kp.v_top = s.v_top;
+    kp.v_norm = s.v_norm;
     kp.ds_top = s.ds_top;
     kp.q_tiles = static_cast<int>(s.job[0].items);
     kp.sp_dout_norm = msp(span_of(s.dout_norm, 1, 0, static_cast<long long>(s.delta_n * 4)));
-    kp.sp_v_top = msp(span_of(s.v_top, 1, 0, 4LL * kDeltaCtas));
+    kp.sp_v_norm = msp(span_of(s.v_norm, 1, 0, static_cast<long long>(s.v_norm_n * 4)));
     kp.sp_ds_top = msp(span_of(s.ds_top, 1, 0, static_cast<long long>(s.ds_top_n * 4)));
   }
 
@@ -655,8 +654,6 @@ qknr_status qknr_pack_backward(const qknr_pack_args* p, qknr_stream_t stream) {
       if (v_grid > grid) grid = v_grid;
     }
     if (grid > 8LL * di.num_sms) grid = 8LL * di.num_sms;
-    if (grid > kDeltaCtas) grid = kDeltaCtas;
-    kp.v_tops = static_cast<int>(grid);
     use(0);
     void* kargs[] = {&kp};
     st = qknr_host::launch_kernel(fn.delta, static_cast<int>(grid), 256, 0, reinterpret_cast<cudaStream_t>(stream), kargs,

@@ -1137,10 +1137,12 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, rows_per_batch=None, unit_
     float32: [C], or a row for each sample where ``rows_per_batch`` is given or
     weight has rows (for its first rows, if x has fewer samples).  ``out``
     receives dx (default: a new tensor; ``out=dy`` is in place)."""
+    T, C = x.shape
+    if T == 0 and weight is not None and weight.dim() == 1:
+        rows_per_batch = None                     # no samples, but a gradient of the one row: zero
     key = ("ln_bwd", _meta(dy), _meta(x), _meta(weight), _meta(out), rows_per_batch, unit_offset, flags,
            wait_limit_ns)
     plan = _plans.get(key)
-    T, C = x.shape
     if plan is None:
         _one_device(x, dy, weight, out)
         a = ln_args(x, weight, None, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags,
@@ -1277,10 +1279,12 @@ def rms_norm_backward(dy, x, weight, rstd, *, dsum=None, rows_per_batch=None, un
     the gradient that reaches h past the norm, is added to it.  dweight is
     float32, [C] or a row for each sample (None without a weight).  ``out``
     receives dx (default: a new tensor; dy or dsum: in place)."""
+    T, C = x.shape
+    if T == 0 and weight is not None and weight.dim() == 1:
+        rows_per_batch = None                     # no samples, but a gradient of the one row: zero
     key = ("rms_bwd", _meta(dy), _meta(x), _meta(weight), _meta(dsum), _meta(out), rows_per_batch, unit_offset, flags,
            wait_limit_ns)
     plan = _plans.get(key)
-    T, C = x.shape
     if plan is None:
         _one_device(x, dy, weight, dsum, out)
         a = rms_args(x, weight, rows_per_batch=rows_per_batch, unit_offset=unit_offset, flags=flags,

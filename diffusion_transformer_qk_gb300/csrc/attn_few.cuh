@@ -63,8 +63,8 @@ __device__ __forceinline__ void few_mma<__half>(float (&c)[4], const uint32_t (&
 // two halves, g + 8; of their accumulators columns 64 cc + 16 t + 0 .. 15.
 // PLANNED: tiles of p.few_rows rows from the plan.  The warps form groups of
 // p.few_group, each on a tile of its own: over a few hundred keys a tile's
-// beginning and end take longer than its steps (64 samples of up to 512 keys of 8
-// heads x 128, beside their prefix: 69 us with all twelve warps on a tile, 62 with
+// beginning and end take longer than its steps (64 samples of 512 keys of 8 heads x
+// 128 beside their prefix of 8190: 77 us with all twelve warps on a tile, 59 with
 // three).
 template <typename T, int D, int H, bool PLANNED = false>
 __global__ void __launch_bounds__(32 * few_warps(8 * H), 1) attn_few_kernel(const __grid_constant__ AttnParams p) {

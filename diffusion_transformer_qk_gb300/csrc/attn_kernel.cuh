@@ -79,7 +79,8 @@ struct AttnTable {
 // (kFromUniform), or samples of a fixed number of rows whose tiles all go out
 // whole, each working out its own lengths (kFromSamples; a few queries).
 // kFromShares: the table's sequences in equal shares, cut inside a tile (a few
-// queries): 16 x 1 query over up to 4096 keys of 24 heads x 128 68 us, 73 with a plan.
+// queries): 7 % less time than with a plan at 16 x 1 query over up to 4096 keys of
+// 24 heads x 128, 70 us.
 enum { kFromPlan, kFromTable, kFromShares, kFromUniform, kFromSamples };
 struct AttnUniform {
   int tiles, units;           // of the line; of each tile
@@ -91,7 +92,7 @@ struct AttnUniform {
 // The pieces of a CTA's share as the forward and dq kernels' planning warp
 // hands them round: the other roles read a piece from shared memory, a few
 // tiles behind, instead of each working it out from global memory where a tile
-// begins and ends (2 x 4608 x 48 x 128, forward: 717 us so, 678 handed round).
+// begins and ends (2 x 4608 x 48 x 128, forward: 5 % of its time).
 constexpr int kPieces = 4;
 struct AttnPieces {
   int4 at[kPieces][3];
@@ -1378,7 +1379,7 @@ __global__ void __launch_bounds__(256, 8) attn_delta_kernel(const __grid_constan
   const int team = threadIdx.x / L, lane = threadIdx.x % L;
   const long long items = static_cast<long long>(p.batch) * p.seq_q * p.heads_q;
   // A plan lets this pass begin once all before it has ended, and runs beside
-  // it (gradients of 9215 tokens x 16 on 4 x 64: 171 us without, 166 so).
+  // it (gradients of 9215 tokens x 16 on 4 x 64, 169 us: 5 more without).
   const bool beside_plan = PLANNED && p.from == kFromPlan;
   if (!beside_plan) grid_dependency_wait();
   // (row, head) with the heads of a row next to each other
@@ -1779,7 +1780,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_dq_kernel(const __grid_c
     for (int s = 0;; ++s) {
       const bool more = work_out(s, g);
       // (A barrier of its own for the bound, which only the workers want, is no faster.  Gradients of 9215 tokens x 16 on 4
-      // x 64: 168 us, 167 with one bound for all sequences.)
+      // x 64, 169 us: 1 % more than with one bound for all sequences.)
       float v_top = 0.0f;
       if (GradScale<T>::kFromData && more && g.n > 0)
         v_top = longest_v(p, g.h / p.group, g.k_row, g.k_row + g.k_len, c.lane);

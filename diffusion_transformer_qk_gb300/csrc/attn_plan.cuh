@@ -6,8 +6,8 @@
 // call's tiles form a line: the costliest items first, those of one cost
 // together, head by head.  CTAs take the line's tiles in waves, every other wave
 // the other way round, so that neighbours read the same keys at the same time
-// (2 x 4608 x 48 x 128, whose keys and values are 226 MB: 3 GB from HBM and 785
-// us where each CTA walks a stretch of the line of its own, 678 in waves) and
+// (2 x 4608 x 48 x 128, whose keys and values are 226 MB: 3 GB from HBM and 16 %
+// more time where each CTA walks a stretch of the line of its own) and
 // all get their part of the costly ones.  The waves end where a CTA would get
 // more than its share of the whole; what is left of the line, its cheapest
 // tiles, is dealt out so that all shares are equal, cut inside a tile where that

@@ -82,16 +82,20 @@ Job job_of(const qknr_attn_args* a, int kind, int rows, int heads, long long of_
   return j;
 }
 
-// A few queries a sequence: the tiles that read keys once for all of them
-// (attn_api.cu).  The host knows their mean only, and any mix comes out right.
+// A few queries a sequence: the tiles that read keys once for 16 of their rows
+// (attn_api.cu).  The host knows their mean only, and one form is the whole
+// call's: any mix comes out right, but the rarer kind takes its time (one causal
+// sequence of 4096 beside 300 single tokens that each see 1500 keys, 24 heads x 128:
+// 2066 us, in two calls 91 and 806; beside 250, now in tiles, 1023 for 91 and 694).
 bool few(long long rows, long long batch) { return rows <= qknr::kFewRows * batch; }
 
 // Warps that share a tile of a few queries: all of a CTA's where there is much
 // to read.  Over a few hundred keys a tile's beginning and end take longer than
 // its steps: then three (of eight: four), so that more tiles are in work at a
-// time (64 samples of up to 512 keys of 8 heads x 128 beside their prefix: 69 us
-// with twelve, 62 with three; 16 x 1 query over up to 4096 keys of 24 heads: 73
-// against 82).
+// time (64 samples of 512 keys of 8 heads x 128 beside their prefix of 8190: 77 us
+// with twelve, 59 with three; 128 x 1 query over up to 400 keys, 32 on 8 heads: 47
+// against 31; over up to 4096 keys of 24 heads twelve take a tenth less than
+// three).
 constexpr long long kFewGroupKeys = 768;
 int few_group(int rows, long long mean_keys) { return mean_keys > kFewGroupKeys ? qknr::few_warps(rows) : rows == 8 ? 3 : 4; }
 

@@ -29,8 +29,9 @@
  *     dk[j,d]  = scale * sum_i ds[i,j] * q[i,d]    (and over the query heads
  *     dv[j,d]  = sum_i p[i,j] * do[i,d]             of a shared key head)
  *
- * A call of at most 16 queries per sample reads every key and value once for
- * all queries of a key head; longer ones take 256-query tiles.
+ * A call of at most 16 queries per sample reads a sample's keys and values once
+ * for each 16 of the queries of a key head (all heads of its group together);
+ * longer ones take 256-query tiles.
  *
  * Products run on the tensor cores with fp32 accumulators; p and ds enter
  * their second product rounded to the activation dtype, times powers of two

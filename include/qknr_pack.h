@@ -23,9 +23,16 @@
  * neither read into a result nor written: o, lse, dq, dk and dv keep what
  * they held there.
  *
- * Work is shared out on the device by the sequences' lengths; a call whose
- * sequences have 16 queries or fewer on average reads every key and value once
- * for all queries of a key head.  No atomics: equal calls give equal bits.
+ * Work is shared out on the device by the sequences' lengths.  A call whose
+ * sequences have 16 queries or fewer on average takes a sequence's group * q_len
+ * query rows of a key head (group = n_heads_q / n_heads_k) 16 at a time, 8 where
+ * they are 8 or fewer on average, and reads the sequence's keys and values once
+ * for each 16 or 8; other calls take tiles of 256 queries of a head.  The form
+ * is the whole call's: long sequences beside many single tokens are better off
+ * in a call of their own.
+ *
+ * No atomics: equal calls give equal bits.  What one sequence's rows hold
+ * changes no bit of another's results.
  *
  * Ownership and errors follow qknr.h: the caller owns every buffer (the
  * workspace included), the library allocates nothing and never

@@ -16,9 +16,10 @@
  * y holds 8-bit floats (e4m3, no infinities) and scales the fp32 factors that
  * take them back, one per row (scale_block 0) or one per 128 columns:
  *
- *     scale = max(max|h * rstd * gain| / 448, 2^-126)      y = h * rstd * gain / scale
+ *     scale = max(max|h * rstd * gain| / 448, 2^-126)      y = h * rstd * gain * (1 / scale)
  *
- * a NaN in the values a scale covers makes all of them, and the scale, NaN.
+ * with the reciprocal rounded to fp32 (a value next to the middle of two 8-bit
+ * ones may go to the other one than the quotient would); a NaN in the values a scale covers makes all of them, and the scale, NaN.
  *
  * The backward pass takes x = h as the forward pass rounded it (its sum, or x
  * where there was no residual), its rstd, dy = dL/dy and, optionally, dsum,

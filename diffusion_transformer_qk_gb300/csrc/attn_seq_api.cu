@@ -275,9 +275,14 @@ struct PackSpace {
 void pack_forward_space(const qknr_pack_args* p, const qknr_attn_args* a, Space* ws, PackSpace* s, qknr::AttnParams* kp) {
   s->job[0] = forward_job(a, p->rows_q, p->batch, p->rows_k, p->batch ? p->rows_k / p->batch : 0);
   Job& j = s->job[0];
-  if (table_does(j, p->batch)) j.from = qknr::kFromTable;
-  else if (is_few(j) && p->batch <= qknr::kTableSeqs && static_cast<double>(j.items) * static_cast<double>(j.units) < 2e9)
-    j.from = qknr::kFromShares;                   // its spans and cut tiles' records take a plan's place
+  if (table_does(j, p->batch)) {
+    j.from = qknr::kFromTable;
+  } else if (is_few(j) && p->batch <= qknr::kTableSeqs && static_cast<double>(j.items) * static_cast<double>(j.units) < 2e9) {
+    // Its spans and cut tiles' records take a plan's place.  Equal shares cut any tile that is long enough, whatever a cut
+    // costs.
+    j.from = qknr::kFromShares;
+    j.cuts = qknr::share_cut(2, static_cast<int>(j.units), over_units(a, j)) == 2;
+  }
   if (j.from != qknr::kFromTable) s->plan[0] = take_plan(ws, j.items > kCtas ? j.items : kCtas, p->batch, false);
   take_parts(ws, a, s->job[0], true, kp);
 }

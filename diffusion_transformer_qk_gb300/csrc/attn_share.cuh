@@ -6,7 +6,7 @@ namespace qknr {
 
 // A share is to begin `o` of `u` units into a tile, `over` of which are its
 // beginning and end: the unit where it does begin, `u` for the next tile's first.
-// No cut where it saves little, two blocks or less from an end of the tile's
+// No cut where it saves little, less than two blocks from an end of the tile's
 // blocks: such a place moves to the nearer end of the tile, and where that is
 // its beginning and the tile may be cut before here, to the last such cut.  A
 // larger `o` never moves before a smaller one's place: shares that began in

@@ -52,9 +52,9 @@ __device__ __forceinline__ float abs_max(const float2 (&v)[4]) {
 // the scale of values up to m, and what they are multiplied by
 __device__ __forceinline__ float f8_scale(float m) { return max_nan(__fdiv_rn(m, kF8Max), kF8ScaleMin); }
 
-// Eight values times f in 8 bits.  f is the scale's reciprocal: a division for
-// each value takes the kernel from 63 to 84 us at 2 x 4608 x 6144, and moves a
-// value by one 8-bit step where the product is next to the middle of two.
+// Eight values times f in 8 bits.  f is the scale's reciprocal: with a division
+// for each value the kernel takes 84 us instead of 63 at 2 x 4608 x 6144, and the
+// results differ, by one 8-bit step, only next to the middle of two 8-bit values.
 __device__ __forceinline__ uint2 pack_f8(const float2 (&v)[4], float f) {
   const float2 F = make_float2(f, f);
   uint32_t h[4];
